@@ -314,6 +314,186 @@ muon_status muon_dp_partition(const int64_t* sizes, const double* loads, const i
 muon_status muon_tp_micro_groups(const double* cost, int32_t n, int32_t ranks, double c_max, int32_t* order,
                                  int32_t* group_of, int32_t* host_of, int32_t* n_groups);
 
+/* ---------------------------------------------------------------------------
+ * Layer operators: what a training step runs around the optimizer step, from a
+ * block's norms to the weight gradients that muon_step reads. Activations that
+ * the backward pass needs are kept in 8 bits.
+ *
+ * These calls keep nothing: every one takes its descriptors by value of the
+ * call, only launches kernels on `stream` (no allocation, copy, memset or host
+ * synchronisation), and may be captured in a HIP graph. Results are bitwise
+ * deterministic. Arguments are validated before any HIP call. rows may be 0
+ * (weight gradients are then 0, or beta*C); views without rows may be NULL. Device pointers named below
+ * address row-major views, rows x cols with a row stride in elements (ld*, at
+ * least cols, at most 2^24); any alignment to the element size and any stride
+ * is right, and views with 16-byte aligned rows and cols a multiple of 8 take
+ * the fast path. Written views must not overlap any other view of the call
+ * (ALIAS); views that are only read may share elements.
+ *
+ * 8-bit checkpoints. A row of cols elements is cut into groups of 32 columns
+ * (the last may be shorter). A group has one exponent byte E; an element is
+ * one byte q and stands for q * 2^(E-127), q being an int8 in [-127, 127]
+ * (MUON_Q8_INT8) or an e4m3 number of at most 448 (MUON_Q8_E4M3).
+ * Saving chooses the smallest E in [17, 254] with max|x| <= 127 * 2^(E-127)
+ * (int8; 448 for e4m3) over the group, so nothing saturates, and rounds
+ * x / 2^(E-127) to nearest, ties to even. A group holding an infinity or a NaN
+ * gets E = 255 and q = 0 and stands for NaNs, so that a bad activation shows up
+ * in the gradients. Every value a checkpoint stands for is exactly a bf16
+ * number. int8 is the more accurate of the two for activations whose groups
+ * are near Gaussian (0.7% against 2.6% relative error), e4m3 where elements of
+ * a group differ by more than two orders of magnitude.
+ *
+ * q     rows x ldq bytes, 16-byte aligned, ldq a multiple of 16 and >= cols;
+ *       the bytes between cols and the next multiple of 16 are padding, which
+ *       the library may read and write;
+ * e     rows x lde bytes, lde >= ceil(cols / 32). */
+typedef enum { MUON_Q8_INT8 = 0, MUON_Q8_E4M3 = 1 } muon_q8_kind;
+
+typedef struct {
+  void* q;
+  void* e;
+  int64_t rows;
+  int64_t cols;
+  int64_t ldq;
+  int64_t lde;
+  int32_t kind; /* muon_q8_kind */
+  int32_t reserved;
+} muon_q8;
+
+/* Saves x (out->rows x out->cols, row stride ldx, MUON_F32 or MUON_BF16) into
+ * the checkpoint out. Errors: INVALID_ARG (null pointers, rows outside
+ * [0, 2^31 - 1], cols outside [1, 2^24], strides), ALIGN, ALIAS, UNSUPPORTED
+ * (dtype, kind), HIP. */
+muon_status muon_q8_save(const void* x, int64_t ldx, int32_t dtype, const muon_q8* out, void* stream);
+
+/* Loads a checkpoint: x gets the values it stands for (fp32, or bf16, which
+ * holds them exactly). Same errors. */
+muon_status muon_q8_load(const muon_q8* in, void* x, int64_t ldx, int32_t dtype, void* stream);
+
+/* The norm site between two blocks: the norm after a block, its gate and the
+ * residual scales, the residual sum, and the norm before the next block, row
+ * by row in one pass:
+ *   v = branch / rms(branch)             (v = branch if w_post is NULL)
+ *   y = res_scale*residual + branch_scale * gate * w_post * v
+ *   u = y / rms(y),   h = w_pre * u      rms(x) = sqrt(mean(x^2) + eps)
+ * All arithmetic is fp32; y and h are rounded to dtype once, at the end (h is
+ * formed from the unrounded y).
+ * branch, residual  rows x cols, read only
+ * w_pre, w_post     cols elements; w_post may be NULL (no norm after the block)
+ * gate              NULL (1), cols elements with ld_gate = 0 (one gate for all
+ *                   rows), or rows x cols with row stride ld_gate >= cols
+ * y, h              rows x cols, written
+ * rstd_y, rstd_b    rows floats, 1/rms(y) and 1/rms(branch), written if not
+ *                   NULL; a backward pass needs rstd_y, and rstd_b with w_post
+ * u, v              8-bit checkpoints, written if their q is not NULL; a
+ *                   backward pass needs u, and v with w_post or gate
+ * cols is at most 32768 (a row stays in one workgroup's registers). */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  const void* branch;
+  int64_t ld_branch;
+  const void* residual;
+  int64_t ld_residual;
+  const void* w_pre;
+  const void* w_post;
+  const void* gate;
+  int64_t ld_gate;
+  void* y;
+  int64_t ld_y;
+  void* h;
+  int64_t ld_h;
+  float* rstd_y;
+  float* rstd_b;
+  muon_q8 u;
+  muon_q8 v;
+  float res_scale;
+  float branch_scale;
+  float eps;
+  int32_t dtype; /* MUON_F32 or MUON_BF16, of every tensor but rstd, u and v */
+} muon_norm_site;
+
+/* Errors: INVALID_ARG (null pointers, sizes, strides, non-finite scales,
+ * eps < 0), ALIGN, ALIAS, UNSUPPORTED (dtype, kind, cols > 32768), HIP. */
+muon_status muon_norm_forward(const muon_norm_site* site, void* stream);
+
+/* Gradients of a norm site from its checkpoints. dy and dh are the gradients
+ * of y (NULL: zero) and h. With s the whole gradient of y,
+ *   s          = dy + rstd_y*(du - u*mean(du*u)),     du = w_pre*dh
+ *   d_residual = res_scale*s
+ *   d_branch   = rstd_b*(dv - v*mean(dv*v)),          dv = branch_scale*s*gate*w_post
+ *                (dv itself if w_post is NULL)
+ *   d_w_pre    = sum over rows of dh*u
+ *   d_w_post   = sum over rows of branch_scale*s*gate*v
+ *   d_gate     = branch_scale*s*w_post*v, summed over rows if ld_gate is 0
+ * d_w_pre, d_w_post (cols elements) and d_gate (cols elements, or rows x cols
+ * with row stride ld_d_gate) may be NULL: not wanted. Weight gradients are
+ * summed in fp32 in a fixed order and rounded to dtype once.
+ * workspace: device memory of at least muon_norm_backward_workspace bytes,
+ * 16-byte aligned, scratch of this call until it has run. */
+typedef struct {
+  const void* dy;
+  int64_t ld_dy;
+  const void* dh;
+  int64_t ld_dh;
+  void* d_residual;
+  int64_t ld_d_residual;
+  void* d_branch;
+  int64_t ld_d_branch;
+  void* d_w_pre;
+  void* d_w_post;
+  void* d_gate;
+  int64_t ld_d_gate;
+  void* workspace;
+  size_t workspace_bytes;
+} muon_norm_grads;
+
+/* Reads rows, cols, w_pre, w_post, gate, rstd_y, rstd_b, u, v, the scales and
+ * dtype of site (branch, residual, y and h may be NULL). Errors: those of
+ * muon_norm_forward, and INVALID_ARG for a missing or short workspace or a
+ * gradient of a weight that the site does not have. */
+muon_status muon_norm_backward(const muon_norm_site* site, const muon_norm_grads* grads, void* stream);
+
+/* Workspace bytes of muon_norm_backward for rows x cols (host, no GPU). */
+muon_status muon_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
+
+/* One weight gradient of a linear layer Y = X W^T, from the saved input:
+ *   G = dY^T (X diag(scale)) + beta*C
+ * dy     rows x n, dtype, row stride ld_dy: the gradient of the output
+ * x      rows x k checkpoint of the input
+ * scale  NULL, or k elements of dtype: a norm weight, when x is the normalised
+ *        row u of a norm site and the layer's input was h = w_pre * u
+ * g      n x k, contiguous, g_dtype, 16-byte aligned: what muon_matrix.g takes
+ * c      n x k, contiguous, g_dtype, 16-byte aligned: read if beta != 0; may
+ *        be g itself (accumulation over micro batches)
+ * bf16 dY: bf16 MFMA with fp32 accumulation; the products are exact, since
+ * checkpoint values are bf16 numbers. fp32 dY is cut into three bf16 numbers
+ * that add up to it (24 bits), for fp32 accuracy on the bf16 matrix cores.
+ * g is rounded to g_dtype once. */
+typedef struct {
+  const void* dy;
+  int64_t ld_dy;
+  muon_q8 x;
+  const void* scale;
+  void* g;
+  const void* c;
+  int64_t n;
+  float beta;
+  int32_t reserved;
+} muon_wgrad_item;
+
+/* Weight gradients of n_items layers in one go (few layers alone fill the
+ * GPU). dtype (of dy and scale) and g_dtype are MUON_F32 or MUON_BF16; every
+ * x has the same kind. Errors: INVALID_ARG (null pointers, n or cols outside
+ * [1, 2^24], rows outside [0, 2^31 - 1], strides, non-finite beta, a short
+ * workspace, checkpoints of different kinds), ALIGN, ALIAS (c == g is fine),
+ * UNSUPPORTED, HIP. workspace is scratch of this call until it has run:
+ * muon_wgrad_workspace bytes (which may be 0), 16-byte aligned. */
+muon_status muon_wgrad(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+muon_status muon_wgrad_workspace(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype,
+                                 size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

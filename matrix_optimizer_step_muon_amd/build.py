@@ -28,6 +28,8 @@ ARCH = "gfx950"
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", f"-I{INCLUDE}", f"-I{CSRC}",
           "-Wall", "-Wno-unused-function"]
+SOURCES = ["muon_kernels.hip", "muon_api.cpp", "muon_partition.cpp", "layer_kernels.hip",
+           "wgrad_kernels.hip", "layer_api.cpp"]
 
 
 def hipcc() -> str:
@@ -52,14 +54,13 @@ def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     cc = hipcc()
-    k_obj = os.path.join(BUILD, "muon_kernels.o")
-    a_obj = os.path.join(BUILD, "muon_api.o")
-    p_obj = os.path.join(BUILD, "muon_partition.o")
-    _run([cc, *COMMON, *DEVICE_FLAGS, "-c", os.path.join(CSRC, "muon_kernels.hip"), "-o", k_obj])
-    _run([cc, *COMMON, "-c", os.path.join(CSRC, "muon_api.cpp"), "-o", a_obj])
-    _run([cc, *COMMON, "-c", os.path.join(CSRC, "muon_partition.cpp"), "-o", p_obj])
+    objs = []
+    for src in SOURCES:
+        objs.append(os.path.join(BUILD, os.path.splitext(src)[0] + ".o"))
+        flags = DEVICE_FLAGS if src.endswith(".hip") else []
+        _run([cc, *COMMON, *flags, "-c", os.path.join(CSRC, src), "-o", objs[-1]])
     tmp = LIB + ".tmp"
-    _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, k_obj, a_obj, p_obj,
+    _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs,
           "-Wl,-soname,libmuon.so", "-Wl,-rpath,/opt/rocm/lib"])
     os.replace(tmp, LIB)
     return LIB

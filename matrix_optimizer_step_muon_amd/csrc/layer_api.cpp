@@ -1,0 +1,436 @@
+// C ABI of the layer operators (include/muon.h): validation, the split of a
+// weight gradient's work over the GPU, and the launches. Nothing is kept
+// between calls.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "layer_internal.h"
+#include "muon.h"
+
+muon_status muon_fail_message(muon_status st, const char* msg);
+
+namespace {
+
+constexpr int64_t kMaxRows = INT32_MAX, kMaxCols = int64_t(1) << 24;
+
+muon_status fail(muon_status st, const std::string& msg) { return muon_fail_message(st, msg.c_str()); }
+muon_status hip_status(hipError_t e) {
+  if (e == hipSuccess) return MUON_OK;
+  (void)hipGetLastError();
+  return fail(MUON_ERR_HIP, std::string("kernel launch: ") + hipGetErrorString(e));
+}
+
+// Runs f, turning a C++ exception (out of host memory) into a status.
+template <class F>
+muon_status guarded(F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return muon_fail_message(MUON_ERR_OOM, "out of host memory");
+  } catch (...) {
+    return muon_fail_message(MUON_ERR_INVALID_ARG, "unexpected error");
+  }
+}
+
+// A strided view in bytes: row i is [base + i*pitch, base + i*pitch + width).
+struct View {
+  uintptr_t base;
+  int64_t rows, width, pitch;
+  bool written;
+  const char* name;
+  int item;
+};
+
+// The views of one call: checked one by one as they are added, and against each
+// other by disjoint(). Empty views (no rows) take part in neither.
+class Views {
+ public:
+  muon_status add(const void* p, int64_t rows, int64_t cols, int64_t ld, int elem, bool written, const char* name,
+                  int item = -1, uintptr_t align = 0) {
+    if (!p && rows > 0) return fail(MUON_ERR_INVALID_ARG, at(item) + name + " is NULL");
+    if (ld < cols || ld > kMaxCols) return fail(MUON_ERR_INVALID_ARG, at(item) + name + ": row stride must be in [cols, 2^24]");
+    const uintptr_t a = align ? align : uintptr_t(elem);
+    if (reinterpret_cast<uintptr_t>(p) % a)
+      return fail(MUON_ERR_ALIGN, at(item) + name + " is not " + std::to_string(a) + "-byte aligned");
+    if (rows > 0) v_.push_back({reinterpret_cast<uintptr_t>(p), rows, cols * elem, ld * elem, written, name, item});
+    return MUON_OK;
+  }
+
+  // One float per row, contiguous.
+  muon_status add_floats(const float* p, int64_t rows, bool written, const char* name) {
+    if (!p && rows > 0) return fail(MUON_ERR_INVALID_ARG, std::string(name) + " is NULL");
+    if (reinterpret_cast<uintptr_t>(p) % 4) return fail(MUON_ERR_ALIGN, std::string(name) + " is not 4-byte aligned");
+    if (rows > 0) v_.push_back({reinterpret_cast<uintptr_t>(p), 1, rows * 4, rows * 4, written, name, -1});
+    return MUON_OK;
+  }
+
+  // Contiguous scratch that the call writes.
+  muon_status add_range(const void* p, size_t bytes, const char* name) {
+    v_.push_back({reinterpret_cast<uintptr_t>(p), 1, int64_t(bytes), int64_t(bytes), true, name, -1});
+    return MUON_OK;
+  }
+
+  muon_status disjoint() {
+    std::sort(v_.begin(), v_.end(), [](const View& x, const View& y) { return x.base < y.base; });
+    for (size_t i = 0; i < v_.size(); ++i) {
+      const uintptr_t end = v_[i].base + uintptr_t((v_[i].rows - 1) * v_[i].pitch + v_[i].width);
+      for (size_t j = i + 1; j < v_.size() && v_[j].base < end; ++j)
+        if ((v_[i].written || v_[j].written) && share(v_[i], v_[j]))
+          return fail(MUON_ERR_ALIAS, at(v_[i].item) + v_[i].name + " overlaps " + at(v_[j].item) + v_[j].name);
+    }
+    return MUON_OK;
+  }
+
+  static std::string at(int item) { return item < 0 ? "" : "item " + std::to_string(item) + ": "; }
+
+ private:
+  // lo starts first and its range reaches hi's. Views of one row pitch are
+  // compared by rows and columns; others count as overlapping.
+  static bool share(const View& lo, const View& hi) {
+    if (lo.pitch != hi.pitch) return true;
+    const int64_t off = int64_t(hi.base - lo.base), dr = off / lo.pitch, dc = off % lo.pitch;
+    if (dc + hi.width > lo.pitch) return true;  // hi's rows wrap into lo's next row
+    return dr < lo.rows && dc < lo.width;
+  }
+  std::vector<View> v_;
+};
+
+#define MUON_TRY(x)                      \
+  do {                                   \
+    const muon_status st_ = (x);         \
+    if (st_ != MUON_OK) return st_;      \
+  } while (0)
+
+muon_status check_dtype(int32_t dtype, const char* what = "dtype") {
+  if (dtype != MUON_F32 && dtype != MUON_BF16)
+    return fail(MUON_ERR_UNSUPPORTED, std::string(what) + " must be MUON_F32 or MUON_BF16");
+  return MUON_OK;
+}
+int elem_of(int32_t dtype) { return dtype == MUON_BF16 ? 2 : 4; }
+
+muon_status check_size(int64_t rows, int64_t cols, int item = -1) {
+  if (rows < 0 || rows > kMaxRows) return fail(MUON_ERR_INVALID_ARG, Views::at(item) + "rows must be in [0, 2^31 - 1]");
+  if (cols < 1 || cols > kMaxCols) return fail(MUON_ERR_INVALID_ARG, Views::at(item) + "cols must be in [1, 2^24]");
+  return MUON_OK;
+}
+
+muon_status check_q8(Views& views, const muon_q8& p, bool written, const char* name, int item = -1) {
+  MUON_TRY(check_size(p.rows, p.cols, item));
+  if (p.kind != MUON_Q8_INT8 && p.kind != MUON_Q8_E4M3)
+    return fail(MUON_ERR_UNSUPPORTED, Views::at(item) + name + ": kind must be MUON_Q8_INT8 or MUON_Q8_E4M3");
+  if (p.ldq % 16) return fail(MUON_ERR_ALIGN, Views::at(item) + name + ": ldq must be a multiple of 16");
+  // the padding up to the next multiple of 16 belongs to the view
+  MUON_TRY(views.add(p.q, p.rows, (p.cols + 15) / 16 * 16, p.ldq, 1, written, name, item, 16));
+  return views.add(p.e, p.rows, (p.cols + muon::kGroup - 1) / muon::kGroup, p.lde, 1, written, name, item);
+}
+
+muon_status q8_call(const void* x, int64_t ldx, int32_t dtype, const muon_q8* p, bool save, void* stream) {
+  return guarded([&]() -> muon_status {
+    if (!p) return fail(MUON_ERR_INVALID_ARG, "the checkpoint is NULL");
+    MUON_TRY(check_dtype(dtype));
+    Views v;
+    MUON_TRY(check_q8(v, *p, save, "checkpoint"));
+    MUON_TRY(v.add(x, p->rows, p->cols, ldx, elem_of(dtype), !save, "x"));
+    MUON_TRY(v.disjoint());
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return hip_status(save ? muon::launch_q8_save(x, ldx, dtype, *p, s)
+                           : muon::launch_q8_load(*p, const_cast<void*>(x), ldx, dtype, s));
+  });
+}
+
+// What the forward and the backward pass of a norm site have in common.
+muon_status check_site(Views& v, const muon_norm_site& s) {
+  MUON_TRY(check_dtype(s.dtype));
+  MUON_TRY(check_size(s.rows, s.cols));
+  if (s.cols > muon::kNormMaxCols) return fail(MUON_ERR_UNSUPPORTED, "cols must be <= 32768");
+  const float f[] = {s.res_scale, s.branch_scale, s.eps};
+  for (float x : f)
+    if (!std::isfinite(x)) return fail(MUON_ERR_INVALID_ARG, "res_scale, branch_scale and eps must be finite");
+  if (s.eps < 0.f) return fail(MUON_ERR_INVALID_ARG, "eps must be >= 0");
+  const int e = elem_of(s.dtype);
+  MUON_TRY(v.add(s.w_pre, 1, s.cols, s.cols, e, false, "w_pre"));
+  if (s.w_post) MUON_TRY(v.add(s.w_post, 1, s.cols, s.cols, e, false, "w_post"));
+  if (s.gate) {
+    if (s.ld_gate == 0) MUON_TRY(v.add(s.gate, 1, s.cols, s.cols, e, false, "gate"));
+    else MUON_TRY(v.add(s.gate, s.rows, s.cols, s.ld_gate, e, false, "gate"));
+  }
+  return MUON_OK;
+}
+
+muon_status check_saved(Views& v, const muon_norm_site& s, const muon_q8& p, bool written, const char* name) {
+  if (p.rows != s.rows || p.cols != s.cols)
+    return fail(MUON_ERR_INVALID_ARG, std::string(name) + " must be a rows x cols checkpoint");
+  return check_q8(v, p, written, name);
+}
+
+muon_status norm_forward(const muon_norm_site* site, void* stream) {
+  if (!site) return fail(MUON_ERR_INVALID_ARG, "site is NULL");
+  const muon_norm_site& s = *site;
+  Views v;
+  MUON_TRY(check_site(v, s));
+  const int e = elem_of(s.dtype);
+  MUON_TRY(v.add(s.branch, s.rows, s.cols, s.ld_branch, e, false, "branch"));
+  MUON_TRY(v.add(s.residual, s.rows, s.cols, s.ld_residual, e, false, "residual"));
+  MUON_TRY(v.add(s.y, s.rows, s.cols, s.ld_y, e, true, "y"));
+  MUON_TRY(v.add(s.h, s.rows, s.cols, s.ld_h, e, true, "h"));
+  if (s.rstd_y) MUON_TRY(v.add_floats(s.rstd_y, s.rows, true, "rstd_y"));
+  if (s.rstd_b) MUON_TRY(v.add_floats(s.rstd_b, s.rows, true, "rstd_b"));
+  if (s.u.q) MUON_TRY(check_saved(v, s, s.u, true, "u"));
+  if (s.v.q) MUON_TRY(check_saved(v, s, s.v, true, "v"));
+  MUON_TRY(v.disjoint());
+  return hip_status(muon::launch_norm_forward(s, static_cast<hipStream_t>(stream)));
+}
+
+size_t norm_workspace(int64_t rows, int64_t cols) {
+  return size_t(muon::norm_backward_blocks(rows, cols)) * 3 * size_t((cols + 7) / 8 * 8) * sizeof(float);
+}
+
+muon_status norm_backward(const muon_norm_site* site, const muon_norm_grads* grads, void* stream) {
+  if (!site || !grads) return fail(MUON_ERR_INVALID_ARG, "site or grads is NULL");
+  const muon_norm_site& s = *site;
+  const muon_norm_grads& g = *grads;
+  Views v;
+  MUON_TRY(check_site(v, s));
+  const int e = elem_of(s.dtype);
+  if (g.dy) MUON_TRY(v.add(g.dy, s.rows, s.cols, g.ld_dy, e, false, "dy"));
+  MUON_TRY(v.add(g.dh, s.rows, s.cols, g.ld_dh, e, false, "dh"));
+  MUON_TRY(v.add_floats(s.rstd_y, s.rows, false, "rstd_y"));
+  MUON_TRY(check_saved(v, s, s.u, false, "u"));
+  if (s.w_post) MUON_TRY(v.add_floats(s.rstd_b, s.rows, false, "rstd_b"));
+  if (s.w_post || s.gate) MUON_TRY(check_saved(v, s, s.v, false, "v"));
+  MUON_TRY(v.add(g.d_residual, s.rows, s.cols, g.ld_d_residual, e, true, "d_residual"));
+  MUON_TRY(v.add(g.d_branch, s.rows, s.cols, g.ld_d_branch, e, true, "d_branch"));
+  if (g.d_w_pre) MUON_TRY(v.add(g.d_w_pre, 1, s.cols, s.cols, e, true, "d_w_pre"));
+  if (g.d_w_post) {
+    if (!s.w_post) return fail(MUON_ERR_INVALID_ARG, "d_w_post is given but the site has no w_post");
+    MUON_TRY(v.add(g.d_w_post, 1, s.cols, s.cols, e, true, "d_w_post"));
+  }
+  if (g.d_gate) {
+    if (!s.gate) return fail(MUON_ERR_INVALID_ARG, "d_gate is given but the site has no gate");
+    if (s.ld_gate == 0) MUON_TRY(v.add(g.d_gate, 1, s.cols, s.cols, e, true, "d_gate"));
+    else MUON_TRY(v.add(g.d_gate, s.rows, s.cols, g.ld_d_gate, e, true, "d_gate"));
+  }
+  const size_t need = norm_workspace(s.rows, s.cols);
+  if (need) {
+    if (g.workspace_bytes < need)
+      return fail(MUON_ERR_INVALID_ARG, "the workspace has " + std::to_string(g.workspace_bytes) + " bytes, " +
+                                            std::to_string(need) + " are needed");
+    if (!g.workspace) return fail(MUON_ERR_INVALID_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(g.workspace) % 16) return fail(MUON_ERR_ALIGN, "workspace is not 16-byte aligned");
+    MUON_TRY(v.add_range(g.workspace, need, "workspace"));
+  }
+  MUON_TRY(v.disjoint());
+  return hip_status(muon::launch_norm_backward(s, g, static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------ weight gradients
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+// dY is read as it is if its rows are 16-byte aligned bf16 with whole 16-byte
+// chunks; otherwise it is rewritten into the workspace.
+bool needs_pack(const muon_wgrad_item& it, int32_t dtype) {
+  return dtype == MUON_F32 || reinterpret_cast<uintptr_t>(it.dy) % 16 || it.ld_dy % 8 || it.n % 8;
+}
+
+// How many pieces the sum over tokens is cut into, for items of which the
+// longest has `longest` stages and all together `tiles` tiles. One workgroup per
+// CU works on one tile at a time, so a launch takes ceil(tiles*s/256) rounds of
+// longest/s stages; pieces cost a partial tile each (256 KB written and read
+// back, about kPartialCost of a stage) and a second launch.
+int choose_splits(int64_t tiles, int64_t longest) {
+  constexpr int64_t kCus = 256;
+  constexpr double kTileCost = 3.0, kPartialCost = 0.13, kLaunchCost = 4.0;
+  int best = 1;
+  double best_cost = 1e300;
+  for (int s = 1; s <= 64 && s <= std::max<int64_t>(1, longest / 2); ++s) {
+    const double rounds = double(ceil_div(tiles * s, kCus));
+    double cost = rounds * (double(ceil_div(longest, s)) + kTileCost);
+    if (s > 1) cost += kLaunchCost + kPartialCost * double(tiles * s);
+    if (cost < best_cost * 0.98) best = s, best_cost = cost;
+    if (tiles * s >= 2 * kCus) break;
+  }
+  return best;
+}
+
+struct WgradPlan {
+  muon::WgArgs args;
+  size_t pack[muon::kWgItems];  // workspace offset of the rewritten dY, or SIZE_MAX
+  size_t partial = 0, bytes = 0;
+};
+
+// The launch of items [0, n), n <= kWgItems: descriptors and workspace layout.
+muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32_t g_dtype, WgradPlan& p) {
+  p.args = muon::WgArgs{};
+  p.args.n_items = n;
+  p.args.scale_f32 = dtype == MUON_F32;
+  p.args.g_f32 = g_dtype == MUON_F32;
+  const int parts = dtype == MUON_F32 ? 3 : 1;
+  int64_t tiles = 0, longest = 0;
+  size_t at = 0;
+  for (int i = 0; i < n; ++i) {
+    const muon_wgrad_item& it = items[i];
+    muon::WgItem& d = p.args.item[i];
+    d.q = static_cast<const uint8_t*>(it.x.q);
+    d.e = static_cast<const uint8_t*>(it.x.e);
+    d.scale = it.scale;
+    d.g = it.g;
+    d.c = it.c;
+    d.ldq = it.x.ldq;
+    d.lde = it.x.lde;
+    d.rows = int32_t(it.x.rows);
+    d.n = int32_t(it.n);
+    d.k = int32_t(it.x.cols);
+    d.na = int32_t(ceil_div(it.n, 8) * 8);
+    d.parts = parts;
+    d.beta = it.beta;
+    d.tiles_n = int32_t(ceil_div(it.n, muon::kWgTile));
+    d.tiles_k = int32_t(ceil_div(it.x.cols, muon::kWgTile));
+    d.dy = it.dy;
+    d.lda = it.ld_dy;
+    p.pack[i] = SIZE_MAX;
+    if (needs_pack(it, dtype)) {
+      p.pack[i] = at;
+      d.lda = d.na;
+      at += round256(size_t(parts) * size_t(it.x.rows) * size_t(d.na) * 2);
+    }
+    tiles += int64_t(d.tiles_n) * d.tiles_k;
+    longest = std::max<int64_t>(longest, ceil_div(it.x.rows, muon::kWgStep) * parts);
+  }
+  const int want = choose_splits(tiles, longest);
+  int64_t units = 0, partials = 0;
+  for (int i = 0; i < n; ++i) {
+    muon::WgItem& d = p.args.item[i];
+    const int64_t t = int64_t(d.tiles_n) * d.tiles_k, stages = ceil_div(d.rows, muon::kWgStep) * parts;
+    d.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(want, stages / 2)));
+    d.unit0 = int32_t(units);
+    d.part0 = int32_t(partials);
+    units += t * d.splits;
+    if (d.splits > 1) partials += t * d.splits;
+    if (units > (int64_t(1) << 30)) return fail(MUON_ERR_INVALID_ARG, "more than 2^30 tiles in one call");
+  }
+  p.args.units = int32_t(units);
+  p.partial = at;
+  p.bytes = at + size_t(partials) * muon::kWgPart * sizeof(float);
+  return MUON_OK;
+}
+
+muon_status check_wgrad(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_t g_dtype, Views& v) {
+  if (!items) return fail(MUON_ERR_INVALID_ARG, "items is NULL");
+  if (n < 1) return fail(MUON_ERR_INVALID_ARG, "n_items must be >= 1");
+  MUON_TRY(check_dtype(dtype));
+  MUON_TRY(check_dtype(g_dtype, "g_dtype"));
+  const int e = elem_of(dtype), ge = elem_of(g_dtype);
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_wgrad_item& it = items[i];
+    if (it.n < 1 || it.n > kMaxCols) return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "n must be in [1, 2^24]");
+    MUON_TRY(check_q8(v, it.x, false, "x", i));
+    if (it.x.kind != items[0].x.kind)
+      return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "every checkpoint of a call must have the same kind");
+    MUON_TRY(v.add(it.dy, it.x.rows, it.n, it.ld_dy, e, false, "dy", i));
+    if (it.scale) MUON_TRY(v.add(it.scale, 1, it.x.cols, it.x.cols, e, false, "scale", i));
+    MUON_TRY(v.add(it.g, it.n, it.x.cols, it.x.cols, ge, true, "g", i, 16));
+    if (!std::isfinite(it.beta)) return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "beta is not finite");
+    if (it.beta != 0.f && it.c != it.g) MUON_TRY(v.add(it.c, it.n, it.x.cols, it.x.cols, ge, false, "c", i, 16));
+  }
+  return MUON_OK;
+}
+
+muon_status wgrad_bytes(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_t g_dtype, size_t* bytes) {
+  *bytes = 0;
+  WgradPlan p;
+  for (int32_t i = 0; i < n; i += muon::kWgItems) {
+    MUON_TRY(plan_wgrad(items + i, std::min(n - i, muon::kWgItems), dtype, g_dtype, p));
+    *bytes = std::max(*bytes, p.bytes);
+  }
+  return MUON_OK;
+}
+
+muon_status wgrad(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_t g_dtype, void* ws, size_t ws_bytes,
+                  void* stream) {
+  Views v;
+  MUON_TRY(check_wgrad(items, n, dtype, g_dtype, v));
+  size_t need = 0;
+  MUON_TRY(wgrad_bytes(items, n, dtype, g_dtype, &need));
+  if (need) {
+    if (ws_bytes < need)
+      return fail(MUON_ERR_INVALID_ARG, "the workspace has " + std::to_string(ws_bytes) + " bytes, " +
+                                            std::to_string(need) + " are needed");
+    if (!ws) return fail(MUON_ERR_INVALID_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(ws) % 16) return fail(MUON_ERR_ALIGN, "workspace is not 16-byte aligned");
+    MUON_TRY(v.add_range(ws, need, "workspace"));
+  }
+  MUON_TRY(v.disjoint());
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  WgradPlan p;
+  for (int32_t i0 = 0; i0 < n; i0 += muon::kWgItems) {
+    const int m = std::min(n - i0, muon::kWgItems);
+    MUON_TRY(plan_wgrad(items + i0, m, dtype, g_dtype, p));
+    p.args.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.partial);
+    for (int i = 0; i < m; ++i) {
+      if (p.pack[i] == SIZE_MAX) continue;
+      const muon_wgrad_item& it = items[i0 + i];
+      void* out = static_cast<char*>(ws) + p.pack[i];
+      p.args.item[i].dy = out;
+      MUON_TRY(hip_status(muon::launch_wgrad_pack(it.dy, it.ld_dy, dtype, out, int32_t(it.x.rows), int32_t(it.n),
+                                                  p.args.item[i].lda, s)));
+    }
+    MUON_TRY(hip_status(muon::launch_wgrad(p.args, items[0].x.kind, s)));
+  }
+  return MUON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_q8_save(const void* x, int64_t ldx, int32_t dtype, const muon_q8* out, void* stream) {
+  return q8_call(x, ldx, dtype, out, true, stream);
+}
+
+muon_status muon_q8_load(const muon_q8* in, void* x, int64_t ldx, int32_t dtype, void* stream) {
+  return q8_call(x, ldx, dtype, in, false, stream);
+}
+
+muon_status muon_norm_forward(const muon_norm_site* site, void* stream) {
+  return guarded([&] { return norm_forward(site, stream); });
+}
+
+muon_status muon_norm_backward(const muon_norm_site* site, const muon_norm_grads* grads, void* stream) {
+  return guarded([&] { return norm_backward(site, grads, stream); });
+}
+
+muon_status muon_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+  return guarded([&]() -> muon_status {
+    if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+    MUON_TRY(check_size(rows, cols));
+    if (cols > muon::kNormMaxCols) return fail(MUON_ERR_UNSUPPORTED, "cols must be <= 32768");
+    *bytes = norm_workspace(rows, cols);
+    return MUON_OK;
+  });
+}
+
+muon_status muon_wgrad(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return guarded([&] { return wgrad(items, n_items, dtype, g_dtype, workspace, workspace_bytes, stream); });
+}
+
+muon_status muon_wgrad_workspace(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype,
+                                 size_t* bytes) {
+  return guarded([&]() -> muon_status {
+    if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+    Views v;
+    MUON_TRY(check_wgrad(items, n_items, dtype, g_dtype, v));
+    return wgrad_bytes(items, n_items, dtype, g_dtype, bytes);
+  });
+}
+
+}  // extern "C"

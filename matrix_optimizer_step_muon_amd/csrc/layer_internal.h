@@ -1,0 +1,77 @@
+// Internal types shared by the host side of the layer operators
+// (layer_api.cpp) and their kernels (layer_kernels.hip, wgrad_kernels.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "muon.h"
+
+namespace muon {
+
+constexpr int kGroup = 32;           // columns that share one exponent byte
+constexpr int kNormMaxCols = 32768;  // 1024 threads x 4 x 8 columns
+constexpr int kMinExp = 17;          // smallest exponent byte: 2^-110
+
+// Threads of a norm workgroup: one row, 8 columns per thread up to 8192
+// columns, then 16 or 32.
+inline int norm_vecs(int64_t cols) { return cols <= 8192 ? 1 : cols <= 16384 ? 2 : 4; }
+inline int norm_threads(int64_t cols) {
+  const int64_t per = 8 * norm_vecs(cols);
+  return int(((cols + per - 1) / per + 63) / 64 * 64);
+}
+
+// Workgroups of the norm backward kernel, each of which leaves one partial sum
+// per column and weight.
+inline int norm_backward_blocks(int64_t rows, int64_t cols) {
+  const int per_cu = std::max(1, std::min(4, 2048 / norm_threads(cols)));
+  return int(std::min<int64_t>(rows, 256 * per_cu));
+}
+
+// ------------------------------------------------------------ weight gradients
+
+constexpr int kWgTile = 256;   // output tile edge
+constexpr int kWgStep = 64;    // tokens per stage
+constexpr int kWgItems = 16;   // matrices per launch
+constexpr int kWgPart = kWgTile * kWgTile;  // floats of one partial tile
+
+// One matrix of a launch. Units (tiles x splits) are numbered consecutively
+// over the items; unit0 is this item's first.
+struct WgItem {
+  const void* dy;      // bf16, 16-byte aligned rows of lda elements; parts planes of `rows` rows
+  const uint8_t* q;
+  const uint8_t* e;
+  const void* scale;   // dtype, or null
+  void* g;
+  const void* c;
+  int64_t lda, ldq, lde;
+  int32_t rows, n, k, na;  // na: columns of dy that may be read (a multiple of 8)
+  int32_t parts;       // 1, or 3 for fp32 dY
+  int32_t tiles_n, tiles_k;
+  int32_t splits;      // > 1: partial tiles go to the workspace
+  int32_t unit0;
+  int32_t part0;       // first partial tile of this item in the workspace
+  float beta;
+};
+
+struct WgArgs {
+  WgItem item[kWgItems];
+  float* partial;
+  int32_t n_items;
+  int32_t units;
+  int32_t scale_f32;  // dtype of scale
+  int32_t g_f32;      // dtype of g and c
+};
+
+hipError_t launch_q8_save(const void* x, int64_t ldx, int dtype, const muon_q8& out, hipStream_t s);
+hipError_t launch_q8_load(const muon_q8& in, void* x, int64_t ldx, int dtype, hipStream_t s);
+hipError_t launch_norm_forward(const muon_norm_site& site, hipStream_t s);
+hipError_t launch_norm_backward(const muon_norm_site& site, const muon_norm_grads& grads, hipStream_t s);
+// dY (any alignment, bf16 or fp32) into `parts` bf16 planes of rows x lda.
+hipError_t launch_wgrad_pack(const void* dy, int64_t ld, int dtype, void* out, int32_t rows, int32_t n, int64_t lda,
+                             hipStream_t s);
+hipError_t launch_wgrad(const WgArgs& args, int kind, hipStream_t s);
+
+}  // namespace muon

@@ -1,0 +1,452 @@
+// gfx950 kernels of 8-bit activation checkpoints and of the norm sites between
+// blocks. All of them are bound by HBM: each tensor is read once and written
+// once, sums are fp32, and every thread owns 8 consecutive columns (16 bytes of
+// bf16, 8 bytes of a checkpoint), so a wave instruction moves whole lines.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device.h"
+#include "layer_internal.h"
+#include "q8.h"
+
+namespace muon {
+
+// ------------------------------------------------------------ eight columns
+
+// Columns c0 .. c0+7 of a row; those at or past cols read as 0 and are not
+// written. VEC: the row is 16-byte aligned and cols a multiple of 8.
+template <class T, bool VEC>
+MUON_INLINE void load8(const T* row, int64_t c0, int64_t cols, float v[8]) {
+  if (c0 >= cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  } else if constexpr (VEC) {
+    if constexpr (sizeof(T) == 2) {
+      const u32x4 t = gload16(row + c0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(t[i] << 16);
+        v[2 * i + 1] = __uint_as_float(t[i] & 0xffff0000u);
+      }
+    } else {
+      Vec4<float>::load(row + c0, v);
+      Vec4<float>::load(row + c0 + 4, v + 4);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c0 + i < cols ? Elem<T>::load(row + c0 + i) : 0.f;
+  }
+}
+
+template <class T, bool VEC>
+MUON_INLINE void store8(T* row, int64_t c0, int64_t cols, const float v[8]) {
+  if (c0 >= cols) return;
+  if constexpr (VEC) {
+    if constexpr (sizeof(T) == 2) {
+      u32x4 t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      *((g_u32x4*)(row + c0)) = t;
+    } else {
+      Vec4<float>::store(row + c0, v);
+      Vec4<float>::store(row + c0 + 4, v + 4);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < cols) Elem<T>::store(row + c0 + i, v[i]);
+  }
+}
+
+// Quantises columns c0 .. c0+7 of one row (4 adjacent lanes hold a group; all
+// of them must be here) and stores them. Rows of q are 16-byte aligned and
+// padded, so the 8 bytes are always one store.
+MUON_INLINE void store_q8(uint8_t* q, uint8_t* e, int64_t c0, int64_t cols, const float v[8], int kind) {
+  u32x2 w;
+  const uint32_t E = q8_encode(v, kind, w);
+  if (c0 >= cols) return;
+  *((g_u32x2*)(q + c0)) = w;
+  if (c0 % kGroup == 0) *((g_u8*)(e + c0 / kGroup)) = (uint8_t)E;
+}
+
+MUON_INLINE void load_q8(const uint8_t* q, const uint8_t* e, int64_t c0, int64_t cols, int kind, float v[8]) {
+  if (c0 >= cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    return;
+  }
+  const u32x2 w = *((const g_u32x2*)(q + c0));
+  q8_decode(w, *((const g_u8*)(e + c0 / kGroup)), kind, v);
+  // padding bytes of the last 8 columns are not the row's
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v[i] = c0 + i < cols ? v[i] : 0.f;
+}
+
+// ------------------------------------------------------------ save and load
+
+// A workgroup is tx lanes wide (8 columns each) and 256/tx rows tall; tx is a
+// power of two >= 4, so a group's four lanes are neighbours.
+struct Q8Args {
+  void* x;
+  int64_t ldx;
+  muon_q8 p;
+  int32_t log_tx;
+};
+
+template <class T, bool VEC, bool SAVE>
+__global__ void __launch_bounds__(256) q8_kernel(Q8Args a) {
+  const int tx = 1 << a.log_tx, ty = 256 >> a.log_tx;
+  const int64_t c0 = ((int64_t)blockIdx.y * tx + (threadIdx.x & (tx - 1))) * 8;
+  const int64_t cols = a.p.cols;
+  for (int64_t row = (int64_t)blockIdx.x * ty + (threadIdx.x >> a.log_tx); row < a.p.rows;
+       row += (int64_t)gridDim.x * ty) {
+    T* x = static_cast<T*>(a.x) + row * a.ldx;
+    uint8_t* q = static_cast<uint8_t*>(a.p.q) + row * a.p.ldq;
+    uint8_t* e = static_cast<uint8_t*>(a.p.e) + row * a.p.lde;
+    float v[8];
+    if constexpr (SAVE) {
+      load8<T, VEC>(x, c0, cols, v);
+      store_q8(q, e, c0, cols, v, a.p.kind);
+    } else {
+      load_q8(q, e, c0, cols, a.p.kind, v);
+      store8<T, VEC>(x, c0, cols, v);
+    }
+  }
+}
+
+static bool rows_aligned(const void* p, int64_t ld, int elem) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * elem % 16 == 0;
+}
+
+template <bool SAVE>
+static hipError_t launch_q8(const void* x, int64_t ldx, int dtype, const muon_q8& p, hipStream_t s) {
+  if (p.rows == 0) return hipSuccess;
+  const int64_t octets = (p.cols + kGroup - 1) / kGroup * 4;
+  Q8Args a{const_cast<void*>(x), ldx, p, 2};
+  while (a.log_tx < 8 && (int64_t(1) << a.log_tx) < octets) ++a.log_tx;
+  const int64_t gy = (octets + (1 << a.log_tx) - 1) >> a.log_tx;  // at most 2^24 / 2048
+  const int64_t gx = (p.rows + (256 >> a.log_tx) - 1) / (256 >> a.log_tx);
+  const dim3 grid((uint32_t)std::min<int64_t>(gx, std::max<int64_t>(1, (1 << 20) / gy)), (uint32_t)gy);
+  const int elem = dtype == MUON_BF16 ? 2 : 4;
+  const bool vec = p.cols % 8 == 0 && rows_aligned(x, ldx, elem);
+  if (dtype == MUON_BF16) {
+    if (vec) hipLaunchKernelGGL((q8_kernel<u16, true, SAVE>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((q8_kernel<u16, false, SAVE>), grid, dim3(256), 0, s, a);
+  } else {
+    if (vec) hipLaunchKernelGGL((q8_kernel<float, true, SAVE>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((q8_kernel<float, false, SAVE>), grid, dim3(256), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_q8_save(const void* x, int64_t ldx, int dtype, const muon_q8& out, hipStream_t s) {
+  return launch_q8<true>(x, ldx, dtype, out, s);
+}
+hipError_t launch_q8_load(const muon_q8& in, void* x, int64_t ldx, int dtype, hipStream_t s) {
+  return launch_q8<false>(x, ldx, dtype, in, s);
+}
+
+// ------------------------------------------------------------ norm sites
+
+// Sum over a wave, in every lane.
+MUON_INLINE float wave_sum(float v) {
+#pragma unroll
+  for (int w = 32; w > 0; w >>= 1) v += __shfl_xor(v, w);
+  return v;
+}
+
+// N sums over the workgroup at once, in every thread, in a fixed order. `red`
+// holds 16*N floats; two calls in a row need two buffers.
+template <int N>
+MUON_INLINE void block_sum(float (&v)[N], float* red) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[(threadIdx.x >> 6) * N + i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = red[i];
+  for (int w = 1; w < waves; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += red[w * N + i];
+}
+
+// One row per workgroup: thread t holds columns 8t .. 8t+7 (VPT times, a
+// workgroup's width apart). The row stays in registers between its two norms,
+// so every tensor moves once.
+template <class T, int VPT, bool VEC>
+__global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
+  __shared__ float red[2][16];
+  const int64_t cols = s.cols;
+  const float inv_cols = 1.f / (float)cols;
+  const bool post = s.w_post != nullptr;
+  int64_t c0[VPT];
+#pragma unroll
+  for (int p = 0; p < VPT; ++p) c0[p] = ((int64_t)p * blockDim.x + threadIdx.x) * 8;
+  for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x) {
+    float v[VPT][8], y[VPT][8];
+    float sum[1] = {0.f};
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      load8<T, VEC>(static_cast<const T*>(s.branch) + row * s.ld_branch, c0[p], cols, v[p]);
+      load8<T, VEC>(static_cast<const T*>(s.residual) + row * s.ld_residual, c0[p], cols, y[p]);
+    }
+    if (post) {
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[0] += v[p][i] * v[p][i];
+      block_sum(sum, red[0]);
+      const float rb = 1.f / sqrtf(sum[0] * inv_cols + s.eps);
+      if (threadIdx.x == 0 && s.rstd_b) *((g_f32*)(s.rstd_b + row)) = rb;
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] *= rb;
+    }
+    sum[0] = 0.f;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      if (s.v.q)
+        store_q8(static_cast<uint8_t*>(s.v.q) + row * s.v.ldq, static_cast<uint8_t*>(s.v.e) + row * s.v.lde, c0[p],
+                 cols, v[p], s.v.kind);
+      float w[8];
+      if (post) {
+        load8<T, VEC>(static_cast<const T*>(s.w_post), c0[p], cols, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] *= w[i];
+      }
+      if (s.gate) {
+        load8<T, VEC>(static_cast<const T*>(s.gate) + row * s.ld_gate, c0[p], cols, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] *= w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[p][i] = s.res_scale * y[p][i] + s.branch_scale * v[p][i];
+        sum[0] += y[p][i] * y[p][i];
+      }
+      store8<T, VEC>(static_cast<T*>(s.y) + row * s.ld_y, c0[p], cols, y[p]);
+    }
+    block_sum(sum, red[1]);
+    const float ry = 1.f / sqrtf(sum[0] * inv_cols + s.eps);
+    if (threadIdx.x == 0 && s.rstd_y) *((g_f32*)(s.rstd_y + row)) = ry;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[p][i] *= ry;
+      if (s.u.q)
+        store_q8(static_cast<uint8_t*>(s.u.q) + row * s.u.ldq, static_cast<uint8_t*>(s.u.e) + row * s.u.lde, c0[p],
+                 cols, y[p], s.u.kind);
+      load8<T, VEC>(static_cast<const T*>(s.w_pre), c0[p], cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] *= y[p][i];
+      store8<T, VEC>(static_cast<T*>(s.h) + row * s.ld_h, c0[p], cols, w);
+    }
+    // The next row's first sum writes red[0], which every thread has read
+    // before this row's second barrier; without a second barrier between
+    // them (no norm after the block) red[1] would be written while it is
+    // still read.
+    if (!post) __syncthreads();
+  }
+}
+
+// Rows blockIdx.x, + gridDim.x, ... The mean over dv*v needs s, which needs the
+// mean over du*u; written out, both follow from three sums that are formed at
+// once: with a = branch_scale*gate*w_post,
+//   mean(dv*v) = mean(a*v*(dy + rstd_y*du)) - rstd_y * mean(du*u) * mean(a*v*u),
+// so a row costs one barrier pair. Each thread keeps its columns' partial sums
+// of the weight gradients in registers and stores them once.
+template <class T, int VPT, bool VEC>
+__global__ void __launch_bounds__(1024) norm_backward_kernel(muon_norm_site s, muon_norm_grads g) {
+  __shared__ float red[2][48];
+  const int64_t cols = s.cols;
+  const float inv_cols = 1.f / (float)cols;
+  const bool post = s.w_post != nullptr, per_row = s.gate && s.ld_gate != 0;
+  const bool need_v = post || s.gate;
+  int64_t c0[VPT];
+#pragma unroll
+  for (int p = 0; p < VPT; ++p) c0[p] = ((int64_t)p * blockDim.x + threadIdx.x) * 8;
+  float acc[3][VPT][8];
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[w][p][i] = 0.f;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x, flip ^= 1) {
+    const float ry = *((const g_f32*)(s.rstd_y + row));
+    const float rb = post ? *((const g_f32*)(s.rstd_b + row)) : 1.f;
+    float u[VPT][8], v[VPT][8], t[VPT][8], gt[VPT][8];  // t: dy + rstd_y*du; gt: the gate
+    float du[VPT][8];
+    float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      float dh[8], w[8];
+      load8<T, VEC>(static_cast<const T*>(g.dh) + row * g.ld_dh, c0[p], cols, dh);
+      if (g.dy) {
+        load8<T, VEC>(static_cast<const T*>(g.dy) + row * g.ld_dy, c0[p], cols, t[p]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[p][i] = 0.f;
+      }
+      load_q8(static_cast<const uint8_t*>(s.u.q) + row * s.u.ldq, static_cast<const uint8_t*>(s.u.e) + row * s.u.lde,
+              c0[p], cols, s.u.kind, u[p]);
+      if (need_v) {
+        load_q8(static_cast<const uint8_t*>(s.v.q) + row * s.v.ldq, static_cast<const uint8_t*>(s.v.e) + row * s.v.lde,
+                c0[p], cols, s.v.kind, v[p]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
+      }
+      if (s.gate) {
+        load8<T, VEC>(static_cast<const T*>(s.gate) + row * s.ld_gate, c0[p], cols, gt[p]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gt[p][i] = 1.f;
+      }
+      load8<T, VEC>(static_cast<const T*>(s.w_pre), c0[p], cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[0][p][i] += dh[i] * u[p][i];
+        du[p][i] = dh[i] * w[i];
+        sum[0] += du[p][i] * u[p][i];
+        t[p][i] += ry * du[p][i];
+      }
+      if (post) {
+        load8<T, VEC>(static_cast<const T*>(s.w_post), c0[p], cols, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float av = gt[p][i] * w[i] * v[p][i];
+          sum[1] += av * t[p][i];
+          sum[2] += av * u[p][i];
+        }
+      }
+    }
+    block_sum(sum, red[flip]);
+    const float c1 = ry * (sum[0] * inv_cols);
+    const float c2 = s.branch_scale * (sum[1] - c1 * sum[2]) * inv_cols;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      float o[8], w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        t[p][i] -= c1 * u[p][i];  // s
+        o[i] = s.res_scale * t[p][i];
+        t[p][i] *= s.branch_scale;
+      }
+      store8<T, VEC>(static_cast<T*>(g.d_residual) + row * g.ld_d_residual, c0[p], cols, o);
+      if (post) {
+        load8<T, VEC>(static_cast<const T*>(s.w_post), c0[p], cols, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i] = t[p][i] * w[i] * v[p][i];
+        acc[2][p][i] += o[i];
+        t[p][i] *= gt[p][i];
+        acc[1][p][i] += t[p][i] * v[p][i];
+      }
+      if (per_row && g.d_gate)
+        store8<T, VEC>(static_cast<T*>(g.d_gate) + row * g.ld_d_gate, c0[p], cols, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = post ? rb * (t[p][i] * w[i] - v[p][i] * c2) : t[p][i];
+      store8<T, VEC>(static_cast<T*>(g.d_branch) + row * g.ld_d_branch, c0[p], cols, o);
+    }
+  }
+  const int64_t pitch = (cols + 7) / 8 * 8;
+  float* part = static_cast<float*>(g.workspace) + (int64_t)blockIdx.x * 3 * pitch;
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      if (c0[p] >= cols) continue;
+      Vec4<float>::store(part + w * pitch + c0[p], acc[w][p]);
+      Vec4<float>::store(part + w * pitch + c0[p] + 4, acc[w][p] + 4);
+    }
+}
+
+// The weight gradients from the partial sums: 64 columns per workgroup, 16
+// waves that each add every 16th partial, joined in order.
+template <class T>
+__global__ void __launch_bounds__(1024) norm_weights_kernel(const float* part, int32_t blocks, int64_t cols, T* d0,
+                                                            T* d1, T* d2) {
+  __shared__ float red[16][64];
+  T* out = blockIdx.y == 0 ? d0 : blockIdx.y == 1 ? d1 : d2;
+  if (!out) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane, pitch = (cols + 7) / 8 * 8;
+  float sum = 0.f;
+  if (c < cols) {
+    const float* p = part + blockIdx.y * pitch + c;
+    for (int b = wave; b < blocks; b += 16) sum += *((const g_f32*)(p + (int64_t)b * 3 * pitch));
+  }
+  red[wave][lane] = sum;
+  __syncthreads();
+  if (wave != 0 || c >= cols) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) sum += red[w][lane];
+  Elem<T>::store(out + c, sum);
+}
+
+template <class T>
+static hipError_t norm_forward(const muon_norm_site& s, hipStream_t st) {
+  if (s.rows == 0) return hipSuccess;
+  const int elem = sizeof(T);
+  const bool vec = s.cols % 8 == 0 && rows_aligned(s.branch, s.ld_branch, elem) &&
+                   rows_aligned(s.residual, s.ld_residual, elem) && rows_aligned(s.y, s.ld_y, elem) &&
+                   rows_aligned(s.h, s.ld_h, elem) && rows_aligned(s.w_pre, 0, elem) &&
+                   rows_aligned(s.w_post, 0, elem) && rows_aligned(s.gate, s.ld_gate, elem);
+  const dim3 grid((uint32_t)std::min<int64_t>(s.rows, 1 << 20)), block(norm_threads(s.cols));
+  const int vpt = norm_vecs(s.cols);
+#define MUON_NORM_F(V, A) hipLaunchKernelGGL((norm_forward_kernel<T, V, A>), grid, block, 0, st, s)
+  if (vec) { if (vpt == 1) MUON_NORM_F(1, true); else if (vpt == 2) MUON_NORM_F(2, true); else MUON_NORM_F(4, true); }
+  else { if (vpt == 1) MUON_NORM_F(1, false); else if (vpt == 2) MUON_NORM_F(2, false); else MUON_NORM_F(4, false); }
+#undef MUON_NORM_F
+  return hipGetLastError();
+}
+
+template <class T>
+static hipError_t norm_backward(const muon_norm_site& s, const muon_norm_grads& g, hipStream_t st) {
+  const int elem = sizeof(T);
+  const bool per_row = s.gate && s.ld_gate != 0;
+  const bool vec = s.cols % 8 == 0 && rows_aligned(g.dy, g.ld_dy, elem) && rows_aligned(g.dh, g.ld_dh, elem) &&
+                   rows_aligned(g.d_residual, g.ld_d_residual, elem) &&
+                   rows_aligned(g.d_branch, g.ld_d_branch, elem) && rows_aligned(s.w_pre, 0, elem) &&
+                   rows_aligned(s.w_post, 0, elem) && rows_aligned(s.gate, s.ld_gate, elem) &&
+                   (!per_row || rows_aligned(g.d_gate, g.ld_d_gate, elem));
+  const int blocks = norm_backward_blocks(s.rows, s.cols), vpt = norm_vecs(s.cols);
+  if (blocks > 0) {
+    const dim3 grid(blocks), block(norm_threads(s.cols));
+#define MUON_NORM_B(V, A) hipLaunchKernelGGL((norm_backward_kernel<T, V, A>), grid, block, 0, st, s, g)
+    if (vec) { if (vpt == 1) MUON_NORM_B(1, true); else if (vpt == 2) MUON_NORM_B(2, true); else MUON_NORM_B(4, true); }
+    else { if (vpt == 1) MUON_NORM_B(1, false); else if (vpt == 2) MUON_NORM_B(2, false); else MUON_NORM_B(4, false); }
+#undef MUON_NORM_B
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  T* dg = per_row ? nullptr : static_cast<T*>(g.d_gate);
+  if (!g.d_w_pre && !g.d_w_post && !dg) return hipSuccess;
+  hipLaunchKernelGGL(norm_weights_kernel<T>, dim3((uint32_t)((s.cols + 63) / 64), 3), dim3(1024), 0, st,
+                     static_cast<const float*>(g.workspace), blocks, s.cols, static_cast<T*>(g.d_w_pre),
+                     static_cast<T*>(g.d_w_post), dg);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_forward(const muon_norm_site& s, hipStream_t st) {
+  return s.dtype == MUON_BF16 ? norm_forward<u16>(s, st) : norm_forward<float>(s, st);
+}
+hipError_t launch_norm_backward(const muon_norm_site& s, const muon_norm_grads& g, hipStream_t st) {
+  return s.dtype == MUON_BF16 ? norm_backward<u16>(s, g, st) : norm_backward<float>(s, g, st);
+}
+
+}  // namespace muon

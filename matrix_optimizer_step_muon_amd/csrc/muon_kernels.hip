@@ -288,17 +288,6 @@ struct EngineBF16 {
   }
 };
 
-// threadIdx.x behind an empty asm: address arithmetic derived from it stays
-// where it is written. Without this the compiler hoists per-lane offsets (of
-// the engines' fragment reads and DMA, and of the epilogues) out of the
-// persistent tile loop as loop invariants, keeps dozens of them live across
-// the GEMM, spills them, and reloads them one by one.
-MUON_INLINE int fresh_tid() {
-  int t = threadIdx.x;
-  asm volatile("" : "+v"(t));
-  return t;
-}
-
 // Operands of one output tile for Engine4: C = P Q^T over K, or P Q for QK
 // engines, with K steps taken from step kt0 on (mod K/BK). diag: the first
 // BM/BK loop steps form the diagonal window (see Engine4).

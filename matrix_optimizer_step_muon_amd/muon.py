@@ -39,6 +39,38 @@ class muon_hparams(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class muon_q8(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("e", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ldq", ctypes.c_int64), ("lde", ctypes.c_int64), ("kind", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class muon_norm_site(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("branch", ctypes.c_void_p), ("ld_branch", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("w_pre", ctypes.c_void_p), ("w_post", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64),
+                ("rstd_y", ctypes.c_void_p), ("rstd_b", ctypes.c_void_p), ("u", muon_q8), ("v", muon_q8),
+                ("res_scale", ctypes.c_float), ("branch_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
+
+
+class muon_norm_grads(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64),
+                ("d_residual", ctypes.c_void_p), ("ld_d_residual", ctypes.c_int64),
+                ("d_branch", ctypes.c_void_p), ("ld_d_branch", ctypes.c_int64),
+                ("d_w_pre", ctypes.c_void_p), ("d_w_post", ctypes.c_void_p),
+                ("d_gate", ctypes.c_void_p), ("ld_d_gate", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class muon_wgrad_item(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("x", muon_q8), ("scale", ctypes.c_void_p),
+                ("g", ctypes.c_void_p), ("c", ctypes.c_void_p), ("n", ctypes.c_int64), ("beta", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"muon: {STATUS_NAMES.get(status, status)}: {message}")
@@ -53,7 +85,9 @@ EXPORTS = ("muon_hparams_default", "muon_plan", "muon_plan_workspace_bytes", "mu
            "muon_plan_kernel_times", "muon_plan_reset_timing", "muon_plan_info",
            "muon_apply_plan", "muon_apply", "muon_apply_plan_destroy",
            "muon_dp_partition_static", "muon_dp_partition", "muon_tp_micro_groups", "muon_mfma_probe",
-           "muon_step_noalloc")
+           "muon_step_noalloc",
+           "muon_q8_save", "muon_q8_load", "muon_norm_forward", "muon_norm_backward",
+           "muon_norm_backward_workspace", "muon_wgrad", "muon_wgrad_workspace")
 
 
 def lib() -> ctypes.CDLL:
@@ -89,6 +123,14 @@ def lib() -> ctypes.CDLL:
     L.muon_tp_micro_groups.argtypes = [ctypes.POINTER(ctypes.c_double), c_i32, c_i32, ctypes.c_double,
                                        ctypes.POINTER(c_i32), ctypes.POINTER(c_i32), ctypes.POINTER(c_i32),
                                        ctypes.POINTER(c_i32)]
+    L.muon_q8_save.argtypes = [c_vp, c_i64, c_i32, ctypes.POINTER(muon_q8), c_vp]
+    L.muon_q8_load.argtypes = [ctypes.POINTER(muon_q8), c_vp, c_i64, c_i32, c_vp]
+    L.muon_norm_forward.argtypes = [ctypes.POINTER(muon_norm_site), c_vp]
+    L.muon_norm_backward.argtypes = [ctypes.POINTER(muon_norm_site), ctypes.POINTER(muon_norm_grads), c_vp]
+    L.muon_norm_backward_workspace.argtypes = [c_i64, c_i64, ctypes.POINTER(ctypes.c_size_t)]
+    L.muon_wgrad.argtypes = [ctypes.POINTER(muon_wgrad_item), c_i32, c_i32, c_i32, c_vp, ctypes.c_size_t, c_vp]
+    L.muon_wgrad_workspace.argtypes = [ctypes.POINTER(muon_wgrad_item), c_i32, c_i32, c_i32,
+                                       ctypes.POINTER(ctypes.c_size_t)]
     for name in EXPORTS:
         if name != "muon_last_error":
             getattr(L, name).restype = c_int
