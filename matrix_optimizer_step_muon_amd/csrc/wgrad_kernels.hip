@@ -13,6 +13,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device.h"
 #include "layer_internal.h"
 #include "q8.h"
@@ -120,8 +122,12 @@ __global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
-  const int rows = it.rows;
-  const int64_t lda = it.lda, ldq = it.ldq, lde = it.lde;
+  // Held in scalar registers: reloaded in the loop, they would make it wait for
+  // every LDS access in flight (scalar loads share that counter).
+  int rows = it.rows;
+  int64_t lda = it.lda, ldq = it.ldq, lde = it.lde;
+  const uint8_t *xq = it.q, *xe = it.e;
+  asm volatile("" : "+s"(rows), "+s"(lda), "+s"(ldq), "+s"(lde), "+s"(xq), "+s"(xe));
 
   // A stage covers tokens t0 .. t0+63 of a plane. The last stage of a plane
   // may be shorter: it still reads 64 token rows, the last 64 (or, in a
@@ -152,11 +158,11 @@ __global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
     dvoff[p] = (uint32_t)min(r, rows - 1) * (uint32_t)(lda * 2) +
                min((lane & 31) ^ lds_swizzle_k(r), (it.na - n0) / 8 - 1) * 16;
   }
-  auto issue_dy = [&](const Stage& g, int buf) __attribute__((always_inline)) {
-    const u16* base = g.dy + min(g.t0, last_base) * lda + n0;
-#pragma unroll
-    for (int p = 0; p < kDmaPerWave; ++p)
-      dma16s(base, dvoff[p], lds0 + buf * kStageBytes + (wave * kDmaPerWave + p) * 1024);
+  auto dy_base = [&](const Stage& g) __attribute__((always_inline)) {
+    return g.dy + min(g.t0, last_base) * lda + n0;
+  };
+  auto copy_dy = [&](const u16* base, int buf, int p) __attribute__((always_inline)) {
+    dma16s(base, dvoff[p], lds0 + buf * kStageBytes + (wave * kDmaPerWave + p) * 1024);
   };
   // X: chunk c of a thread is bytes 16*(tid % 16) .. of token row 16c + tid/16.
   const int qr = tid >> 4, qc = tid & 15;
@@ -168,34 +174,28 @@ __global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
     qvoff[c] = r * (uint32_t)ldq + qcol;
     evoff[c] = r * (uint32_t)lde + qcol / kGroup;
   }
-  u32x4 qv[kChunks];
-  uint32_t ev[kChunks];
-  auto load_x = [&](const Stage& g) __attribute__((always_inline)) {
+  // Two sets of registers: one is decoded while the next stage's bytes arrive
+  // in the other.
+  u32x4 qv[2][kChunks];
+  uint32_t ev[2][kChunks];
+  auto load_x = [&](const Stage& g, int set, int c) __attribute__((always_inline)) {
     const int64_t t = min(g.t0, last_base);
-    const uint8_t* q = it.q + t * ldq;
-    const uint8_t* e = it.e + t * lde;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      qv[c] = gload16(q + qvoff[c]);
-      ev[c] = *((const g_u8*)(e + evoff[c]));
-    }
+    qv[set][c] = gload16(xq + t * ldq + qvoff[c]);
+    ev[set][c] = *((const g_u8*)(xe + t * lde + evoff[c]));
   };
+  // Bytes 4w .. 4w+3 of chunk c as bf16; w odd completes 16 bytes, which are
+  // stored. Rows that are not the stage's become zeros.
   const uint32_t xoff = kOpBytes + qr * kRowBytes, xslot = (uint32_t)(2 * qc) ^ lds_swizzle_k(qr);
-  auto write_x = [&](const Stage& g, int buf, int c) __attribute__((always_inline)) {
-    const int r = 16 * c + qr, skip = g.t0 - min(g.t0, last_base);
+  u32x4 half;
+  auto write_x = [&](int skip, int set, int buf, int c, int w) __attribute__((always_inline)) {
+    const int r = 16 * c + qr;
     const bool live = r >= skip && r < rows;
-    const float unit = live ? q8_unit(ev[c]) : 0.f;
-    unsigned char* row = smem + buf * kStageBytes + xoff + 16 * c * kRowBytes;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
-      q8_decode4(live ? qv[c][2 * h] : 0u, unit, KIND, v);
-      q8_decode4(live ? qv[c][2 * h + 1] : 0u, unit, KIND, v + 4);
-      u32x4 o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<u32x4*>(row + ((xslot ^ h) << 4)) = o;
-    }
+    float v[4];
+    q8_decode4(live ? qv[set][c][w] : 0u, live ? q8_unit(ev[set][c]) : 0.f, KIND, v);
+    half[2 * (w & 1)] = pack_bf16x2(v[0], v[1]);
+    half[2 * (w & 1) + 1] = pack_bf16x2(v[2], v[3]);
+    if (w & 1)
+      *reinterpret_cast<u32x4*>(smem + buf * kStageBytes + xoff + 16 * c * kRowBytes + ((xslot ^ (w >> 1)) << 4)) = half;
   };
   // The same for dY, once it is in LDS.
   auto clear_dy = [&](const Stage& g, int buf) __attribute__((always_inline)) {
@@ -221,65 +221,84 @@ __global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
     foff[1][j] = kOpBytes + frow + ((((wn * 128 + col) >> 3) ^ lds_swizzle_k(i16 >> 2)) << 4) + 8 * (i16 & 1);
   }
   bf16x8 fy[2][4], fx[2][4];
-  auto read_frags = [&](int b, int buf, int kk) __attribute__((always_inline)) {
-    const unsigned char* st = smem + buf * kStageBytes + kk * 16 * kRowBytes;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const v4i16 lo = lds_read_tr(st + foff[0][j]), hi = lds_read_tr(st + foff[0][j] + 4 * kRowBytes);
-      fy[b][j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const v4i16 lo = lds_read_tr(st + foff[1][j]), hi = lds_read_tr(st + foff[1][j] + 4 * kRowBytes);
-      fx[b][j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    }
+  // Fragment f of a sub-step, in the order in which the MFMAs need them:
+  // dY block 0, X blocks 0 .. 3, dY blocks 1 .. 3.
+  auto read_frag = [&](int b, int buf, int kk, int f) __attribute__((always_inline)) {
+    const bool is_x = f >= 1 && f <= 4;
+    const int j = is_x ? f - 1 : f == 0 ? 0 : f - 4;
+    const unsigned char* p = smem + buf * kStageBytes + kk * 16 * kRowBytes + foff[is_x][j];
+    const v4i16 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * kRowBytes);
+    const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    if (is_x) fx[b][j] = v;
+    else fy[b][j] = v;
   };
-  auto mfmas = [&](int b) __attribute__((always_inline)) {
+
+  // One stage is 64 MFMAs per wave. Between two of them goes a little of
+  // everything else, in a fixed order: the fragments of the next sub-step, the
+  // copies of the next stage's dY, the loads of the X bytes after that, and
+  // the decoding of the next stage's X. The last sub-step's fragments are in
+  // registers halfway through it: there the workgroup meets, and the next
+  // stage's first fragments are read under the remaining MFMAs.
+  auto stage = [&](int s, Stage& gd, Stage& gx) __attribute__((always_inline)) {
+    const int P = (s - s_begin) & 1;
+    if (s + 1 < s_end) next(gd);
+    if (s + 2 < s_end) next(gx);
+    const u16* base = dy_base(gd);
+    const int skip = gd.t0 - min(gd.t0, last_base);
+    // The next stage's X bytes have arrived (the last wait was for
+    // everything). Naming them here places the compiler's own wait for them
+    // before the copies of dY, which it would otherwise wait for too.
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int c = 0; c < kChunks; ++c) {
+      qv[0][c] = qv[1][c];
+      ev[0][c] = ev[1][c];
+      asm volatile("" : "+v"(qv[0][c]), "+v"(ev[0][c]));
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[b][j], fy[b][i], acc[i][j], 0, 0, 0);
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int m = 0; m < 16; ++m) {
+        const int slot = 16 * kk + m;
+        if (slot == 56) {
+          wait_vmcnt<0>();
+          __syncthreads();
+          clear_dy(gd, P ^ 1);
+        }
+        acc[m >> 2][m & 3] =
+            __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[kk & 1][m & 3], fy[kk & 1][m >> 2], acc[m >> 2][m & 3], 0, 0, 0);
+        if (kk < 3 && m < 8) read_frag((kk + 1) & 1, P, kk + 1, m);
+        if (slot >= 56) read_frag(0, P ^ 1, 0, slot - 56);
+        if (slot < 16 && m % 2 == 1) copy_dy(base, P ^ 1, m / 2);
+        if (slot >= 16 && slot < 24 && m % 2 == 0) load_x(gx, 1, m / 2);
+        if (slot >= 3 && slot < 51 && slot % 3 == 0) write_x(skip, 0, P ^ 1, (slot / 3 - 1) / 4, (slot / 3 - 1) % 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   };
 
   if (s_begin < s_end) {
     const int plane = s_begin / per_plane;
     Stage gd{static_cast<const u16*>(it.dy) + (int64_t)plane * rows * lda, (s_begin - plane * per_plane) * kWgStep};
     Stage gx = gd;  // one stage further: the loads of X run two stages ahead
-    load_x(gx);
-    issue_dy(gd, 0);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) write_x(gx, 0, c);
+    for (int c = 0; c < kChunks; ++c) load_x(gx, 0, c);
+    const u16* base = dy_base(gd);
+#pragma unroll
+    for (int p = 0; p < kDmaPerWave; ++p) copy_dy(base, 0, p);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) write_x(gd.t0 - min(gd.t0, last_base), 0, 0, c, w);
     if (s_begin + 1 < s_end) next(gx);
-    load_x(gx);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) load_x(gx, 1, c);
     wait_vmcnt<0>();
     __syncthreads();
     clear_dy(gd, 0);
-    // Steps past the last load a stage again and use nothing of it.
-    for (int s = s_begin; s < s_end; ++s) {
-      const int buf = (s - s_begin) & 1;
-      if (s + 1 < s_end) next(gd);
-      issue_dy(gd, buf ^ 1);
-      read_frags(0, buf, 0);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (kk < 3) read_frags((kk + 1) & 1, buf, kk + 1);
-        mfmas(kk & 1);
-        if (kk < 2) {
-          write_x(gd, buf ^ 1, 2 * kk);
-          write_x(gd, buf ^ 1, 2 * kk + 1);
-        }
-        if (kk == 1) {
-          if (s + 2 < s_end) next(gx);
-          load_x(gx);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      wait_vmcnt<0>();
-      __syncthreads();
-      clear_dy(gd, buf ^ 1);
-    }
+    for (int f = 0; f < 8; ++f) read_frag(0, 0, 0, f);
+    // Steps past the last load a stage again and use nothing of it.
+    for (int s = s_begin; s < s_end; ++s) stage(s, gd, gx);
+    __syncthreads();  // the last fragments have been read
   }
 
   // The tile leaves through LDS, in fp32 and in two halves (blocks 0, 1 and
