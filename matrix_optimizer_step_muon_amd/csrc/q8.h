@@ -74,4 +74,45 @@ MUON_INLINE void q8_decode(u32x2 w, uint32_t E, int kind, float v[8]) {
   q8_decode4(w[1], unit, kind, v + 4);
 }
 
+// Four bytes as packed bf16, for an exponent byte that several of them share;
+// `live` false gives zeros. Both ways are exact, since q has at most 8
+// significant bits and the unit is a power of two.
+// int8: bytes with the sign bit flipped are put behind 0x64, which makes the
+// fp16 numbers 1024 + 128 + q; times the unit minus 1152 units is the value
+// (one mixed-precision fma per element, two instructions per element in all).
+// e4m3: the converting instruction scales by the unit itself (three
+// instructions per four elements); q is replaced by NaN codes for E = 255.
+template <int KIND>
+struct Q8Group {
+  float unit, bias;
+  uint32_t keep, set;
+  MUON_INLINE Q8Group(uint32_t E, bool live) {
+    if constexpr (KIND == MUON_Q8_INT8) {
+      unit = live ? q8_unit(E) : 0.f;
+      bias = -1152.f * unit;
+    } else {
+      unit = __uint_as_float(E << 23);
+      keep = live ? ~0u : 0u;
+      set = live && E == 255u ? 0x7f7f7f7fu : 0u;
+    }
+  }
+  MUON_INLINE u32x2 bf16x4(uint32_t w) const {
+    u32x2 o;
+    if constexpr (KIND == MUON_Q8_INT8) {
+      typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+      const uint32_t t = w ^ 0x80808080u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f16x2 f = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, t, h ? 0x04030402u : 0x04010400u));
+        o[h] = pack_bf16x2(fmaf((float)f[0], unit, bias), fmaf((float)f[1], unit, bias));
+      }
+    } else {
+      const int t = (int)((w & keep) | set);
+      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(t, unit, false));
+      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(t, unit, true));
+    }
+    return o;
+  }
+};
+
 }  // namespace muon

@@ -21,12 +21,14 @@
 
 namespace muon {
 
-// Stage geometry: 64 tokens of 256 bf16 columns per operand, two stages.
+// Stage geometry: 64 tokens of 256 bf16 columns per operand. dY has a ring of
+// three buffers, since its copies run two stages ahead; X, which waits in
+// registers, has two. Together they are all of a CU's 160 KB.
 constexpr int kRowBytes = kWgTile * 2;
 constexpr int kOpBytes = kWgStep * kRowBytes;  // 32 KB
-constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kDmaPerWave = kOpBytes / 1024 / 4;       // 8
-constexpr int kChunks = kWgStep * kWgTile / 16 / 256;  // 16-byte checkpoint chunks per thread: 4
+constexpr int kDyBufs = 3, kXBufs = 2;
+constexpr int kWaves = 8;  // 2 rows of 4: each wave owns 128 x 64 of the tile
+constexpr int kLdsBytes = (kDyBufs + kXBufs) * kOpBytes;
 
 typedef const __attribute__((address_space(4))) WgArgs* ArgsPtr;
 
@@ -93,8 +95,13 @@ MUON_INLINE void store_grad(const __attribute__((address_space(4))) WgItem& it, 
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
-  __shared__ __align__(1024) unsigned char smem[2 * kStageBytes];
+__global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) {
+  constexpr int NW = kWaves, NT = 64 * NW;
+  constexpr int NB = 16 / NW;                            // 32-column blocks of X per wave
+  constexpr int kDmaPerWave = kOpBytes / 1024 / NW;      // copies of dY per wave and stage
+  constexpr int kChunks = kWgStep * kWgTile / 16 / NT;   // 16-byte checkpoint chunks per thread
+  constexpr int kRowStep = NT / 16;                      // token rows between them
+  __shared__ __align__(1024) unsigned char smem[kLdsBytes];
   const ArgsPtr a = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
   const int unit = xcd_unit(blockIdx.x, a->units);
   int idx = 0;
@@ -112,12 +119,12 @@ __global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
   const int s_end = (int)((int64_t)total * (split + 1) / it.splits);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
-  f32x16 acc[4][4];
+  const int wm = wave / (NW / 2), wn = wave % (NW / 2);
+  f32x16 acc[4][NB];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
@@ -147,64 +154,68 @@ __global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
     }
   };
 
-  // dY: instruction (wave, p) copies token rows 2*(8*wave + p) and the next;
+  // dY: instruction (wave, p) copies token rows 2*(kDmaPerWave*wave + p) and the next;
   // lane l carries slot l % 32 of row l / 32, which holds chunk slot ^ swz(row).
   // Chunks past the last column read the last one: columns are independent,
   // and those are never stored.
   uint32_t dvoff[kDmaPerWave];
 #pragma unroll
   for (int p = 0; p < kDmaPerWave; ++p) {
-    const int r = 16 * wave + 2 * p + (lane >> 5);
+    const int r = 2 * (kDmaPerWave * wave + p) + (lane >> 5);
     dvoff[p] = (uint32_t)min(r, rows - 1) * (uint32_t)(lda * 2) +
                min((lane & 31) ^ lds_swizzle_k(r), (it.na - n0) / 8 - 1) * 16;
   }
   auto dy_base = [&](const Stage& g) __attribute__((always_inline)) {
     return g.dy + min(g.t0, last_base) * lda + n0;
   };
-  auto copy_dy = [&](const u16* base, int buf, int p) __attribute__((always_inline)) {
-    dma16s(base, dvoff[p], lds0 + buf * kStageBytes + (wave * kDmaPerWave + p) * 1024);
+  auto copy_dy = [&](const u16* base, uint32_t buf, int p) __attribute__((always_inline)) {
+    dma16s(base, dvoff[p], lds0 + buf + (wave * kDmaPerWave + p) * 1024);
   };
-  // X: chunk c of a thread is bytes 16*(tid % 16) .. of token row 16c + tid/16.
+  // X: chunk c of a thread is bytes 16*(tid % 16) .. of token row kRowStep*c + tid/16.
   const int qr = tid >> 4, qc = tid & 15;
   const int qcol = k0 + 16 * min(qc, (it.k - 1 - k0) / 16);  // the last chunk with a column of this matrix
   uint32_t qvoff[kChunks], evoff[kChunks];
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
-    const uint32_t r = (uint32_t)min(16 * c + qr, rows - 1);
+    const uint32_t r = (uint32_t)min(kRowStep * c + qr, rows - 1);
     qvoff[c] = r * (uint32_t)ldq + qcol;
     evoff[c] = r * (uint32_t)lde + qcol / kGroup;
   }
-  // Two sets of registers: one is decoded while the next stage's bytes arrive
-  // in the other.
-  u32x4 qv[2][kChunks];
-  uint32_t ev[2][kChunks];
+  u32x4 qv[2][kChunks], qd[kChunks];  // two stages on their way, one being decoded
+  uint32_t ev[2][kChunks], ed[kChunks];
   auto load_x = [&](const Stage& g, int set, int c) __attribute__((always_inline)) {
     const int64_t t = min(g.t0, last_base);
     qv[set][c] = gload16(xq + t * ldq + qvoff[c]);
     ev[set][c] = *((const g_u8*)(xe + t * lde + evoff[c]));
   };
+  auto take_x = [&](int set) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      qd[c] = qv[set][c];
+      ed[c] = ev[set][c];
+      asm volatile("" : "+v"(qd[c]), "+v"(ed[c]));
+    }
+  };
   // Bytes 4w .. 4w+3 of chunk c as bf16; w odd completes 16 bytes, which are
   // stored. Rows that are not the stage's become zeros.
-  const uint32_t xoff = kOpBytes + qr * kRowBytes, xslot = (uint32_t)(2 * qc) ^ lds_swizzle_k(qr);
+  const uint32_t xoff = qr * kRowBytes, xslot = (uint32_t)(2 * qc) ^ lds_swizzle_k(qr);
   u32x4 half;
-  auto write_x = [&](int skip, int set, int buf, int c, int w) __attribute__((always_inline)) {
-    const int r = 16 * c + qr;
-    const bool live = r >= skip && r < rows;
-    float v[4];
-    q8_decode4(live ? qv[set][c][w] : 0u, live ? q8_unit(ev[set][c]) : 0.f, KIND, v);
-    half[2 * (w & 1)] = pack_bf16x2(v[0], v[1]);
-    half[2 * (w & 1) + 1] = pack_bf16x2(v[2], v[3]);
+  auto write_x = [&](int skip, uint32_t buf, int c, int w) __attribute__((always_inline)) {
+    const int r = kRowStep * c + qr;
+    const u32x2 t = Q8Group<KIND>(ed[c], r >= skip && r < rows).bf16x4(qd[c][w]);
+    half[2 * (w & 1)] = t[0];
+    half[2 * (w & 1) + 1] = t[1];
     if (w & 1)
-      *reinterpret_cast<u32x4*>(smem + buf * kStageBytes + xoff + 16 * c * kRowBytes + ((xslot ^ (w >> 1)) << 4)) = half;
+      *reinterpret_cast<u32x4*>(smem + buf + xoff + kRowStep * c * kRowBytes + ((xslot ^ (w >> 1)) << 4)) = half;
   };
   // The same for dY, once it is in LDS.
-  auto clear_dy = [&](const Stage& g, int buf) __attribute__((always_inline)) {
+  auto clear_dy = [&](const Stage& g, uint32_t buf) __attribute__((always_inline)) {
     const int skip = g.t0 - min(g.t0, last_base);
     if (skip == 0 && rows >= kWgStep) return;
     const u32x4 z = {0u, 0u, 0u, 0u};
-    for (int o = tid * 16; o < kOpBytes; o += 256 * 16) {
+    for (int o = tid * 16; o < kOpBytes; o += NT * 16) {
       const int r = o / kRowBytes;
-      if (r < skip || r >= rows) *reinterpret_cast<u32x4*>(smem + buf * kStageBytes + o) = z;
+      if (r < skip || r >= rows) *reinterpret_cast<u32x4*>(smem + buf + o) = z;
     }
     __syncthreads();
   };
@@ -218,87 +229,120 @@ __global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
   for (int j = 0; j < 4; ++j) {
     const int col = 32 * j + 16 * (G & 1) + 4 * (i16 & 3);
     foff[0][j] = frow + ((((wm * 128 + col) >> 3) ^ lds_swizzle_k(i16 >> 2)) << 4) + 8 * (i16 & 1);
-    foff[1][j] = kOpBytes + frow + ((((wn * 128 + col) >> 3) ^ lds_swizzle_k(i16 >> 2)) << 4) + 8 * (i16 & 1);
+    foff[1][j] = frow + ((((wn * NB * 32 + col) >> 3) ^ lds_swizzle_k(i16 >> 2)) << 4) + 8 * (i16 & 1);
   }
-  bf16x8 fy[2][4], fx[2][4];
+  bf16x8 fy[2][4], fx[2][NB];
   // Fragment f of a sub-step, in the order in which the MFMAs need them:
-  // dY block 0, X blocks 0 .. 3, dY blocks 1 .. 3.
-  auto read_frag = [&](int b, int buf, int kk, int f) __attribute__((always_inline)) {
-    const bool is_x = f >= 1 && f <= 4;
-    const int j = is_x ? f - 1 : f == 0 ? 0 : f - 4;
-    const unsigned char* p = smem + buf * kStageBytes + kk * 16 * kRowBytes + foff[is_x][j];
+  // dY block 0, the blocks of X, dY blocks 1 .. 3.
+  uint32_t fat[2][4];  // where this stage's lie
+  auto frags_at = [&](uint32_t dybuf, uint32_t xbuf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      fat[0][j] = foff[0][j] + dybuf;
+      fat[1][j] = foff[1][j] + xbuf;
+    }
+  };
+  auto read_frag = [&](int b, int kk, int f) __attribute__((always_inline)) {
+    const bool is_x = f >= 1 && f <= NB;
+    const int j = is_x ? f - 1 : f == 0 ? 0 : f - NB;
+    const unsigned char* p = smem + fat[is_x][j] + kk * 16 * kRowBytes;
     const v4i16 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * kRowBytes);
     const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     if (is_x) fx[b][j] = v;
     else fy[b][j] = v;
   };
 
-  // One stage is 64 MFMAs per wave. Between two of them goes a little of
-  // everything else, in a fixed order: the fragments of the next sub-step, the
-  // copies of the next stage's dY, the loads of the X bytes after that, and
-  // the decoding of the next stage's X. The last sub-step's fragments are in
-  // registers halfway through it: there the workgroup meets, and the next
-  // stage's first fragments are read under the remaining MFMAs.
-  auto stage = [&](int s, Stage& gd, Stage& gx) __attribute__((always_inline)) {
-    const int P = (s - s_begin) & 1;
-    if (s + 1 < s_end) next(gd);
-    if (s + 2 < s_end) next(gx);
-    const u16* base = dy_base(gd);
-    const int skip = gd.t0 - min(gd.t0, last_base);
-    // The next stage's X bytes have arrived (the last wait was for
-    // everything). Naming them here places the compiler's own wait for them
-    // before the copies of dY, which it would otherwise wait for too.
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      qv[0][c] = qv[1][c];
-      ev[0][c] = ev[1][c];
-      asm volatile("" : "+v"(qv[0][c]), "+v"(ev[0][c]));
-    }
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-      for (int m = 0; m < 16; ++m) {
-        const int slot = 16 * kk + m;
-        if (slot == 56) {
-          wait_vmcnt<0>();
-          __syncthreads();
-          clear_dy(gd, P ^ 1);
-        }
-        acc[m >> 2][m & 3] =
-            __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[kk & 1][m & 3], fy[kk & 1][m >> 2], acc[m >> 2][m & 3], 0, 0, 0);
-        if (kk < 3 && m < 8) read_frag((kk + 1) & 1, P, kk + 1, m);
-        if (slot >= 56) read_frag(0, P ^ 1, 0, slot - 56);
-        if (slot < 16 && m % 2 == 1) copy_dy(base, P ^ 1, m / 2);
-        if (slot >= 16 && slot < 24 && m % 2 == 0) load_x(gx, 1, m / 2);
-        if (slot >= 3 && slot < 51 && slot % 3 == 0) write_x(skip, 0, P ^ 1, (slot / 3 - 1) / 4, (slot / 3 - 1) % 4);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-  };
-
   if (s_begin < s_end) {
     const int plane = s_begin / per_plane;
-    Stage gd{static_cast<const u16*>(it.dy) + (int64_t)plane * rows * lda, (s_begin - plane * per_plane) * kWgStep};
-    Stage gx = gd;  // one stage further: the loads of X run two stages ahead
+    Stage g1{static_cast<const u16*>(it.dy) + (int64_t)plane * rows * lda, (s_begin - plane * per_plane) * kWgStep};
+    auto skip_of = [&](const Stage& g) { return g.t0 - min(g.t0, last_base); };
+    uint32_t d0 = 0, d1 = kOpBytes, d2 = 2 * kOpBytes;  // dY of this stage, the next, the one after
+    uint32_t x0 = kDyBufs * kOpBytes, x1 = x0 + kOpBytes;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) load_x(gx, 0, c);
-    const u16* base = dy_base(gd);
+    for (int c = 0; c < kChunks; ++c) load_x(g1, 0, c);
+    const u16* base = dy_base(g1);
 #pragma unroll
-    for (int p = 0; p < kDmaPerWave; ++p) copy_dy(base, 0, p);
+    for (int p = 0; p < kDmaPerWave; ++p) copy_dy(base, d0, p);
+    take_x(0);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) write_x(gd.t0 - min(gd.t0, last_base), 0, 0, c, w);
-    if (s_begin + 1 < s_end) next(gx);
+      for (int w = 0; w < 4; ++w) write_x(skip_of(g1), x0, c, w);
+    // g1, g2, g3: one, two and three stages ahead of the loop's. Stages past
+    // the last one are the last one again, and nothing of them is used.
+    const Stage first = g1;
+    if (s_begin + 1 < s_end) next(g1);
+    Stage g2 = g1;
+    if (s_begin + 2 < s_end) next(g2);
+    Stage g3 = g2;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) load_x(gx, 1, c);
+    for (int c = 0; c < kChunks; ++c) load_x(g1, 0, c);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) load_x(g2, 1, c);
+    base = dy_base(g1);
+#pragma unroll
+    for (int p = 0; p < kDmaPerWave; ++p) copy_dy(base, d1, p);
     wait_vmcnt<0>();
     __syncthreads();
-    clear_dy(gd, 0);
+    clear_dy(first, d0);
+    frags_at(d0, x0);
 #pragma unroll
-    for (int f = 0; f < 8; ++f) read_frag(0, 0, 0, f);
-    // Steps past the last load a stage again and use nothing of it.
-    for (int s = s_begin; s < s_end; ++s) stage(s, gd, gx);
-    __syncthreads();  // the last fragments have been read
+    for (int f = 0; f < 4 + NB; ++f) read_frag(0, 0, f);
+
+    // One stage is kSlots MFMAs per wave. Between two of them goes a little of
+    // everything else, in a fixed order: the fragments of the next sub-step,
+    // the loads of X three stages ahead and the copies of dY two ahead, and
+    // the decoding of the next stage's X. The last sub-step's fragments are in
+    // registers a few MFMAs before its end: there the workgroup meets, and the
+    // next stage's first fragments are read under the remaining MFMAs.
+    //
+    // What a wave waits for is always a whole stage old. take_x() makes the
+    // compiler wait for this set's loads, issued two stages ago; it counts the
+    // other set's as issued since and leaves as many in flight, which are the
+    // copies of the stage before (it does not know of those). The wait at the
+    // meeting is for these copies; since then this wave has issued its loads
+    // of X, two per chunk, and kDmaPerWave copies.
+    constexpr int kPer = 4 * NB, kSlots = 4 * kPer, kMeet = kSlots - 4 - NB;
+    auto stage = [&](auto parity, int s) __attribute__((always_inline)) {
+      constexpr int P = decltype(parity)::value;
+      const int skip = skip_of(g1);
+      if (s + 3 < s_end) next(g3);
+      const u16* base2 = dy_base(g2);
+      take_x(P);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int m = 0; m < kPer; ++m) {
+          const int slot = kPer * kk + m;
+          if (slot == kMeet) {
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * kChunks + kDmaPerWave) : "memory");
+            clear_dy(g1, d1);
+            frags_at(d1, x1);
+          }
+          const int i = m / NB, j = m % NB;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[kk & 1][j], fy[kk & 1][i], acc[i][j], 0, 0, 0);
+          if (kk < 3 && m < 4 + NB) read_frag((kk + 1) & 1, kk + 1, m);
+          if (slot >= kMeet) read_frag(0, 0, slot - kMeet);
+          if (slot < 2 * kChunks && m % 2 == 1) load_x(g3, P, m / 2);
+          if (slot >= 2 * kChunks && slot < 2 * (kChunks + kDmaPerWave) && m % 2 == 1) copy_dy(base2, d2, slot / 2 - kChunks);
+          if (slot >= 3 && slot < 3 + 12 * kChunks && slot % 3 == 0) write_x(skip, x1, (slot / 3 - 1) / 4, (slot / 3 - 1) % 4);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      g1 = g2;
+      g2 = g3;
+      const uint32_t d = d0;
+      d0 = d1, d1 = d2, d2 = d;
+      const uint32_t x = x0;
+      x0 = x1, x1 = x;
+    };
+    int s = s_begin;
+    for (; s + 1 < s_end; s += 2) {
+      stage(std::integral_constant<int, 0>{}, s);
+      stage(std::integral_constant<int, 1>{}, s + 1);
+    }
+    if (s < s_end) stage(std::integral_constant<int, 0>{}, s);
+    wait_vmcnt<0>();  // the copies past the last stage, before this LDS is used again
+    __syncthreads();
   }
 
   // The tile leaves through LDS, in fp32 and in two halves (blocks 0, 1 and
@@ -312,18 +356,18 @@ __global__ void __launch_bounds__(256, 1) wgrad_kernel(WgArgs) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int r = wm * 64 + 32 * i + (flane & 31), u = wn * 32 + 8 * j + 2 * g + (flane >> 5);
+          const int r = wm * 64 + 32 * i + (flane & 31), u = wn * 8 * NB + 8 * j + 2 * g + (flane >> 5);
           const f32x16& t = acc[2 * half + i][j];
           *reinterpret_cast<f32x4*>(smem + r * 1024 + ((u ^ (r & 63)) << 4)) =
               f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
         }
     __syncthreads();
 #pragma unroll 4
-    for (int q = 0; q < 32; ++q) {
-      const int r = 4 * q + wave;
+    for (int q = 0; q < 128 / NW; ++q) {
+      const int r = NW * q + wave;
       const f32x4 t = *reinterpret_cast<const f32x4*>(smem + r * 1024 + ((flane ^ (r & 63)) << 4));
       const float v[4] = {t[0], t[1], t[2], t[3]};
       const int n = (r >> 6) * 128 + half * 64 + (r & 63);
@@ -365,8 +409,8 @@ __global__ void __launch_bounds__(256) wgrad_reduce_kernel(WgArgs) {
 
 hipError_t launch_wgrad(const WgArgs& args, int kind, hipStream_t s) {
   if (args.units > 0) {
-    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_INT8>, dim3(args.units), dim3(256), 0, s, args);
-    else hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_E4M3>, dim3(args.units), dim3(256), 0, s, args);
+    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_INT8>, dim3(args.units), dim3(64 * kWaves), 0, s, args);
+    else hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_E4M3>, dim3(args.units), dim3(64 * kWaves), 0, s, args);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
