@@ -235,28 +235,47 @@ muon_status norm_backward(const muon_norm_site* site, const muon_norm_grads* gra
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
-// dY is read as it is if its rows are 16-byte aligned bf16 with whole 16-byte
-// chunks; otherwise it is rewritten into the workspace.
-bool needs_pack(const muon_wgrad_item& it, int32_t dtype) {
-  return dtype == MUON_F32 || reinterpret_cast<uintptr_t>(it.dy) % 16 || it.ld_dy % 8 || it.n % 8;
+// The large kernel reads dY as it is if its rows are 16-byte aligned bf16 with
+// whole 16-byte chunks; otherwise it is rewritten into the workspace first.
+bool dy_aligned(const muon_wgrad_item& it, int32_t dtype) {
+  return reinterpret_cast<uintptr_t>(it.dy) % 16 == 0 && it.ld_dy * elem_of(dtype) % 16 == 0 && it.n % 8 == 0;
 }
 
-// How many pieces the sum over tokens is cut into, for items of which the
-// longest has `longest` stages and all together `tiles` tiles. One workgroup per
-// CU works on one tile at a time, so a launch takes ceil(tiles*s/256) rounds of
-// longest/s stages; pieces cost a partial tile each (256 KB written and read
-// back, about kPartialCost of a stage) and a second launch.
-int choose_splits(int64_t tiles, int64_t longest) {
+// A way to run a launch, and what it is expected to take.
+struct Choice {
+  int edge, splits;
+  double us;
+};
+
+// Which tile edge, and how many pieces the sum over tokens is cut into, for
+// items with t256 and t64 tiles in all, at most `rows` tokens, and `packed`
+// bytes of dY that the large kernel would have rewritten first. The estimates
+// are in microseconds, from a sweep on one MI355X (64 x 64 to 2048 x 2048 and
+// 1024 x 5120 outputs, 16 to 8192 tokens, 1 to 16 pieces):
+// - a round is one workgroup per CU. The large kernel takes 1.4 to 1.75 us per
+//   stage of 64 tokens and 8 to fill and empty a tile; the small one 1.2 (fp32:
+//   1.55) per 128 tokens and 2;
+// - pieces cost their partial tiles, written and read back (256 KB each at
+//   about 3.5 TB/s; 16 KB), one more launch, and 0.3 us per piece in it;
+// - rewriting dY costs a launch and its bytes at about 3 TB/s.
+// At 1024 x 1024 and 512 bf16 tokens, for example, one round of the small
+// kernel takes 14 us and the large one 28; at 8192 tokens 139 and, in 8 pieces, 61.
+Choice choose(int64_t t256, int64_t t64, int64_t rows, int parts, int64_t packed) {
   constexpr int64_t kCus = 256;
-  constexpr double kTileCost = 3.0, kPartialCost = 0.13, kLaunchCost = 4.0;
-  int best = 1;
-  double best_cost = 1e300;
-  for (int s = 1; s <= 64 && s <= std::max<int64_t>(1, longest / 2); ++s) {
-    const double rounds = double(ceil_div(tiles * s, kCus));
-    double cost = rounds * (double(ceil_div(longest, s)) + kTileCost);
-    if (s > 1) cost += kLaunchCost + kPartialCost * double(tiles * s);
-    if (cost < best_cost * 0.98) best = s, best_cost = cost;
-    if (tiles * s >= 2 * kCus) break;
+  const int64_t stages = ceil_div(rows, muon::kWgStep) * parts, blocks = ceil_div(rows, 128);
+  const double pack = packed ? 3.0 + double(packed) * 3.3e-7 : 0.0;
+  Choice best{muon::kWgTile, 1, 1e300};
+  for (int s = 1; s <= 64; ++s) {
+    if (s == 1 || s <= stages / 2) {
+      double us = pack + double(ceil_div(t256 * s, kCus)) * (8.0 + 1.65 * double(ceil_div(stages, s)));
+      if (s > 1) us += 3.0 + 0.3 * s + 0.145 * double(t256 * s);
+      if (us < best.us) best = {muon::kWgTile, s, us};
+    }
+    if (s == 1 || s <= blocks) {
+      double us = double(ceil_div(t64 * s, kCus)) * (2.0 + (parts == 3 ? 1.55 : 1.2) * double(ceil_div(blocks, s)));
+      if (s > 1) us += 3.0 + 0.3 * s + 0.011 * double(t64 * s);
+      if (us < best.us) best = {muon::kWgSmall, s, us};
+    }
   }
   return best;
 }
@@ -271,14 +290,27 @@ struct WgradPlan {
 muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32_t g_dtype, WgradPlan& p) {
   p.args = muon::WgArgs{};
   p.args.n_items = n;
-  p.args.scale_f32 = dtype == MUON_F32;
+  p.args.dy_f32 = dtype == MUON_F32;
   p.args.g_f32 = g_dtype == MUON_F32;
   const int parts = dtype == MUON_F32 ? 3 : 1;
-  int64_t tiles = 0, longest = 0;
+  int64_t t256 = 0, t64 = 0, rows = 0, packed = 0;
+  for (int i = 0; i < n; ++i) {
+    const muon_wgrad_item& it = items[i];
+    t256 += ceil_div(it.n, muon::kWgTile) * ceil_div(it.x.cols, muon::kWgTile);
+    t64 += ceil_div(it.n, muon::kWgSmall) * ceil_div(it.x.cols, muon::kWgSmall);
+    rows = std::max(rows, it.x.rows);
+    if (dtype == MUON_F32 || !dy_aligned(it, dtype)) packed += it.x.rows * it.n * (dtype == MUON_F32 ? 10 : 4);
+  }
+  const Choice choice = choose(t256, t64, rows, parts, packed);
+  const bool large = choice.edge == muon::kWgTile;
+  p.args.edge = choice.edge;
   size_t at = 0;
+  int64_t units = 0, partials = 0;
   for (int i = 0; i < n; ++i) {
     const muon_wgrad_item& it = items[i];
     muon::WgItem& d = p.args.item[i];
+    d.dy = it.dy;
+    d.lda = it.ld_dy;
     d.q = static_cast<const uint8_t*>(it.x.q);
     d.e = static_cast<const uint8_t*>(it.x.e);
     d.scale = it.scale;
@@ -291,26 +323,19 @@ muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32
     d.k = int32_t(it.x.cols);
     d.na = int32_t(ceil_div(it.n, 8) * 8);
     d.parts = parts;
+    d.dy_vec = dy_aligned(it, dtype);
     d.beta = it.beta;
-    d.tiles_n = int32_t(ceil_div(it.n, muon::kWgTile));
-    d.tiles_k = int32_t(ceil_div(it.x.cols, muon::kWgTile));
-    d.dy = it.dy;
-    d.lda = it.ld_dy;
     p.pack[i] = SIZE_MAX;
-    if (needs_pack(it, dtype)) {
+    if (large && (dtype == MUON_F32 || !dy_aligned(it, dtype))) {
       p.pack[i] = at;
       d.lda = d.na;
       at += round256(size_t(parts) * size_t(it.x.rows) * size_t(d.na) * 2);
     }
-    tiles += int64_t(d.tiles_n) * d.tiles_k;
-    longest = std::max<int64_t>(longest, ceil_div(it.x.rows, muon::kWgStep) * parts);
-  }
-  const int want = choose_splits(tiles, longest);
-  int64_t units = 0, partials = 0;
-  for (int i = 0; i < n; ++i) {
-    muon::WgItem& d = p.args.item[i];
-    const int64_t t = int64_t(d.tiles_n) * d.tiles_k, stages = ceil_div(d.rows, muon::kWgStep) * parts;
-    d.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(want, stages / 2)));
+    const int64_t pieces = large ? ceil_div(d.rows, muon::kWgStep) * parts / 2 : ceil_div(d.rows, 128);
+    d.tiles_n = int32_t(ceil_div(it.n, choice.edge));
+    d.tiles_k = int32_t(ceil_div(it.x.cols, choice.edge));
+    const int64_t t = int64_t(d.tiles_n) * d.tiles_k;
+    d.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(choice.splits, pieces)));
     d.unit0 = int32_t(units);
     d.part0 = int32_t(partials);
     units += t * d.splits;
@@ -319,7 +344,7 @@ muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32
   }
   p.args.units = int32_t(units);
   p.partial = at;
-  p.bytes = at + size_t(partials) * muon::kWgPart * sizeof(float);
+  p.bytes = at + size_t(partials) * choice.edge * choice.edge * sizeof(float);
   return MUON_OK;
 }
 

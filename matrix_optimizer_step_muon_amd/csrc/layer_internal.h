@@ -32,15 +32,17 @@ inline int norm_backward_blocks(int64_t rows, int64_t cols) {
 
 // ------------------------------------------------------------ weight gradients
 
-constexpr int kWgTile = 256;   // output tile edge
-constexpr int kWgStep = 64;    // tokens per stage
+constexpr int kWgTile = 256;   // output tile edge of the large kernel
+constexpr int kWgStep = 64;    // tokens per stage of it
+constexpr int kWgSmall = 64;   // output tile edge of the small kernel
 constexpr int kWgItems = 16;   // matrices per launch
 constexpr int kWgPart = kWgTile * kWgTile;  // floats of one partial tile
 
 // One matrix of a launch. Units (tiles x splits) are numbered consecutively
 // over the items; unit0 is this item's first.
 struct WgItem {
-  const void* dy;      // bf16, 16-byte aligned rows of lda elements; parts planes of `rows` rows
+  const void* dy;      // large kernel: bf16, 16-byte aligned rows of lda elements, parts planes of
+                       // `rows` rows; small kernel: the caller's
   const uint8_t* q;
   const uint8_t* e;
   const void* scale;   // dtype, or null
@@ -48,7 +50,8 @@ struct WgItem {
   const void* c;
   int64_t lda, ldq, lde;
   int32_t rows, n, k, na;  // na: columns of dy that may be read (a multiple of 8)
-  int32_t parts;       // 1, or 3 for fp32 dY
+  int32_t parts;       // 1, or 3 for fp32 dY (large kernel)
+  int32_t dy_vec;      // 16-byte loads of dY (small kernel)
   int32_t tiles_n, tiles_k;
   int32_t splits;      // > 1: partial tiles go to the workspace
   int32_t unit0;
@@ -61,8 +64,9 @@ struct WgArgs {
   float* partial;
   int32_t n_items;
   int32_t units;
-  int32_t scale_f32;  // dtype of scale
-  int32_t g_f32;      // dtype of g and c
+  int32_t edge;   // kWgTile or kWgSmall
+  int32_t dy_f32; // dtype of dY (as given) and scale
+  int32_t g_f32;  // dtype of g and c
 };
 
 hipError_t launch_q8_save(const void* x, int64_t ldx, int dtype, const muon_q8& out, hipStream_t s);

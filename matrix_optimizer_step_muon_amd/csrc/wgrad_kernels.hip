@@ -48,51 +48,79 @@ MUON_INLINE void tile_of(int t, int tiles_n, int tiles_k, int& tn, int& tk) {
   tn = 4 * band + (r - tk * h);
 }
 
-// Four consecutive columns k .. k+3 of row n of the gradient.
-MUON_INLINE void store_grad(const __attribute__((address_space(4))) WgItem& it, bool scale_f32, bool g_f32, int n, int k,
-                            const float* v) {
-  if (n >= it.n || k >= it.k) return;
-  const int64_t at = (int64_t)n * it.k + k;
-  const int cnt = min(4, it.k - k);
-  float o[4];
+// The gradient's side of a kernel. A row of a tile is stored by LW lanes of
+// four columns each: consecutive ones, as one vector, where a row of the
+// gradient is a multiple of four long, and otherwise every LW-th, so that a
+// store instruction still covers whole lines.
+template <int LW>
+struct GradOut {
+  const __attribute__((address_space(4))) WgItem& it;
+  bool g_f32, vec;
+  int lane, k0;
+  float scale[4];
+
+  MUON_INLINE GradOut(const __attribute__((address_space(4))) WgItem& item, ArgsPtr a, int lane_, int k0_)
+      : it(item), g_f32(a->g_f32), vec((item.k & 3) == 0), lane(lane_), k0(k0_) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = v[i];
-  if (it.scale) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < cnt)
-        o[i] *= scale_f32 ? Elem<float>::load(static_cast<const float*>(it.scale) + k + i)
-                          : Elem<u16>::load(static_cast<const u16*>(it.scale) + k + i);
-  }
-  const bool vec = (it.k & 3) == 0;  // g and c are 16-byte aligned, k is a multiple of 4
-  if (it.beta != 0.f) {
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
-    if (g_f32) {
-      const float* p = static_cast<const float*>(it.c) + at;
-      if (vec) Vec4<float>::load(p, c);
-      else
-        for (int i = 0; i < cnt; ++i) c[i] = Elem<float>::load(p + i);
-    } else {
-      const u16* p = static_cast<const u16*>(it.c) + at;
-      if (vec) Vec4<u16>::load(p, c);
-      else
-        for (int i = 0; i < cnt; ++i) c[i] = Elem<u16>::load(p + i);
+    for (int i = 0; i < 4; ++i) {
+      scale[i] = 1.f;
+      if (it.scale && k0 + col(i) < it.k)
+        scale[i] = a->dy_f32 ? Elem<float>::load(static_cast<const float*>(it.scale) + k0 + col(i))
+                             : Elem<u16>::load(static_cast<const u16*>(it.scale) + k0 + col(i));
     }
+  }
+  // Column i of this lane, within the tile.
+  MUON_INLINE int col(int i) const { return vec ? 4 * lane + i : lane + LW * i; }
+  // This lane's columns (or, with four, 4*lane .. 4*lane+3 anyway) of a row in
+  // LDS whose 16-byte unit u, columns 4u .. 4u+3, is at unit(u).
+  template <class F>
+  MUON_INLINE void gather(float v[4], F unit, bool four) const {
+    if (vec || four) {
+      const f32x4 t = *reinterpret_cast<const f32x4*>(unit(lane));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] += it.beta * c[i];
+      for (int i = 0; i < 4; ++i) v[i] = t[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = unit(col(i) >> 2)[col(i) & 3];
+    }
   }
-  if (g_f32) {
-    float* p = static_cast<float*>(it.g) + at;
-    if (vec) Vec4<float>::store(p, o);
-    else
-      for (int i = 0; i < cnt; ++i) Elem<float>::store(p + i, o[i]);
-  } else {
-    u16* p = static_cast<u16*>(it.g) + at;
-    if (vec) Vec4<u16>::store(p, o);
-    else
-      for (int i = 0; i < cnt; ++i) Elem<u16>::store(p + i, o[i]);
+  // Row n of the gradient: the sums v of this lane's columns.
+  MUON_INLINE void store(int n, const float v[4]) const {
+    if (n >= it.n || k0 + col(0) >= it.k) return;
+    const int64_t at = (int64_t)n * it.k + k0;
+    float o[4], c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = v[i] * scale[i];
+    if (it.beta != 0.f) {
+      if (g_f32) load(static_cast<const float*>(it.c) + at, c);
+      else load(static_cast<const u16*>(it.c) + at, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += it.beta * c[i];
+    }
+    if (g_f32) put(static_cast<float*>(it.g) + at, o);
+    else put(static_cast<u16*>(it.g) + at, o);
   }
-}
+  template <class T>
+  MUON_INLINE void load(const T* p, float c[4]) const {
+    if (vec) {
+      Vec4<T>::load(p + 4 * lane, c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k0 + col(i) < it.k) c[i] = Elem<T>::load(p + col(i));
+    }
+  }
+  template <class T>
+  MUON_INLINE void put(T* p, const float o[4]) const {
+    if (vec) {
+      Vec4<T>::store(p + 4 * lane, o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k0 + col(i) < it.k) Elem<T>::store(p + col(i), o[i]);
+    }
+  }
+};
 
 template <int KIND>
 __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) {
@@ -348,8 +376,8 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
   // The tile leaves through LDS, in fp32 and in two halves (blocks 0, 1 and
   // 2, 3 of every wave: 128 rows of 256), so that a wave stores whole rows. The 16-byte
   // unit u of row r sits at unit u ^ (r % 64).
-  const bool scale_f32 = a->scale_f32, g_f32 = a->g_f32;
-  const int ftid = fresh_tid(), flane = ftid & 63;  // keeps these addresses out of the loop's registers
+  const int flane = fresh_tid() & 63;  // keeps these addresses out of the loop's registers
+  const GradOut<64> out(it, a, flane, k0);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if (half) __syncthreads();
@@ -367,67 +395,283 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
     __syncthreads();
 #pragma unroll 4
     for (int q = 0; q < 128 / NW; ++q) {
-      const int r = NW * q + wave;
-      const f32x4 t = *reinterpret_cast<const f32x4*>(smem + r * 1024 + ((flane ^ (r & 63)) << 4));
-      const float v[4] = {t[0], t[1], t[2], t[3]};
-      const int n = (r >> 6) * 128 + half * 64 + (r & 63);
-      if (it.splits > 1)
-        Vec4<float>::store(a->partial + (int64_t)(it.part0 + local) * kWgPart + n * kWgTile + flane * 4, v);
-      else
-        store_grad(it, scale_f32, g_f32, n0 + n, k0 + flane * 4, v);
+      const int r = NW * q + wave, n = (r >> 6) * 128 + half * 64 + (r & 63);
+      const unsigned char* row = smem + r * 1024;
+      float v[4];
+      out.gather(v, [&](int u) { return reinterpret_cast<const float*>(row + ((u ^ (r & 63)) << 4)); }, it.splits > 1);
+      if (it.splits > 1) Vec4<float>::store(a->partial + (int64_t)(it.part0 + local) * kWgPart + n * kWgTile + 4 * flane, v);
+      else out.store(n0 + n, v);
     }
   }
 }
 
+// ------------------------------------------------------------ small tiles
+//
+// 64 x 64 output tiles for products that would leave most CUs without a
+// 256 x 256 one: a call of a few small matrices is over in the time of its
+// memory round trips, and what counts is how many of these it takes. Each of
+// the four waves sums every fourth block of 32 tokens for the whole tile, on
+// its own: it stages both operands in an LDS region that only it uses, with
+// the next block's loads in flight, and nothing synchronises the workgroup
+// until the four sums are added. dY is read as it is, in any alignment, and
+// fp32 values are cut into their three bf16 parts on the way to LDS, so there
+// is no other launch.
+
+constexpr int kSmRow = kWgSmall * 2;     // bytes of an LDS row: 64 bf16 of one token
+constexpr int kSmOp = 32 * kSmRow;       // one operand of 32 tokens: 4 KB
+
+// x = hi + mid + lo, each the rest rounded toward zero to bf16: 8 bits each,
+// all 24 of a normal fp32 number, and never past the largest finite value.
+// Infinities and NaNs stay in hi alone. Returned as fp32 bit patterns whose
+// low halves are zero.
+MUON_INLINE void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  const uint32_t bits = __float_as_uint(x);
+  const bool fine = (bits & 0x7f800000u) != 0x7f800000u;
+  hi = fine ? bits & 0xffff0000u : __float_as_uint(bf16_to_f32(f32_to_bf16(x)));
+  const float r = fine ? x - __uint_as_float(hi) : 0.f;
+  mid = __float_as_uint(r) & 0xffff0000u;
+  lo = __float_as_uint(r - __uint_as_float(mid)) & 0xffff0000u;
+}
+
+// The slot of 16-byte chunk c of token row r: rows r .. r+3, which a
+// transposing read takes together, lie in different banks.
+MUON_INLINE int small_slot(int c, int r) { return c ^ ((r & 3) << 1); }
+
+template <int KIND, class T>
+__global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
+  constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+  __shared__ __align__(1024) unsigned char smem[4 * 4 * kSmOp];
+  const ArgsPtr a = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  const int unit = xcd_unit(blockIdx.x, a->units);
+  int idx = 0;
+  while (idx + 1 < a->n_items && unit >= a->item[idx + 1].unit0) ++idx;
+  const __attribute__((address_space(4))) WgItem& it = a->item[idx];
+  const int tiles = it.tiles_n * it.tiles_k;
+  const int local = unit - it.unit0, split = local / tiles, tile = local - split * tiles;
+  int tn, tk;
+  tile_of(tile, it.tiles_n, it.tiles_k, tn, tk);
+  const int n0 = tn * kWgSmall, k0 = tk * kWgSmall;
+  const int rows = it.rows, blocks = (rows + 31) / 32;
+  const int b_begin = (int)((int64_t)blocks * split / it.splits), b_end = (int)((int64_t)blocks * (split + 1) / it.splits);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  unsigned char* sy = smem + wave * 4 * kSmOp;   // PARTS planes of dY
+  unsigned char* sx = sy + 3 * kSmOp;
+
+  // dY: chunk c of a lane is 8 columns of token row 8c + lane/8; X: 16 bytes of
+  // token row 16c + lane/4.
+  const int yr = lane >> 3, yc = (lane & 7) * 8, xr = lane >> 2, xc = k0 + 16 * min(lane & 3, (it.k - 1 - k0) / 16);
+  const T* dy = static_cast<const T*>(it.dy) + n0 + yc;
+  const int ycols = it.n - n0 - yc;  // of these 8, the ones that exist
+  const bool vec = it.dy_vec;
+  float yv[4][8];
+  u32x4 xv[2];
+  uint32_t ev[2];
+  // Tokens past the last one read as zeros (X: as exponent bytes and codes of
+  // the last one, cleared when they are decoded).
+  auto load = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int t = 32 * b + 8 * c + yr;
+      const T* p = dy + (int64_t)t * it.lda;
+      if (t >= rows || ycols <= 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) yv[c][i] = 0.f;
+      } else if (vec) {
+        if constexpr (sizeof(T) == 4) {
+          Vec4<float>::load(p, yv[c]);
+          Vec4<float>::load(p + 4, yv[c] + 4);
+        } else {
+          const u32x4 w = gload16(p);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            yv[c][2 * i] = __uint_as_float(w[i] << 16);
+            yv[c][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) yv[c][i] = i < ycols ? Elem<T>::load(p + i) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t t = min(32 * b + 16 * c + xr, rows - 1);
+      xv[c] = gload16(it.q + t * it.ldq + xc);
+      ev[c] = *((const g_u8*)(it.e + t * it.lde + xc / kGroup));
+    }
+  };
+  auto stage = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int r = 8 * c + yr;
+      u32x4 o[PARTS];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (PARTS == 1) {
+          o[0][i] = pack_bf16x2(yv[c][2 * i], yv[c][2 * i + 1]);
+        } else {
+          uint32_t w[2][3];
+          split3(yv[c][2 * i], w[0][2], w[0][1], w[0][0]);
+          split3(yv[c][2 * i + 1], w[1][2], w[1][1], w[1][0]);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) o[q][i] = (w[0][q] >> 16) | w[1][q];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q)
+        *reinterpret_cast<u32x4*>(sy + q * kSmOp + r * kSmRow + (small_slot(lane & 7, r) << 4)) = o[q];
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = 16 * c + xr;
+      const Q8Group<KIND> grp(ev[c], 32 * b + r < rows);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x2 lo = grp.bf16x4(xv[c][2 * h]), hi = grp.bf16x4(xv[c][2 * h + 1]);
+        *reinterpret_cast<u32x4*>(sx + r * kSmRow + (small_slot(2 * (lane & 3) + h, r) << 4)) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+    }
+  };
+  // As in the large kernel, with 64 columns: block j is columns 32j ..
+  const int G = lane >> 4, i16 = lane & 15;
+  auto frag = [&](const unsigned char* op, int kk, int j) __attribute__((always_inline)) {
+    const int r = 16 * kk + 8 * (G >> 1) + (i16 >> 2), c = 32 * j + 16 * (G & 1) + 4 * (i16 & 3);
+    const unsigned char* p = op + r * kSmRow + (small_slot(c >> 3, r) << 4) + 8 * (i16 & 1);
+    const v4i16 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * kSmRow);  // rows r and r + 4 share their slots
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  int b = b_begin + wave;
+  if (b < b_end) load(b);
+  for (; b < b_end; b += 4) {
+    stage(b);
+    if (b + 4 < b_end) load(b + 4);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const bf16x8 x0 = frag(sx, kk, 0), x1 = frag(sx, kk, 1);
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bf16x8 y = frag(sy + q * kSmOp, kk, i);
+          acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x0, y, acc[i][0], 0, 0, 0);
+          acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x1, y, acc[i][1], 0, 0, 0);
+        }
+    }
+  }
+
+  // Every wave's sums, 16 KB each (16-byte unit u of row r at u ^ (r % 16)),
+  // then added in wave order: 16 lanes a row, 16 rows at a time.
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int r = 32 * i + (lane & 31), u = 8 * j + 2 * g + (lane >> 5);
+        const f32x16& t = acc[i][j];
+        *reinterpret_cast<f32x4*>(sy + r * 256 + ((u ^ (r & 15)) << 4)) = f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
+      }
+  __syncthreads();
+  const GradOut<16> out(it, a, lane & 15, k0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = 16 * q + (tid >> 4);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const unsigned char* row = smem + w * 4 * kSmOp + r * 256;
+      float t[4];
+      out.gather(t, [&](int u) { return reinterpret_cast<const float*>(row + ((u ^ (r & 15)) << 4)); }, it.splits > 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += t[i];
+    }
+    if (it.splits > 1)
+      Vec4<float>::store(a->partial + (int64_t)(it.part0 + local) * kWgSmall * kWgSmall + r * kWgSmall + 4 * out.lane, v);
+    else
+      out.store(n0 + r, v);
+  }
+}
+
+// ------------------------------------------------------------ joins
+
 // Adds an item's partial tiles in split order and stores the gradient. A
-// workgroup takes four rows of one tile: 64 workgroups per tile.
+// workgroup takes 1024 elements of one tile: whole rows.
+template <int EDGE>
 __global__ void __launch_bounds__(256) wgrad_reduce_kernel(WgArgs) {
+  constexpr int LW = EDGE / 4, PER = EDGE * EDGE / 1024;  // lanes per row, workgroups per tile
   const ArgsPtr a = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
   // workgroups are numbered over the tiles of the items with splits
   int b = blockIdx.x, idx = 0;
   for (; idx < a->n_items; ++idx) {
-    const int mine = a->item[idx].splits > 1 ? a->item[idx].tiles_n * a->item[idx].tiles_k * 64 : 0;
+    const int mine = a->item[idx].splits > 1 ? a->item[idx].tiles_n * a->item[idx].tiles_k * PER : 0;
     if (b < mine) break;
     b -= mine;
   }
   const __attribute__((address_space(4))) WgItem& it = a->item[idx];
-  const int tiles = it.tiles_n * it.tiles_k, tile = b >> 6;
-  const int f = (b & 63) * 256 + threadIdx.x;
-  const float* p = a->partial + (int64_t)(it.part0 + tile) * kWgPart + f * 4;
-  float v[4];
-  Vec4<float>::load(p, v);
-  for (int s = 1; s < it.splits; ++s) {
-    float w[4];
-    Vec4<float>::load(p + (int64_t)s * tiles * kWgPart, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += w[i];
-  }
+  const int tiles = it.tiles_n * it.tiles_k, tile = b / PER;
+  const int row = (b % PER) * (256 / LW) + threadIdx.x / LW;
   int tn, tk;
   tile_of(tile, it.tiles_n, it.tiles_k, tn, tk);
-  store_grad(it, a->scale_f32, a->g_f32, tn * kWgTile + f / 64, tk * kWgTile + f % 64 * 4, v);
+  const GradOut<LW> out(it, a, threadIdx.x % LW, tk * EDGE);
+  const float* p = a->partial + (int64_t)(it.part0 + tile) * EDGE * EDGE + row * EDGE;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  const int64_t step = (int64_t)tiles * EDGE * EDGE;
+  if (out.vec) {
+#pragma unroll 4
+    for (int s = 0; s < it.splits; ++s) {
+      float t[4];
+      Vec4<float>::load(p + s * step + 4 * out.lane, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += t[i];
+    }
+  } else {
+#pragma unroll 4
+    for (int s = 0; s < it.splits; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += Elem<float>::load(p + s * step + out.col(i));
+  }
+  out.store(tn * EDGE + row, v);
 }
 
-hipError_t launch_wgrad(const WgArgs& args, int kind, hipStream_t s) {
-  if (args.units > 0) {
-    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_INT8>, dim3(args.units), dim3(64 * kWaves), 0, s, args);
-    else hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_E4M3>, dim3(args.units), dim3(64 * kWaves), 0, s, args);
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+template <int EDGE>
+static hipError_t launch_reduce(const WgArgs& args, hipStream_t s) {
   int64_t blocks = 0;
   for (int i = 0; i < args.n_items; ++i)
-    if (args.item[i].splits > 1) blocks += (int64_t)args.item[i].tiles_n * args.item[i].tiles_k * 64;
+    if (args.item[i].splits > 1) blocks += (int64_t)args.item[i].tiles_n * args.item[i].tiles_k * (EDGE * EDGE / 1024);
   if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((uint32_t)blocks), dim3(256), 0, s, args);
+  hipLaunchKernelGGL(wgrad_reduce_kernel<EDGE>, dim3((uint32_t)blocks), dim3(256), 0, s, args);
   return hipGetLastError();
 }
 
-// dY in other layouts than the product's (fp32, unaligned rows, a width that is
-// no multiple of 8): rewritten once, as one bf16 plane or as the three planes
-// lo, mid, hi of fp32 values, rows of lda columns (zeros past n). hi is x
-// rounded toward zero to bf16, mid and lo the same of what is left: 8 bits
-// each, exact for the 24 bits of a normal fp32 number, and never past the
-// largest finite value. Infinities and NaNs stay in hi alone.
+hipError_t launch_wgrad(const WgArgs& args, int kind, hipStream_t s) {
+  const dim3 grid(args.units);
+  if (args.edge == kWgTile) {
+    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_INT8>, grid, dim3(64 * kWaves), 0, s, args);
+    else hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_E4M3>, grid, dim3(64 * kWaves), 0, s, args);
+  } else if (args.dy_f32) {
+    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL((wgrad_small_kernel<MUON_Q8_INT8, float>), grid, dim3(256), 0, s, args);
+    else hipLaunchKernelGGL((wgrad_small_kernel<MUON_Q8_E4M3, float>), grid, dim3(256), 0, s, args);
+  } else {
+    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL((wgrad_small_kernel<MUON_Q8_INT8, u16>), grid, dim3(256), 0, s, args);
+    else hipLaunchKernelGGL((wgrad_small_kernel<MUON_Q8_E4M3, u16>), grid, dim3(256), 0, s, args);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return args.edge == kWgTile ? launch_reduce<kWgTile>(args, s) : launch_reduce<kWgSmall>(args, s);
+}
+
+// dY in other layouts than the large kernel's (fp32, unaligned rows, a width
+// that is no multiple of 8): rewritten once, as one bf16 plane or as the three
+// planes lo, mid, hi of fp32 values, rows of lda columns (zeros past n).
 template <class T, int PARTS>
 __global__ void __launch_bounds__(256) wgrad_pack_kernel(const T* dy, int64_t ld, u16* out, int32_t rows, int32_t n,
                                                          int64_t lda) {
@@ -449,15 +693,7 @@ __global__ void __launch_bounds__(256) wgrad_pack_kernel(const T* dy, int64_t ld
       for (int e = 0; e < 4; ++e) {
         uint32_t b[3][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x = v[2 * e + h];
-          const uint32_t bits = __float_as_uint(x);
-          const bool fine = (bits & 0x7f800000u) != 0x7f800000u;
-          b[2][h] = fine ? bits & 0xffff0000u : __float_as_uint(bf16_to_f32(f32_to_bf16(x)));
-          const float r = fine ? x - __uint_as_float(b[2][h]) : 0.f;
-          b[1][h] = __float_as_uint(r) & 0xffff0000u;
-          b[0][h] = __float_as_uint(r - __uint_as_float(b[1][h])) & 0xffff0000u;
-        }
+        for (int h = 0; h < 2; ++h) split3(v[2 * e + h], b[2][h], b[1][h], b[0][h]);
 #pragma unroll
         for (int p = 0; p < 3; ++p) t[p][e] = (b[p][0] >> 16) | b[p][1];
       }

@@ -42,12 +42,13 @@ def _matrix(t, name: str, shape=None, dtype=None, vector=False):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _bad(f"{name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         _bad(f"{name} is on {t.device}, not on the current device")
-    if t.dim() != (1 if vector else 2) or (t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1):
+    size = t.shape
+    if len(size) != (1 if vector else 2) or (t.stride(-1) != 1 and size[-1] > 1 and t.numel()):
         _bad(f"{name} must be a {1 if vector else 2}-D tensor with unit column stride")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        _bad(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if shape is not None and size != shape:
+        _bad(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
     if dtype is not None and t.dtype != dtype:
         _bad(f"{name} must be {dtype}, not {t.dtype}")
     return t
@@ -62,14 +63,14 @@ def _stream(stream, tensors: Sequence):
     """The stream's handle. Memory that another stream uses than the current
     one is kept from reuse until that stream is done with it."""
     import torch
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the handle alone: making a Stream object takes 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if hasattr(stream, "cuda_stream"):
         if stream != torch.cuda.current_stream():
             for t in tensors:
                 t.record_stream(stream)
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _ptr(t) -> Optional[int]:
@@ -212,8 +213,8 @@ class NormSite:
                                           self._workspace) if t is not None]
         g = self._grads
         g.dy, g.ld_dy, g.dh, g.ld_dh = _ptr(dy), 0 if dy is None else _ld(dy), dh.data_ptr(), _ld(dh)
-        check(lib().muon_norm_backward(ctypes.byref(self._c), ctypes.byref(g),
-                                       _stream(stream, self._tensors + [t for t in (dy, dh) if t is not None])))
+        used = self._tensors if stream is None else self._tensors + [t for t in (dy, dh) if t is not None]
+        check(lib().muon_norm_backward(ctypes.byref(self._c), ctypes.byref(g), _stream(stream, used)))
 
 
 class WGrad:

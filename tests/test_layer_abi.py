@@ -186,8 +186,10 @@ def test_wgrad_types_counts_and_workspace():
     last(L.muon_wgrad(one, 1, 1, 0, None, need.value, None), -1, "workspace is NULL")
     last(L.muon_wgrad(one, 1, 1, 0, at(30) + 8, need.value, None), -3, "workspace")
     last(L.muon_wgrad(one, 1, 1, 0, at(3) + 64, need.value, None), -2, "workspace")
-    # fp32 dY is rewritten as three bf16 planes of a width that is a multiple of 8
-    assert L.muon_wgrad_workspace(one, 1, 0, 0, ctypes.byref(need)) == 0 and need.value >= 3 * 2 * 5000 * 304
+    # A large product of fp32 dY rewrites it as three bf16 planes of a width that is a multiple of 8.
+    big = (muon.muon_wgrad_item * 1)(item(0, rows=5000, n=8100, k=6000))
+    big[0].x.ldq, big[0].x.lde = 6000, 188
+    assert L.muon_wgrad_workspace(big, 1, 0, 0, ctypes.byref(need)) == 0 and need.value >= 3 * 2 * 5000 * 8104
 
 
 @no_gpu

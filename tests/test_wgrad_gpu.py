@@ -83,6 +83,24 @@ def test_one_matrix(rows, n, k, dtype, gdtype, kind):
     run(Item(rows, n, k, dtype, gdtype, kind, scale=rows % 2 == 0, beta=0.5 if k % 2 else 0.0, seed=rows))
 
 
+# Outputs of hundreds of 256 x 256 tiles take the kernel of that tile; the ones
+# above mostly the one of 64 x 64.
+LARGE = [  # rows, n, k, dtype, gdtype, kind, ld, offset
+    (1, 4096, 4096, "bf16", "bf16", "int8", None, 0), (63, 4104, 2100, "bf16", "f32", "e4m3", None, 0),
+    (64, 2048, 4112, "bf16", "bf16", "e4m3", 2056, 8), (65, 2101, 4099, "bf16", "bf16", "int8", None, 0),
+    (130, 2100, 2200, "bf16", "f32", "int8", 2111, 3), (129, 4096, 2048, "bf16", "bf16", "int8", None, 0),
+    (300, 4100, 2999, "f32", "f32", "int8", None, 0), (70, 3001, 4096, "f32", "bf16", "e4m3", 3003, 1),
+    (4000, 1030, 1101, "bf16", "f32", "int8", None, 0), (4033, 1024, 1200, "bf16", "bf16", "e4m3", None, 0),
+]
+
+
+@pytest.mark.parametrize("rows,n,k,dtype,gdtype,kind,ld,offset", LARGE)
+def test_large_tiles(rows, n, k, dtype, gdtype, kind, ld, offset):
+    say("case", rows, n, k, dtype, gdtype, kind, ld, offset)
+    run(Item(rows, n, k, dtype, gdtype, kind, scale=k % 2 == 0, beta=0.25 if n % 2 else 1.0, own_c=n % 2 == 1, seed=rows, ld=ld,
+             offset=offset))
+
+
 @pytest.mark.parametrize("gdtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", [0, 1, 100, 900])
 def test_accumulation_into_g(rows, gdtype):
@@ -111,9 +129,11 @@ def test_more_tiles_than_the_gpu_has_cus():
     run(Item(96, 4100, 5000, "bf16", "bf16", "int8", seed=8))
 
 
-@pytest.mark.parametrize("rows", [70, 1001])
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("rows,n,k", [(70, 24, 100), (1001, 24, 100), (70, 2048, 4100), (40, 2048, 4100)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_non_finite_values_reach_their_rows_and_columns_only(rows, dtype):
+def test_non_finite_values_reach_their_rows_and_columns_only(rows, n, k, dtype, kind):
+    say("case", rows, n, k, dtype, kind)
     # An infinity in the last token's dY, where a short last stage could meet a
     # zero; a NaN elsewhere; a group of the checkpoint that stands for NaNs.
     def edit(it):
@@ -121,7 +141,7 @@ def test_non_finite_values_reach_their_rows_and_columns_only(rows, dtype):
         it.e[rows // 2, 1] = 255
         it.q[rows // 2, 32:64] = 0
         it.q[rows - 1, :] = np.where(it.q[rows - 1, :] == 0, 1, it.q[rows - 1, :])  # inf * 0 would be NaN, rightly
-    run(Item(rows, 24, 100, dtype, "f32", "int8", edit=edit))
+    run(Item(rows, n, k, dtype, "f32", kind, edit=edit))
 
 
 def test_extreme_magnitudes_fp32():
