@@ -15,19 +15,30 @@ constexpr int kGroup = 32;           // columns that share one exponent byte
 constexpr int kNormMaxCols = 32768;  // 1024 threads x 4 x 8 columns
 constexpr int kMinExp = 17;          // smallest exponent byte: 2^-110
 
-// Threads of a norm workgroup: one row, 8 columns per thread up to 8192
-// columns, then 16 or 32.
-inline int norm_vecs(int64_t cols) { return cols <= 8192 ? 1 : cols <= 16384 ? 2 : 4; }
-inline int norm_threads(int64_t cols) {
-  const int64_t per = 8 * norm_vecs(cols);
+// A norm workgroup holds one row, 8 columns per thread, `vecs` times. The
+// forward kernel needs few registers and goes to 1024 threads first; the
+// backward kernel's partial sums need 24 per 8 columns, so it takes at most 768
+// threads (168 registers each), then 512 (256).
+inline int norm_forward_vecs(int64_t cols) { return cols <= 8192 ? 1 : cols <= 16384 ? 2 : 4; }
+inline int norm_backward_vecs(int64_t cols) { return cols <= 6144 ? 1 : cols <= 8192 ? 2 : 4; }
+inline int norm_threads(int64_t cols, int vecs) {
+  const int64_t per = 8 * vecs;
   return int(((cols + per - 1) / per + 63) / 64 * 64);
 }
 
-// Workgroups of the norm backward kernel, each of which leaves one partial sum
-// per column and weight.
+// Workgroups of the norm kernels, which take rows in turn: up to two per CU
+// forward (4096 x 5120 bf16: 28 us; one 33, three or four 30) and up to three
+// backward, as many as its registers allow (16384 x 2048 bf16: 92 us; two 98,
+// one 151, four 115: the fourth waits). Each workgroup of the backward kernel
+// leaves one partial sum per column and weight.
+inline int norm_blocks(int64_t rows, int threads, int per_cu_threads, int most) {
+  return int(std::min<int64_t>(rows, 256 * std::max(1, std::min(most, per_cu_threads / threads))));
+}
+inline int norm_forward_blocks(int64_t rows, int64_t cols) {
+  return norm_blocks(rows, norm_threads(cols, norm_forward_vecs(cols)), 2048, 2);
+}
 inline int norm_backward_blocks(int64_t rows, int64_t cols) {
-  const int per_cu = std::max(1, std::min(4, 2048 / norm_threads(cols)));
-  return int(std::min<int64_t>(rows, 256 * per_cu));
+  return norm_blocks(rows, norm_threads(cols, norm_backward_vecs(cols)), 1024, 3);
 }
 
 // ------------------------------------------------------------ weight gradients

@@ -149,53 +149,149 @@ hipError_t launch_q8_load(const muon_q8& in, void* x, int64_t ldx, int dtype, hi
 
 // ------------------------------------------------------------ norm sites
 
-// Sum over a wave, in every lane.
-MUON_INLINE float wave_sum(float v) {
+// Eight columns as they lie in memory, to be widened later: rows that are
+// loaded ahead, and weights that stay in registers, take half the space so.
+template <class T>
+struct Raw8 {
+  u32x4 w[sizeof(T) / 2];
+};
+
+template <class T, bool VEC>
+MUON_INLINE Raw8<T> load_raw(const T* row, int64_t c0, int64_t cols) {
+  Raw8<T> r;
+  if constexpr (VEC) {
 #pragma unroll
-  for (int w = 32; w > 0; w >>= 1) v += __shfl_xor(v, w);
-  return v;
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+      r.w[h] = u32x4{0u, 0u, 0u, 0u};
+      if (c0 < cols) r.w[h] = gload16(row + c0 + 4 * h);
+    }
+  } else {
+    float v[8];
+    load8<T, false>(row, c0, cols, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) r.w[i >> 2][i & 3] = __float_as_uint(v[i]);
+      else if (i & 1) r.w[0][i >> 1] = (__float_as_uint(v[i - 1]) >> 16) | __float_as_uint(v[i]);
+    }
+  }
+  return r;
+}
+
+template <class T>
+MUON_INLINE void widen(const Raw8<T>& r, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
+    else v[i] = __uint_as_float(i & 1 ? r.w[0][i >> 1] & 0xffff0000u : r.w[0][i >> 1] << 16);
+  }
+}
+
+struct RawQ8 {
+  u32x2 w;
+  uint32_t e;
+};
+
+MUON_INLINE RawQ8 load_raw_q8(const muon_q8& p, int64_t row, int64_t c0) {
+  RawQ8 r{{0u, 0u}, 127u};
+  if (c0 < p.cols) {
+    r.w = *((const g_u32x2*)(static_cast<const uint8_t*>(p.q) + row * p.ldq + c0));
+    r.e = *((const g_u8*)(static_cast<const uint8_t*>(p.e) + row * p.lde + c0 / kGroup));
+  }
+  return r;
+}
+
+MUON_INLINE void widen_q8(const RawQ8& r, int64_t c0, int64_t cols, int kind, float v[8]) {
+  q8_decode(r.w, r.e, kind, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c0 + i < cols ? v[i] : 0.f;  // padding bytes are not the row's
+}
+
+// x plus x of the lane that DPP control C names (0 where it names none).
+template <int C, int ROWS = 0xf>
+MUON_INLINE float dpp_add(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), C, ROWS, 0xf, true));
+}
+// Sums over rows of 16 lanes, in the last lane of each; over the wave, in lane 63.
+MUON_INLINE float row16_sum(float x) {
+  x = dpp_add<0x111>(x);  // row_shr 1, 2, 4, 8
+  x = dpp_add<0x112>(x);
+  x = dpp_add<0x114>(x);
+  return dpp_add<0x118>(x);
+}
+MUON_INLINE float wave_sum(float x) {
+  x = row16_sum(x);
+  x = dpp_add<0x142, 0xa>(x);     // lane 15 of a row to the next, rows 1 and 3
+  return dpp_add<0x143, 0xc>(x);  // lane 31 to rows 2 and 3
+}
+MUON_INLINE float lane_value(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
 
 // N sums over the workgroup at once, in every thread, in a fixed order. `red`
 // holds 16*N floats; two calls in a row need two buffers.
 template <int N>
 MUON_INLINE void block_sum(float (&v)[N], float* red) {
+  const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  const int waves = blockDim.x >> 6;
-  if (waves == 1) return;
-  if ((threadIdx.x & 63) == 0) {
+  if (waves == 1) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[(threadIdx.x >> 6) * N + i] = v[i];
+    for (int i = 0; i < N; ++i) v[i] = lane_value(v[i], 63);
+    return;
+  }
+  if (lane == 63) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[16 * i + (threadIdx.x >> 6)] = v[i];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = red[i];
-  for (int w = 1; w < waves; ++w)
+  for (int i = 0; i < N; ++i) v[i] = (lane & 15) < waves ? red[16 * i + (lane & 15)] : 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += red[w * N + i];
+  for (int i = 0; i < N; ++i) v[i] = lane_value(row16_sum(v[i]), 15);
 }
 
-// One row per workgroup: thread t holds columns 8t .. 8t+7 (VPT times, a
-// workgroup's width apart). The row stays in registers between its two norms,
-// so every tensor moves once.
+// One row per workgroup at a time: thread t holds columns 8t .. 8t+7 (VPT
+// times, a workgroup's width apart). The row stays in registers between its two
+// norms, so every tensor moves once. With VPT = 1 there are registers left to
+// load the weights once and to have the next row's loads in flight.
 template <class T, int VPT, bool VEC>
 __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
   __shared__ float red[2][16];
   const int64_t cols = s.cols;
   const float inv_cols = 1.f / (float)cols;
-  const bool post = s.w_post != nullptr;
+  const bool post = s.w_post != nullptr, per_row = s.gate && s.ld_gate != 0;
   int64_t c0[VPT];
-#pragma unroll
-  for (int p = 0; p < VPT; ++p) c0[p] = ((int64_t)p * blockDim.x + threadIdx.x) * 8;
-  for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x) {
-    float v[VPT][8], y[VPT][8];
-    float sum[1] = {0.f};
+  Raw8<T> b[VPT], r[VPT], gt[VPT], w1[VPT], w2[VPT];
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      load8<T, VEC>(static_cast<const T*>(s.branch) + row * s.ld_branch, c0[p], cols, v[p]);
-      load8<T, VEC>(static_cast<const T*>(s.residual) + row * s.ld_residual, c0[p], cols, y[p]);
+      b[p] = load_raw<T, VEC>(static_cast<const T*>(s.branch) + row * s.ld_branch, c0[p], cols);
+      r[p] = load_raw<T, VEC>(static_cast<const T*>(s.residual) + row * s.ld_residual, c0[p], cols);
+      if (per_row) gt[p] = load_raw<T, VEC>(static_cast<const T*>(s.gate) + row * s.ld_gate, c0[p], cols);
     }
+  };
+  auto load_weights = [&](int p) __attribute__((always_inline)) {
+    w1[p] = load_raw<T, VEC>(static_cast<const T*>(s.w_pre), c0[p], cols);
+    if (post) w2[p] = load_raw<T, VEC>(static_cast<const T*>(s.w_post), c0[p], cols);
+    if (s.gate && !per_row) gt[p] = load_raw<T, VEC>(static_cast<const T*>(s.gate), c0[p], cols);
+  };
+#pragma unroll
+  for (int p = 0; p < VPT; ++p) c0[p] = ((int64_t)p * blockDim.x + threadIdx.x) * 8;
+  if (VPT == 1) {
+    load(blockIdx.x);
+    load_weights(0);
+  }
+  for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x) {
+    float v[VPT][8], y[VPT][8], g[VPT][8];
+    float sum[1] = {0.f};
+    if (VPT > 1) load(row);
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      widen(b[p], v[p]);
+      widen(r[p], y[p]);
+      if (per_row) widen(gt[p], g[p]);
+    }
+    if (VPT == 1 && row + gridDim.x < s.rows) load(row + gridDim.x);
     if (post) {
 #pragma unroll
       for (int p = 0; p < VPT; ++p)
@@ -212,19 +308,20 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
     sum[0] = 0.f;
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
+      if (VPT > 1) load_weights(p);
       if (s.v.q)
         store_q8(static_cast<uint8_t*>(s.v.q) + row * s.v.ldq, static_cast<uint8_t*>(s.v.e) + row * s.v.lde, c0[p],
                  cols, v[p], s.v.kind);
       float w[8];
       if (post) {
-        load8<T, VEC>(static_cast<const T*>(s.w_post), c0[p], cols, w);
+        widen(w2[p], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[p][i] *= w[i];
       }
       if (s.gate) {
-        load8<T, VEC>(static_cast<const T*>(s.gate) + row * s.ld_gate, c0[p], cols, w);
+        if (!per_row) widen(gt[p], g[p]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] *= w[i];
+        for (int i = 0; i < 8; ++i) v[p][i] *= g[p][i];
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -244,15 +341,14 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
       if (s.u.q)
         store_q8(static_cast<uint8_t*>(s.u.q) + row * s.u.ldq, static_cast<uint8_t*>(s.u.e) + row * s.u.lde, c0[p],
                  cols, y[p], s.u.kind);
-      load8<T, VEC>(static_cast<const T*>(s.w_pre), c0[p], cols, w);
+      widen(w1[p], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] *= y[p][i];
       store8<T, VEC>(static_cast<T*>(s.h) + row * s.ld_h, c0[p], cols, w);
     }
     // The next row's first sum writes red[0], which every thread has read
-    // before this row's second barrier; without a second barrier between
-    // them (no norm after the block) red[1] would be written while it is
-    // still read.
+    // before this row's second barrier; without a norm after the block there
+    // is only red[1], which would be written while it is still read.
     if (!post) __syncthreads();
   }
 }
@@ -261,18 +357,18 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
 // mean over du*u; written out, both follow from three sums that are formed at
 // once: with a = branch_scale*gate*w_post,
 //   mean(dv*v) = mean(a*v*(dy + rstd_y*du)) - rstd_y * mean(du*u) * mean(a*v*u),
-// so a row costs one barrier pair. Each thread keeps its columns' partial sums
-// of the weight gradients in registers and stores them once.
-template <class T, int VPT, bool VEC>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(muon_norm_site s, muon_norm_grads g) {
+// so a row costs one barrier. Each thread keeps its columns' partial sums of
+// the weight gradients in registers and stores them once. With VPT = 1 the row
+// stays in registers too, weights are loaded once and loads run a row ahead;
+// wider rows are read again (from cache) after their sums. MAXT: the most
+// threads of a workgroup, which sets the registers of each.
+template <class T, int VPT, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, muon_norm_grads g) {
   __shared__ float red[2][48];
   const int64_t cols = s.cols;
   const float inv_cols = 1.f / (float)cols;
   const bool post = s.w_post != nullptr, per_row = s.gate && s.ld_gate != 0;
   const bool need_v = post || s.gate;
-  int64_t c0[VPT];
-#pragma unroll
-  for (int p = 0; p < VPT; ++p) c0[p] = ((int64_t)p * blockDim.x + threadIdx.x) * 8;
   float acc[3][VPT][8];
 #pragma unroll
   for (int w = 0; w < 3; ++w)
@@ -280,87 +376,140 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(muon_norm_site s, m
     for (int p = 0; p < VPT; ++p)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[w][p][i] = 0.f;
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x, flip ^= 1) {
-    const float ry = *((const g_f32*)(s.rstd_y + row));
-    const float rb = post ? *((const g_f32*)(s.rstd_b + row)) : 1.f;
-    float u[VPT][8], v[VPT][8], t[VPT][8], gt[VPT][8];  // t: dy + rstd_y*du; gt: the gate
-    float du[VPT][8];
-    float sum[3] = {0.f, 0.f, 0.f};
+
+  Raw8<T> rdh, rdy, rg, w1, w2;  // of one row's eight columns, as loaded
+  RawQ8 ru, rv;
+  float ry = 0.f, rb = 1.f;
+  auto col0 = [&](int p) { return ((int64_t)p * blockDim.x + threadIdx.x) * 8; };
+  auto load = [&](int64_t row, int p) __attribute__((always_inline)) {
+    const int64_t c0 = col0(p);
+    rdh = load_raw<T, VEC>(static_cast<const T*>(g.dh) + row * g.ld_dh, c0, cols);
+    if (g.dy) rdy = load_raw<T, VEC>(static_cast<const T*>(g.dy) + row * g.ld_dy, c0, cols);
+    ru = load_raw_q8(s.u, row, c0);
+    if (need_v) rv = load_raw_q8(s.v, row, c0);
+    if (per_row) rg = load_raw<T, VEC>(static_cast<const T*>(s.gate) + row * s.ld_gate, c0, cols);
+    ry = *((const g_f32*)(s.rstd_y + row));
+    if (post) rb = *((const g_f32*)(s.rstd_b + row));
+  };
+  auto load_weights = [&](int p) __attribute__((always_inline)) {
+    const int64_t c0 = col0(p);
+    w1 = load_raw<T, VEC>(static_cast<const T*>(s.w_pre), c0, cols);
+    if (post) w2 = load_raw<T, VEC>(static_cast<const T*>(s.w_post), c0, cols);
+    if (s.gate && !per_row) rg = load_raw<T, VEC>(static_cast<const T*>(s.gate), c0, cols);
+  };
+  // Eight columns of the row: t is dy + rstd_y*du, gt the gate as loaded.
+  struct Cols {
+    float u[8], v[8], t[8];
+    Raw8<T> gt;
+    float ry, rb;
+  };
+  auto widen_row = [&](Cols& c, float dh[8], int p) __attribute__((always_inline)) {
+    const int64_t c0 = col0(p);
+    widen(rdh, dh);
 #pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-      float dh[8], w[8];
-      load8<T, VEC>(static_cast<const T*>(g.dh) + row * g.ld_dh, c0[p], cols, dh);
-      if (g.dy) {
-        load8<T, VEC>(static_cast<const T*>(g.dy) + row * g.ld_dy, c0[p], cols, t[p]);
-      } else {
+    for (int i = 0; i < 8; ++i) c.t[i] = c.v[i] = 0.f;
+    if (g.dy) widen(rdy, c.t);
+    widen_q8(ru, c0, cols, s.u.kind, c.u);
+    if (need_v) widen_q8(rv, c0, cols, s.v.kind, c.v);
+    if (per_row) c.gt = rg;
+    c.ry = ry, c.rb = rb;
+  };
+  auto gate_of = [&](const Cols& c, float gt[8]) __attribute__((always_inline)) {
+    if (s.gate) {
+      widen(per_row ? c.gt : rg, gt);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[p][i] = 0.f;
-      }
-      load_q8(static_cast<const uint8_t*>(s.u.q) + row * s.u.ldq, static_cast<const uint8_t*>(s.u.e) + row * s.u.lde,
-              c0[p], cols, s.u.kind, u[p]);
-      if (need_v) {
-        load_q8(static_cast<const uint8_t*>(s.v.q) + row * s.v.ldq, static_cast<const uint8_t*>(s.v.e) + row * s.v.lde,
-                c0[p], cols, s.v.kind, v[p]);
-      } else {
+      for (int i = 0; i < 8; ++i) gt[i] = 1.f;
+    }
+  };
+  // The row's share of its three sums.
+  auto add_sums = [&](Cols& c, const float dh[8], float (&sum)[3]) __attribute__((always_inline)) {
+    float w[8];
+    widen(w1, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
-      }
-      if (s.gate) {
-        load8<T, VEC>(static_cast<const T*>(s.gate) + row * s.ld_gate, c0[p], cols, gt[p]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) gt[p][i] = 1.f;
-      }
-      load8<T, VEC>(static_cast<const T*>(s.w_pre), c0[p], cols, w);
+    for (int i = 0; i < 8; ++i) {
+      const float du = dh[i] * w[i];
+      sum[0] += du * c.u[i];
+      c.t[i] += c.ry * du;
+    }
+    if (post) {
+      float gt[8];
+      widen(w2, w);
+      gate_of(c, gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        acc[0][p][i] += dh[i] * u[p][i];
-        du[p][i] = dh[i] * w[i];
-        sum[0] += du[p][i] * u[p][i];
-        t[p][i] += ry * du[p][i];
-      }
-      if (post) {
-        load8<T, VEC>(static_cast<const T*>(s.w_post), c0[p], cols, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float av = gt[p][i] * w[i] * v[p][i];
-          sum[1] += av * t[p][i];
-          sum[2] += av * u[p][i];
-        }
+        const float av = gt[i] * w[i] * c.v[i];
+        sum[1] += av * c.t[i];
+        sum[2] += av * c.u[i];
       }
     }
-    block_sum(sum, red[flip]);
-    const float c1 = ry * (sum[0] * inv_cols);
+  };
+  auto finish = [&](Cols& c, int64_t row, int p, const float (&sum)[3]) __attribute__((always_inline)) {
+    const int64_t c0 = col0(p);
+    const float c1 = c.ry * (sum[0] * inv_cols);
     const float c2 = s.branch_scale * (sum[1] - c1 * sum[2]) * inv_cols;
+    float o[8], w[8], gt[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c.t[i] -= c1 * c.u[i];  // s
+      o[i] = s.res_scale * c.t[i];
+      c.t[i] *= s.branch_scale;
+    }
+    store8<T, VEC>(static_cast<T*>(g.d_residual) + row * g.ld_d_residual, c0, cols, o);
+    if (post) {
+      widen(w2, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    }
+    gate_of(c, gt);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[i] = c.t[i] * w[i] * c.v[i];
+      acc[2][p][i] += o[i];
+      c.t[i] *= gt[i];
+      acc[1][p][i] += c.t[i] * c.v[i];
+    }
+    if (per_row && g.d_gate) store8<T, VEC>(static_cast<T*>(g.d_gate) + row * g.ld_d_gate, c0, cols, o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = post ? c.rb * (c.t[i] * w[i] - c.v[i] * c2) : c.t[i];
+    store8<T, VEC>(static_cast<T*>(g.d_branch) + row * g.ld_d_branch, c0, cols, o);
+  };
+
+  if (VPT == 1) {
+    load(blockIdx.x, 0);
+    load_weights(0);
+  }
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x, flip ^= 1) {
+    float sum[3] = {0.f, 0.f, 0.f};
+    Cols c;
+    float dh[8];
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      float o[8], w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        t[p][i] -= c1 * u[p][i];  // s
-        o[i] = s.res_scale * t[p][i];
-        t[p][i] *= s.branch_scale;
+      if (VPT > 1) {
+        load(row, p);
+        load_weights(p);
       }
-      store8<T, VEC>(static_cast<T*>(g.d_residual) + row * g.ld_d_residual, c0[p], cols, o);
-      if (post) {
-        load8<T, VEC>(static_cast<const T*>(s.w_post), c0[p], cols, w);
-      } else {
+      widen_row(c, dh, p);
+      if (VPT == 1 && row + gridDim.x < s.rows) load(row + gridDim.x, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.f;
+      for (int i = 0; i < 8; ++i) acc[0][p][i] += dh[i] * c.u[i];
+      add_sums(c, dh, sum);
+      if (VPT > 1) __builtin_amdgcn_sched_barrier(0);  // eight columns' registers at a time
+    }
+    block_sum(sum, red[flip]);
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      if (VPT > 1) {
+        float none[3] = {0.f, 0.f, 0.f};
+        load(row, p);
+        load_weights(p);
+        widen_row(c, dh, p);
+        add_sums(c, dh, none);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i] = t[p][i] * w[i] * v[p][i];
-        acc[2][p][i] += o[i];
-        t[p][i] *= gt[p][i];
-        acc[1][p][i] += t[p][i] * v[p][i];
-      }
-      if (per_row && g.d_gate)
-        store8<T, VEC>(static_cast<T*>(g.d_gate) + row * g.ld_d_gate, c0[p], cols, o);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = post ? rb * (t[p][i] * w[i] - v[p][i] * c2) : t[p][i];
-      store8<T, VEC>(static_cast<T*>(g.d_branch) + row * g.ld_d_branch, c0[p], cols, o);
+      finish(c, row, p, sum);
+      if (VPT > 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
   const int64_t pitch = (cols + 7) / 8 * 8;
@@ -369,9 +518,9 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(muon_norm_site s, m
   for (int w = 0; w < 3; ++w)
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      if (c0[p] >= cols) continue;
-      Vec4<float>::store(part + w * pitch + c0[p], acc[w][p]);
-      Vec4<float>::store(part + w * pitch + c0[p] + 4, acc[w][p] + 4);
+      if (col0(p) >= cols) continue;
+      Vec4<float>::store(part + w * pitch + col0(p), acc[w][p]);
+      Vec4<float>::store(part + w * pitch + col0(p) + 4, acc[w][p] + 4);
     }
 }
 
@@ -406,8 +555,8 @@ static hipError_t norm_forward(const muon_norm_site& s, hipStream_t st) {
                    rows_aligned(s.residual, s.ld_residual, elem) && rows_aligned(s.y, s.ld_y, elem) &&
                    rows_aligned(s.h, s.ld_h, elem) && rows_aligned(s.w_pre, 0, elem) &&
                    rows_aligned(s.w_post, 0, elem) && rows_aligned(s.gate, s.ld_gate, elem);
-  const dim3 grid((uint32_t)std::min<int64_t>(s.rows, 1 << 20)), block(norm_threads(s.cols));
-  const int vpt = norm_vecs(s.cols);
+  const int vpt = norm_forward_vecs(s.cols);
+  const dim3 grid(norm_forward_blocks(s.rows, s.cols)), block(norm_threads(s.cols, vpt));
 #define MUON_NORM_F(V, A) hipLaunchKernelGGL((norm_forward_kernel<T, V, A>), grid, block, 0, st, s)
   if (vec) { if (vpt == 1) MUON_NORM_F(1, true); else if (vpt == 2) MUON_NORM_F(2, true); else MUON_NORM_F(4, true); }
   else { if (vpt == 1) MUON_NORM_F(1, false); else if (vpt == 2) MUON_NORM_F(2, false); else MUON_NORM_F(4, false); }
@@ -424,12 +573,19 @@ static hipError_t norm_backward(const muon_norm_site& s, const muon_norm_grads& 
                    rows_aligned(g.d_branch, g.ld_d_branch, elem) && rows_aligned(s.w_pre, 0, elem) &&
                    rows_aligned(s.w_post, 0, elem) && rows_aligned(s.gate, s.ld_gate, elem) &&
                    (!per_row || rows_aligned(g.d_gate, g.ld_d_gate, elem));
-  const int blocks = norm_backward_blocks(s.rows, s.cols), vpt = norm_vecs(s.cols);
+  const int blocks = norm_backward_blocks(s.rows, s.cols), vpt = norm_backward_vecs(s.cols);
   if (blocks > 0) {
-    const dim3 grid(blocks), block(norm_threads(s.cols));
-#define MUON_NORM_B(V, A) hipLaunchKernelGGL((norm_backward_kernel<T, V, A>), grid, block, 0, st, s, g)
-    if (vec) { if (vpt == 1) MUON_NORM_B(1, true); else if (vpt == 2) MUON_NORM_B(2, true); else MUON_NORM_B(4, true); }
-    else { if (vpt == 1) MUON_NORM_B(1, false); else if (vpt == 2) MUON_NORM_B(2, false); else MUON_NORM_B(4, false); }
+    const dim3 grid(blocks), block(norm_threads(s.cols, vpt));
+#define MUON_NORM_B(V, M)                                                                                 \
+  do {                                                                                                    \
+    if (vec) hipLaunchKernelGGL((norm_backward_kernel<T, V, true, M>), grid, block, 0, st, s, g);         \
+    else hipLaunchKernelGGL((norm_backward_kernel<T, V, false, M>), grid, block, 0, st, s, g);            \
+  } while (0)
+    if (vpt == 1 && block.x <= 512) MUON_NORM_B(1, 512);
+    else if (vpt == 1) MUON_NORM_B(1, 768);
+    else if (vpt == 2) MUON_NORM_B(2, 512);
+    else if (block.x <= 512) MUON_NORM_B(4, 512);
+    else MUON_NORM_B(4, 1024);
 #undef MUON_NORM_B
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
