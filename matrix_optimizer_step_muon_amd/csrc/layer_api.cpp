@@ -289,6 +289,7 @@ struct WgradPlan {
 // The launch of items [0, n), n <= kWgItems: descriptors and workspace layout.
 muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32_t g_dtype, WgradPlan& p) {
   p.args = muon::WgArgs{};
+  std::fill(p.args.unit0, p.args.unit0 + muon::kWgItems, INT32_MAX);
   p.args.n_items = n;
   p.args.dy_f32 = dtype == MUON_F32;
   p.args.g_f32 = g_dtype == MUON_F32;
@@ -336,7 +337,7 @@ muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32
     d.tiles_k = int32_t(ceil_div(it.x.cols, choice.edge));
     const int64_t t = int64_t(d.tiles_n) * d.tiles_k;
     d.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(choice.splits, pieces)));
-    d.unit0 = int32_t(units);
+    p.args.unit0[i] = int32_t(units);
     d.part0 = int32_t(partials);
     units += t * d.splits;
     if (d.splits > 1) partials += t * d.splits;

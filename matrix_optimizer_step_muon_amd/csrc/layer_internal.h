@@ -50,7 +50,7 @@ constexpr int kWgItems = 16;   // matrices per launch
 constexpr int kWgPart = kWgTile * kWgTile;  // floats of one partial tile
 
 // One matrix of a launch. Units (tiles x splits) are numbered consecutively
-// over the items; unit0 is this item's first.
+// over the items.
 struct WgItem {
   const void* dy;      // large kernel: bf16, 16-byte aligned rows of lda elements, parts planes of
                        // `rows` rows; small kernel: the caller's
@@ -65,12 +65,12 @@ struct WgItem {
   int32_t dy_vec;      // 16-byte loads of dY (small kernel)
   int32_t tiles_n, tiles_k;
   int32_t splits;      // > 1: partial tiles go to the workspace
-  int32_t unit0;
   int32_t part0;       // first partial tile of this item in the workspace
   float beta;
 };
 
 struct WgArgs {
+  int32_t unit0[kWgItems];  // each item's first unit; past the last item, INT32_MAX
   WgItem item[kWgItems];
   float* partial;
   int32_t n_items;

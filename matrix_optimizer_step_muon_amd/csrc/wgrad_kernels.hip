@@ -39,6 +39,14 @@ MUON_INLINE int xcd_unit(int b, int units) {
   return x * per + min(x, rest) + i;
 }
 
+// The item of a unit, from one scalar load of all first units.
+MUON_INLINE int item_of(ArgsPtr a, int unit) {
+  int idx = 0;
+#pragma unroll
+  for (int i = 1; i < kWgItems; ++i) idx += unit >= a->unit0[i];
+  return idx;
+}
+
 // Tile (tn, tk) of local tile number t: bands of 4 tile rows walked column by
 // column, so 32 consecutive tiles cover 4 x 8.
 MUON_INLINE void tile_of(int t, int tiles_n, int tiles_k, int& tn, int& tk) {
@@ -52,7 +60,9 @@ MUON_INLINE void tile_of(int t, int tiles_n, int tiles_k, int& tn, int& tk) {
 // four columns each: consecutive ones, as one vector, where a row of the
 // gradient is a multiple of four long, and otherwise every LW-th, so that a
 // store instruction still covers whole lines.
-template <int LW>
+// NT: nontemporal stores, for tiles that all CUs store at once: the seven
+// 1.7B-layer gradients over 4096 tokens take 362 us with them, 372 without.
+template <int LW, bool NT = false>
 struct GradOut {
   const __attribute__((address_space(4))) WgItem& it;
   bool g_f32, vec;
@@ -112,7 +122,12 @@ struct GradOut {
   }
   template <class T>
   MUON_INLINE void put(T* p, const float o[4]) const {
-    if (vec) {
+    if (vec && NT) {
+      if constexpr (sizeof(T) == 4)
+        __builtin_nontemporal_store(f32x4{o[0], o[1], o[2], o[3]}, (g_f32x4*)(p + 4 * lane));
+      else
+        __builtin_nontemporal_store(u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])}, (g_u32x2*)(p + 4 * lane));
+    } else if (vec) {
       Vec4<T>::store(p + 4 * lane, o);
     } else {
 #pragma unroll
@@ -132,11 +147,10 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
   __shared__ __align__(1024) unsigned char smem[kLdsBytes];
   const ArgsPtr a = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
   const int unit = xcd_unit(blockIdx.x, a->units);
-  int idx = 0;
-  while (idx + 1 < a->n_items && unit >= a->item[idx + 1].unit0) ++idx;
+  const int idx = item_of(a, unit);
   const __attribute__((address_space(4))) WgItem& it = a->item[idx];
   const int tiles = it.tiles_n * it.tiles_k;
-  const int local = unit - it.unit0, split = local / tiles, tile = local - split * tiles;
+  const int local = unit - a->unit0[idx], split = local / tiles, tile = local - split * tiles;
   int tn, tk;
   tile_of(tile, it.tiles_n, it.tiles_k, tn, tk);
   const int n0 = tn * kWgTile, k0 = tk * kWgTile;
@@ -377,7 +391,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
   // 2, 3 of every wave: 128 rows of 256), so that a wave stores whole rows. The 16-byte
   // unit u of row r sits at unit u ^ (r % 64).
   const int flane = fresh_tid() & 63;  // keeps these addresses out of the loop's registers
-  const GradOut<64> out(it, a, flane, k0);
+  const GradOut<64, true> out(it, a, flane, k0);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if (half) __syncthreads();
@@ -443,11 +457,10 @@ __global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
   __shared__ __align__(1024) unsigned char smem[4 * 4 * kSmOp];
   const ArgsPtr a = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
   const int unit = xcd_unit(blockIdx.x, a->units);
-  int idx = 0;
-  while (idx + 1 < a->n_items && unit >= a->item[idx + 1].unit0) ++idx;
+  const int idx = item_of(a, unit);
   const __attribute__((address_space(4))) WgItem& it = a->item[idx];
   const int tiles = it.tiles_n * it.tiles_k;
-  const int local = unit - it.unit0, split = local / tiles, tile = local - split * tiles;
+  const int local = unit - a->unit0[idx], split = local / tiles, tile = local - split * tiles;
   int tn, tk;
   tile_of(tile, it.tiles_n, it.tiles_k, tn, tk);
   const int n0 = tn * kWgSmall, k0 = tk * kWgSmall;
