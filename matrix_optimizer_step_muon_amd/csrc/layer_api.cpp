@@ -52,6 +52,7 @@ struct View {
 // other by disjoint(). Empty views (no rows) take part in neither.
 class Views {
  public:
+  Views() { v_.reserve(32); }
   muon_status add(const void* p, int64_t rows, int64_t cols, int64_t ld, int elem, bool written, const char* name,
                   int item = -1, uintptr_t align = 0) {
     if (!p && rows > 0) return fail(MUON_ERR_INVALID_ARG, at(item) + name + " is NULL");
@@ -189,7 +190,7 @@ muon_status norm_forward(const muon_norm_site* site, void* stream) {
 }
 
 size_t norm_workspace(int64_t rows, int64_t cols) {
-  return size_t(muon::norm_backward_blocks(rows, cols)) * 3 * size_t((cols + 7) / 8 * 8) * sizeof(float);
+  return size_t(muon::norm_backward_launch(rows, cols).blocks) * 3 * size_t((cols + 7) / 8 * 8) * sizeof(float);
 }
 
 muon_status norm_backward(const muon_norm_site* site, const muon_norm_grads* grads, void* stream) {
@@ -265,7 +266,8 @@ Choice choose(int64_t t256, int64_t t64, int64_t rows, int parts, int64_t packed
   const int64_t stages = ceil_div(rows, muon::kWgStep) * parts, blocks = ceil_div(rows, 128);
   const double pack = packed ? 3.0 + double(packed) * 3.3e-7 : 0.0;
   Choice best{muon::kWgTile, 1, 1e300};
-  for (int s = 1; s <= 64; ++s) {
+  const int64_t most = std::min<int64_t>(64, std::max(stages / 2, blocks));
+  for (int s = 1; s <= std::max<int64_t>(1, most); ++s) {
     if (s == 1 || s <= stages / 2) {
       double us = pack + double(ceil_div(t256 * s, kCus)) * (8.0 + 1.65 * double(ceil_div(stages, s)));
       if (s > 1) us += 3.0 + 0.3 * s + 0.145 * double(t256 * s);
@@ -370,12 +372,16 @@ muon_status check_wgrad(const muon_wgrad_item* items, int32_t n, int32_t dtype, 
   return MUON_OK;
 }
 
-muon_status wgrad_bytes(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_t g_dtype, size_t* bytes) {
+// Plans of all launches, and the workspace of the largest: launches follow each
+// other on one stream and share it.
+muon_status plan_all(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_t g_dtype, std::vector<WgradPlan>& plans,
+                     size_t* bytes) {
   *bytes = 0;
-  WgradPlan p;
-  for (int32_t i = 0; i < n; i += muon::kWgItems) {
-    MUON_TRY(plan_wgrad(items + i, std::min(n - i, muon::kWgItems), dtype, g_dtype, p));
-    *bytes = std::max(*bytes, p.bytes);
+  plans.resize((n + muon::kWgItems - 1) / muon::kWgItems);
+  for (size_t i = 0; i < plans.size(); ++i) {
+    const int32_t first = int32_t(i) * muon::kWgItems;
+    MUON_TRY(plan_wgrad(items + first, std::min(n - first, muon::kWgItems), dtype, g_dtype, plans[i]));
+    *bytes = std::max(*bytes, plans[i].bytes);
   }
   return MUON_OK;
 }
@@ -385,7 +391,8 @@ muon_status wgrad(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_
   Views v;
   MUON_TRY(check_wgrad(items, n, dtype, g_dtype, v));
   size_t need = 0;
-  MUON_TRY(wgrad_bytes(items, n, dtype, g_dtype, &need));
+  std::vector<WgradPlan> plans;
+  MUON_TRY(plan_all(items, n, dtype, g_dtype, plans, &need));
   if (need) {
     if (ws_bytes < need)
       return fail(MUON_ERR_INVALID_ARG, "the workspace has " + std::to_string(ws_bytes) + " bytes, " +
@@ -396,14 +403,12 @@ muon_status wgrad(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_
   }
   MUON_TRY(v.disjoint());
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  WgradPlan p;
-  for (int32_t i0 = 0; i0 < n; i0 += muon::kWgItems) {
-    const int m = std::min(n - i0, muon::kWgItems);
-    MUON_TRY(plan_wgrad(items + i0, m, dtype, g_dtype, p));
+  for (size_t j = 0; j < plans.size(); ++j) {
+    WgradPlan& p = plans[j];
     p.args.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.partial);
-    for (int i = 0; i < m; ++i) {
+    for (int i = 0; i < p.args.n_items; ++i) {
       if (p.pack[i] == SIZE_MAX) continue;
-      const muon_wgrad_item& it = items[i0 + i];
+      const muon_wgrad_item& it = items[j * muon::kWgItems + i];
       void* out = static_cast<char*>(ws) + p.pack[i];
       p.args.item[i].dy = out;
       MUON_TRY(hip_status(muon::launch_wgrad_pack(it.dy, it.ld_dy, dtype, out, int32_t(it.x.rows), int32_t(it.n),
@@ -455,7 +460,8 @@ muon_status muon_wgrad_workspace(const muon_wgrad_item* items, int32_t n_items, 
     if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
     Views v;
     MUON_TRY(check_wgrad(items, n_items, dtype, g_dtype, v));
-    return wgrad_bytes(items, n_items, dtype, g_dtype, bytes);
+    std::vector<WgradPlan> plans;
+    return plan_all(items, n_items, dtype, g_dtype, plans, bytes);
   });
 }
 

@@ -26,19 +26,40 @@ inline int norm_threads(int64_t cols, int vecs) {
   return int(((cols + per - 1) / per + 63) / 64 * 64);
 }
 
-// Workgroups of the norm kernels, which take rows in turn: up to two per CU
-// forward (4096 x 5120 bf16: 28 us; one 33, three or four 30) and up to three
-// backward, as many as its registers allow (16384 x 2048 bf16: 92 us; two 98,
-// one 151, four 115: the fourth waits). Each workgroup of the backward kernel
-// leaves one partial sum per column and weight.
-inline int norm_blocks(int64_t rows, int threads, int per_cu_threads, int most) {
-  return int(std::min<int64_t>(rows, 256 * std::max(1, std::min(most, per_cu_threads / threads))));
+// Rows of up to 512 columns are one wave each, several to a workgroup: forward
+// 4; backward 8, which leave fewer partial sums (8192 x 512 bf16: 16.9 us, with
+// 4 17.5, with 2 21; one row per workgroup 26).
+constexpr int kNormRowsForward = 4, kNormRowsBackward = 8;
+
+// Workgroups of the norm kernels, which take rows in turn: as many as give a CU
+// `per_cu` threads. Forward 1280, two of 640 for 5120 columns (4096 x 5120 bf16:
+// 28.7 us; 1024 or 640 threads 33, 2048 36), five of 256 for 2048 (16384 x 2048
+// bf16: 42.5 us, with 640 threads 53). Backward 768, which is what its registers
+// allow (16384 x 2048 bf16: 80 us; 512 threads 93, 1024 100: some wait).
+constexpr int kNormThreadsForward = 1280, kNormThreadsBackward = 768;
+inline int norm_blocks(int64_t rows, int threads, int rows_per, int per_cu) {
+  return int(std::min<int64_t>((rows + rows_per - 1) / rows_per, 256 * std::max(1, per_cu / (threads * rows_per))));
 }
-inline int norm_forward_blocks(int64_t rows, int64_t cols) {
-  return norm_blocks(rows, norm_threads(cols, norm_forward_vecs(cols)), 2048, 2);
+
+// A launch of either kernel. The backward kernel's workgroups each leave one
+// partial sum per column and weight; where one workgroup takes all rows, the
+// sums are whole and the second launch is saved.
+struct NormLaunch {
+  int vecs, threads, rows_per, blocks;
+};
+inline NormLaunch norm_forward_launch(int64_t rows, int64_t cols) {
+  NormLaunch l{norm_forward_vecs(cols), 0, 1, 0};
+  l.threads = norm_threads(cols, l.vecs);
+  l.rows_per = l.threads == 64 ? kNormRowsForward : 1;
+  l.blocks = norm_blocks(rows, l.threads, l.rows_per, kNormThreadsForward);
+  return l;
 }
-inline int norm_backward_blocks(int64_t rows, int64_t cols) {
-  return norm_blocks(rows, norm_threads(cols, norm_backward_vecs(cols)), 1024, 3);
+inline NormLaunch norm_backward_launch(int64_t rows, int64_t cols) {
+  NormLaunch l{norm_backward_vecs(cols), 0, 1, 0};
+  l.threads = norm_threads(cols, l.vecs);
+  l.rows_per = l.threads == 64 ? kNormRowsBackward : 1;
+  l.blocks = norm_blocks(rows, l.threads, l.rows_per, kNormThreadsBackward);
+  return l;
 }
 
 // ------------------------------------------------------------ weight gradients

@@ -253,8 +253,9 @@ MUON_INLINE void block_sum(float (&v)[N], float* red) {
   for (int i = 0; i < N; ++i) v[i] = lane_value(row16_sum(v[i]), 15);
 }
 
-// One row per workgroup at a time: thread t holds columns 8t .. 8t+7 (VPT
-// times, a workgroup's width apart). The row stays in registers between its two
+// One row per workgroup at a time, or, in rows of one wave, one per wave
+// (blockDim.y of them): thread x holds columns 8x .. 8x+7 (VPT times, blockDim.x
+// threads apart). The row stays in registers between its two
 // norms, so every tensor moves once. With VPT = 1 there are registers left to
 // load the weights once and to have the next row's loads in flight.
 template <class T, int VPT, bool VEC>
@@ -280,11 +281,15 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
   };
 #pragma unroll
   for (int p = 0; p < VPT; ++p) c0[p] = ((int64_t)p * blockDim.x + threadIdx.x) * 8;
+  // The same in a whole wave, and said so: row addresses stay in scalar registers.
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.y);
+  const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + sub, step = (int64_t)gridDim.x * blockDim.y;
+  if (row0 >= s.rows) return;  // a wave of its own: nothing waits for it
   if (VPT == 1) {
-    load(blockIdx.x);
+    load(row0);
     load_weights(0);
   }
-  for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x) {
+  for (int64_t row = row0; row < s.rows; row += step) {
     float v[VPT][8], y[VPT][8], g[VPT][8];
     float sum[1] = {0.f};
     if (VPT > 1) load(row);
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
       widen(r[p], y[p]);
       if (per_row) widen(gt[p], g[p]);
     }
-    if (VPT == 1 && row + gridDim.x < s.rows) load(row + gridDim.x);
+    if (VPT == 1 && row + step < s.rows) load(row + step);
     if (post) {
 #pragma unroll
       for (int p = 0; p < VPT; ++p)
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
     // The next row's first sum writes red[0], which every thread has read
     // before this row's second barrier; without a norm after the block there
     // is only red[1], which would be written while it is still read.
-    if (!post) __syncthreads();
+    if (!post && blockDim.x > 64) __syncthreads();
   }
 }
 
@@ -363,11 +368,14 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
 // so a row costs one barrier. Each thread keeps its columns' partial sums of
 // the weight gradients in registers and stores them once. With VPT = 1 the row
 // stays in registers too, weights are loaded once and loads run a row ahead;
-// wider rows are read again (from cache) after their sums. MAXT: the most
-// threads of a workgroup, which sets the registers of each.
+// wider rows are read again (from cache) after their sums. Rows of one wave go
+// one to a wave, whose sums are added at the end; a launch of one workgroup
+// stores the weight gradients themselves. MAXT: the most threads of a
+// workgroup, which sets the registers of each.
 template <class T, int VPT, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, muon_norm_grads g) {
   __shared__ float red[2][48];
+  __shared__ float join[MAXT == 512 && VPT == 1 ? kNormRowsBackward * 512 : 1];
   const int64_t cols = s.cols;
   const float inv_cols = 1.f / (float)cols;
   const bool post = s.w_post != nullptr, per_row = s.gate && s.ld_gate != 0;
@@ -479,12 +487,15 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
     store8<T, VEC>(static_cast<T*>(g.d_branch) + row * g.ld_d_branch, c0, cols, o);
   };
 
-  if (VPT == 1) {
-    load(blockIdx.x, 0);
+  // The same in a whole wave, and said so: row addresses stay in scalar registers.
+  const int y = __builtin_amdgcn_readfirstlane(threadIdx.y);
+  const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + y, step = (int64_t)gridDim.x * blockDim.y;
+  if (VPT == 1 && row0 < s.rows) {
+    load(row0, 0);
     load_weights(0);
   }
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x, flip ^= 1) {
+  for (int64_t row = row0; row < s.rows; row += step, flip ^= 1) {
     float sum[3] = {0.f, 0.f, 0.f};
     Cols c;
     float dh[8];
@@ -495,7 +506,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
         load_weights(p);
       }
       widen_row(c, dh, p);
-      if (VPT == 1 && row + gridDim.x < s.rows) load(row + gridDim.x, 0);
+      if (VPT == 1 && row + step < s.rows) load(row + step, 0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[0][p][i] += dh[i] * c.u[i];
       add_sums(c, dh, sum);
@@ -514,6 +525,32 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
       finish(c, row, p, sum);
       if (VPT > 1) __builtin_amdgcn_sched_barrier(0);
     }
+  }
+  if constexpr (MAXT == 512 && VPT == 1) {
+    if (blockDim.y > 1) {
+#pragma unroll
+      for (int w = 0; w < 3; ++w) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) join[y * 512 + threadIdx.x * 8 + i] = acc[w][0][i];
+        __syncthreads();
+        if (y == 0) {
+          for (int o = 1; o < (int)blockDim.y; ++o)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[w][0][i] += join[o * 512 + threadIdx.x * 8 + i];
+        }
+      }
+      if (y != 0) return;
+    }
+  }
+  if (gridDim.x == 1) {
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      if (g.d_w_pre) store8<T, VEC>(static_cast<T*>(g.d_w_pre), col0(p), cols, acc[0][p]);
+      if (g.d_w_post) store8<T, VEC>(static_cast<T*>(g.d_w_post), col0(p), cols, acc[1][p]);
+      if (g.d_gate && !per_row) store8<T, VEC>(static_cast<T*>(g.d_gate), col0(p), cols, acc[2][p]);
+    }
+    return;
   }
   const int64_t pitch = (cols + 7) / 8 * 8;
   float* part = static_cast<float*>(g.workspace) + (int64_t)blockIdx.x * 3 * pitch;
@@ -566,8 +603,9 @@ static hipError_t norm_forward(const muon_norm_site& s, hipStream_t st) {
                    rows_aligned(s.residual, s.ld_residual, elem) && rows_aligned(s.y, s.ld_y, elem) &&
                    rows_aligned(s.h, s.ld_h, elem) && rows_aligned(s.w_pre, 0, elem) &&
                    rows_aligned(s.w_post, 0, elem) && rows_aligned(s.gate, s.ld_gate, elem);
-  const int vpt = norm_forward_vecs(s.cols);
-  const dim3 grid(norm_forward_blocks(s.rows, s.cols)), block(norm_threads(s.cols, vpt));
+  const NormLaunch l = norm_forward_launch(s.rows, s.cols);
+  const int vpt = l.vecs;
+  const dim3 grid(l.blocks), block(l.threads, l.rows_per);
 #define MUON_NORM_F(V, A) hipLaunchKernelGGL((norm_forward_kernel<T, V, A>), grid, block, 0, st, s)
   if (vec) { if (vpt == 1) MUON_NORM_F(1, true); else if (vpt == 2) MUON_NORM_F(2, true); else MUON_NORM_F(4, true); }
   else { if (vpt == 1) MUON_NORM_F(1, false); else if (vpt == 2) MUON_NORM_F(2, false); else MUON_NORM_F(4, false); }
@@ -583,10 +621,12 @@ static hipError_t norm_backward(const muon_norm_site& s, const muon_norm_grads& 
                    rows_aligned(g.d_residual, g.ld_d_residual, elem) &&
                    rows_aligned(g.d_branch, g.ld_d_branch, elem) && rows_aligned(s.w_pre, 0, elem) &&
                    rows_aligned(s.w_post, 0, elem) && rows_aligned(s.gate, s.ld_gate, elem) &&
-                   (!per_row || rows_aligned(g.d_gate, g.ld_d_gate, elem));
-  const int blocks = norm_backward_blocks(s.rows, s.cols), vpt = norm_backward_vecs(s.cols);
-  if (blocks > 0) {
-    const dim3 grid(blocks), block(norm_threads(s.cols, vpt));
+                   rows_aligned(g.d_gate, per_row ? g.ld_d_gate : 0, elem) && rows_aligned(g.d_w_pre, 0, elem) &&
+                   rows_aligned(g.d_w_post, 0, elem);
+  const NormLaunch l = norm_backward_launch(s.rows, s.cols);
+  const int vpt = l.vecs;
+  if (l.blocks > 0) {
+    const dim3 grid(l.blocks), block(l.threads, l.rows_per);
 #define MUON_NORM_B(V, M)                                                                                 \
   do {                                                                                                    \
     if (vec) hipLaunchKernelGGL((norm_backward_kernel<T, V, true, M>), grid, block, 0, st, s, g);         \
@@ -599,12 +639,12 @@ static hipError_t norm_backward(const muon_norm_site& s, const muon_norm_grads& 
     else MUON_NORM_B(4, 1024);
 #undef MUON_NORM_B
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || l.blocks == 1) return e;
   }
   T* dg = per_row ? nullptr : static_cast<T*>(g.d_gate);
   if (!g.d_w_pre && !g.d_w_post && !dg) return hipSuccess;
   hipLaunchKernelGGL(norm_weights_kernel<T>, dim3((uint32_t)((s.cols + 63) / 64), 3), dim3(1024), 0, st,
-                     static_cast<const float*>(g.workspace), blocks, s.cols, static_cast<T*>(g.d_w_pre),
+                     static_cast<const float*>(g.workspace), l.blocks, s.cols, static_cast<T*>(g.d_w_pre),
                      static_cast<T*>(g.d_w_post), dg);
   return hipGetLastError();
 }

@@ -555,6 +555,7 @@ __global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
+  const GradOut<16> out(it, a, lane & 15, k0);  // here, so that the scale arrives during the sum
   f32x16 acc[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -594,7 +595,6 @@ __global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
         *reinterpret_cast<f32x4*>(sy + r * 256 + ((u ^ (r & 15)) << 4)) = f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
       }
   __syncthreads();
-  const GradOut<16> out(it, a, lane & 15, k0);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int r = 16 * q + (tid >> 4);
