@@ -362,7 +362,7 @@ typedef struct {
 
 /* Saves x (out->rows x out->cols, row stride ldx, MUON_F32 or MUON_BF16) into
  * the checkpoint out. Errors: INVALID_ARG (null pointers, rows outside
- * [0, 2^31 - 1], cols outside [1, 2^24], strides), ALIGN, ALIAS, UNSUPPORTED
+ * [0, 2^30], cols outside [1, 2^24], strides), ALIGN, ALIAS, UNSUPPORTED
  * (dtype, kind), HIP. */
 muon_status muon_q8_save(const void* x, int64_t ldx, int32_t dtype, const muon_q8* out, void* stream);
 
@@ -485,10 +485,11 @@ typedef struct {
 /* Weight gradients of n_items layers in one go (few layers alone fill the
  * GPU). dtype (of dy and scale) and g_dtype are MUON_F32 or MUON_BF16; every
  * x has the same kind. Errors: INVALID_ARG (null pointers, n or cols outside
- * [1, 2^24], rows outside [0, 2^31 - 1], strides, non-finite beta, a short
- * workspace, checkpoints of different kinds), ALIGN, ALIAS (c == g is fine),
+ * [1, 2^24], rows outside [0, 2^30], strides, non-finite beta, a short
+ * workspace, checkpoints of different kinds, more than 2^22 output tiles), ALIGN, ALIAS (c == g is fine),
  * UNSUPPORTED, HIP. workspace is scratch of this call until it has run:
- * muon_wgrad_workspace bytes (which may be 0), 16-byte aligned. */
+ * muon_wgrad_workspace bytes (which may be 0), 16-byte aligned.
+ * muon_wgrad_workspace makes the same checks of the items, without a GPU. */
 muon_status muon_wgrad(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype,
                        void* workspace, size_t workspace_bytes, void* stream);
 muon_status muon_wgrad_workspace(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype,

@@ -18,7 +18,8 @@ muon_status muon_fail_message(muon_status st, const char* msg);
 
 namespace {
 
-constexpr int64_t kMaxRows = INT32_MAX, kMaxCols = int64_t(1) << 24;
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxCols = int64_t(1) << 24;
+constexpr int64_t kMaxUnits = int64_t(1) << 22;  // workgroups of 512 threads in a 32-bit grid
 
 muon_status fail(muon_status st, const std::string& msg) { return muon_fail_message(st, msg.c_str()); }
 muon_status hip_status(hipError_t e) {
@@ -27,15 +28,18 @@ muon_status hip_status(hipError_t e) {
   return fail(MUON_ERR_HIP, std::string("kernel launch: ") + hipGetErrorString(e));
 }
 
-// Runs f, turning a C++ exception (out of host memory) into a status.
+// Runs f, turning a C++ exception (out of host memory) into a status; there may
+// be no memory for the message either.
 template <class F>
 muon_status guarded(F f) {
   try {
     return f();
-  } catch (const std::bad_alloc&) {
-    return muon_fail_message(MUON_ERR_OOM, "out of host memory");
   } catch (...) {
-    return muon_fail_message(MUON_ERR_INVALID_ARG, "unexpected error");
+    try {
+      muon_fail_message(MUON_ERR_OOM, "out of host memory");
+    } catch (...) {
+    }
+    return MUON_ERR_OOM;
   }
 }
 
@@ -117,7 +121,7 @@ muon_status check_dtype(int32_t dtype, const char* what = "dtype") {
 int elem_of(int32_t dtype) { return dtype == MUON_BF16 ? 2 : 4; }
 
 muon_status check_size(int64_t rows, int64_t cols, int item = -1) {
-  if (rows < 0 || rows > kMaxRows) return fail(MUON_ERR_INVALID_ARG, Views::at(item) + "rows must be in [0, 2^31 - 1]");
+  if (rows < 0 || rows > kMaxRows) return fail(MUON_ERR_INVALID_ARG, Views::at(item) + "rows must be in [0, 2^30]");
   if (cols < 1 || cols > kMaxCols) return fail(MUON_ERR_INVALID_ARG, Views::at(item) + "cols must be in [1, 2^24]");
   return MUON_OK;
 }
@@ -343,7 +347,7 @@ muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32
     d.part0 = int32_t(partials);
     units += t * d.splits;
     if (d.splits > 1) partials += t * d.splits;
-    if (units > (int64_t(1) << 30)) return fail(MUON_ERR_INVALID_ARG, "more than 2^30 tiles in one call");
+    if (units > kMaxUnits) return fail(MUON_ERR_INVALID_ARG, "more than 2^22 tiles in one launch");
   }
   p.args.units = int32_t(units);
   p.partial = at;
@@ -460,6 +464,7 @@ muon_status muon_wgrad_workspace(const muon_wgrad_item* items, int32_t n_items, 
     if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
     Views v;
     MUON_TRY(check_wgrad(items, n_items, dtype, g_dtype, v));
+    MUON_TRY(v.disjoint());
     std::vector<WgradPlan> plans;
     return plan_all(items, n_items, dtype, g_dtype, plans, bytes);
   });

@@ -20,11 +20,14 @@ from __future__ import annotations
 import ctypes
 from typing import Iterable, List, Optional, Sequence
 
-from . import muon as _m
-from .muon import MuonError, check, lib, muon_norm_grads, muon_norm_site, muon_q8, muon_wgrad_item
+import torch
+
+from .muon import (MUON_BF16, MUON_F32, MuonError, check, lib, muon_norm_grads, muon_norm_site, muon_q8,
+                   muon_wgrad_item)
 
 GROUP = 32
 KINDS = {"int8": 0, "e4m3": 1}
+_CODES = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32}
 
 
 def _bad(message: str):
@@ -37,9 +40,15 @@ def _kind(kind: str) -> int:
     return KINDS[kind]
 
 
+def _code(t) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise MuonError(-4, f"unsupported tensor dtype {t.dtype}")
+    return code
+
+
 def _matrix(t, name: str, shape=None, dtype=None, vector=False):
     """Checks one tensor of a call: where it is, its layout, shape and type."""
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _bad(f"{name} must be a device tensor")
     if t.get_device() != torch.cuda.current_device():
@@ -62,15 +71,17 @@ def _ld(t) -> int:
 def _stream(stream, tensors: Sequence):
     """The stream's handle. Memory that another stream uses than the current
     one is kept from reuse until that stream is done with it."""
-    import torch
     if stream is None:  # the handle alone: making a Stream object takes 3 us
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    if hasattr(stream, "cuda_stream"):
-        if stream != torch.cuda.current_stream():
-            for t in tensors:
-                t.record_stream(stream)
-        return stream.cuda_stream
-    return int(stream)
+    stream = _stream_object(stream)
+    if stream != torch.cuda.current_stream():
+        for t in tensors:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _stream_object(stream):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
 
 
 def _ptr(t) -> Optional[int]:
@@ -84,7 +95,6 @@ class Q8:
     view of them; otherwise it allocates them."""
 
     def __init__(self, rows: int, cols: int, kind: str = "int8", *, q=None, e=None):
-        import torch
         if rows < 0 or cols < 1:
             _bad("a checkpoint needs rows >= 0 and cols >= 1")
         self.rows, self.cols, self.kind = int(rows), int(cols), kind
@@ -112,7 +122,7 @@ class Q8:
 def q8_save(x, out: Q8, stream=None) -> Q8:
     """Saves x (bf16 or fp32) into the checkpoint ``out``."""
     _matrix(x, "x", (out.rows, out.cols))
-    check(lib().muon_q8_save(x.data_ptr(), _ld(x), _m._dtype_code(x), ctypes.byref(out._c),
+    check(lib().muon_q8_save(x.data_ptr(), _ld(x), _code(x), ctypes.byref(out._c),
                              _stream(stream, (x, out.q, out.e))))
     return out
 
@@ -121,7 +131,7 @@ def q8_load(ckpt: Q8, out, stream=None):
     """Writes the values that the checkpoint stands for into ``out`` (bf16, which
     holds them exactly, or fp32)."""
     _matrix(out, "out", (ckpt.rows, ckpt.cols))
-    check(lib().muon_q8_load(ctypes.byref(ckpt._c), out.data_ptr(), _ld(out), _m._dtype_code(out),
+    check(lib().muon_q8_load(ctypes.byref(ckpt._c), out.data_ptr(), _ld(out), _code(out),
                              _stream(stream, (out, ckpt.q, ckpt.e))))
     return out
 
@@ -149,9 +159,8 @@ class NormSite:
 
     def __init__(self, branch, residual, w_pre, *, w_post=None, gate=None, res_scale: float = 1.0,
                  branch_scale: float = 1.0, eps: float = 1e-6, kind: Optional[str] = "int8", saved=None):
-        import torch
         _matrix(branch, "branch")
-        code, dt = _m._dtype_code(branch), branch.dtype
+        code, dt = _code(branch), branch.dtype
         rows, cols = branch.shape
         _matrix(residual, "residual", (rows, cols), dt)
         _matrix(w_pre, "w_pre", (cols,), dt, vector=True)
@@ -192,7 +201,6 @@ class NormSite:
         check(lib().muon_norm_forward(ctypes.byref(self._c), _stream(stream, self._tensors)))
 
     def backward(self, dy, dh, stream=None) -> None:
-        import torch
         shape, dt = tuple(self.y.shape), self.y.dtype
         if self.u is None or self.rstd_y is None:
             _bad("the site keeps no checkpoints: make it with a kind")
@@ -200,21 +208,27 @@ class NormSite:
             _matrix(dy, "dy", shape, dt)
         _matrix(dh, "dh", shape, dt)
         if self._grads is None:
-            empty = lambda t: None if t is None else torch.empty(t.shape, dtype=dt, device=t.device)  # noqa: E731
-            self.d_residual, self.d_branch = empty(self.y), empty(self.y)
-            self.d_w_pre, self.d_w_post, self.d_gate = empty(self.w_pre), empty(self.w_post), empty(self.gate)
-            need = ctypes.c_size_t()
-            check(lib().muon_norm_backward_workspace(shape[0], shape[1], ctypes.byref(need)))
-            self._workspace = torch.empty(need.value, dtype=torch.uint8, device=self.y.device)
-            self._grads = muon_norm_grads(
-                None, 0, None, 0, self.d_residual.data_ptr(), shape[1], self.d_branch.data_ptr(), shape[1],
-                _ptr(self.d_w_pre), _ptr(self.d_w_post), _ptr(self.d_gate), shape[1], self._workspace.data_ptr(), need.value)
-            self._tensors += [t for t in (self.d_residual, self.d_branch, self.d_w_pre, self.d_w_post, self.d_gate,
-                                          self._workspace) if t is not None]
+            # new memory belongs to the stream that uses it first
+            with torch.cuda.stream(None if stream is None else _stream_object(stream)):
+                self._make_grads()
         g = self._grads
         g.dy, g.ld_dy, g.dh, g.ld_dh = _ptr(dy), 0 if dy is None else _ld(dy), dh.data_ptr(), _ld(dh)
         used = self._tensors if stream is None else self._tensors + [t for t in (dy, dh) if t is not None]
         check(lib().muon_norm_backward(ctypes.byref(self._c), ctypes.byref(g), _stream(stream, used)))
+
+    def _make_grads(self) -> None:
+        shape, dt = tuple(self.y.shape), self.y.dtype
+        empty = lambda t: None if t is None else torch.empty(t.shape, dtype=dt, device=t.device)  # noqa: E731
+        self.d_residual, self.d_branch = empty(self.y), empty(self.y)
+        self.d_w_pre, self.d_w_post, self.d_gate = empty(self.w_pre), empty(self.w_post), empty(self.gate)
+        need = ctypes.c_size_t()
+        check(lib().muon_norm_backward_workspace(shape[0], shape[1], ctypes.byref(need)))
+        self._workspace = torch.empty(need.value, dtype=torch.uint8, device=self.y.device)
+        self._grads = muon_norm_grads(
+            None, 0, None, 0, self.d_residual.data_ptr(), shape[1], self.d_branch.data_ptr(), shape[1],
+            _ptr(self.d_w_pre), _ptr(self.d_w_post), _ptr(self.d_gate), shape[1], self._workspace.data_ptr(), need.value)
+        self._tensors += [t for t in (self.d_residual, self.d_branch, self.d_w_pre, self.d_w_post, self.d_gate,
+                                      self._workspace) if t is not None]
 
 
 class WGrad:
@@ -229,7 +243,6 @@ class WGrad:
     type, C like G (default: G itself, to accumulate)."""
 
     def __init__(self, items: Iterable[Sequence]):
-        import torch
         self._tensors: List = []
         descs = []
         self._dtype = self._gdtype = None
@@ -240,7 +253,7 @@ class WGrad:
             if not isinstance(x, Q8):
                 _bad("the second entry of an item must be a Q8 checkpoint")
             if dts is None:
-                self._dtype, self._gdtype, dts = _m._dtype_code(dY), _m._dtype_code(G), (dY.dtype, G.dtype)
+                self._dtype, self._gdtype, dts = _code(dY), _code(G), (dY.dtype, G.dtype)
             _matrix(G, "G", dtype=dts[1])
             if not G.is_contiguous():
                 _bad("G must be contiguous")

@@ -191,3 +191,52 @@ def test_feeds_an_optimizer_step():
     torch.cuda.synchronize()
     a.check(), b.check()
     assert all(torch.isfinite(w).all() and w.any() for w in W)
+
+
+def test_python_refusals():
+    import torch
+    from matrix_optimizer_step_muon_amd.muon import MuonError
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q = layer.Q8(10, 64)
+    G = bf(32, 64)
+    site = lambda **k: layer.NormSite(bf(10, 64), bf(10, 64), bf(64), **k)  # noqa: E731
+    for call in (lambda: layer.WGrad([(bf(9, 32), q, G)]),                        # rows
+                 lambda: layer.WGrad([(bf(10, 32), q, bf(32, 65))]),              # columns
+                 lambda: layer.WGrad([(bf(10, 32), q, bf(64, 32).t())]),          # G not contiguous
+                 lambda: layer.WGrad([(bf(32, 10).t(), q, G)]),                   # dY by columns
+                 lambda: layer.WGrad([(bf(1, 32).expand(10, 32), q, G)]),         # dY with row stride 0
+                 lambda: layer.WGrad([(bf(10, 32), q, G), (bf(10, 32).float(), q, G.clone())]),
+                 lambda: layer.WGrad([(bf(10, 32), q, G), (bf(10, 32), layer.Q8(10, 64, "e4m3"), G.clone())]),
+                 lambda: layer.WGrad([(bf(10, 32), q, G), (bf(10, 32), q, G)]),   # one G twice
+                 lambda: layer.WGrad([(bf(10, 32), q, G, bf(63))]),
+                 lambda: layer.WGrad([(bf(10, 32), q, G, None, 1.0, bf(32, 64).float())]),
+                 lambda: layer.WGrad([(bf(10, 32).half(), q, G)]),
+                 lambda: layer.q8_save(bf(10, 65), q), lambda: layer.q8_load(q, bf(64, 10).t()),
+                 lambda: layer.q8_save(bf(10, 64).half(), q),
+                 lambda: layer.Q8(10, 64, q=q.q[:, :48], e=q.e), lambda: layer.Q8(10, 64, q=q.q, e=q.e[:, :1]),
+                 lambda: layer.Q8(10, 64, q=q.q[:9], e=q.e),
+                 lambda: layer.NormSite(bf(10, 64), bf(10, 63), bf(64)), lambda: layer.NormSite(bf(10, 64), bf(10, 64).float(), bf(64)),
+                 lambda: layer.NormSite(bf(10, 64), bf(10, 64), bf(63)), lambda: site(gate=bf(9, 64)), lambda: site(w_post=bf(64).float()),
+                 lambda: site(kind=None).backward(None, bf(10, 64)), lambda: site(kind="int4"),
+                 lambda: site().backward(None, bf(10, 63)), lambda: site().backward(bf(10, 64).float(), bf(10, 64)),
+                 lambda: site(res_scale=float("nan")).forward(), lambda: site(eps=-1.0).forward()):
+        with pytest.raises(MuonError):
+            call()
+    torch.cuda.synchronize()
+
+
+def test_a_raw_stream_handle_and_memory_freed_early():
+    import torch
+    it = Item(500, 300, 200, "bf16", "f32", "int8", scale=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    plan = layer.WGrad([it.item])
+    torch.cuda.synchronize()
+    plan.run(side.cuda_stream)
+    workspace = plan.workspace.numel()
+    del plan                              # its workspace may not be reused before the side stream is done
+    junk = torch.full((max(workspace, 1),), 255, dtype=torch.uint8, device="cuda")
+    side.synchronize()
+    torch.cuda.synchronize()
+    it.check()
+    del junk
