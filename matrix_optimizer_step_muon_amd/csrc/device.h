@@ -30,6 +30,13 @@ typedef float __attribute__((address_space(1))) g_f32;
 
 MUON_INLINE u32x4 gload16(const void* p) { return *((const g_u32x4*)(p)); }
 
+// 16 bytes at any element's address: one instruction too, which the hardware
+// takes apart where it has to.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x4_any __attribute__((address_space(1))) g_u32x4_any;
+MUON_INLINE u32x4 gload16_any(const void* p) { return *((const g_u32x4_any*)(p)); }
+MUON_INLINE void gstore16_any(void* p, u32x4 v) { *((g_u32x4_any*)(p)) = v; }
+
 MUON_INLINE float bf16_to_f32(u16 v) { return __uint_as_float((uint32_t)v << 16); }
 
 // fp32 -> bf16 with gfx950's v_cvt_pk_bf16_f32: rounds to nearest even under

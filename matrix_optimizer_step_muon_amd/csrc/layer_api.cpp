@@ -330,7 +330,6 @@ muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32
     d.k = int32_t(it.x.cols);
     d.na = int32_t(ceil_div(it.n, 8) * 8);
     d.parts = parts;
-    d.dy_vec = dy_aligned(it, dtype);
     d.beta = it.beta;
     p.pack[i] = SIZE_MAX;
     if (large && (dtype == MUON_F32 || !dy_aligned(it, dtype))) {

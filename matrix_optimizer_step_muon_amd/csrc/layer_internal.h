@@ -29,7 +29,12 @@ inline int norm_threads(int64_t cols, int vecs) {
 // Rows of up to 512 columns are one wave each, several to a workgroup: forward
 // 4; backward 8, which leave fewer partial sums (8192 x 512 bf16: 16.9 us, with
 // 4 17.5, with 2 21; one row per workgroup 26).
+// Few rows take a workgroup each, so that they run at once (37 x 201 fp32
+// backward: 5.6 us, 8 to a workgroup 10).
 constexpr int kNormRowsForward = 4, kNormRowsBackward = 8;
+inline int norm_rows(int64_t rows, int threads, int most) {
+  return threads == 64 ? int(std::max<int64_t>(1, std::min<int64_t>(most, rows / 256))) : 1;
+}
 
 // Workgroups of the norm kernels, which take rows in turn: as many as give a CU
 // `per_cu` threads. Forward 1280, two of 640 for 5120 columns (4096 x 5120 bf16:
@@ -50,14 +55,14 @@ struct NormLaunch {
 inline NormLaunch norm_forward_launch(int64_t rows, int64_t cols) {
   NormLaunch l{norm_forward_vecs(cols), 0, 1, 0};
   l.threads = norm_threads(cols, l.vecs);
-  l.rows_per = l.threads == 64 ? kNormRowsForward : 1;
+  l.rows_per = norm_rows(rows, l.threads, kNormRowsForward);
   l.blocks = norm_blocks(rows, l.threads, l.rows_per, kNormThreadsForward);
   return l;
 }
 inline NormLaunch norm_backward_launch(int64_t rows, int64_t cols) {
   NormLaunch l{norm_backward_vecs(cols), 0, 1, 0};
   l.threads = norm_threads(cols, l.vecs);
-  l.rows_per = l.threads == 64 ? kNormRowsBackward : 1;
+  l.rows_per = norm_rows(rows, l.threads, kNormRowsBackward);
   l.blocks = norm_blocks(rows, l.threads, l.rows_per, kNormThreadsBackward);
   return l;
 }
@@ -83,7 +88,6 @@ struct WgItem {
   int64_t lda, ldq, lde;
   int32_t rows, n, k, na;  // na: columns of dy that may be read (a multiple of 8)
   int32_t parts;       // 1, or 3 for fp32 dY (large kernel)
-  int32_t dy_vec;      // 16-byte loads of dY (small kernel)
   int32_t tiles_n, tiles_k;
   int32_t splits;      // > 1: partial tiles go to the workspace
   int32_t part0;       // first partial tile of this item in the workspace

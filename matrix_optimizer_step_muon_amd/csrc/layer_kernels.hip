@@ -14,45 +14,64 @@ namespace muon {
 
 // ------------------------------------------------------------ eight columns
 
-// Columns c0 .. c0+7 of a row; those at or past cols read as 0 and are not
-// written. VEC: the row is 16-byte aligned and cols a multiple of 8.
+// Columns c0 .. c0+7 of a row, as they lie in memory: rows that are loaded
+// ahead, and weights that stay in registers, take half the space so. Columns at
+// or past cols read as 0 and are not written. VEC: the row is 16-byte aligned
+// and cols a multiple of 8; otherwise only a row's last columns are loaded one
+// by one (at clamped addresses, so that the loads need no branches).
+template <class T>
+struct Raw8 {
+  u32x4 w[sizeof(T) / 2];
+};
+
 template <class T, bool VEC>
-MUON_INLINE void load8(const T* row, int64_t c0, int64_t cols, float v[8]) {
-  if (c0 >= cols) {
+MUON_INLINE Raw8<T> load_raw(const T* row, int64_t c0, int64_t cols) {
+  constexpr int N = sizeof(T) / 2, PER = 16 / sizeof(T);
+  Raw8<T> r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  } else if constexpr (VEC) {
-    if constexpr (sizeof(T) == 2) {
-      const u32x4 t = gload16(row + c0);
+  for (int h = 0; h < N; ++h) r.w[h] = u32x4{0u, 0u, 0u, 0u};
+  if (VEC ? c0 < cols : c0 + 8 <= cols) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(t[i] << 16);
-        v[2 * i + 1] = __uint_as_float(t[i] & 0xffff0000u);
-      }
-    } else {
-      Vec4<float>::load(row + c0, v);
-      Vec4<float>::load(row + c0 + 4, v + 4);
+    for (int h = 0; h < N; ++h) r.w[h] = VEC ? gload16(row + c0 + h * PER) : gload16_any(row + c0 + h * PER);
+  } else if (!VEC && c0 < cols) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = Elem<T>::load(row + min(c0 + i, cols - 1));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t bits = c0 + i < cols ? __float_as_uint(v[i]) : 0u;
+      if constexpr (sizeof(T) == 4) r.w[i >> 2][i & 3] = bits;
+      else r.w[0][i >> 1] |= i & 1 ? bits : bits >> 16;
     }
-  } else {
+  }
+  return r;
+}
+
+template <class T>
+MUON_INLINE void widen(const Raw8<T>& r, float v[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c0 + i < cols ? Elem<T>::load(row + c0 + i) : 0.f;
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
+    else v[i] = __uint_as_float(i & 1 ? r.w[0][i >> 1] & 0xffff0000u : r.w[0][i >> 1] << 16);
   }
 }
 
 template <class T, bool VEC>
 MUON_INLINE void store8(T* row, int64_t c0, int64_t cols, const float v[8]) {
-  if (c0 >= cols) return;
-  if constexpr (VEC) {
-    if constexpr (sizeof(T) == 2) {
+  constexpr int N = sizeof(T) / 2, PER = 16 / sizeof(T);
+  if (VEC ? c0 < cols : c0 + 8 <= cols) {
+#pragma unroll
+    for (int h = 0; h < N; ++h) {
       u32x4 t;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      *((g_u32x4*)(row + c0)) = t;
-    } else {
-      Vec4<float>::store(row + c0, v);
-      Vec4<float>::store(row + c0 + 4, v + 4);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) t[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        else t[i] = __float_as_uint(v[4 * h + i]);
+      }
+      if (VEC) *((g_u32x4*)(row + c0 + h * PER)) = t;
+      else gstore16_any(row + c0 + h * PER, t);
     }
-  } else {
+  } else if (!VEC) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c0 + i < cols) Elem<T>::store(row + c0 + i, v[i]);
@@ -68,43 +87,6 @@ MUON_INLINE void store_q8(uint8_t* q, uint8_t* e, int64_t c0, int64_t cols, cons
   if (c0 >= cols) return;
   *((g_u32x2*)(q + c0)) = w;
   if (c0 % kGroup == 0) *((g_u8*)(e + c0 / kGroup)) = (uint8_t)E;
-}
-
-// Eight columns as they lie in memory, to be widened later: rows that are
-// loaded ahead, and weights that stay in registers, take half the space so.
-template <class T>
-struct Raw8 {
-  u32x4 w[sizeof(T) / 2];
-};
-
-template <class T, bool VEC>
-MUON_INLINE Raw8<T> load_raw(const T* row, int64_t c0, int64_t cols) {
-  Raw8<T> r;
-  if constexpr (VEC) {
-#pragma unroll
-    for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-      r.w[h] = u32x4{0u, 0u, 0u, 0u};
-      if (c0 < cols) r.w[h] = gload16(row + c0 + 4 * h);
-    }
-  } else {
-    float v[8];
-    load8<T, false>(row, c0, cols, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (sizeof(T) == 4) r.w[i >> 2][i & 3] = __float_as_uint(v[i]);
-      else if (i & 1) r.w[0][i >> 1] = (__float_as_uint(v[i - 1]) >> 16) | __float_as_uint(v[i]);
-    }
-  }
-  return r;
-}
-
-template <class T>
-MUON_INLINE void widen(const Raw8<T>& r, float v[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
-    else v[i] = __uint_as_float(i & 1 ? r.w[0][i >> 1] & 0xffff0000u : r.w[0][i >> 1] << 16);
-  }
 }
 
 struct RawQ8 {

@@ -447,6 +447,33 @@ MUON_INLINE void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   lo = __float_as_uint(r - __uint_as_float(mid)) & 0xffff0000u;
 }
 
+// Columns c0 .. c0+7 of a row of n elements at any alignment; past n, the last
+// column again. Only a row's last columns are loaded one by one. Nothing here
+// waits for the loads, so the caller clears what is past n later.
+template <class T>
+MUON_INLINE void load_dy8(const T* row, int c0, int n, float v[8]) {
+  if (c0 + 8 <= n) {
+    if constexpr (sizeof(T) == 4) {
+      const u32x4 lo = gload16_any(row + c0), hi = gload16_any(row + c0 + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(lo[i]);
+        v[4 + i] = __uint_as_float(hi[i]);
+      }
+    } else {
+      const u32x4 w = gload16_any(row + c0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = Elem<T>::load(row + min(c0 + i, n - 1));
+  }
+}
+
 // The slot of 16-byte chunk c of token row r: rows r .. r+3, which a
 // transposing read takes together, lie in different banks.
 MUON_INLINE int small_slot(int c, int r) { return c ^ ((r & 3) << 1); }
@@ -474,38 +501,17 @@ __global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
   // dY: chunk c of a lane is 8 columns of token row 8c + lane/8; X: 16 bytes of
   // token row 16c + lane/4.
   const int yr = lane >> 3, yc = (lane & 7) * 8, xr = lane >> 2, xc = k0 + 16 * min(lane & 3, (it.k - 1 - k0) / 16);
-  const T* dy = static_cast<const T*>(it.dy) + n0 + yc;
-  const int ycols = it.n - n0 - yc;  // of these 8, the ones that exist
-  const bool vec = it.dy_vec;
+  const T* dy = static_cast<const T*>(it.dy);
+  const int ycols = it.n - n0 - yc;  // of a lane's 8 columns, the ones that exist
   float yv[4][8];
   u32x4 xv[2];
   uint32_t ev[2];
-  // Tokens past the last one read as zeros (X: as exponent bytes and codes of
-  // the last one, cleared when they are decoded).
+  // Tokens past the last one read the last one, and become zeros when they are
+  // staged.
   auto load = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int t = 32 * b + 8 * c + yr;
-      const T* p = dy + (int64_t)t * it.lda;
-      if (t >= rows || ycols <= 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) yv[c][i] = 0.f;
-      } else if (vec) {
-        if constexpr (sizeof(T) == 4) {
-          Vec4<float>::load(p, yv[c]);
-          Vec4<float>::load(p + 4, yv[c] + 4);
-        } else {
-          const u32x4 w = gload16(p);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            yv[c][2 * i] = __uint_as_float(w[i] << 16);
-            yv[c][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) yv[c][i] = i < ycols ? Elem<T>::load(p + i) : 0.f;
-      }
+      load_dy8(dy + (int64_t)min(32 * b + 8 * c + yr, rows - 1) * it.lda, n0 + yc, it.n, yv[c]);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -518,6 +524,9 @@ __global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int r = 8 * c + yr;
+      const int live = 32 * b + r < rows ? ycols : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) yv[c][i] = i < live ? yv[c][i] : 0.f;
       u32x4 o[PARTS];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -692,8 +701,9 @@ __global__ void __launch_bounds__(256) wgrad_pack_kernel(const T* dy, int64_t ld
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / octets, c0 = (i - row * octets) * 8;
     float v[8];
+    load_dy8(dy + row * ld, (int)c0, n, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c0 + e < n ? Elem<T>::load(dy + row * ld + c0 + e) : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e < n ? v[e] : 0.f;
     u16* o = out + row * lda + c0;
     if constexpr (PARTS == 1) {
       u32x4 t;
