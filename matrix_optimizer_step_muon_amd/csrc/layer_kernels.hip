@@ -103,10 +103,13 @@ MUON_INLINE RawQ8 load_raw_q8(const muon_q8& p, int64_t row, int64_t c0) {
   return r;
 }
 
+template <bool VEC>
 MUON_INLINE void widen_q8(const RawQ8& r, int64_t c0, int64_t cols, int kind, float v[8]) {
   q8_decode(r.w, r.e, kind, v);
+  if constexpr (!VEC) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c0 + i < cols ? v[i] : 0.f;  // padding bytes are not the row's
+    for (int i = 0; i < 8; ++i) v[i] = c0 + i < cols ? v[i] : 0.f;  // padding bytes are not the row's
+  }
 }
 
 // ------------------------------------------------------------ save and load
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(256) q8_kernel(Q8Args a) {
         store_q8(static_cast<uint8_t*>(a.p.q) + row * a.p.ldq, static_cast<uint8_t*>(a.p.e) + row * a.p.lde, c0, cols, v,
                  a.p.kind);
       } else {
-        widen_q8(q[u], c0, cols, a.p.kind, v);
+        widen_q8<VEC>(q[u], c0, cols, a.p.kind, v);
         store8<T, VEC>(static_cast<T*>(a.x) + row * a.ldx, c0, cols, v);
       }
     }
@@ -236,12 +239,12 @@ MUON_INLINE void block_sum(float (&v)[N], float* red) {
 }
 
 // One row per workgroup at a time, or, in rows of one wave, one per wave
-// (blockDim.y of them): thread x holds columns 8x .. 8x+7 (VPT times, blockDim.x
+// (rows_per of them): thread x holds columns 8x .. 8x+7 (VPT times, blockDim.x
 // threads apart). The row stays in registers between its two
 // norms, so every tensor moves once. With VPT = 1 there are registers left to
 // load the weights once and to have the next row's loads in flight.
 template <class T, int VPT, bool VEC>
-__global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
+__global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, int32_t rows_per) {
   __shared__ float red[2][16];
   const int64_t cols = s.cols;
   const float inv_cols = 1.f / (float)cols;
@@ -264,8 +267,9 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
 #pragma unroll
   for (int p = 0; p < VPT; ++p) c0[p] = ((int64_t)p * blockDim.x + threadIdx.x) * 8;
   // The same in a whole wave, and said so: row addresses stay in scalar registers.
+  // rows_per is blockDim.y, which would take another load to know.
   const int sub = __builtin_amdgcn_readfirstlane(threadIdx.y);
-  const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + sub, step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t row0 = (int64_t)blockIdx.x * rows_per + sub, step = (int64_t)gridDim.x * rows_per;
   if (row0 >= s.rows) return;  // a wave of its own: nothing waits for it
   if (VPT == 1) {
     load(row0);
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s) {
 // stores the weight gradients themselves. MAXT: the most threads of a
 // workgroup, which sets the registers of each.
 template <class T, int VPT, bool VEC, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, muon_norm_grads g) {
+__global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, muon_norm_grads g, int32_t rows_per) {
   __shared__ float red[2][48];
   __shared__ float join[MAXT == 512 && VPT == 1 ? kNormRowsBackward * 512 : 1];
   const int64_t cols = s.cols;
@@ -402,8 +406,8 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
 #pragma unroll
     for (int i = 0; i < 8; ++i) c.t[i] = c.v[i] = 0.f;
     if (g.dy) widen(rdy, c.t);
-    widen_q8(ru, c0, cols, s.u.kind, c.u);
-    if (need_v) widen_q8(rv, c0, cols, s.v.kind, c.v);
+    widen_q8<VEC>(ru, c0, cols, s.u.kind, c.u);
+    if (need_v) widen_q8<VEC>(rv, c0, cols, s.v.kind, c.v);
     if (per_row) c.gt = rg;
     c.ry = ry, c.rb = rb;
   };
@@ -469,9 +473,8 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
     store8<T, VEC>(static_cast<T*>(g.d_branch) + row * g.ld_d_branch, c0, cols, o);
   };
 
-  // The same in a whole wave, and said so: row addresses stay in scalar registers.
   const int y = __builtin_amdgcn_readfirstlane(threadIdx.y);
-  const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + y, step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t row0 = (int64_t)blockIdx.x * rows_per + y, step = (int64_t)gridDim.x * rows_per;
   if (VPT == 1 && row0 < s.rows) {
     load(row0, 0);
     load_weights(0);
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
     }
   }
   if constexpr (MAXT == 512 && VPT == 1) {
-    if (blockDim.y > 1) {
+    if (rows_per > 1) {
 #pragma unroll
       for (int w = 0; w < 3; ++w) {
         __syncthreads();
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
         for (int i = 0; i < 8; ++i) join[y * 512 + threadIdx.x * 8 + i] = acc[w][0][i];
         __syncthreads();
         if (y == 0) {
-          for (int o = 1; o < (int)blockDim.y; ++o)
+          for (int o = 1; o < rows_per; ++o)
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[w][0][i] += join[o * 512 + threadIdx.x * 8 + i];
         }
@@ -588,7 +591,7 @@ static hipError_t norm_forward(const muon_norm_site& s, hipStream_t st) {
   const NormLaunch l = norm_forward_launch(s.rows, s.cols);
   const int vpt = l.vecs;
   const dim3 grid(l.blocks), block(l.threads, l.rows_per);
-#define MUON_NORM_F(V, A) hipLaunchKernelGGL((norm_forward_kernel<T, V, A>), grid, block, 0, st, s)
+#define MUON_NORM_F(V, A) hipLaunchKernelGGL((norm_forward_kernel<T, V, A>), grid, block, 0, st, s, l.rows_per)
   if (vec) { if (vpt == 1) MUON_NORM_F(1, true); else if (vpt == 2) MUON_NORM_F(2, true); else MUON_NORM_F(4, true); }
   else { if (vpt == 1) MUON_NORM_F(1, false); else if (vpt == 2) MUON_NORM_F(2, false); else MUON_NORM_F(4, false); }
 #undef MUON_NORM_F
@@ -611,8 +614,8 @@ static hipError_t norm_backward(const muon_norm_site& s, const muon_norm_grads& 
     const dim3 grid(l.blocks), block(l.threads, l.rows_per);
 #define MUON_NORM_B(V, M)                                                                                 \
   do {                                                                                                    \
-    if (vec) hipLaunchKernelGGL((norm_backward_kernel<T, V, true, M>), grid, block, 0, st, s, g);         \
-    else hipLaunchKernelGGL((norm_backward_kernel<T, V, false, M>), grid, block, 0, st, s, g);            \
+    if (vec) hipLaunchKernelGGL((norm_backward_kernel<T, V, true, M>), grid, block, 0, st, s, g, l.rows_per);         \
+    else hipLaunchKernelGGL((norm_backward_kernel<T, V, false, M>), grid, block, 0, st, s, g, l.rows_per);            \
   } while (0)
     if (vpt == 1 && block.x <= 512) MUON_NORM_B(1, 512);
     else if (vpt == 1) MUON_NORM_B(1, 768);
