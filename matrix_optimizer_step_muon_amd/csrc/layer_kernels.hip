@@ -16,9 +16,10 @@ namespace muon {
 
 // Columns c0 .. c0+7 of a row, as they lie in memory: rows that are loaded
 // ahead, and weights that stay in registers, take half the space so. Columns at
-// or past cols read as 0 and are not written. VEC: the row is 16-byte aligned
-// and cols a multiple of 8; otherwise only a row's last columns are loaded one
-// by one (at clamped addresses, so that the loads need no branches).
+// or past cols are 0 once widened, and are not written. VEC: the row is 16-byte
+// aligned and cols a multiple of 8; otherwise only a row's last columns are
+// loaded one by one, at clamped addresses, and nothing is done to what was
+// loaded until it is widened, so that no load waits for another.
 template <class T>
 struct Raw8 {
   u32x4 w[sizeof(T) / 2];
@@ -34,25 +35,22 @@ MUON_INLINE Raw8<T> load_raw(const T* row, int64_t c0, int64_t cols) {
 #pragma unroll
     for (int h = 0; h < N; ++h) r.w[h] = VEC ? gload16(row + c0 + h * PER) : gload16_any(row + c0 + h * PER);
   } else if (!VEC && c0 < cols) {
-    float v[8];
+    typedef T Tx8 __attribute__((ext_vector_type(8)));
+    Tx8 t;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = Elem<T>::load(row + min(c0 + i, cols - 1));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t bits = c0 + i < cols ? __float_as_uint(v[i]) : 0u;
-      if constexpr (sizeof(T) == 4) r.w[i >> 2][i & 3] = bits;
-      else r.w[0][i >> 1] |= i & 1 ? bits : bits >> 16;
-    }
+    for (int i = 0; i < 8; ++i) t[i] = *((const T __attribute__((address_space(1)))*)(row + min(c0 + i, cols - 1)));
+    r = __builtin_bit_cast(Raw8<T>, t);
   }
   return r;
 }
 
-template <class T>
-MUON_INLINE void widen(const Raw8<T>& r, float v[8]) {
+template <class T, bool VEC>
+MUON_INLINE void widen(const Raw8<T>& r, int64_t c0, int64_t cols, float v[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
     else v[i] = __uint_as_float(i & 1 ? r.w[0][i >> 1] & 0xffff0000u : r.w[0][i >> 1] << 16);
+    if (!VEC) v[i] = c0 + i < cols ? v[i] : 0.f;
   }
 }
 
@@ -149,7 +147,7 @@ __global__ void __launch_bounds__(256) q8_kernel(Q8Args a) {
       if (row >= rows) break;
       float v[8];
       if constexpr (SAVE) {
-        widen(x[u], v);
+        widen<T, VEC>(x[u], c0, cols, v);
         store_q8(static_cast<uint8_t*>(a.p.q) + row * a.p.ldq, static_cast<uint8_t*>(a.p.e) + row * a.p.lde, c0, cols, v,
                  a.p.kind);
       } else {
@@ -281,9 +279,9 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, in
     if (VPT > 1) load(row);
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      widen(b[p], v[p]);
-      widen(r[p], y[p]);
-      if (per_row) widen(gt[p], g[p]);
+      widen<T, VEC>(b[p], c0[p], cols, v[p]);
+      widen<T, VEC>(r[p], c0[p], cols, y[p]);
+      if (per_row) widen<T, VEC>(gt[p], c0[p], cols, g[p]);
     }
     if (VPT == 1 && row + step < s.rows) load(row + step);
     if (post) {
@@ -308,12 +306,12 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, in
                  cols, v[p], s.v.kind);
       float w[8];
       if (post) {
-        widen(w2[p], w);
+        widen<T, VEC>(w2[p], c0[p], cols, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[p][i] *= w[i];
       }
       if (s.gate) {
-        if (!per_row) widen(gt[p], g[p]);
+        if (!per_row) widen<T, VEC>(gt[p], c0[p], cols, g[p]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[p][i] *= g[p][i];
       }
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, in
       if (s.u.q)
         store_q8(static_cast<uint8_t*>(s.u.q) + row * s.u.ldq, static_cast<uint8_t*>(s.u.e) + row * s.u.lde, c0[p],
                  cols, y[p], s.u.kind);
-      widen(w1[p], w);
+      widen<T, VEC>(w1[p], c0[p], cols, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] *= y[p][i];
       store8<T, VEC>(static_cast<T*>(s.h) + row * s.ld_h, c0[p], cols, w);
@@ -402,27 +400,27 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
   };
   auto widen_row = [&](Cols& c, float dh[8], int p) __attribute__((always_inline)) {
     const int64_t c0 = col0(p);
-    widen(rdh, dh);
+    widen<T, VEC>(rdh, c0, cols, dh);
 #pragma unroll
     for (int i = 0; i < 8; ++i) c.t[i] = c.v[i] = 0.f;
-    if (g.dy) widen(rdy, c.t);
+    if (g.dy) widen<T, VEC>(rdy, c0, cols, c.t);
     widen_q8<VEC>(ru, c0, cols, s.u.kind, c.u);
     if (need_v) widen_q8<VEC>(rv, c0, cols, s.v.kind, c.v);
     if (per_row) c.gt = rg;
     c.ry = ry, c.rb = rb;
   };
-  auto gate_of = [&](const Cols& c, float gt[8]) __attribute__((always_inline)) {
+  auto gate_of = [&](const Cols& c, int p, float gt[8]) __attribute__((always_inline)) {
     if (s.gate) {
-      widen(per_row ? c.gt : rg, gt);
+      widen<T, VEC>(per_row ? c.gt : rg, col0(p), cols, gt);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) gt[i] = 1.f;
     }
   };
   // The row's share of its three sums.
-  auto add_sums = [&](Cols& c, const float dh[8], float (&sum)[3]) __attribute__((always_inline)) {
+  auto add_sums = [&](Cols& c, int p, const float dh[8], float (&sum)[3]) __attribute__((always_inline)) {
     float w[8];
-    widen(w1, w);
+    widen<T, VEC>(w1, col0(p), cols, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float du = dh[i] * w[i];
@@ -431,8 +429,8 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
     }
     if (post) {
       float gt[8];
-      widen(w2, w);
-      gate_of(c, gt);
+      widen<T, VEC>(w2, col0(p), cols, w);
+      gate_of(c, p, gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float av = gt[i] * w[i] * c.v[i];
@@ -454,12 +452,12 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
     }
     store8<T, VEC>(static_cast<T*>(g.d_residual) + row * g.ld_d_residual, c0, cols, o);
     if (post) {
-      widen(w2, w);
+      widen<T, VEC>(w2, col0(p), cols, w);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = 1.f;
     }
-    gate_of(c, gt);
+    gate_of(c, p, gt);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       o[i] = c.t[i] * w[i] * c.v[i];
@@ -494,7 +492,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
       if (VPT == 1 && row + step < s.rows) load(row + step, 0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[0][p][i] += dh[i] * c.u[i];
-      add_sums(c, dh, sum);
+      add_sums(c, p, dh, sum);
       if (VPT > 1) __builtin_amdgcn_sched_barrier(0);  // eight columns' registers at a time
     }
     block_sum(sum, red[flip]);
@@ -505,7 +503,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
         load(row, p);
         load_weights(p);
         widen_row(c, dh, p);
-        add_sums(c, dh, none);
+        add_sums(c, p, dh, none);
       }
       finish(c, row, p, sum);
       if (VPT > 1) __builtin_amdgcn_sched_barrier(0);
