@@ -255,30 +255,35 @@ struct Choice {
 // Which tile edge, and how many pieces the sum over tokens is cut into, for
 // items with t256 and t64 tiles in all, at most `rows` tokens, and `packed`
 // bytes of dY that the large kernel would have rewritten first. The estimates
-// are in microseconds, from a sweep on one MI355X (64 x 64 to 2048 x 2048 and
-// 1024 x 5120 outputs, 16 to 8192 tokens, 1 to 16 pieces):
-// - a round is one workgroup per CU. The large kernel takes 1.4 to 1.75 us per
-//   stage of 64 tokens and 8 to fill and empty a tile; the small one 1.2 (fp32:
-//   1.55) per 128 tokens and 2;
+// are in microseconds, from sweeps on one MI355X (64 x 64 to 4000 x 4000 outputs,
+// 16 to 8192 tokens, bf16 and fp32, each kernel in 1 to 16 pieces; of 107 sizes
+// the pick is over 10% behind the best in two, 0.4% on average):
+// - large kernel: rounds of one workgroup per CU, 1.65 per stage of 64 tokens
+//   and 8 to fill and empty the tile;
+// - small kernel: rounds of two per CU, per 128 tokens 2.2 (fp32: 3.2), or 1.6
+//   (2.1) where one per CU is left, and 2;
 // - pieces cost their partial tiles, written and read back (256 KB each at
-//   about 3.5 TB/s; 16 KB), one more launch, and 0.3 us per piece in it;
-// - rewriting dY costs a launch and its bytes at about 3 TB/s.
-// At 1024 x 1024 and 512 bf16 tokens, for example, one round of the small
-// kernel takes 14 us and the large one 28; at 8192 tokens 139 and, in 8 pieces, 61.
+//   about 4 TB/s; 16 KB), one more launch, and 0.3 per piece in it;
+// - rewriting dY costs a launch and its bytes at about 8 TB/s (of cache).
+// At 1024 x 1024 and 300 bf16 tokens, for example, the small kernel takes 13 us
+// and the large one 24; at 8192 tokens 87 in 2 pieces, and the large one 47 in 16.
 Choice choose(int64_t t256, int64_t t64, int64_t rows, int parts, int64_t packed) {
   constexpr int64_t kCus = 256;
   const int64_t stages = ceil_div(rows, muon::kWgStep) * parts, blocks = ceil_div(rows, 128);
-  const double pack = packed ? 3.0 + double(packed) * 3.3e-7 : 0.0;
+  const double pack = packed ? 3.0 + double(packed) * 1.2e-7 : 0.0;
   Choice best{muon::kWgTile, 1, 1e300};
   const int64_t most = std::min<int64_t>(64, std::max(stages / 2, blocks));
   for (int s = 1; s <= std::max<int64_t>(1, most); ++s) {
     if (s == 1 || s <= stages / 2) {
-      double us = pack + double(ceil_div(t256 * s, kCus)) * (8.0 + 1.65 * double(ceil_div(stages, s)));
-      if (s > 1) us += 3.0 + 0.3 * s + 0.145 * double(t256 * s);
+      double us = 2.0 + pack + double(ceil_div(t256 * s, kCus)) * (8.0 + 1.65 * double(ceil_div(stages, s)));
+      if (s > 1) us += 3.0 + 0.3 * s + 0.13 * double(t256 * s);
       if (us < best.us) best = {muon::kWgTile, s, us};
     }
     if (s == 1 || s <= blocks) {
-      double us = double(ceil_div(t64 * s, kCus)) * (2.0 + (parts == 3 ? 1.55 : 1.2) * double(ceil_div(blocks, s)));
+      const int64_t full = t64 * s / (2 * kCus), rest = t64 * s % (2 * kCus);
+      const double two = parts == 3 ? 3.2 : 2.2, one = parts == 3 ? 2.1 : 1.6;
+      const double per = double(full) * two + (rest == 0 ? 0.0 : rest <= kCus ? one : two);
+      double us = 2.0 * double(full + (rest != 0)) + per * double(ceil_div(blocks, s));
       if (s > 1) us += 3.0 + 0.3 * s + 0.011 * double(t64 * s);
       if (us < best.us) best = {muon::kWgSmall, s, us};
     }
