@@ -240,7 +240,9 @@ MUON_INLINE void block_sum(float (&v)[N], float* red) {
 // (rows_per of them): thread x holds columns 8x .. 8x+7 (VPT times, blockDim.x
 // threads apart). The row stays in registers between its two
 // norms, so every tensor moves once. With VPT = 1 there are registers left to
-// load the weights once and to have the next row's loads in flight.
+// load the weights once and to have the next row's loads in flight. 4096 x 5120
+// bf16: 29 us with its tensors partly in cache, 36 without (4.7 TB/s; a copy
+// 4.9); one row 4.1 to 4.8 us, a chain of loads and two sums.
 template <class T, int VPT, bool VEC>
 __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, int32_t rows_per) {
   __shared__ float red[2][16];
@@ -355,7 +357,9 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, in
 // wider rows are read again (from cache) after their sums. Rows of one wave go
 // one to a wave, whose sums are added at the end; a launch of one workgroup
 // stores the weight gradients themselves. MAXT: the most threads of a
-// workgroup, which sets the registers of each.
+// workgroup, which sets the registers of each. 16384 x 2048 bf16: 73 us, 4.6
+// TB/s; 4096 x 5120: 56 us, 3.8 TB/s, where one workgroup of 10 waves is what a
+// CU's registers hold and its row's arithmetic (40% of the time) is not hidden.
 template <class T, int VPT, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, muon_norm_grads g, int32_t rows_per) {
   __shared__ float red[2][48];
@@ -548,7 +552,8 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, m
 }
 
 // The weight gradients from the partial sums: 64 columns per workgroup, 16
-// waves that each add every 16th partial, joined in order.
+// waves that each add every 16th partial, joined in order. Three weights of 2048
+// columns from 768 workgroups: 4.8 us (15.8 with one load in flight).
 template <class T>
 __global__ void __launch_bounds__(1024) norm_weights_kernel(const float* part, int32_t blocks, int64_t cols, T* d0,
                                                             T* d1, T* d2) {
