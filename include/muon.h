@@ -19,6 +19,9 @@
  *   O  = X (or X^T if r > c)
  *   W' = W - lr * sqrt(max(1, r/c)) * O      weights, updated in place
  *
+ * Beside the step: the tensor-parallel local update, the host-side planners,
+ * and the layer operators that make the gradients it reads.
+ *
  * Conventions for every function:
  * - It returns muon_status (0 = MUON_OK) and never throws or aborts across the
  *   ABI. On error, muon_last_error() gives this thread's message.

@@ -1,7 +1,9 @@
 """Whole-tensor Muon optimizer step on MI355X (gfx950).
 
 The compute lives in the HIP library ``_lib/libmuon.so``. ``muon`` is its ctypes
-binding, and ``workloads`` makes seeded synthetic inputs. The library loads on
+binding, ``layer`` binds the operators around the step (8-bit activation
+checkpoints, norm sites, weight gradients; it needs torch), and ``workloads``
+makes seeded synthetic inputs. The library loads on
 first use, and importing the package does not touch the GPU.
 """
 
