@@ -253,38 +253,49 @@ struct Choice {
 };
 
 // Which tile edge, and how many pieces the sum over tokens is cut into, for
-// items with t256 and t64 tiles in all, at most `rows` tokens, and `packed`
-// bytes of dY that the large kernel would have rewritten first. The estimates
+// items with t256, t128 and t64 tiles in all, at most `rows` tokens, and `packed`
+// bytes of dY that the two larger kernels would have rewritten first. The estimates
 // are in microseconds, from sweeps on one MI355X (64 x 64 to 4000 x 4000 outputs,
-// 16 to 8192 tokens, bf16 and fp32, each kernel in 1 to 16 pieces; of 107 sizes
-// the pick is over 10% behind the best in two, 0.4% on average):
-// - large kernel: rounds of one workgroup per CU, 1.65 per stage of 64 tokens
-//   and 8 to fill and empty the tile;
-// - small kernel: rounds of two per CU, per 128 tokens 2.2 (fp32: 3.2), or 1.6
-//   (2.1) where one per CU is left, and 2;
-// - pieces cost their partial tiles, written and read back (256 KB each at
-//   about 4 TB/s; 16 KB), one more launch, and 0.3 per piece in it;
-// - rewriting dY costs a launch and its bytes at about 8 TB/s (of cache).
-// At 1024 x 1024 and 300 bf16 tokens, for example, the small kernel takes 13 us
-// and the large one 24; at 8192 tokens 87 in 2 pieces, and the large one 47 in 16.
-Choice choose(int64_t t256, int64_t t64, int64_t rows, int parts, int64_t packed) {
+// 16 to 8192 tokens, bf16 and fp32, each kernel in 1 to 16 pieces; of 174 sizes,
+// 95 of them not used for the fit, the pick is over 10% behind the best in two,
+// 0.2% on average):
+// - large kernel: rounds of one workgroup per CU, 1.4 per stage of 64 tokens
+//   and 15 to fill and empty the tile;
+// - medium kernel: rounds of two per CU, 1.16 per stage, or 0.72 where one per
+//   CU is left, and 10;
+// - small kernel: rounds of two per CU, per 128 tokens 2.4 (fp32: 3.0), or 2.0
+//   (2.3) where one per CU is left, and 2.7;
+// - pieces cost their partial tiles, written and read back (256, 64 or 16 KB
+//   each, at 5 to 12 TB/s, as they find a place in the caches), and one more launch;
+// - rewriting dY costs a launch and its bytes at about 9 TB/s (of cache).
+// For bf16, small against medium against large, each in its best number of
+// pieces: 1024 x 1024 and 300 tokens 13, 15, 24 us; 2048 x 2048 and 300 tokens
+// 24, 16, 25; 1024 x 1024 and 8192 tokens 87, 42, 47; 2048 x 2048 and 8192
+// tokens 303, 100, 89.
+Choice choose(int64_t t256, int64_t t128, int64_t t64, int64_t rows, int parts, int64_t packed) {
   constexpr int64_t kCus = 256;
   const int64_t stages = ceil_div(rows, muon::kWgStep) * parts, blocks = ceil_div(rows, 128);
-  const double pack = packed ? 3.0 + double(packed) * 1.2e-7 : 0.0;
+  // Rounds of two workgroups per CU (the last may be of one): `fixed` each, and
+  // `two` (`one`) per step.
+  auto rounds = [](int64_t units, double fixed, double one, double two, double steps) {
+    const int64_t full = units / (2 * kCus), rest = units % (2 * kCus);
+    return fixed * double(full + (rest != 0)) + steps * (double(full) * two + (rest == 0 ? 0.0 : rest <= kCus ? one : two));
+  };
+  const double pack = packed ? 3.0 + double(packed) * 1.1e-7 : 0.0;
   Choice best{muon::kWgTile, 1, 1e300};
   const int64_t most = std::min<int64_t>(64, std::max(stages / 2, blocks));
   for (int s = 1; s <= std::max<int64_t>(1, most); ++s) {
     if (s == 1 || s <= stages / 2) {
-      double us = 2.0 + pack + double(ceil_div(t256 * s, kCus)) * (8.0 + 1.65 * double(ceil_div(stages, s)));
-      if (s > 1) us += 3.0 + 0.3 * s + 0.13 * double(t256 * s);
+      double us = 2.0 + pack + double(ceil_div(t256 * s, kCus)) * (15.0 + 1.4 * double(ceil_div(stages, s)));
+      if (s > 1) us += 4.0 + 0.14 * s + 0.058 * double(t256 * s);
       if (us < best.us) best = {muon::kWgTile, s, us};
+      us = 2.0 + pack + rounds(t128 * s, 10.0, 0.72, 1.16, double(ceil_div(stages, s)));
+      if (s > 1) us += 4.0 + 0.14 * s + 0.011 * double(t128 * s);
+      if (us < best.us) best = {muon::kWgMedium, s, us};
     }
     if (s == 1 || s <= blocks) {
-      const int64_t full = t64 * s / (2 * kCus), rest = t64 * s % (2 * kCus);
-      const double two = parts == 3 ? 3.2 : 2.2, one = parts == 3 ? 2.1 : 1.6;
-      const double per = double(full) * two + (rest == 0 ? 0.0 : rest <= kCus ? one : two);
-      double us = 2.0 * double(full + (rest != 0)) + per * double(ceil_div(blocks, s));
-      if (s > 1) us += 3.0 + 0.3 * s + 0.011 * double(t64 * s);
+      double us = rounds(t64 * s, 2.7, parts == 3 ? 2.3 : 2.0, parts == 3 ? 3.0 : 2.4, double(ceil_div(blocks, s)));
+      if (s > 1) us += 4.0 + 0.14 * s + 0.006 * double(t64 * s);
       if (us < best.us) best = {muon::kWgSmall, s, us};
     }
   }
@@ -305,16 +316,17 @@ muon_status plan_wgrad(const muon_wgrad_item* items, int n, int32_t dtype, int32
   p.args.dy_f32 = dtype == MUON_F32;
   p.args.g_f32 = g_dtype == MUON_F32;
   const int parts = dtype == MUON_F32 ? 3 : 1;
-  int64_t t256 = 0, t64 = 0, rows = 0, packed = 0;
+  int64_t t256 = 0, t128 = 0, t64 = 0, rows = 0, packed = 0;
   for (int i = 0; i < n; ++i) {
     const muon_wgrad_item& it = items[i];
     t256 += ceil_div(it.n, muon::kWgTile) * ceil_div(it.x.cols, muon::kWgTile);
+    t128 += ceil_div(it.n, muon::kWgMedium) * ceil_div(it.x.cols, muon::kWgMedium);
     t64 += ceil_div(it.n, muon::kWgSmall) * ceil_div(it.x.cols, muon::kWgSmall);
     rows = std::max(rows, it.x.rows);
     if (dtype == MUON_F32 || !dy_aligned(it, dtype)) packed += it.x.rows * it.n * (dtype == MUON_F32 ? 10 : 4);
   }
-  const Choice choice = choose(t256, t64, rows, parts, packed);
-  const bool large = choice.edge == muon::kWgTile;
+  const Choice choice = choose(t256, t128, t64, rows, parts, packed);
+  const bool large = choice.edge != muon::kWgSmall;
   p.args.edge = choice.edge;
   size_t at = 0;
   int64_t units = 0, partials = 0;

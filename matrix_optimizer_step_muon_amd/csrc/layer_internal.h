@@ -71,9 +71,9 @@ inline NormLaunch norm_backward_launch(int64_t rows, int64_t cols) {
 
 constexpr int kWgTile = 256;   // output tile edge of the large kernel
 constexpr int kWgStep = 64;    // tokens per stage of it
+constexpr int kWgMedium = 128; // output tile edge of the medium kernel
 constexpr int kWgSmall = 64;   // output tile edge of the small kernel
 constexpr int kWgItems = 16;   // matrices per launch
-constexpr int kWgPart = kWgTile * kWgTile;  // floats of one partial tile
 
 // One matrix of a launch. Units (tiles x splits) are numbered consecutively
 // over the items.

@@ -21,14 +21,27 @@
 
 namespace muon {
 
-// Stage geometry: 64 tokens of 256 bf16 columns per operand. dY has a ring of
-// three buffers, since its copies run two stages ahead; X, which waits in
-// registers, has two. Together they are all of a CU's 160 KB.
-constexpr int kRowBytes = kWgTile * 2;
-constexpr int kOpBytes = kWgStep * kRowBytes;  // 32 KB
-constexpr int kDyBufs = 3, kXBufs = 2;
-constexpr int kWaves = 8;  // 2 rows of 4: each wave owns 128 x 64 of the tile
-constexpr int kLdsBytes = (kDyBufs + kXBufs) * kOpBytes;
+// Geometry of a tile of EDGE x EDGE outputs: stages of 64 tokens, EDGE bf16
+// columns per operand. dY has a ring of three buffers, since its copies run two
+// stages ahead; X, which waits in registers, has two. 256: all of a CU's 160 KB
+// and eight waves, 2 rows of 4, each of 128 x 64 outputs. 128: half of that,
+// two workgroups of four waves per CU, each wave 64 x 64.
+template <int EDGE>
+struct Geo {
+  static constexpr int NW = EDGE / 32, NT = 64 * NW;
+  static constexpr int ROW = EDGE * 2;               // bytes of an LDS row
+  static constexpr int OP = kWgStep * ROW;           // one operand of a stage
+  static constexpr int DY_BUFS = 3, X_BUFS = 2;
+  static constexpr int LDS = (DY_BUFS + X_BUFS) * OP;
+  static constexpr int FM = EDGE / 64, NB = 2;       // 32-row blocks of dY and of X per wave
+  static constexpr int DMA = OP / 1024 / NW;         // copies of dY per wave and stage
+  static constexpr int DMA_ROWS = 1024 / ROW;        // token rows of one copy
+  static constexpr int ROW_CHUNKS = EDGE / 16;       // 16-byte checkpoint chunks of a token row
+  static constexpr int ROW_STEP = NT / ROW_CHUNKS;   // token rows between a thread's chunks
+  static constexpr int CHUNKS = kWgStep / ROW_STEP;  // chunks per thread
+  static constexpr int PER = FM * NB, SLOTS = 4 * PER, MEET = SLOTS - FM - NB;
+  static constexpr int DEC0 = EDGE == 256 ? 3 : 2, DEC = EDGE == 256 ? 3 : 1;  // decoding: first slot, spacing
+};
 
 typedef const __attribute__((address_space(4))) WgArgs* ArgsPtr;
 
@@ -147,14 +160,11 @@ struct GradOut {
 // product reaches on the GPU and the 1070 to 1080 it reaches in this layout.
 // What bounds it is power: MFMAs and their LDS reads alone run at 1650 TFLOP/s,
 // the copies and loads cost 17 to 20% and decoding 10 to 13%.
-template <int KIND>
-__global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) {
-  constexpr int NW = kWaves, NT = 64 * NW;
-  constexpr int NB = 16 / NW;                            // 32-column blocks of X per wave
-  constexpr int kDmaPerWave = kOpBytes / 1024 / NW;      // copies of dY per wave and stage
-  constexpr int kChunks = kWgStep * kWgTile / 16 / NT;   // 16-byte checkpoint chunks per thread
-  constexpr int kRowStep = NT / 16;                      // token rows between them
-  __shared__ __align__(1024) unsigned char smem[kLdsBytes];
+template <int KIND, int EDGE>
+MUON_INLINE void wgrad_tile() {
+  typedef Geo<EDGE> Z;
+  __shared__ __align__(1024) unsigned char smem[Z::LDS];
+  constexpr int NW = Z::NW, NT = Z::NT, FM = Z::FM, NB = Z::NB;
   const ArgsPtr a = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
   const int unit = xcd_unit(blockIdx.x, a->units);
   const int idx = item_of(a, unit);
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
   const int local = unit - a->unit0[idx], split = local / tiles, tile = local - split * tiles;
   int tn, tk;
   tile_of(tile, it.tiles_n, it.tiles_k, tn, tk);
-  const int n0 = tn * kWgTile, k0 = tk * kWgTile;
+  const int n0 = tn * EDGE, k0 = tk * EDGE;
   const int per_plane = (it.rows + kWgStep - 1) / kWgStep;
   const int total = per_plane * it.parts;
   // split s takes stages [total*s/splits, total*(s+1)/splits)
@@ -172,9 +182,9 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / (NW / 2), wn = wave % (NW / 2);
-  f32x16 acc[4][NB];
+  f32x16 acc[FM][NB];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
@@ -206,35 +216,37 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
     }
   };
 
-  // dY: instruction (wave, p) copies token rows 2*(kDmaPerWave*wave + p) and the next;
-  // lane l carries slot l % 32 of row l / 32, which holds chunk slot ^ swz(row).
+  // dY: instruction (wave, p) copies DMA_ROWS token rows from row DMA_ROWS*(DMA*wave
+  // + p) on; of them lane l carries slot l % (EDGE/8) of row l / (EDGE/8), which
+  // holds chunk slot ^ swz(row).
   // Chunks past the last column read the last one: columns are independent,
   // and those are never stored.
-  uint32_t dvoff[kDmaPerWave];
+  uint32_t dvoff[Z::DMA];
 #pragma unroll
-  for (int p = 0; p < kDmaPerWave; ++p) {
-    const int r = 2 * (kDmaPerWave * wave + p) + (lane >> 5);
+  for (int p = 0; p < Z::DMA; ++p) {
+    const int r = Z::DMA_ROWS * (Z::DMA * wave + p) + lane / (EDGE / 8);
     dvoff[p] = (uint32_t)min(r, rows - 1) * (uint32_t)(lda * 2) +
-               min((lane & 31) ^ lds_swizzle_k(r), (it.na - n0) / 8 - 1) * 16;
+               min((lane % (EDGE / 8)) ^ lds_swizzle_k(r), (it.na - n0) / 8 - 1) * 16;
   }
   auto dy_base = [&](const Stage& g) __attribute__((always_inline)) {
     return g.dy + min(g.t0, last_base) * lda + n0;
   };
   auto copy_dy = [&](const u16* base, uint32_t buf, int p) __attribute__((always_inline)) {
-    dma16s(base, dvoff[p], lds0 + buf + (wave * kDmaPerWave + p) * 1024);
+    dma16s(base, dvoff[p], lds0 + buf + (wave * Z::DMA + p) * 1024);
   };
-  // X: chunk c of a thread is bytes 16*(tid % 16) .. of token row kRowStep*c + tid/16.
-  const int qr = tid >> 4, qc = tid & 15;
+  // X: chunk c of a thread is bytes 16*(tid % ROW_CHUNKS) .. of token row ROW_STEP*c +
+  // tid / ROW_CHUNKS.
+  const int qr = tid / Z::ROW_CHUNKS, qc = tid % Z::ROW_CHUNKS;
   const int qcol = k0 + 16 * min(qc, (it.k - 1 - k0) / 16);  // the last chunk with a column of this matrix
-  uint32_t qvoff[kChunks], evoff[kChunks];
+  uint32_t qvoff[Z::CHUNKS], evoff[Z::CHUNKS];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const uint32_t r = (uint32_t)min(kRowStep * c + qr, rows - 1);
+  for (int c = 0; c < Z::CHUNKS; ++c) {
+    const uint32_t r = (uint32_t)min(Z::ROW_STEP * c + qr, rows - 1);
     qvoff[c] = r * (uint32_t)ldq + qcol;
     evoff[c] = r * (uint32_t)lde + qcol / kGroup;
   }
-  u32x4 qv[2][kChunks], qd[kChunks];  // two stages on their way, one being decoded
-  uint32_t ev[2][kChunks], ed[kChunks];
+  u32x4 qv[2][Z::CHUNKS], qd[Z::CHUNKS];  // two stages on their way, one being decoded
+  uint32_t ev[2][Z::CHUNKS], ed[Z::CHUNKS];
   auto load_x = [&](const Stage& g, int set, int c) __attribute__((always_inline)) {
     const int64_t t = min(g.t0, last_base);
     qv[set][c] = gload16(xq + t * ldq + qvoff[c]);
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
   };
   auto take_x = [&](int set) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
+    for (int c = 0; c < Z::CHUNKS; ++c) {
       qd[c] = qv[set][c];
       ed[c] = ev[set][c];
       asm volatile("" : "+v"(qd[c]), "+v"(ed[c]));
@@ -250,23 +262,23 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
   };
   // Bytes 4w .. 4w+3 of chunk c as bf16; w odd completes 16 bytes, which are
   // stored. Rows that are not the stage's become zeros.
-  const uint32_t xoff = qr * kRowBytes, xslot = (uint32_t)(2 * qc) ^ lds_swizzle_k(qr);
+  const uint32_t xoff = qr * Z::ROW, xslot = (uint32_t)(2 * qc) ^ lds_swizzle_k(qr);
   u32x4 half;
   auto write_x = [&](int skip, uint32_t buf, int c, int w) __attribute__((always_inline)) {
-    const int r = kRowStep * c + qr;
+    const int r = Z::ROW_STEP * c + qr;
     const u32x2 t = Q8Group<KIND>(ed[c], r >= skip && r < rows).bf16x4(qd[c][w]);
     half[2 * (w & 1)] = t[0];
     half[2 * (w & 1) + 1] = t[1];
     if (w & 1)
-      *reinterpret_cast<u32x4*>(smem + buf + xoff + kRowStep * c * kRowBytes + ((xslot ^ (w >> 1)) << 4)) = half;
+      *reinterpret_cast<u32x4*>(smem + buf + xoff + Z::ROW_STEP * c * Z::ROW + ((xslot ^ (w >> 1)) << 4)) = half;
   };
   // The same for dY, once it is in LDS.
   auto clear_dy = [&](const Stage& g, uint32_t buf) __attribute__((always_inline)) {
     const int skip = g.t0 - min(g.t0, last_base);
     if (skip == 0 && rows >= kWgStep) return;
     const u32x4 z = {0u, 0u, 0u, 0u};
-    for (int o = tid * 16; o < kOpBytes; o += NT * 16) {
-      const int r = o / kRowBytes;
+    for (int o = tid * 16; o < Z::OP; o += NT * 16) {
+      const int r = o / Z::ROW;
       if (r < skip || r >= rows) *reinterpret_cast<u32x4*>(smem + buf + o) = z;
     }
     __syncthreads();
@@ -275,21 +287,21 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
   // Fragments: lane group G = lane/16, lane i16 points at token row 8*(G/2) +
   // i16/4 (+4 for the upper half, +16 per sub-step) and four columns.
   const int G = lane >> 4, i16 = lane & 15;
-  const uint32_t frow = (8 * (G >> 1) + (i16 >> 2)) * kRowBytes;
-  uint32_t foff[2][4];
+  const uint32_t frow = (8 * (G >> 1) + (i16 >> 2)) * Z::ROW;
+  uint32_t foff[2][FM];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < FM; ++j) {  // FM >= NB
     const int col = 32 * j + 16 * (G & 1) + 4 * (i16 & 3);
-    foff[0][j] = frow + ((((wm * 128 + col) >> 3) ^ lds_swizzle_k(i16 >> 2)) << 4) + 8 * (i16 & 1);
+    foff[0][j] = frow + ((((wm * (EDGE / 2) + col) >> 3) ^ lds_swizzle_k(i16 >> 2)) << 4) + 8 * (i16 & 1);
     foff[1][j] = frow + ((((wn * NB * 32 + col) >> 3) ^ lds_swizzle_k(i16 >> 2)) << 4) + 8 * (i16 & 1);
   }
-  bf16x8 fy[2][4], fx[2][NB];
+  bf16x8 fy[2][FM], fx[2][NB];
   // Fragment f of a sub-step, in the order in which the MFMAs need them:
-  // dY block 0, the blocks of X, dY blocks 1 .. 3.
-  uint32_t fat[2][4];  // where this stage's lie
+  // dY block 0, the blocks of X, the other blocks of dY.
+  uint32_t fat[2][FM];  // where this stage's lie
   auto frags_at = [&](uint32_t dybuf, uint32_t xbuf) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < FM; ++j) {
       fat[0][j] = foff[0][j] + dybuf;
       fat[1][j] = foff[1][j] + xbuf;
     }
@@ -297,8 +309,8 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
   auto read_frag = [&](int b, int kk, int f) __attribute__((always_inline)) {
     const bool is_x = f >= 1 && f <= NB;
     const int j = is_x ? f - 1 : f == 0 ? 0 : f - NB;
-    const unsigned char* p = smem + fat[is_x][j] + kk * 16 * kRowBytes;
-    const v4i16 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * kRowBytes);
+    const unsigned char* p = smem + fat[is_x][j] + kk * 16 * Z::ROW;
+    const v4i16 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * Z::ROW);
     const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     if (is_x) fx[b][j] = v;
     else fy[b][j] = v;
@@ -308,16 +320,16 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
     const int plane = s_begin / per_plane;
     Stage g1{static_cast<const u16*>(it.dy) + (int64_t)plane * rows * lda, (s_begin - plane * per_plane) * kWgStep};
     auto skip_of = [&](const Stage& g) { return g.t0 - min(g.t0, last_base); };
-    uint32_t d0 = 0, d1 = kOpBytes, d2 = 2 * kOpBytes;  // dY of this stage, the next, the one after
-    uint32_t x0 = kDyBufs * kOpBytes, x1 = x0 + kOpBytes;
+    uint32_t d0 = 0, d1 = Z::OP, d2 = 2 * Z::OP;  // dY of this stage, the next, the one after
+    uint32_t x0 = Z::DY_BUFS * Z::OP, x1 = x0 + Z::OP;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) load_x(g1, 0, c);
+    for (int c = 0; c < Z::CHUNKS; ++c) load_x(g1, 0, c);
     const u16* base = dy_base(g1);
 #pragma unroll
-    for (int p = 0; p < kDmaPerWave; ++p) copy_dy(base, d0, p);
+    for (int p = 0; p < Z::DMA; ++p) copy_dy(base, d0, p);
     take_x(0);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+    for (int c = 0; c < Z::CHUNKS; ++c)
 #pragma unroll
       for (int w = 0; w < 4; ++w) write_x(skip_of(g1), x0, c, w);
     // g1, g2, g3: one, two and three stages ahead of the loop's. Stages past
@@ -328,20 +340,20 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
     if (s_begin + 2 < s_end) next(g2);
     Stage g3 = g2;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) load_x(g1, 0, c);
+    for (int c = 0; c < Z::CHUNKS; ++c) load_x(g1, 0, c);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) load_x(g2, 1, c);
+    for (int c = 0; c < Z::CHUNKS; ++c) load_x(g2, 1, c);
     base = dy_base(g1);
 #pragma unroll
-    for (int p = 0; p < kDmaPerWave; ++p) copy_dy(base, d1, p);
+    for (int p = 0; p < Z::DMA; ++p) copy_dy(base, d1, p);
     wait_vmcnt<0>();
     __syncthreads();
     clear_dy(first, d0);
     frags_at(d0, x0);
 #pragma unroll
-    for (int f = 0; f < 4 + NB; ++f) read_frag(0, 0, f);
+    for (int f = 0; f < FM + NB; ++f) read_frag(0, 0, f);
 
-    // One stage is kSlots MFMAs per wave. Between two of them goes a little of
+    // One stage is SLOTS MFMAs per wave. Between two of them goes a little of
     // everything else, in a fixed order: the fragments of the next sub-step,
     // the loads of X three stages ahead and the copies of dY two ahead, and
     // the decoding of the next stage's X. The last sub-step's fragments are in
@@ -353,8 +365,8 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
     // other set's as issued since and leaves as many in flight, which are the
     // copies of the stage before (it does not know of those). The wait at the
     // meeting is for these copies; since then this wave has issued its loads
-    // of X, two per chunk, and kDmaPerWave copies.
-    constexpr int kPer = 4 * NB, kSlots = 4 * kPer, kMeet = kSlots - 4 - NB;
+    // of X, two per chunk, and Z::DMA copies.
+    constexpr int kPer = Z::PER, kMeet = Z::MEET;
     auto stage = [&](auto parity, int s) __attribute__((always_inline)) {
       constexpr int P = decltype(parity)::value;
       const int skip = skip_of(g1);
@@ -367,17 +379,18 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
         for (int m = 0; m < kPer; ++m) {
           const int slot = kPer * kk + m;
           if (slot == kMeet) {
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * kChunks + kDmaPerWave) : "memory");
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * Z::CHUNKS + Z::DMA) : "memory");
             clear_dy(g1, d1);
             frags_at(d1, x1);
           }
           const int i = m / NB, j = m % NB;
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[kk & 1][j], fy[kk & 1][i], acc[i][j], 0, 0, 0);
-          if (kk < 3 && m < 4 + NB) read_frag((kk + 1) & 1, kk + 1, m);
+          if (kk < 3 && m < FM + NB) read_frag((kk + 1) & 1, kk + 1, m);
           if (slot >= kMeet) read_frag(0, 0, slot - kMeet);
-          if (slot < 2 * kChunks && m % 2 == 1) load_x(g3, P, m / 2);
-          if (slot >= 2 * kChunks && slot < 2 * (kChunks + kDmaPerWave) && m % 2 == 1) copy_dy(base2, d2, slot / 2 - kChunks);
-          if (slot >= 3 && slot < 3 + 12 * kChunks && slot % 3 == 0) write_x(skip, x1, (slot / 3 - 1) / 4, (slot / 3 - 1) % 4);
+          if (slot < 2 * Z::CHUNKS && m % 2 == 1) load_x(g3, P, m / 2);
+          if (slot >= 2 * Z::CHUNKS && slot < 2 * (Z::CHUNKS + Z::DMA) && m % 2 == 1) copy_dy(base2, d2, slot / 2 - Z::CHUNKS);
+          const int piece = (slot - Z::DEC0) / Z::DEC;
+          if (slot >= Z::DEC0 && piece < 4 * Z::CHUNKS && (slot - Z::DEC0) % Z::DEC == 0) write_x(skip, x1, piece / 4, piece % 4);
           __builtin_amdgcn_sched_barrier(0);
         }
       g1 = g2;
@@ -397,13 +410,14 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
     __syncthreads();
   }
 
-  // The tile leaves through LDS, in fp32 and in two halves (blocks 0, 1 and
-  // 2, 3 of every wave: 128 rows of 256), so that a wave stores whole rows. The 16-byte
-  // unit u of row r sits at unit u ^ (r % 64).
-  const int flane = fresh_tid() & 63;  // keeps these addresses out of the loop's registers
-  const GradOut<64, true> out(it, a, flane, k0);
+  // The tile leaves through LDS in fp32 (256: in two halves, blocks 0, 1 and 2,
+  // 3 of every wave), 128 rows at a time, so that a wave stores whole rows. The
+  // 16-byte unit u of row r sits at unit u ^ (r % 64) (128: r % 32).
+  constexpr int LW = EDGE / 4, HALVES = FM / 2, MASK = LW - 1;
+  const int ftid = fresh_tid(), flane = ftid & 63;  // keeps these addresses out of the loop's registers
+  const GradOut<LW, true> out(it, a, ftid % LW, k0);
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; half < HALVES; ++half) {
     if (half) __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -413,26 +427,43 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves / 4) wgrad_kernel(WgArgs) 
         for (int g = 0; g < 4; ++g) {
           const int r = wm * 64 + 32 * i + (flane & 31), u = wn * 8 * NB + 8 * j + 2 * g + (flane >> 5);
           const f32x16& t = acc[2 * half + i][j];
-          *reinterpret_cast<f32x4*>(smem + r * 1024 + ((u ^ (r & 63)) << 4)) =
+          *reinterpret_cast<f32x4*>(smem + r * EDGE * 4 + ((u ^ (r & MASK)) << 4)) =
               f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
         }
     __syncthreads();
 #pragma unroll 4
-    for (int q = 0; q < 128 / NW; ++q) {
-      const int r = NW * q + wave, n = (r >> 6) * 128 + half * 64 + (r & 63);
-      const unsigned char* row = smem + r * 1024;
+    for (int q = 0; q < 128 * LW / NT; ++q) {
+      const int r = q * (NT / LW) + (LW == 64 ? wave : ftid / LW), n = (r >> 6) * (EDGE / 2) + half * 64 + (r & 63);
+      const unsigned char* row = smem + r * EDGE * 4;
       float v[4];
-      out.gather(v, [&](int u) { return reinterpret_cast<const float*>(row + ((u ^ (r & 63)) << 4)); }, it.splits > 1);
-      if (it.splits > 1) Vec4<float>::store(a->partial + (int64_t)(it.part0 + local) * kWgPart + n * kWgTile + 4 * flane, v);
+      out.gather(v, [&](int u) { return reinterpret_cast<const float*>(row + ((u ^ (r & MASK)) << 4)); }, it.splits > 1);
+      if (it.splits > 1) Vec4<float>::store(a->partial + ((int64_t)(it.part0 + local) * EDGE + n) * EDGE + 4 * out.lane, v);
       else out.store(n0 + n, v);
     }
   }
 }
 
+template <int KIND>
+__global__ void __launch_bounds__(Geo<256>::NT, 2) wgrad_kernel(WgArgs) {
+  wgrad_tile<KIND, 256>();
+}
+
+// 128 x 128 tiles, two workgroups per CU: for products with too few 256 x 256
+// tiles for the CUs but long enough a sum to be bound by arithmetic, not by the
+// chain of one tile. 16 us at 300 bf16 tokens, 2048 x 2048 (160 TFLOP/s; 25
+// with 256 x 256 tiles, 24 with 64 x 64), 30 at 1000 tokens, 1024 x 5120 (350
+// TFLOP/s; 40 with either). A round of 512 takes 1.16 us per stage, the same
+// outputs in 256 x 256 tiles half of a round's 1.4: a byte of an operand moved
+// to LDS feeds half as many MFMAs, and a byte read from it two thirds.
+template <int KIND>
+__global__ void __launch_bounds__(Geo<128>::NT, 2) wgrad_medium_kernel(WgArgs) {
+  wgrad_tile<KIND, 128>();
+}
+
 // ------------------------------------------------------------ small tiles
 //
 // 64 x 64 output tiles for products that would leave most CUs without a
-// 256 x 256 one: a call of a few small matrices is over in the time of its
+// larger one: a call of a few small matrices is over in the time of its
 // memory round trips, and what counts is how many of these it takes. Each of
 // the four waves sums every fourth block of 32 tokens for the whole tile, on
 // its own: it stages both operands in an LDS region that only it uses, with
@@ -690,8 +721,11 @@ static hipError_t launch_reduce(const WgArgs& args, hipStream_t s) {
 hipError_t launch_wgrad(const WgArgs& args, int kind, hipStream_t s) {
   const dim3 grid(args.units);
   if (args.edge == kWgTile) {
-    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_INT8>, grid, dim3(64 * kWaves), 0, s, args);
-    else hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_E4M3>, grid, dim3(64 * kWaves), 0, s, args);
+    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_INT8>, grid, dim3(Geo<256>::NT), 0, s, args);
+    else hipLaunchKernelGGL(wgrad_kernel<MUON_Q8_E4M3>, grid, dim3(Geo<256>::NT), 0, s, args);
+  } else if (args.edge == kWgMedium) {
+    if (kind == MUON_Q8_INT8) hipLaunchKernelGGL(wgrad_medium_kernel<MUON_Q8_INT8>, grid, dim3(Geo<128>::NT), 0, s, args);
+    else hipLaunchKernelGGL(wgrad_medium_kernel<MUON_Q8_E4M3>, grid, dim3(Geo<128>::NT), 0, s, args);
   } else if (args.dy_f32) {
     if (kind == MUON_Q8_INT8) hipLaunchKernelGGL((wgrad_small_kernel<MUON_Q8_INT8, float>), grid, dim3(256), 0, s, args);
     else hipLaunchKernelGGL((wgrad_small_kernel<MUON_Q8_E4M3, float>), grid, dim3(256), 0, s, args);
@@ -701,7 +735,8 @@ hipError_t launch_wgrad(const WgArgs& args, int kind, hipStream_t s) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return args.edge == kWgTile ? launch_reduce<kWgTile>(args, s) : launch_reduce<kWgSmall>(args, s);
+  return args.edge == kWgTile ? launch_reduce<kWgTile>(args, s)
+         : args.edge == kWgMedium ? launch_reduce<kWgMedium>(args, s) : launch_reduce<kWgSmall>(args, s);
 }
 
 // dY in other layouts than the large kernel's (fp32, unaligned rows, a width

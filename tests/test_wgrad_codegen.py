@@ -1,4 +1,4 @@
-"""The generated gfx950 code of the large weight-gradient kernel.
+"""The generated gfx950 code of the weight-gradient kernels of large tiles.
 
 Its loop waits for copies into LDS that the compiler does not know of, by
 counting the memory instructions issued since: the wait lets 2 loads per chunk
@@ -67,3 +67,43 @@ def test_the_wait_never_allows_more_than_was_issued_since(kernels, kind):
 @pytest.mark.parametrize("kind", [0, 1])
 def test_no_spills(kernels, kind):
     assert not [l for l in kernels[kind] if l.startswith("scratch_")]
+
+
+# The kernel of 128 x 128 tiles is the same loop with 16 MFMAs a stage.
+@pytest.fixture(scope="module")
+def medium(tmp_path_factory):
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    out = tmp_path_factory.mktemp("asm") / "wgrad.s"
+    cmd = [HIPCC, "-O3", "-std=c++17", "--offload-arch=gfx950", "--cuda-device-only", "-S",
+           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+           f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}", os.path.join(CSRC, "wgrad_kernels.hip"), "-o", str(out)]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    lines = out.read_text().split("\n")
+    found = {}
+    for i, l in enumerate(lines):
+        m = re.match(r"^(_ZN4muon\d+wgrad_medium_kernelILi(\d)EEEv\S*):", l)
+        if m:
+            end = next(j for j in range(i, len(lines)) if "s_endpgm" in lines[j])
+            found[int(m.group(2))] = [x.strip() for x in lines[i:end]]
+    assert sorted(found) == [0, 1], "one kernel for each element type"
+    return found
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_medium_tiles_wait_and_keep_their_registers(medium, kind):
+    body = medium[kind]
+    assert not [l for l in body if l.startswith("scratch_")]
+    waits = [i for i, l in enumerate(body) if re.match(r"s_waitcnt vmcnt\(\d+\) lgkmcnt\(0\)", l) and "s_barrier" in "".join(body[i:i + 2])]
+    assert len(waits) == 3, "two stages in the loop and an odd last one"
+    for i in waits[:2]:
+        allowed = int(re.search(r"vmcnt\((\d+)\)", body[i]).group(1))
+        # back to this stage's first MFMA: 12 of them go before the meeting
+        issued = mfma = 0
+        for l in reversed(body[:i]):
+            mfma += l.startswith("v_mfma")
+            if mfma > 12:
+                break
+            issued += bool(VMEM.match(l))
+        assert issued >= allowed, (issued, allowed)

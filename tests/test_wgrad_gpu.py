@@ -101,6 +101,31 @@ def test_large_tiles(rows, n, k, dtype, gdtype, kind, ld, offset):
              offset=offset))
 
 
+# Between them, outputs of some hundreds of 128 x 128 tiles and shorter sums take
+# the kernel of that tile, in one piece or a few.
+MEDIUM = [  # rows, n, k, dtype, gdtype, kind, ld, offset
+    (300, 2048, 2048, "bf16", "bf16", "int8", None, 0), (257, 1001, 5003, "bf16", "f32", "e4m3", None, 0),
+    (1000, 1024, 5120, "bf16", "bf16", "e4m3", 1040, 8), (1001, 2000, 2050, "bf16", "f32", "int8", 2003, 1),
+    (65, 2560, 2500, "f32", "bf16", "int8", None, 0), (300, 2040, 2100, "f32", "f32", "e4m3", None, 0),
+    (2700, 1024, 1030, "bf16", "f32", "int8", None, 0), (4097, 259, 5341, "bf16", "bf16", "int8", None, 0),
+    (4095, 260, 5300, "f32", "f32", "e4m3", None, 0),
+]
+
+
+@pytest.mark.parametrize("rows,n,k,dtype,gdtype,kind,ld,offset", MEDIUM)
+def test_medium_tiles(rows, n, k, dtype, gdtype, kind, ld, offset):
+    say("case", rows, n, k, dtype, gdtype, kind, ld, offset)
+    run(Item(rows, n, k, dtype, gdtype, kind, scale=k % 2 == 0, beta=0.25 if n % 2 else 1.0, own_c=n % 2 == 1, seed=rows, ld=ld,
+             offset=offset))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_medium_tiles_among_others(dtype):
+    sizes = [(300, 2048, 1500), (0, 40, 50), (130, 700, 900), (64, 1030, 2100), (1, 129, 127)]
+    run(*[Item(r, n, k, dtype, "bf16", "int8", scale=i % 2 == 0, beta=float(i % 2), seed=30 + i)
+          for i, (r, n, k) in enumerate(sizes)])
+
+
 @pytest.mark.parametrize("gdtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", [0, 1, 100, 900])
 def test_accumulation_into_g(rows, gdtype):
