@@ -156,7 +156,7 @@ struct GradOut {
 // copies and address arithmetic take nearly as many issue slots as one wave has
 // beside its MFMAs: 1902 us against 2006 with four waves of 128 x 128 (25600 x
 // 5120 outputs, 8192 tokens). With the loads further ahead that product takes
-// 1757 to 1802 us, 1190 to 1222 TFLOP/s, of the 1380 that a large library
+// 1757 to 1849 us, 1161 to 1222 TFLOP/s, of the 1380 that a large library
 // product reaches on the GPU and the 1070 to 1080 it reaches in this layout.
 // What bounds it is power: MFMAs and their LDS reads alone run at 1650 TFLOP/s,
 // the copies and loads cost 17 to 20% and decoding 10 to 13%.
