@@ -80,8 +80,12 @@ MUON_INLINE void q8_decode(u32x2 w, uint32_t E, int kind, float v[8]) {
 // int8: bytes with the sign bit flipped are put behind 0x64, which makes the
 // fp16 numbers 1024 + 128 + q; times the unit minus 1152 units is the value
 // (one mixed-precision fma per element, two instructions per element in all).
+// From E = kQ8WideExp on, 1152 units are past the largest fp32 number: there the
+// caller takes q8_bf16x4_wide instead, or its results in place of these.
 // e4m3: the converting instruction scales by the unit itself (three
 // instructions per four elements); q is replaced by NaN codes for E = 255.
+constexpr uint32_t kQ8WideExp = 245;
+
 template <int KIND>
 struct Q8Group {
   float unit, bias;
@@ -114,5 +118,13 @@ struct Q8Group {
     return o;
   }
 };
+
+// The same of int8 bytes for every exponent byte (255: NaN), an instruction more
+// per element.
+MUON_INLINE u32x2 q8_bf16x4_wide(uint32_t w, uint32_t E, bool live) {
+  float v[4];
+  q8_decode4(w, live ? q8_unit(E) : 0.f, MUON_Q8_INT8, v);
+  return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
 
 }  // namespace muon

@@ -272,7 +272,23 @@ MUON_INLINE void wgrad_tile() {
     if (w & 1)
       *reinterpret_cast<u32x4*>(smem + buf + xoff + Z::ROW_STEP * c * Z::ROW + ((xslot ^ (w >> 1)) << 4)) = half;
   };
-  // The same for dY, once it is in LDS.
+  // A chunk whose exponent write_x cannot take is written once more. Rare, so the
+  // test is all it costs, two instructions a chunk.
+  auto rewrite_wide_x = [&](int skip, uint32_t buf, int c) __attribute__((always_inline)) {
+    if constexpr (KIND == MUON_Q8_INT8) {
+      if (__builtin_expect(ed[c] >= kQ8WideExp, 0)) {
+        const int r = Z::ROW_STEP * c + qr;
+        const bool live = r >= skip && r < rows;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x2 lo = q8_bf16x4_wide(qd[c][2 * h], ed[c], live), hi = q8_bf16x4_wide(qd[c][2 * h + 1], ed[c], live);
+          *reinterpret_cast<u32x4*>(smem + buf + xoff + Z::ROW_STEP * c * Z::ROW + ((xslot ^ h) << 4)) =
+              u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+      }
+    }
+  };
+  // Rows of dY that are not the stage's become zeros once they are in LDS.
   auto clear_dy = [&](const Stage& g, uint32_t buf) __attribute__((always_inline)) {
     const int skip = g.t0 - min(g.t0, last_base);
     if (skip == 0 && rows >= kWgStep) return;
@@ -329,9 +345,11 @@ MUON_INLINE void wgrad_tile() {
     for (int p = 0; p < Z::DMA; ++p) copy_dy(base, d0, p);
     take_x(0);
 #pragma unroll
-    for (int c = 0; c < Z::CHUNKS; ++c)
+    for (int c = 0; c < Z::CHUNKS; ++c) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) write_x(skip_of(g1), x0, c, w);
+      rewrite_wide_x(skip_of(g1), x0, c);
+    }
     // g1, g2, g3: one, two and three stages ahead of the loop's. Stages past
     // the last one are the last one again, and nothing of them is used.
     const Stage first = g1;
@@ -390,7 +408,10 @@ MUON_INLINE void wgrad_tile() {
           if (slot < 2 * Z::CHUNKS && m % 2 == 1) load_x(g3, P, m / 2);
           if (slot >= 2 * Z::CHUNKS && slot < 2 * (Z::CHUNKS + Z::DMA) && m % 2 == 1) copy_dy(base2, d2, slot / 2 - Z::CHUNKS);
           const int piece = (slot - Z::DEC0) / Z::DEC;
-          if (slot >= Z::DEC0 && piece < 4 * Z::CHUNKS && (slot - Z::DEC0) % Z::DEC == 0) write_x(skip, x1, piece / 4, piece % 4);
+          if (slot >= Z::DEC0 && piece < 4 * Z::CHUNKS && (slot - Z::DEC0) % Z::DEC == 0) {
+            write_x(skip, x1, piece / 4, piece % 4);
+            if (piece % 4 == 3) rewrite_wide_x(skip, x1, piece / 4);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       g1 = g2;
@@ -589,10 +610,15 @@ __global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int r = 16 * c + xr;
-      const Q8Group<KIND> grp(ev[c], 32 * b + r < rows);
+      const bool live_x = 32 * b + r < rows;
+      const Q8Group<KIND> grp(ev[c], live_x);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const u32x2 lo = grp.bf16x4(xv[c][2 * h]), hi = grp.bf16x4(xv[c][2 * h + 1]);
+        u32x2 lo = grp.bf16x4(xv[c][2 * h]), hi = grp.bf16x4(xv[c][2 * h + 1]);
+        if (KIND == MUON_Q8_INT8 && __builtin_expect(ev[c] >= kQ8WideExp, 0)) {
+          lo = q8_bf16x4_wide(xv[c][2 * h], ev[c], live_x);
+          hi = q8_bf16x4_wide(xv[c][2 * h + 1], ev[c], live_x);
+        }
         *reinterpret_cast<u32x4*>(sx + r * kSmRow + (small_slot(2 * (lane & 3) + h, r) << 4)) = u32x4{lo[0], lo[1], hi[0], hi[1]};
       }
     }
