@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, in
       if (per_row) widen<T, VEC>(gt[p], c0[p], cols, g[p]);
     }
     if (VPT == 1 && row + step < s.rows) load(row + step);
-    if (post) {
+    if (post || s.rstd_b) {  // without a norm after the block it is only kept
 #pragma unroll
       for (int p = 0; p < VPT; ++p)
 #pragma unroll
@@ -294,10 +294,12 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, in
       block_sum(sum, red[0]);
       const float rb = 1.f / sqrtf(sum[0] * inv_cols + s.eps);
       if (threadIdx.x == 0 && s.rstd_b) *((g_f32*)(s.rstd_b + row)) = rb;
+      if (post) {
 #pragma unroll
-      for (int p = 0; p < VPT; ++p)
+        for (int p = 0; p < VPT; ++p)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] *= rb;
+          for (int i = 0; i < 8; ++i) v[p][i] *= rb;
+      }
     }
     sum[0] = 0.f;
 #pragma unroll
