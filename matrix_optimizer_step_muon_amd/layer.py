@@ -169,6 +169,8 @@ class NormSite:
         if gate is not None:
             vector = gate.dim() == 1
             _matrix(gate, "gate", (cols,) if vector else (rows, cols), dt, vector=vector)
+            if not vector and _ld(gate) < cols:  # 0 would tell muon_norm_site that all rows share one gate
+                _bad("gate's rows overlap; a gate that all rows share is 1-D")
         self.branch, self.residual, self.w_pre, self.w_post, self.gate = branch, residual, w_pre, w_post, gate
         self.y, self.h = torch.empty_like(branch, memory_format=torch.contiguous_format), \
             torch.empty_like(branch, memory_format=torch.contiguous_format)
