@@ -135,6 +135,17 @@ MUON_INLINE v4i16 lds_read_tr(const unsigned char* p) {
       (__attribute__((address_space(3))) v4i16*)(const_cast<unsigned char*>(p)));
 }
 
+// Between lanes of one wave that hand each other data through LDS: what is
+// written before is there for every lane's reads after it, and what is read
+// before is not overwritten. The hardware keeps a wave's LDS accesses in order,
+// so this is no instruction; it holds the compiler, which sees one lane's
+// addresses only and may reorder those that differ.
+MUON_INLINE void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Direct global -> LDS copy of 16 bytes per lane, addressed as a uniform
 // 64-bit base plus a per-lane 32-bit byte offset (the saddr form of
 // global_load_lds_dwordx4). Same M0 handling as dma16.

@@ -644,6 +644,7 @@ __global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
   if (b < b_end) load(b);
   for (; b < b_end; b += 4) {
     stage(b);
+    wave_lds_order();
     if (b + 4 < b_end) load(b + 4);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
@@ -657,6 +658,7 @@ __global__ void __launch_bounds__(256, 2) wgrad_small_kernel(WgArgs) {
           acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x1, y, acc[i][1], 0, 0, 0);
         }
     }
+    wave_lds_order();
   }
 
   // Every wave's sums, 16 KB each (16-byte unit u of row r at u ^ (r % 16)),
