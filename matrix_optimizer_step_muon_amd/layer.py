@@ -81,7 +81,10 @@ def _stream(stream, tensors: Sequence):
 
 
 def _stream_object(stream):
-    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    # torch makes a stream of its own out of the handle 0, which is the default stream's
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
 
 
 def _ptr(t) -> Optional[int]:
