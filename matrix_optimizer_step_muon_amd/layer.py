@@ -10,9 +10,11 @@ optimizer step reads.
 
 Like the optimizer's plans, ``NormSite`` and ``WGrad`` take their tensors once
 and keep them referenced; every call after that only launches kernels, on the
-current stream or the one it is given. Tensors are 2-D (weights 1-D) device
-tensors with unit column stride, on the current device. There is no CPU
-fallback.
+current stream or the one it is given (a torch stream or a raw handle). They may
+be dropped while a stream still works on their buffers. Each has one set of
+buffers: calls on two streams need an order between them, as any two writers of
+a tensor do. Tensors are 2-D (weights 1-D) device tensors with unit column
+stride, on the current device. There is no CPU fallback.
 """
 
 from __future__ import annotations
@@ -68,16 +70,39 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
-def _stream(stream, tensors: Sequence):
-    """The stream's handle. Memory that another stream uses than the current
-    one is kept from reuse until that stream is done with it."""
-    if stream is None:  # the handle alone: making a Stream object takes 3 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    stream = _stream_object(stream)
-    if stream != torch.cuda.current_stream():
+class _Streams:
+    """The streams that use a set of tensors. Memory is kept from reuse until
+    every stream that ever used it is done with it; that takes one record per
+    tensor and stream, made when a stream comes up first."""
+
+    def __init__(self, tensors: Iterable = ()):
+        self.tensors: List = list(tensors)
+        self._seen = set()
+
+    def add(self, tensors: Iterable) -> None:
+        self.tensors += tensors
+        self._seen.clear()
+
+    def use(self, stream, call: Sequence = ()) -> int:
+        """The handle of the stream to launch on (None: the current one). Tensors
+        of this call alone are recorded if the call names a stream that is not
+        the current one: with the current one they are the caller's to keep, as
+        with any torch operation."""
+        # the handle alone: making a Stream object takes 3 us
+        now = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        handle = now if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle not in self._seen:
+            self._record(stream, self.tensors)
+            self._seen.add(handle)
+        if handle != now:
+            self._record(stream, call)
+        return handle
+
+    @staticmethod
+    def _record(stream, tensors) -> None:
+        stream = torch.cuda.current_stream() if stream is None else _stream_object(stream)
         for t in tensors:
-            t.record_stream(stream)
-    return stream.cuda_stream
+            t.record_stream(stream)  # nothing to do on the stream that the memory was made on
 
 
 def _stream_object(stream):
@@ -115,6 +140,7 @@ class Q8:
         if q.shape[1] < -(-cols // 16) * 16 or e.shape[1] < -(-cols // GROUP):
             _bad("q needs cols rounded up to a multiple of 16, e one byte per 32 columns")
         self.q, self.e = q, e
+        self._streams = _Streams((q, e))
         ldq = _ld(q) if rows > 1 else -(-q.shape[1] // 16) * 16
         self._c = muon_q8(q.data_ptr(), e.data_ptr(), rows, cols, ldq, _ld(e), code, 0)
 
@@ -126,7 +152,7 @@ def q8_save(x, out: Q8, stream=None) -> Q8:
     """Saves x (bf16 or fp32) into the checkpoint ``out``."""
     _matrix(x, "x", (out.rows, out.cols))
     check(lib().muon_q8_save(x.data_ptr(), _ld(x), _code(x), ctypes.byref(out._c),
-                             _stream(stream, (x, out.q, out.e))))
+                             out._streams.use(stream, (x,))))
     return out
 
 
@@ -135,7 +161,7 @@ def q8_load(ckpt: Q8, out, stream=None):
     holds them exactly, or fp32)."""
     _matrix(out, "out", (ckpt.rows, ckpt.cols))
     check(lib().muon_q8_load(ctypes.byref(ckpt._c), out.data_ptr(), _ld(out), _code(out),
-                             _stream(stream, (out, ckpt.q, ckpt.e))))
+                             ckpt._streams.use(stream, (out,))))
     return out
 
 
@@ -199,11 +225,11 @@ class NormSite:
             self.y.data_ptr(), cols, self.h.data_ptr(), cols, _ptr(self.rstd_y), _ptr(self.rstd_b),
             self.u._c if self.u is not None else none, self.v._c if self.v is not None else none,
             res_scale, branch_scale, eps, code)
-        self._tensors = [t for t in (branch, residual, w_pre, w_post, gate, self.y, self.h, self.rstd_y, self.rstd_b)
-                         if t is not None] + [t for q in (self.u, self.v) if q is not None for t in (q.q, q.e)]
+        self._streams = _Streams([t for t in (branch, residual, w_pre, w_post, gate, self.y, self.h, self.rstd_y, self.rstd_b)
+                                  if t is not None] + [t for q in (self.u, self.v) if q is not None for t in (q.q, q.e)])
 
     def forward(self, stream=None) -> None:
-        check(lib().muon_norm_forward(ctypes.byref(self._c), _stream(stream, self._tensors)))
+        check(lib().muon_norm_forward(ctypes.byref(self._c), self._streams.use(stream)))
 
     def backward(self, dy, dh, stream=None) -> None:
         shape, dt = tuple(self.y.shape), self.y.dtype
@@ -218,8 +244,8 @@ class NormSite:
                 self._make_grads()
         g = self._grads
         g.dy, g.ld_dy, g.dh, g.ld_dh = _ptr(dy), 0 if dy is None else _ld(dy), dh.data_ptr(), _ld(dh)
-        used = self._tensors if stream is None else self._tensors + [t for t in (dy, dh) if t is not None]
-        check(lib().muon_norm_backward(ctypes.byref(self._c), ctypes.byref(g), _stream(stream, used)))
+        handle = self._streams.use(stream, (dh,) if dy is None else (dy, dh))
+        check(lib().muon_norm_backward(ctypes.byref(self._c), ctypes.byref(g), handle))
 
     def _make_grads(self) -> None:
         shape, dt = tuple(self.y.shape), self.y.dtype
@@ -232,8 +258,8 @@ class NormSite:
         self._grads = muon_norm_grads(
             None, 0, None, 0, self.d_residual.data_ptr(), shape[1], self.d_branch.data_ptr(), shape[1],
             _ptr(self.d_w_pre), _ptr(self.d_w_post), _ptr(self.d_gate), shape[1], self._workspace.data_ptr(), need.value)
-        self._tensors += [t for t in (self.d_residual, self.d_branch, self.d_w_pre, self.d_w_post, self.d_gate,
-                                      self._workspace) if t is not None]
+        self._streams.add([t for t in (self.d_residual, self.d_branch, self.d_w_pre, self.d_w_post, self.d_gate,
+                                       self._workspace) if t is not None])
 
 
 class WGrad:
@@ -248,7 +274,7 @@ class WGrad:
     type, C like G (default: G itself, to accumulate)."""
 
     def __init__(self, items: Iterable[Sequence]):
-        self._tensors: List = []
+        tensors: List = []
         descs = []
         self._dtype = self._gdtype = None
         dts = None
@@ -275,16 +301,16 @@ class WGrad:
                     _bad("C must be contiguous")
             descs.append(muon_wgrad_item(dY.data_ptr(), _ld(dY), x._c, _ptr(scale), G.data_ptr(), C.data_ptr(), n,
                                          float(beta), 0))
-            self._tensors += [t for t in (dY, x.q, x.e, G, C, scale) if t is not None]
+            tensors += [t for t in (dY, x.q, x.e, G, C, scale) if t is not None]
         if not descs:
             _bad("no items")
         self._n = len(descs)
         self._items = (muon_wgrad_item * self._n)(*descs)
         need = ctypes.c_size_t()
         check(lib().muon_wgrad_workspace(self._items, self._n, self._dtype, self._gdtype, ctypes.byref(need)))
-        self.workspace = torch.empty(need.value, dtype=torch.uint8, device=self._tensors[0].device)
-        self._tensors.append(self.workspace)
+        self.workspace = torch.empty(need.value, dtype=torch.uint8, device=tensors[0].device)
+        self._streams = _Streams(tensors + [self.workspace])
 
     def run(self, stream=None) -> None:
         check(lib().muon_wgrad(self._items, self._n, self._dtype, self._gdtype, self.workspace.data_ptr(),
-                               self.workspace.numel(), _stream(stream, self._tensors)))
+                               self.workspace.numel(), self._streams.use(stream)))
