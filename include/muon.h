@@ -498,6 +498,13 @@ muon_status muon_wgrad(const muon_wgrad_item* items, int32_t n_items, int32_t dt
 muon_status muon_wgrad_workspace(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype,
                                  size_t* bytes);
 
+/* How muon_wgrad runs these items, without a GPU: item i in output tiles of
+ * tile[i] x tile[i] (256, 128 or 64, of its launch of 16 items), its sum over
+ * rows in pieces[i] pieces that a second launch adds. Same checks and errors as
+ * muon_wgrad_workspace. */
+muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype,
+                            int32_t* tile, int32_t* pieces);
+
 #ifdef __cplusplus
 }
 #endif

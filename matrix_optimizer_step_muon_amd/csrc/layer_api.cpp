@@ -406,6 +406,15 @@ muon_status plan_all(const muon_wgrad_item* items, int32_t n, int32_t dtype, int
   return MUON_OK;
 }
 
+// The same for items that are checked first, without a workspace.
+muon_status checked_plans(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_t g_dtype,
+                          std::vector<WgradPlan>& plans, size_t* bytes) {
+  Views v;
+  MUON_TRY(check_wgrad(items, n, dtype, g_dtype, v));
+  MUON_TRY(v.disjoint());
+  return plan_all(items, n, dtype, g_dtype, plans, bytes);
+}
+
 muon_status wgrad(const muon_wgrad_item* items, int32_t n, int32_t dtype, int32_t g_dtype, void* ws, size_t ws_bytes,
                   void* stream) {
   Views v;
@@ -478,11 +487,24 @@ muon_status muon_wgrad_workspace(const muon_wgrad_item* items, int32_t n_items, 
                                  size_t* bytes) {
   return guarded([&]() -> muon_status {
     if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
-    Views v;
-    MUON_TRY(check_wgrad(items, n_items, dtype, g_dtype, v));
-    MUON_TRY(v.disjoint());
     std::vector<WgradPlan> plans;
-    return plan_all(items, n_items, dtype, g_dtype, plans, bytes);
+    return checked_plans(items, n_items, dtype, g_dtype, plans, bytes);
+  });
+}
+
+muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32_t dtype, int32_t g_dtype,
+                            int32_t* tile, int32_t* pieces) {
+  return guarded([&]() -> muon_status {
+    if (!tile || !pieces) return fail(MUON_ERR_INVALID_ARG, "tile or pieces is NULL");
+    std::vector<WgradPlan> plans;
+    size_t bytes;
+    MUON_TRY(checked_plans(items, n_items, dtype, g_dtype, plans, &bytes));
+    for (int32_t i = 0; i < n_items; ++i) {
+      const muon::WgArgs& a = plans[i / muon::kWgItems].args;
+      tile[i] = a.edge;
+      pieces[i] = a.item[i % muon::kWgItems].splits;
+    }
+    return MUON_OK;
   });
 }
 

@@ -314,3 +314,9 @@ class WGrad:
     def run(self, stream=None) -> None:
         check(lib().muon_wgrad(self._items, self._n, self._dtype, self._gdtype, self.workspace.data_ptr(),
                                self.workspace.numel(), self._streams.use(stream)))
+
+    def info(self) -> List[dict]:
+        """Per item: the edge of its output tiles, and the pieces of its sum over rows."""
+        tile, pieces = (ctypes.c_int32 * self._n)(), (ctypes.c_int32 * self._n)()
+        check(lib().muon_wgrad_info(self._items, self._n, self._dtype, self._gdtype, tile, pieces))
+        return [{"tile": t, "pieces": p} for t, p in zip(tile, pieces)]

@@ -87,7 +87,7 @@ EXPORTS = ("muon_hparams_default", "muon_plan", "muon_plan_workspace_bytes", "mu
            "muon_dp_partition_static", "muon_dp_partition", "muon_tp_micro_groups", "muon_mfma_probe",
            "muon_step_noalloc",
            "muon_q8_save", "muon_q8_load", "muon_norm_forward", "muon_norm_backward",
-           "muon_norm_backward_workspace", "muon_wgrad", "muon_wgrad_workspace")
+           "muon_norm_backward_workspace", "muon_wgrad", "muon_wgrad_workspace", "muon_wgrad_info")
 
 
 def lib() -> ctypes.CDLL:
@@ -131,6 +131,8 @@ def lib() -> ctypes.CDLL:
     L.muon_wgrad.argtypes = [ctypes.POINTER(muon_wgrad_item), c_i32, c_i32, c_i32, c_vp, ctypes.c_size_t, c_vp]
     L.muon_wgrad_workspace.argtypes = [ctypes.POINTER(muon_wgrad_item), c_i32, c_i32, c_i32,
                                        ctypes.POINTER(ctypes.c_size_t)]
+    L.muon_wgrad_info.argtypes = [ctypes.POINTER(muon_wgrad_item), c_i32, c_i32, c_i32, ctypes.POINTER(c_i32),
+                                  ctypes.POINTER(c_i32)]
     for name in EXPORTS:
         if name != "muon_last_error":
             getattr(L, name).restype = c_int
