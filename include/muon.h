@@ -326,23 +326,29 @@ muon_status muon_tp_micro_groups(const double* cost, int32_t n, int32_t ranks, d
  * call, only launches kernels on `stream` (no allocation, copy, memset or host
  * synchronisation), and may be captured in a HIP graph. Results are bitwise
  * deterministic. Arguments are validated before any HIP call. rows may be 0
- * (weight gradients are then 0, or beta*C); views without rows may be NULL. Device pointers named below
- * address row-major views, rows x cols with a row stride in elements (ld*, at
- * least cols, at most 2^24); any alignment to the element size and any stride
- * is right, and views with 16-byte aligned rows and cols a multiple of 8 take
- * the fast path. Written views must not overlap any other view of the call
- * (ALIAS); views that are only read may share elements.
+ * (weight gradients are then 0, or beta*C); views without rows may be NULL.
+ * Device pointers named below address row-major views, rows x cols with a row
+ * stride in elements (ld*, at least cols, at most 2^24); any alignment to the
+ * element size and any stride is right, and views with 16-byte aligned rows and
+ * cols a multiple of 8 take the fast path. Written views must not overlap any
+ * other view of the call (ALIAS; column blocks of one buffer may lie side by
+ * side, but views of different row strides in bytes must not reach into each
+ * other's address range); views that are only read may share elements.
  *
  * 8-bit checkpoints. A row of cols elements is cut into groups of 32 columns
  * (the last may be shorter). A group has one exponent byte E; an element is
  * one byte q and stands for q * 2^(E-127), q being an int8 in [-127, 127]
  * (MUON_Q8_INT8) or an e4m3 number of at most 448 (MUON_Q8_E4M3).
- * Saving chooses the smallest E in [17, 254] with max|x| <= 127 * 2^(E-127)
- * (int8; 448 for e4m3) over the group, so nothing saturates, and rounds
- * x / 2^(E-127) to nearest, ties to even. A group holding an infinity or a NaN
- * gets E = 255 and q = 0 and stands for NaNs, so that a bad activation shows up
- * in the gradients. Every value a checkpoint stands for is exactly a bf16
- * number. int8 is the more accurate of the two for activations whose groups
+ * Saving chooses the smallest E >= 17 with max|x| <= 127 * 2^(E-127) (int8; 448
+ * for e4m3) over the group, so nothing saturates, and rounds x / 2^(E-127) to
+ * nearest, ties to even. A group holding an infinity or a NaN gets E = 255 and
+ * q = 0 and stands for NaNs, so that a bad activation shows up in the gradients.
+ * Every finite value that a saved checkpoint stands for is exactly a bf16 number.
+ * At the end of fp32's range some are not finite: int8 elements of at least
+ * 1.984375 * 2^127 in a group whose largest is above that, and e4m3 elements of
+ * at least 1.9375 * 2^127, round to 2^128, an infinity, as the largest fp32
+ * numbers do in bf16. E of 0 to 16 is not written and not meant to be read.
+ * int8 is the more accurate of the two for activations whose groups
  * are near Gaussian (0.7% against 2.6% relative error), e4m3 where elements of
  * a group differ by more than two orders of magnitude.
  *
@@ -387,7 +393,7 @@ muon_status muon_q8_load(const muon_q8* in, void* x, int64_t ldx, int32_t dtype,
  *                   rows), or rows x cols with row stride ld_gate >= cols
  * y, h              rows x cols, written
  * rstd_y, rstd_b    rows floats, 1/rms(y) and 1/rms(branch), written if not
- *                   NULL; a backward pass needs rstd_y, and rstd_b with w_post
+ *                   NULL, with or without w_post; a backward pass needs rstd_y, and rstd_b with w_post
  * u, v              8-bit checkpoints, written if their q is not NULL; a
  *                   backward pass needs u, and v with w_post or gate
  * cols is at most 32768 (a row stays in one workgroup's registers). */
@@ -471,7 +477,10 @@ muon_status muon_norm_backward_workspace(int64_t rows, int64_t cols, size_t* byt
  *        be g itself (accumulation over micro batches)
  * bf16 dY: bf16 MFMA with fp32 accumulation; the products are exact, since
  * checkpoint values are bf16 numbers. fp32 dY is cut into three bf16 numbers
- * that add up to it (24 bits), for fp32 accuracy on the bf16 matrix cores.
+ * that add up to it (24 bits; of numbers below 2^-110 the bits down to 2^-133,
+ * the smallest bf16 number), for fp32 accuracy on the bf16 matrix cores. Where x
+ * stands for an infinity, its column of G is infinite or NaN, with fp32 dY NaN
+ * in general (some of the three numbers are 0).
  * g is rounded to g_dtype once. */
 typedef struct {
   const void* dy;

@@ -498,7 +498,8 @@ constexpr int kSmRow = kWgSmall * 2;     // bytes of an LDS row: 64 bf16 of one 
 constexpr int kSmOp = 32 * kSmRow;       // one operand of 32 tokens: 4 KB
 
 // x = hi + mid + lo, each the rest rounded toward zero to bf16: 8 bits each,
-// all 24 of a normal fp32 number, and never past the largest finite value.
+// all 24 of an fp32 number of at least 2^-110 (of smaller ones the bits down to
+// 2^-133), and never past the largest finite value.
 // Infinities and NaNs stay in hi alone. Returned as fp32 bit patterns whose
 // low halves are zero.
 MUON_INLINE void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
