@@ -70,33 +70,38 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
+def _current_handle() -> int:
+    """The current stream's handle: making a Stream object of it takes 3 us."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 class _Streams:
-    """The streams that use a set of tensors. Memory is kept from reuse until
-    every stream that ever used it is done with it; that takes one record per
-    tensor and stream, made when a stream comes up first."""
+    """The streams that use a set of tensors, made on or ready for the stream
+    that is current now. The tensors' memory is kept from reuse until every other
+    stream that ever used it is done with it; that takes one record per tensor
+    and stream, made when a stream comes up first."""
 
-    def __init__(self, tensors: Iterable = ()):
-        self.tensors: List = list(tensors)
-        self._seen = set()
-
-    def add(self, tensors: Iterable) -> None:
-        self.tensors += tensors
-        self._seen.clear()
+    def __init__(self, tensors: Iterable):
+        self._tensors = tuple(tensors)
+        self._seen = {_current_handle()}
 
     def use(self, stream, call: Sequence = ()) -> int:
         """The handle of the stream to launch on (None: the current one). Tensors
         of this call alone are recorded if the call names a stream that is not
         the current one: with the current one they are the caller's to keep, as
         with any torch operation."""
-        # the handle alone: making a Stream object takes 3 us
-        now = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        now = _current_handle()
         handle = now if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if handle not in self._seen:
-            self._record(stream, self.tensors)
-            self._seen.add(handle)
+        self.add(stream, handle)
         if handle != now:
             self._record(stream, call)
         return handle
+
+    def add(self, stream, handle: int) -> None:
+        """The stream, of this handle, uses the tensors from now on."""
+        if handle not in self._seen:
+            self._record(stream, self._tensors)
+            self._seen.add(handle)
 
     @staticmethod
     def _record(stream, tensors) -> None:
@@ -217,7 +222,7 @@ class NormSite:
             if t is not None:
                 _matrix(t, name, (rows,), torch.float32, vector=True)
         self.d_residual = self.d_branch = self.d_w_pre = self.d_w_post = self.d_gate = None
-        self._grads = self._workspace = None
+        self._grads = self._workspace = self._grad_streams = None
         none = muon_q8()
         self._c = muon_norm_site(
             rows, cols, branch.data_ptr(), _ld(branch), residual.data_ptr(), _ld(residual), w_pre.data_ptr(),
@@ -245,6 +250,7 @@ class NormSite:
         g = self._grads
         g.dy, g.ld_dy, g.dh, g.ld_dh = _ptr(dy), 0 if dy is None else _ld(dy), dh.data_ptr(), _ld(dh)
         handle = self._streams.use(stream, (dh,) if dy is None else (dy, dh))
+        self._grad_streams.add(stream, handle)
         check(lib().muon_norm_backward(ctypes.byref(self._c), ctypes.byref(g), handle))
 
     def _make_grads(self) -> None:
@@ -258,8 +264,8 @@ class NormSite:
         self._grads = muon_norm_grads(
             None, 0, None, 0, self.d_residual.data_ptr(), shape[1], self.d_branch.data_ptr(), shape[1],
             _ptr(self.d_w_pre), _ptr(self.d_w_post), _ptr(self.d_gate), shape[1], self._workspace.data_ptr(), need.value)
-        self._streams.add([t for t in (self.d_residual, self.d_branch, self.d_w_pre, self.d_w_post, self.d_gate,
-                                       self._workspace) if t is not None])
+        self._grad_streams = _Streams([t for t in (self.d_residual, self.d_branch, self.d_w_pre, self.d_w_post, self.d_gate,
+                                                   self._workspace) if t is not None])
 
 
 class WGrad:

@@ -18,10 +18,10 @@ class Stream:
     __hash__ = None
 
     def __enter__(self):
-        pass
+        self.before, self.world.now = self.world.now, self.cuda_stream
 
     def __exit__(self, *a):
-        pass
+        self.world.now = self.before
 
 
 class World:
@@ -41,6 +41,7 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(w.now))
     monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: Stream(0))
     monkeypatch.setattr(torch.cuda, "stream", lambda s: s or Stream(w.now))
+    monkeypatch.setattr(Stream, "world", w, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: w.now, raising=False)
     # what torch does with a handle: 0 gives a stream of its pool
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, *a: Stream(handle or 0xBAD))
@@ -97,21 +98,19 @@ def test_a_raw_handle_names_that_stream(world, now):
 def test_the_current_stream_is_recorded_on_all_memory_that_the_object_holds(world):
     # Inside `with torch.cuda.stream(side)`: dropping the object afterwards must
     # not hand its buffers out before side is done with them.
-    p, memory = plan()
+    (p, memory), (s, tensors), ckpt, x = plan(), site(), q8(4, 64), torch.zeros(4, 64)
     world.now = 7
     p.run()
     assert world.on(7) == memory
-    s, tensors = site()
-    world.recorded.clear()
-    s.forward()
-    assert world.on(7) == {t.data_ptr() for t in tensors}
-    ckpt, x = q8(4, 64), torch.zeros(4, 64)
     world.now = 8
-    layer.q8_save(x, ckpt)
-    assert world.on(8) == {ckpt.q.data_ptr(), ckpt.e.data_ptr()}
+    s.forward()
+    assert world.on(8) == {t.data_ptr() for t in tensors}
     world.now = 9
-    layer.q8_load(ckpt, x)
+    layer.q8_save(x, ckpt)
     assert world.on(9) == {ckpt.q.data_ptr(), ckpt.e.data_ptr()}
+    world.now = 10
+    layer.q8_load(ckpt, x)
+    assert world.on(10) == {ckpt.q.data_ptr(), ckpt.e.data_ptr()}
 
 
 def test_gradients_made_on_one_stream_are_recorded_on_the_others_that_use_them(world):
@@ -119,11 +118,13 @@ def test_gradients_made_on_one_stream_are_recorded_on_the_others_that_use_them(w
     dh = torch.zeros(4, 64)
     s.backward(None, dh, Stream(7))
     made = [s.d_residual, s.d_branch, s.d_w_pre, s.d_w_post, s._workspace]
-    assert world.on(7) == {t.data_ptr() for t in tensors + made + [dh]}
+    assert world.on(7) >= {t.data_ptr() for t in tensors + [dh]}
     s.backward(None, dh)
-    assert world.on(0) == {t.data_ptr() for t in tensors + made}
+    assert world.on(0) == {t.data_ptr() for t in made}
     world.now = 3
     s.forward()
+    assert world.on(3) == {t.data_ptr() for t in tensors}
+    s.backward(None, dh)
     assert world.on(3) == {t.data_ptr() for t in tensors + made}
 
 
@@ -138,11 +139,10 @@ def test_a_named_stream_is_recorded_on_the_calls_own_tensors(world):
     assert world.on(6) == {ckpt.q.data_ptr(), ckpt.e.data_ptr(), x.data_ptr()}
 
 
-def test_a_stream_is_recorded_once(world):
+def test_a_stream_is_recorded_once_and_the_first_one_never(world):
     p, memory = plan()
-    for _ in range(2):
+    for expected in (memory, set()):
         for world.now in (0, 7):
             p.run()
-            assert world.on(world.now) == memory
+        assert not world.on(0) and world.on(7) == expected
         world.recorded.clear()
-        memory = set()
