@@ -396,7 +396,10 @@ muon_status muon_q8_load(const muon_q8* in, void* x, int64_t ldx, int32_t dtype,
  *                   NULL, with or without w_post; a backward pass needs rstd_y, and rstd_b with w_post
  * u, v              8-bit checkpoints, written if their q is not NULL; a
  *                   backward pass needs u, and v with w_post or gate
- * cols is at most 32768 (a row stays in one workgroup's registers). */
+ * cols is at most 32768. Up to 8192 columns (backward pass: 6144) a row is read
+ * once and stays in registers; wider rows are read again from cache or spill, and
+ * run at a fraction of the memory's rate (a backward pass of 16384 bf16 columns
+ * takes 6 times its bytes' time). */
 typedef struct {
   int64_t rows;
   int64_t cols;

@@ -240,8 +240,9 @@ muon_status norm_backward(const muon_norm_site* site, const muon_norm_grads* gra
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
-// The large kernel reads dY as it is if its rows are 16-byte aligned bf16 with
-// whole 16-byte chunks; otherwise it is rewritten into the workspace first.
+// The large and the medium kernel read dY as it is if its rows are 16-byte
+// aligned bf16 with whole 16-byte chunks; otherwise it is rewritten into the
+// workspace first.
 bool dy_aligned(const muon_wgrad_item& it, int32_t dtype) {
   return reinterpret_cast<uintptr_t>(it.dy) % 16 == 0 && it.ld_dy * elem_of(dtype) % 16 == 0 && it.n % 8 == 0;
 }

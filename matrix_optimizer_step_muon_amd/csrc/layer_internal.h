@@ -18,7 +18,8 @@ constexpr int kMinExp = 17;          // smallest exponent byte: 2^-110
 // A norm workgroup holds one row, 8 columns per thread, `vecs` times. The
 // forward kernel needs few registers and goes to 1024 threads first; the
 // backward kernel's partial sums need 24 per 8 columns, so it takes at most 768
-// threads (168 registers each), then 512 (256).
+// threads (168 registers each), then 512 (256). Rows past 8192 columns do not fit
+// the registers either way and spill.
 inline int norm_forward_vecs(int64_t cols) { return cols <= 8192 ? 1 : cols <= 16384 ? 2 : 4; }
 inline int norm_backward_vecs(int64_t cols) { return cols <= 6144 ? 1 : cols <= 8192 ? 2 : 4; }
 inline int norm_threads(int64_t cols, int vecs) {
@@ -40,7 +41,11 @@ inline int norm_rows(int64_t rows, int threads, int most) {
 // `per_cu` threads. Forward 1280, two of 640 for 5120 columns (4096 x 5120 bf16:
 // 28.7 us; 1024 or 640 threads 33, 2048 36), five of 256 for 2048 (16384 x 2048
 // bf16: 42.5 us, with 640 threads 53). Backward 768, which is what its registers
-// allow (16384 x 2048 bf16: 80 us; 512 threads 93, 1024 100: some wait).
+// allow (16384 x 2048 bf16: 80 us; 512 threads 93, 1024 100: some wait). Both were
+// chosen at these widths. At others, 2^24 bf16 elements take 28 to 29 us forward
+// from 512 to 5120 columns and 33 to 36 from 6144 to 8192; backward 48 to 52 us
+// from 512 to 6144 columns, but 69 at 2560 and 55 at 3584 (workgroups of 5 and
+// 7 waves, for 12 places in a CU).
 constexpr int kNormThreadsForward = 1280, kNormThreadsBackward = 768;
 inline int norm_blocks(int64_t rows, int threads, int rows_per, int per_cu) {
   return int(std::min<int64_t>((rows + rows_per - 1) / rows_per, 256 * std::max(1, per_cu / (threads * rows_per))));
@@ -70,7 +75,7 @@ inline NormLaunch norm_backward_launch(int64_t rows, int64_t cols) {
 // ------------------------------------------------------------ weight gradients
 
 constexpr int kWgTile = 256;   // output tile edge of the large kernel
-constexpr int kWgStep = 64;    // tokens per stage of it
+constexpr int kWgStep = 64;    // tokens per stage of it and of the medium kernel
 constexpr int kWgMedium = 128; // output tile edge of the medium kernel
 constexpr int kWgSmall = 64;   // output tile edge of the small kernel
 constexpr int kWgItems = 16;   // matrices per launch
@@ -78,8 +83,8 @@ constexpr int kWgItems = 16;   // matrices per launch
 // One matrix of a launch. Units (tiles x splits) are numbered consecutively
 // over the items.
 struct WgItem {
-  const void* dy;      // large kernel: bf16, 16-byte aligned rows of lda elements, parts planes of
-                       // `rows` rows; small kernel: the caller's
+  const void* dy;      // large and medium kernel: bf16, 16-byte aligned rows of lda elements, parts
+                       // planes of `rows` rows; small kernel: the caller's
   const uint8_t* q;
   const uint8_t* e;
   const void* scale;   // dtype, or null
@@ -87,7 +92,7 @@ struct WgItem {
   const void* c;
   int64_t lda, ldq, lde;
   int32_t rows, n, k, na;  // na: columns of dy that may be read (a multiple of 8)
-  int32_t parts;       // 1, or 3 for fp32 dY (large kernel)
+  int32_t parts;       // 1, or 3 for fp32 dY (planes of dy; the small kernel makes them itself)
   int32_t tiles_n, tiles_k;
   int32_t splits;      // > 1: partial tiles go to the workspace
   int32_t part0;       // first partial tile of this item in the workspace
@@ -100,7 +105,7 @@ struct WgArgs {
   float* partial;
   int32_t n_items;
   int32_t units;
-  int32_t edge;   // kWgTile or kWgSmall
+  int32_t edge;   // kWgTile, kWgMedium or kWgSmall
   int32_t dy_f32; // dtype of dY (as given) and scale
   int32_t g_f32;  // dtype of g and c
 };

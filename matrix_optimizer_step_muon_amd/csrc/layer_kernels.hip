@@ -1,7 +1,9 @@
 // gfx950 kernels of 8-bit activation checkpoints and of the norm sites between
-// blocks. All of them are bound by HBM: each tensor is read once and written
-// once, sums are fp32, and every thread owns 8 consecutive columns (16 bytes of
-// bf16, 8 bytes of a checkpoint), so a wave instruction moves whole lines.
+// blocks. Up to 8192 columns (backward: 6144) they are bound by HBM: each tensor
+// is read once and written once, sums are fp32, and every thread owns 8
+// consecutive columns (16 bytes of bf16, 8 bytes of a checkpoint), so a wave
+// instruction moves whole lines. Wider rows are right but slow; each kernel says
+// what it does with them.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -242,7 +244,10 @@ MUON_INLINE void block_sum(float (&v)[N], float* red) {
 // norms, so every tensor moves once. With VPT = 1 there are registers left to
 // load the weights once and to have the next row's loads in flight. 4096 x 5120
 // bf16: 29 us with its tensors partly in cache, 36 without (4.7 TB/s; a copy
-// 4.9); one row 4.1 to 4.8 us, a chain of loads and two sums.
+// 4.9); one row 4.1 to 4.8 us, a chain of loads and two sums. 1024 threads have
+// 128 registers each, which hold VPT = 2 of aligned bf16 only (1024 x 16384: 35
+// us, 3.9 TB/s); other rows past 8192 columns spill 2 to 78 registers, and VPT =
+// 4 73 to 386 (512 x 32768 bf16: 63 us, 2.1 TB/s; unaligned 119).
 template <class T, int VPT, bool VEC>
 __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, int32_t rows_per) {
   __shared__ float red[2][16];
@@ -359,9 +364,14 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(muon_norm_site s, in
 // wider rows are read again (from cache) after their sums. Rows of one wave go
 // one to a wave, whose sums are added at the end; a launch of one workgroup
 // stores the weight gradients themselves. MAXT: the most threads of a
-// workgroup, which sets the registers of each. 16384 x 2048 bf16: 73 us, 4.6
-// TB/s; 4096 x 5120: 56 us, 3.8 TB/s, where one workgroup of 10 waves is what a
-// CU's registers hold and its row's arithmetic (40% of the time) is not hidden.
+// workgroup, which sets the registers of each. 16384 x 2048 bf16: 72 to 76 us,
+// 4.4 to 4.6 TB/s; 4096 x 5120: 56 to 59 us, 3.6 to 3.8 TB/s, where one workgroup
+// of 10 waves is on a CU, its vector units are at work 43% of the time and its
+// waves wait for memory 57% of theirs. Reading rows twice costs 6145 to 8192
+// columns half of that (4096 x 8192: 119 us, 2.8 TB/s). Past those the sums of a
+// thread's 32 columns do not fit its registers and 117 to 556 of them spill: 1024
+// x 16384 takes 198 us, 0.85 TB/s. Unaligned rows spill 86 to 90 from 6145
+// columns on (2048 x 8191 bf16: 162 us), and in fp32 10 from 4097.
 template <class T, int VPT, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(muon_norm_site s, muon_norm_grads g, int32_t rows_per) {
   __shared__ float red[2][48];

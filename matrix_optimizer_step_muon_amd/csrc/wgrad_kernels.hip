@@ -73,8 +73,8 @@ MUON_INLINE void tile_of(int t, int tiles_n, int tiles_k, int& tn, int& tk) {
 // four columns each: consecutive ones, as one vector, where a row of the
 // gradient is a multiple of four long, and otherwise every LW-th, so that a
 // store instruction still covers whole lines.
-// NT: nontemporal stores, for tiles that all CUs store at once: the seven
-// 1.7B-layer gradients over 4096 tokens take 362 us with them, 372 without.
+// NT: nontemporal stores, for tiles that all CUs store at once: on one GPU the
+// seven 1.7B-layer gradients over 4096 tokens took 362 us with them, 372 without.
 template <int LW, bool NT = false>
 struct GradOut {
   const __attribute__((address_space(4))) WgItem& it;
@@ -157,9 +157,12 @@ struct GradOut {
 // beside its MFMAs: 1902 us against 2006 with four waves of 128 x 128 (25600 x
 // 5120 outputs, 8192 tokens). With the loads further ahead that product takes
 // 1757 to 1849 us, 1161 to 1222 TFLOP/s, of the 1380 that a large library
-// product reaches on the GPU and the 1070 to 1080 it reaches in this layout.
-// What bounds it is power: MFMAs and their LDS reads alone run at 1650 TFLOP/s,
-// the copies and loads cost 17 to 20% and decoding 10 to 13%.
+// product reaches on the GPU and the 1060 to 1080 it reaches in this layout.
+// What bounds it is power: the matrix units are busy 59% of the cycles, at a clock
+// of 1.83 GHz (of 2.4). In copies with parts left out, MFMAs and their LDS reads
+// alone ran at 1650 TFLOP/s, the copies and loads cost 17 to 20% and decoding 10
+// to 13%. These are times of a GPU at work: its first 40 or so launches after an
+// idle time take up to a quarter longer.
 template <int KIND, int EDGE>
 MUON_INLINE void wgrad_tile() {
   typedef Geo<EDGE> Z;
@@ -471,8 +474,8 @@ __global__ void __launch_bounds__(Geo<256>::NT, 2) wgrad_kernel(WgArgs) {
 
 // 128 x 128 tiles, two workgroups per CU: for products with too few 256 x 256
 // tiles for the CUs but long enough a sum to be bound by arithmetic, not by the
-// chain of one tile. 16 us at 300 bf16 tokens, 2048 x 2048 (160 TFLOP/s; 25
-// with 256 x 256 tiles, 24 with 64 x 64), 30 at 1000 tokens, 1024 x 5120 (350
+// chain of one tile. 13 to 16 us at 300 bf16 tokens, 2048 x 2048 (160 to 195
+// TFLOP/s; 25 us with 256 x 256 tiles, 24 with 64 x 64), 30 at 1000 tokens, 1024 x 5120 (350
 // TFLOP/s; 40 with either). A round of 512 takes 1.16 us per stage, the same
 // outputs in 256 x 256 tiles half of a round's 1.4: a byte of an operand moved
 // to LDS feeds half as many MFMAs, and a byte read from it two thirds.
