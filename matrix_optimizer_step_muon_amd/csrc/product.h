@@ -1,0 +1,626 @@
+// The tile engine of the layers' products on gfx950, C[m][n] = sum_k A[m][k] B[n][k]
+// (or B[k][n]), and the way its tiles leave: shared by the kernels of the gated
+// block and of the 8-bit linear product.
+//
+// A workgroup of four waves, 2 x 2, sums one BM x BN tile, or a piece of its sum,
+// in MFMA accumulators. A stage is RB bytes of K of every row of both operands,
+// copied global -> LDS directly, in a ring of ST stages; the copies of later
+// stages and the fragments of the next sub-step go between the MFMAs, in a fixed
+// order. Then the tile goes through LDS once more in fp32, so that a thread holds
+// eight consecutive columns of a row, which is what an epilogue works on: a store
+// instruction covers whole lines, and a group of a checkpoint is four lanes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "device.h"
+#include "layer_internal.h"
+#include "product_internal.h"
+#include "q8.h"
+
+namespace muon {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef const __attribute__((address_space(4))) PrArgs* PrArgsPtr;
+typedef const __attribute__((address_space(4))) PrItem& PrItemRef;
+typedef uint32_t __attribute__((aligned(1))) u32_any;
+typedef u32_any __attribute__((address_space(1))) g_u32_any;
+
+// kNT16, kNN16: bf16 operands, B as n x k or as k x n. kNT8: e4m3 operands with
+// scales, in the 8-bit MFMA that applies them: twice the rate, but it adds the 64
+// products of an instruction on a common grid (measured: a term below 2^-13 or so
+// of the largest is lost, 5e-5 relative in a sum). kNT8X, for fp32 results: the
+// same operands decoded to bf16 on their way from LDS, exactly, and the bf16 MFMA.
+enum PrMode { kNT16, kNN16, kNT8, kNT8X };
+
+// The slot of 16-byte chunk c of row r in an LDS row of S slots is c ^ swz(r):
+// the rows that the lanes of a fragment read together lie in different banks.
+template <int S>
+MUON_INLINE int pr_swz(int r) {
+  if constexpr (S == 4) return ((r >> 1) ^ (r >> 3)) & 3;
+  else return (r & 7) ^ ((r >> 3) & 1);
+}
+// The same for a row of K of a transposed B, read four rows at a time.
+template <int BN>
+MUON_INLINE int pr_swz_k(int r) {
+  if constexpr (BN >= 128) return lds_swizzle_k(r);
+  else return (r & 3) << 1;
+}
+
+template <int BM_, int BN_, int RB_, int ST_, int MODE_, int WG_>
+struct PrCfg {
+  static constexpr int BM = BM_, BN = BN_, RB = RB_, ST = ST_, MODE = MODE_, WG = WG_;  // WG: workgroups per CU
+  static constexpr int NT = 256, NW = 4;
+  static constexpr int WM = BM / 2, WN = BN / 2, FM = WM / 32, FN = WN / 32;
+  static constexpr bool F8 = MODE == kNT8 || MODE == kNT8X, NN = MODE == kNN16;
+  static constexpr int BK = RB / (F8 ? 1 : 2);       // elements of K per stage
+  static constexpr int S = RB / 16;                  // 16-byte slots of a row
+  static constexpr int AB = BM * RB, BB = BN * RB, STAGE = AB + BB, RING = ST * STAGE;
+  static constexpr int DA = AB / 1024 / NW, DB = BB / 1024 / NW, PS = DA + DB;  // copies per wave and stage
+  static constexpr int RPI = 1024 / RB;              // rows of one copy
+  static constexpr int BROW = BN * 2, BRPI = 1024 / BROW, BS = BN / 8;  // the same of a transposed B
+  static constexpr int SUB = MODE == kNT8 ? 64 : MODE == kNT8X ? 16 : 32;  // bytes of K of a sub-step
+  static constexpr int KK = RB / SUB, PER = FM * FN, SLOTS = KK * PER, NF = FM + FN;
+  // The slot at which the workgroup meets: the last sub-step's fragments are in
+  // registers, the next stage must be in LDS.
+  static constexpr int MEET = SLOTS - (PER >= 16 ? 4 : PER >= 4 ? 2 : 1);
+  // 8-bit operands: exponents of eight stages (RB = 128: 1024 of K), twice
+  static constexpr int EX_A = 8 * BM * 4, EX_B = 8 * 2 * 4, EX = F8 ? 2 * (EX_A + EX_B) : 0;
+  static constexpr int LDS = RING + EX;
+  static constexpr int PASSES = (BM * BN * 4 + RING - 1) / RING, IPP = FM / PASSES;  // of the epilogue
+  static_assert(KK % 2 == 0 && FM % PASSES == 0 && MEET >= SLOTS - PER && (!F8 || RB == 128), "schedule assumptions");
+  typedef std::conditional_t<MODE == kNT8, i32x8, bf16x8> Frag;
+};
+
+// The unit of workgroup b: XCD b % 8 gets a contiguous range of units, so that
+// the tiles that run there together share operand panels in its L2.
+MUON_INLINE int pr_unit(int b, int units) {
+  const int x = b & 7, i = b >> 3, per = units >> 3, rest = units & 7;
+  return x * per + min(x, rest) + i;
+}
+MUON_INLINE int pr_item(PrArgsPtr a, int unit) {
+  int idx = 0;
+#pragma unroll
+  for (int i = 1; i < kPrItems; ++i) idx += unit >= a->unit0[i];
+  return idx;
+}
+// Tile (tm, tn) of local tile number t: bands of 4 tile rows walked column by
+// column, so 32 consecutive tiles cover 4 x 8.
+MUON_INLINE void pr_tile(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int band = t / (4 * tiles_n), r = t - band * 4 * tiles_n;
+  const int h = min(4, tiles_m - 4 * band);
+  tn = r / h;
+  tm = 4 * band + (r - tn * h);
+}
+
+// Which planes the p-th of the six products of two fp32 numbers takes, smallest
+// products first (0 lo, 1 mid, 2 hi): lo hi, hi lo, mid mid, mid hi, hi mid, hi
+// hi. What is left out is below 2^-24 of hi hi.
+MUON_INLINE int pr_plane_a(int p) { return p == 0 ? 0 : p == 1 ? 2 : p == 2 ? 1 : p == 3 ? 1 : 2; }
+MUON_INLINE int pr_plane_b(int p) { return p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 : p == 3 ? 2 : p == 4 ? 1 : 2; }
+
+// Sums units of stages [s_begin, s_end) of tile (m0, n0) into acc. DUAL: the tile's
+// first BN/2 columns are columns n0/2.. of b[0], the others the same of b[1].
+template <class Z, bool DUAL>
+MUON_INLINE void pr_sum(PrArgsPtr args, PrItemRef it, int m0, int n0, int s_begin, int s_end, unsigned char* smem,
+                        f32x16 (&acc)[Z::FM][Z::FN]) {
+  constexpr int FM = Z::FM, FN = Z::FN, RB = Z::RB, S = Z::S;
+  const int tid = fresh_tid(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  if (s_begin >= s_end) return;
+
+  // Held in scalar registers: reloaded in the loop, they would make it wait for
+  // every LDS access in flight (scalar loads share that counter).
+  int m = it.m, n = it.n, k = it.k;
+  int64_t lda = it.lda, ldb = it.ldb;
+  asm volatile("" : "+s"(m), "+s"(n), "+s"(k), "+s"(lda), "+s"(ldb));
+  const int kbytes = Z::F8 ? k : 2 * k;              // of an A row; whole 16-byte chunks are readable
+  const int kt = (k + Z::BK - 1) / Z::BK;            // stages of one pair of planes
+  const int pairs = args->parts == 3 ? 6 : 1;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+
+  // Where a stage is read from: of its pair of planes, K step `ks`.
+  struct Cursor {
+    const uint8_t *a, *b0, *b1;
+    int seg, ks;
+  };
+  auto seat = [&](Cursor& c) __attribute__((always_inline)) {
+    const int sum = c.seg / pairs, p = c.seg - sum * pairs;
+    const int64_t pa = pairs == 6 ? pr_plane_a(p) * it.pa : 0, pb = pairs == 6 ? pr_plane_b(p) * it.pb : 0;
+    c.a = it.a[sum] + pa + (int64_t)m0 * lda;
+    if constexpr (DUAL) {
+      c.b0 = it.b[0] + pb + (int64_t)(n0 >> 1) * ldb;
+      c.b1 = it.b[1] + pb + (int64_t)(n0 >> 1) * ldb;
+    } else if constexpr (Z::NN) {
+      c.b0 = it.b[sum] + pb + 2 * n0;
+    } else {
+      c.b0 = it.b[sum] + pb + (int64_t)n0 * ldb;
+    }
+    c.a += (int64_t)c.ks * RB;
+    c.b0 += Z::NN ? (int64_t)c.ks * Z::BK * ldb : (int64_t)c.ks * RB;
+    if constexpr (DUAL) c.b1 += (int64_t)c.ks * RB;
+  };
+  auto advance = [&](Cursor& c) __attribute__((always_inline)) {
+    if (++c.ks == kt) {
+      c.ks = 0;
+      ++c.seg;
+      seat(c);
+    } else {
+      c.a += RB;
+      c.b0 += Z::NN ? (int64_t)Z::BK * ldb : (int64_t)RB;
+      if constexpr (DUAL) c.b1 += RB;
+    }
+  };
+  const bool ragged = kt * RB != kbytes;             // a plane's last stage is not whole
+  auto short_stage = [&](int ks) __attribute__((always_inline)) { return ragged && ks == kt - 1; };
+
+  // Copy q of an operand fills 1 KB: rows RPI*q .. +RPI-1, lane l slot l % S of row
+  // l / S, which holds chunk slot ^ swz(row). Rows past the last one read the last
+  // one, and are never stored. In a short stage, chunks past the end of a row read
+  // its last chunk (for a transposed B: rows of K past the last one the last one);
+  // what is not the product's becomes zero once it is in LDS.
+  uint32_t va[Z::DA], vb[Z::DB];
+  const int rows_a = m - m0, cols_b = DUAL ? n - (n0 >> 1) : n - n0;
+#pragma unroll
+  for (int p = 0; p < Z::DA; ++p) {
+    const int r = (wave * Z::DA + p) * Z::RPI + lane / S;
+    va[p] = (uint32_t)min(r, rows_a - 1) * (uint32_t)lda + (((lane % S) ^ pr_swz<S>(r)) << 4);
+  }
+#pragma unroll
+  for (int p = 0; p < Z::DB; ++p) {
+    if constexpr (Z::NN) {
+      const int r = (wave * Z::DB + p) * Z::BRPI + lane / Z::BS;
+      vb[p] = (uint32_t)r * (uint32_t)ldb + (min((lane % Z::BS) ^ pr_swz_k<Z::BN>(r), (cols_b + 7) / 8 - 1) << 4);
+    } else {
+      const int r = (wave * Z::DB + p) * Z::RPI + lane / S, c = DUAL ? r & (Z::BN / 2 - 1) : r;
+      vb[p] = (uint32_t)min(c, cols_b - 1) * (uint32_t)ldb + (((lane % S) ^ pr_swz<S>(r)) << 4);
+    }
+  }
+  auto copy = [&](const Cursor& c, uint32_t buf, int d, auto SHORT_) __attribute__((always_inline)) {
+    constexpr bool SHORT = decltype(SHORT_)::value;
+    const bool is_a = d < Z::DA;
+    const int p = is_a ? d : d - Z::DA, q = wave * (is_a ? Z::DA : Z::DB) + p;
+    const uint8_t* base = is_a ? c.a : DUAL && q * Z::RPI >= Z::BN / 2 ? c.b1 : c.b0;
+    uint32_t v = is_a ? va[p] : vb[p];
+    if constexpr (SHORT) {
+      if (is_a || !Z::NN) {
+        const int r = q * Z::RPI + lane / S, ch = (lane % S) ^ pr_swz<S>(r);
+        const int last = (kbytes - c.ks * RB + 15) / 16 - 1;
+        v -= (uint32_t)max(ch - last, 0) << 4;
+      } else {
+        const int r = q * Z::BRPI + lane / Z::BS, last = k - 1 - c.ks * Z::BK;
+        v -= (uint32_t)max(r - last, 0) * (uint32_t)ldb;
+      }
+    }
+    dma16s(base, v, lds0 + buf + (is_a ? 0 : Z::AB) + q * 1024);
+  };
+  // Zeros behind the end of K, in both operands (the other one may hold an
+  // infinity).
+  auto clear = [&](int ks, uint32_t buf) __attribute__((always_inline)) {
+    const int left = kbytes - ks * RB;               // bytes of K that are there
+    constexpr int ROWS = Z::NN ? Z::BM : Z::BM + Z::BN;
+    for (int i = tid; i < ROWS * S; i += Z::NT) {
+      const int r = i / S, ch = i % S;
+      const int br = r < Z::BM ? r : r - Z::BM;
+      u32x4* at = reinterpret_cast<u32x4*>(smem + buf + (r < Z::BM ? 0 : Z::AB) + br * RB + ((ch ^ pr_swz<S>(br)) << 4));
+      const int have = left - 16 * ch;
+      if (have <= 0) {
+        *at = u32x4{0u, 0u, 0u, 0u};
+      } else if (have < 16) {
+        u32x4 v = *at;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int b = have - 4 * w;
+          v[w] &= b >= 4 ? ~0u : b <= 0 ? 0u : (1u << (8 * b)) - 1u;
+        }
+        *at = v;
+      }
+    }
+    if constexpr (Z::NN) {
+      const int have = k - ks * Z::BK;
+      for (int i = tid; i < Z::BK * Z::BS; i += Z::NT)
+        if (i / Z::BS >= have) *reinterpret_cast<u32x4*>(smem + buf + Z::AB + i * 16) = u32x4{0u, 0u, 0u, 0u};
+    }
+    __syncthreads();
+  };
+
+  // Exponents (8-bit operands): eight stages of both, one dword of four groups per
+  // row of A and stage, one byte per 128 columns of B and stage. Thread t holds row
+  // t's on their way; groups past the end of K get 127, whatever they scale is 0.
+  const int groups = (k + kGroup - 1) / kGroup, kblocks = (k + kBlock - 1) / kBlock;
+  uint32_t ev[8], evb = 0;
+  auto load_ex = [&](int chunk) __attribute__((always_inline)) {
+    if constexpr (Z::F8) {
+      if (tid < Z::BM) {
+        const uint8_t* row = it.ea + (int64_t)(m0 + min(tid, rows_a - 1)) * it.lde + 32 * chunk;
+        if (32 * chunk + 32 <= groups) {
+#pragma unroll
+          for (int w = 0; w < 8; ++w) ev[w] = *((const g_u32_any*)(row + 4 * w));
+        } else {
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            ev[w] = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int g = 4 * w + b;
+              ev[w] |= (32 * chunk + g < groups ? (uint32_t)*((const g_u8*)(row + g)) : 127u) << (8 * b);
+            }
+          }
+        }
+      }
+      if (tid < 16) {
+        const int nb = n0 / kBlock + (tid >> 3), kb = 8 * chunk + (tid & 7);
+        evb = nb * kBlock < n && kb < kblocks ? (uint32_t)*((const g_u8*)(it.eb + nb * it.ldeb_n + kb * it.ldeb_k)) : 127u;
+      }
+    }
+  };
+  auto write_ex = [&](int chunk) __attribute__((always_inline)) {
+    if constexpr (Z::F8) {
+      unsigned char* t = smem + Z::RING + (chunk & 1) * (Z::EX_A + Z::EX_B);
+      if (tid < Z::BM)
+#pragma unroll
+        for (int w = 0; w < 8; ++w) *reinterpret_cast<uint32_t*>(t + (w * Z::BM + tid) * 4) = ev[w];
+      if (tid < 16) *reinterpret_cast<uint32_t*>(t + Z::EX_A + tid * 4) = evb;
+    }
+  };
+
+  // Fragments. Lane l of a 32-row block reads row l % 32; of a sub-step of 16 bf16
+  // its half l / 32 takes chunk 2 kk + half (8 consecutive k), of 64 e4m3 chunks
+  // 4 kk + half and 4 kk + 2 + half: the 8-bit MFMA's halves hold k 0-15, 32-47 and
+  // 16-31, 48-63, and its scale of half h is that of k 32 h .. 32 h + 31.
+  const int r32 = lane & 31, h = lane >> 5, sw = pr_swz<S>(r32);
+  const int G = lane >> 4, i16 = lane & 15;
+  typename Z::Frag fa[2][FM], fb[2][FN];
+  uint32_t sa[FM], sb = 127;                         // this stage's scales
+  uint32_t na[FM], nb_ = 127;                        // the next one's
+  auto read_frag = [&](int b, uint32_t buf, int kk, int f) __attribute__((always_inline)) {
+    const bool is_a = f < FM;
+    const int i = is_a ? f : f - FM;
+    typename Z::Frag v;
+    if (Z::NN && !is_a) {
+      if constexpr (Z::NN) {
+        const int col = wn * Z::WN + 32 * i + 16 * (G & 1) + 4 * (i16 & 3);
+        const unsigned char* p = smem + buf + Z::AB + (kk * 16 + 8 * (G >> 1) + (i16 >> 2)) * Z::BROW +
+                                 (((col >> 3) ^ pr_swz_k<Z::BN>(i16 >> 2)) << 4) + 8 * (i16 & 1);
+        const v4i16 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * Z::BROW);
+        v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    } else {
+      const unsigned char* row = smem + buf + (is_a ? (wm * Z::WM + 32 * i + r32) * RB : Z::AB + (wn * Z::WN + 32 * i + r32) * RB);
+      if constexpr (Z::MODE == kNT8) {
+        const u32x4 lo = *reinterpret_cast<const u32x4*>(row + (((4 * kk + h) ^ sw) << 4));
+        const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((4 * kk + 2 + h) ^ sw) << 4));
+        v = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+      } else if constexpr (Z::MODE == kNT8X) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(row + ((kk ^ sw) << 4) + 8 * h);
+        const uint32_t E = is_a ? (sa[i] >> (8 * (kk >> 1))) & 255u : sb;
+        const Q8Group<MUON_Q8_E4M3> grp(E, true);
+        const u32x2 x = grp.bf16x4(w[0]), y = grp.bf16x4(w[1]);
+        v = __builtin_bit_cast(bf16x8, (u32x4{x[0], x[1], y[0], y[1]}));
+      } else {
+        v = *reinterpret_cast<const bf16x8*>(row + (((2 * kk + h) ^ sw) << 4));
+      }
+    }
+    if (is_a) fa[b][i] = v;
+    else fb[b][i] = v;
+  };
+  // Scales of the K step ks, from the table.
+  auto read_ex = [&](int ks) __attribute__((always_inline)) {
+    if constexpr (Z::F8) {
+      const unsigned char* t = smem + Z::RING + ((ks >> 3) & 1) * (Z::EX_A + Z::EX_B);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        na[i] = *reinterpret_cast<const uint32_t*>(t + ((ks & 7) * Z::BM + wm * Z::WM + 32 * i + r32) * 4);
+      nb_ = *reinterpret_cast<const uint32_t*>(t + Z::EX_A + ((ks & 7) + 8 * ((wn * Z::WN) / kBlock)) * 4);
+    }
+  };
+  auto take_ex = [&]() __attribute__((always_inline)) {
+    if constexpr (Z::F8) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) sa[i] = Z::MODE == kNT8 ? na[i] >> (8 * h) : na[i];
+      sb = nb_;
+    }
+  };
+  auto mfma = [&](int b, int kk, int q) __attribute__((always_inline)) {
+    const int i = q / FN, j = q % FN;
+    if constexpr (Z::MODE == kNT8) {
+      if (kk == 0)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0, (int)sb, 0, (int)sa[i]);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0, (int)sb, 2, (int)sa[i]);
+    } else {
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  // The ring.
+  const int total = s_end - s_begin;
+  Cursor next{nullptr, nullptr, nullptr, s_begin / kt, s_begin % kt};  // the next stage to load
+  seat(next);
+  int loaded = 0;
+  const int first_chunk = next.ks >> 3;
+  load_ex(first_chunk);
+  write_ex(first_chunk);
+  int ks = next.ks;                                  // of the stage at hand
+  auto load_stage = [&](uint32_t buf) __attribute__((always_inline)) {
+    if (short_stage(next.ks)) {
+#pragma unroll
+      for (int d = 0; d < Z::PS; ++d) copy(next, buf, d, std::true_type{});
+    } else {
+#pragma unroll
+      for (int d = 0; d < Z::PS; ++d) copy(next, buf, d, std::false_type{});
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < Z::ST - 1; ++s)
+    if (loaded < total) {
+      load_stage(s * Z::STAGE);
+      if (++loaded < total) advance(next);
+    }
+  wait_vmcnt<0>();
+  __syncthreads();
+  if (short_stage(ks)) clear(ks, 0);
+  read_ex(ks);
+  take_ex();
+#pragma unroll
+  for (int f = 0; f < Z::NF; ++f) read_frag(0, 0, 0, f);
+
+  uint32_t cur = 0, to = (Z::ST - 1) * Z::STAGE;     // the ring's stage at hand, and the one that is loaded
+  // One stage. LOAD: 0 nothing more to load, 1 a whole stage, 2 a short one.
+  auto stage = [&](int t, auto LOAD_) __attribute__((always_inline)) {
+    constexpr int LOAD = decltype(LOAD_)::value;
+    const uint32_t after = cur + Z::STAGE == Z::RING ? 0 : cur + Z::STAGE;
+    const int ks1 = ks + 1 == kt ? 0 : ks + 1;
+    if constexpr (Z::F8) {
+      if ((t == 0 || (ks & 7) == 0) && 8 * (ks >> 3) + 8 < kt) load_ex((ks >> 3) + 1);
+    }
+#pragma unroll
+    for (int kk = 0; kk < Z::KK; ++kk)
+#pragma unroll
+      for (int q = 0; q < Z::PER; ++q) {
+        const int slot = kk * Z::PER + q, b = kk & 1;
+        if (slot == Z::MEET) {
+          if constexpr (Z::F8) {
+            if ((ks & 7) == 7) write_ex((ks >> 3) + 1);
+          }
+          // the next stage's copies are the oldest in flight
+          if constexpr (LOAD != 0 && Z::ST > 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((Z::ST - 2) * Z::PS) : "memory");
+          else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          if (t + 1 < total && short_stage(ks1)) clear(ks1, after);
+          read_ex(ks1);
+        }
+        mfma(b, kk, q);
+        if (kk + 1 < Z::KK) {
+#pragma unroll
+          for (int f = 0; f < Z::NF; ++f)
+            if (f * Z::PER / Z::NF == q) read_frag(b ^ 1, cur, kk + 1, f);
+        }
+        if (slot == Z::SLOTS - 1) take_ex();
+        if constexpr (Z::MODE != kNT8X) {
+          if (slot >= Z::MEET) {
+#pragma unroll
+            for (int f = 0; f < Z::NF; ++f)
+              if (f * (Z::SLOTS - Z::MEET) / Z::NF == slot - Z::MEET) read_frag(0, after, 0, f);
+          }
+        }
+        if constexpr (LOAD != 0) {
+#pragma unroll
+          for (int d = 0; d < Z::PS; ++d)
+            if (d * Z::MEET / (Z::PS * (Z::ST == 2 ? 2 : 1)) == slot)
+              copy(next, to, d, std::integral_constant<bool, LOAD == 2>{});
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    if constexpr (Z::MODE == kNT8X) {  // these need the next stage's scales
+#pragma unroll
+      for (int f = 0; f < Z::NF; ++f) read_frag(0, after, 0, f);
+    }
+    if constexpr (LOAD != 0) {
+      if (++loaded < total) advance(next);
+    }
+    ks = ks1;
+    cur = after;
+    to = to + Z::STAGE == Z::RING ? 0 : to + Z::STAGE;
+  };
+  for (int t = 0; t < total; ++t) {
+    if (loaded >= total) stage(t, std::integral_constant<int, 0>{});
+    else if (short_stage(next.ks)) stage(t, std::integral_constant<int, 2>{});
+    else stage(t, std::integral_constant<int, 1>{});
+  }
+  __syncthreads();
+}
+
+// Columns of a tile that a thread holds together, and the rest of an epilogue's
+// common side.
+constexpr int kRun = 8;
+
+template <class T>
+MUON_INLINE void load_run(const T* p, int live, float v[8]) {  // p at any alignment of T; past `live` columns 0
+  if (live >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const u32x4 lo = gload16_any(p), hi = gload16_any(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(lo[i]);
+        v[4 + i] = __uint_as_float(hi[i]);
+      }
+    } else {
+      const u32x4 w = gload16_any(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < live ? Elem<T>::load(p + i) : 0.f;
+  }
+}
+template <class T>
+MUON_INLINE void store_run(T* p, int live, const float v[8]) {
+  if (live >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      gstore16_any(p, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+      gstore16_any(p + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
+    } else {
+      gstore16_any(p, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])});
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < live) Elem<T>::store(p + i, v[i]);
+  }
+}
+
+// C's store: eight columns of a row, plus beta times those of c, rounded once.
+struct PrStoreOut {
+  static constexpr int OPS = 1;
+  PrItemRef it;
+  bool f32;
+  MUON_INLINE PrStoreOut(PrItemRef item, PrArgsPtr a) : it(item), f32(a->f32) {}
+  MUON_INLINE void emit(int row, int col, float v[8], float*) const {
+    const int live = row < it.m ? it.n - col : 0;
+    if (live <= 0) return;
+    if (it.beta != 0.f) {
+      float c[8];
+      if (f32) load_run(static_cast<const float*>(it.c) + (int64_t)row * it.ldc + col, live, c);
+      else load_run(static_cast<const u16*>(it.c) + (int64_t)row * it.ldc + col, live, c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += it.beta * c[i];
+    }
+    if (f32) store_run(static_cast<float*>(it.out) + (int64_t)row * it.ldo + col, live, v);
+    else store_run(static_cast<u16*>(it.out) + (int64_t)row * it.ldo + col, live, v);
+  }
+};
+
+// One unit of a launch: its part of the sum, then either its partial tile or the
+// epilogue Out. A tile's partial sums are BM x BN floats.
+template <class Z, class Out>
+MUON_INLINE void pr_unit_of(unsigned char* smem) {
+  constexpr bool DUAL = Out::OPS == 2;
+  const PrArgsPtr args = (PrArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  const int unit = pr_unit(blockIdx.x, args->units);
+  const int idx = pr_item(args, unit);
+  PrItemRef it = args->item[idx];
+  const int tiles = it.tiles_m * it.tiles_n;
+  const int local = unit - args->unit0[idx], split = local / tiles, tile = local - split * tiles;
+  int tm, tn;
+  pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
+  const int m0 = tm * Z::BM, n0 = tn * Z::BN;
+  const int total = (it.k + Z::BK - 1) / Z::BK * it.sums * (args->parts == 3 ? 6 : 1);
+  f32x16 acc[Z::FM][Z::FN];
+  pr_sum<Z, DUAL>(args, it, m0, n0, (int)((int64_t)total * split / it.splits), (int)((int64_t)total * (split + 1) / it.splits),
+                  smem, acc);
+
+  // Through LDS, IPP blocks of rows of every wave at a time: staged row r, whose
+  // 16-byte unit u sits at u ^ (r % the row's units), is row
+  // WM*(r / (32 IPP)) + 32*IPP*pass + r % (32 IPP) of the tile.
+  constexpr int UNITS = Z::BN / 4, MASK = UNITS - 1, ROWS = 64 * Z::IPP, PR = 32 * Z::IPP;
+  constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;  // lanes of a row
+  const int tid = fresh_tid(), lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  const Out out(it, args);
+#pragma unroll
+  for (int pass = 0; pass < Z::PASSES; ++pass) {
+    if (pass) __syncthreads();
+#pragma unroll
+    for (int ii = 0; ii < Z::IPP; ++ii)
+#pragma unroll
+      for (int j = 0; j < Z::FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int r = wm * PR + 32 * ii + (lane & 31), u = wn * (Z::WN / 4) + 8 * j + 2 * g + (lane >> 5);
+          const f32x16& t = acc[pass * Z::IPP + ii][j];
+          *reinterpret_cast<f32x4*>(smem + r * Z::BN * 4 + ((u ^ (r & MASK)) << 4)) =
+              f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
+        }
+    __syncthreads();
+    auto run_of = [&](int r, int col, float v[8]) __attribute__((always_inline)) {
+      const unsigned char* row = smem + r * Z::BN * 4;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const f32x4 t = *reinterpret_cast<const f32x4*>(row + (((col / 4 + q) ^ (r & MASK)) << 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * q + e] = t[e];
+      }
+    };
+    auto tile_row = [&](int r) __attribute__((always_inline)) { return Z::WM * (r / PR) + PR * pass + r % PR; };
+    if (it.splits > 1) {
+      float* p = args->partial + (int64_t)(it.part0 + local) * Z::BM * Z::BN;
+#pragma unroll 2
+      for (int q = 0; q < ROWS * (Z::BN / kRun) / Z::NT; ++q) {
+        const int i = q * Z::NT + tid, r = i / (Z::BN / kRun), col = i % (Z::BN / kRun) * kRun;
+        float v[8];
+        run_of(r, col, v);
+        store_run(p + tile_row(r) * Z::BN + col, 8, v);
+      }
+    } else {
+#pragma unroll 2
+      for (int q = 0; q < ROWS * LW / Z::NT; ++q) {
+        const int i = q * Z::NT + tid, r = i / LW, col = i % LW * kRun;
+        float v[8], w[8];
+        run_of(r, col, v);
+        if constexpr (DUAL) run_of(r, Z::BN / 2 + col, w);
+        out.emit(m0 + tile_row(r), (DUAL ? n0 >> 1 : n0) + col, v, w);
+      }
+    }
+  }
+}
+
+// Adds the pieces of a tile in order, then the epilogue. A workgroup takes 1024
+// columns' worth of runs of one tile: 256 threads, a run of eight each.
+template <class Out>
+MUON_INLINE void pr_join_of(int edge) {
+  constexpr bool DUAL = Out::OPS == 2;
+  const PrArgsPtr args = (PrArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  const int cols = DUAL ? edge / 2 : edge, lw = cols / kRun, per = edge * lw / 256;  // workgroups per tile
+  int b = blockIdx.x, idx = 0;
+  for (; idx < args->n_items; ++idx) {
+    const int mine = args->item[idx].splits > 1 ? args->item[idx].tiles_m * args->item[idx].tiles_n * per : 0;
+    if (b < mine) break;
+    b -= mine;
+  }
+  PrItemRef it = args->item[idx];
+  const int tiles = it.tiles_m * it.tiles_n, tile = b / per;
+  int tm, tn;
+  pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
+  const int i = (b - tile * per) * 256 + threadIdx.x, r = i / lw, col = i % lw * kRun;
+  const float* p = args->partial + ((int64_t)(it.part0 + tile) * edge + r) * edge + col;
+  const int64_t step = (int64_t)tiles * edge * edge;
+  float v[8], w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < it.splits; ++s) {
+    float x[8], y[8];
+    load_run(p + s * step, 8, x);
+    if constexpr (DUAL) load_run(p + s * step + edge / 2, 8, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] += x[e];
+      if constexpr (DUAL) w[e] += y[e];
+    }
+  }
+  const Out out(it, args);
+  out.emit(tm * edge + r, (DUAL ? tn * edge / 2 : tn * edge) + col, v, w);
+}
+
+// Workgroups of a launch's join.
+inline int64_t pr_join_blocks(const PrArgs& a, bool dual) {
+  const int edge = kPrEdge[a.tile];
+  int64_t n = 0;
+  for (int i = 0; i < a.n_items; ++i)
+    if (a.item[i].splits > 1) n += (int64_t)a.item[i].tiles_m * a.item[i].tiles_n * (edge * (dual ? edge / 2 : edge) / kRun / 256);
+  return n;
+}
+
+}  // namespace muon

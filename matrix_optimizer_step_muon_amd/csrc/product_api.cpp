@@ -1,0 +1,497 @@
+// C ABI of the layers' products (include/muon.h): the gated feed-forward block and
+// the 8-bit linear product. Validation, the workspace's layout, which tiles a
+// product is cut into, and the launches. Nothing is kept between calls.
+
+#include "layer_checks.h"
+#include "product_internal.h"
+
+namespace {
+
+using namespace muon::abi;
+
+constexpr int64_t kMaxWidth = int64_t(1) << 22;
+constexpr int64_t kMaxUnits = int64_t(1) << 22;
+// Row strides, in bytes, up to which 256 rows are within 32-bit offsets.
+constexpr int64_t kMaxPitch = int64_t(1) << 24;
+
+// The tiles of a launch, how many pieces its sums are cut into, and what it is
+// expected to take.
+struct Choice {
+  int tile, splits;
+  double us;
+};
+
+// For products with t[i] tiles of kind i in all, and `stages` stages of 128 bytes of
+// K each.
+Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, int64_t most) {
+  constexpr int64_t kCus = 256;
+  // Per kind: workgroups per CU; us to fill and empty a tile; us per stage with one
+  // and with all of a CU's; us per partial tile, written and read.
+  static const struct { int per_cu; double fixed, one, all, part; } kCost[muon::kPrTiles] = {
+      {1, 12.0, 1.6, 1.6, 0.058}, {2, 7.0, 0.6, 1.0, 0.011}, {2, 3.0, 0.3, 0.45, 0.004}};
+  Choice best{muon::kPrLarge, 1, 1e300};
+  for (int i = 0; i < muon::kPrTiles; ++i)
+    for (int64_t s = 1; s <= std::min<int64_t>(most, std::max<int64_t>(1, stages / 4)); ++s) {
+      const int64_t units = t[i] * s, each = ceil_div(stages, s), round = kCus * kCost[i].per_cu;
+      if (units > kMaxUnits) continue;
+      const int64_t full = units / round, rest = units % round;
+      double us = 2.0 + double(full) * (kCost[i].fixed + kCost[i].all * double(each));
+      if (rest) us += kCost[i].fixed + (rest <= kCus ? kCost[i].one : kCost[i].all) * double(each);
+      if (s > 1) us += 4.0 + 0.1 * double(s) + kCost[i].part * double(units);
+      if (us < best.us) best = {i, int(s), us};
+    }
+  return best;
+}
+
+// A launch's items laid out: tiles, pieces, and the bytes of partial tiles.
+muon_status lay_out(muon::PrArgs& a, bool dual, int elem, size_t* bytes) {
+  int64_t t[muon::kPrTiles] = {0, 0, 0}, stages = 0;
+  const int pairs = a.parts == 3 ? 6 : 1, bk = 128 / elem;
+  for (int i = 0; i < a.n_items; ++i) {
+    const muon::PrItem& it = a.item[i];
+    for (int j = 0; j < muon::kPrTiles; ++j)
+      t[j] += ceil_div(it.m, muon::kPrEdge[j]) * ceil_div(it.n, dual ? muon::kPrEdge[j] / 2 : muon::kPrEdge[j]);
+    stages = std::max(stages, ceil_div(it.k, bk) * it.sums * pairs);
+  }
+  const Choice c = choose(t, stages, 64);
+  a.tile = c.tile;
+  const int edge = muon::kPrEdge[c.tile];
+  int64_t units = 0, partials = 0;
+  std::fill(a.unit0, a.unit0 + muon::kPrItems, INT32_MAX);
+  for (int i = 0; i < a.n_items; ++i) {
+    muon::PrItem& it = a.item[i];
+    const int64_t mine = ceil_div(it.k, bk) * it.sums * pairs;
+    const int64_t tm = ceil_div(it.m, edge), tn = ceil_div(it.n, dual ? edge / 2 : edge);
+    it.tiles_m = int32_t(tm);
+    it.tiles_n = int32_t(tn);
+    it.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(c.splits, mine / 2)));
+    a.unit0[i] = int32_t(units);
+    it.part0 = int32_t(partials);
+    units += tm * tn * it.splits;
+    if (it.splits > 1) partials += tm * tn * it.splits;
+    if (units > kMaxUnits) return fail(MUON_ERR_INVALID_ARG, "more than 2^22 tiles in one launch");
+  }
+  a.units = int32_t(units);
+  *bytes = round256(size_t(partials) * edge * edge * sizeof(float));
+  return MUON_OK;
+}
+
+// ------------------------------------------------------------ the gated block
+
+muon_status check_mlp(const muon_mlp& p) {
+  MUON_TRY(check_dtype(p.dtype));
+  if (p.rows < 0 || p.rows > kMaxRows) return fail(MUON_ERR_INVALID_ARG, "rows must be in [0, 2^30]");
+  const struct { int64_t v; const char* name; } sizes[] = {{p.width, "width"}, {p.inner, "inner"}, {p.out, "out"}};
+  for (const auto& s : sizes)
+    if (s.v < 1 || s.v > kMaxWidth) return fail(MUON_ERR_INVALID_ARG, std::string(s.name) + " must be in [1, 2^22]");
+  return MUON_OK;
+}
+
+muon_status check_mlp_weights(Views& v, const muon_mlp& p) {
+  if (p.act < MUON_ACT_SILU || p.act > MUON_ACT_RELU) return fail(MUON_ERR_UNSUPPORTED, "act must be a muon_act");
+  const int e = elem_of(p.dtype);
+  MUON_TRY(v.add(p.w_gate, p.inner, p.width, p.width, e, false, "w_gate"));
+  MUON_TRY(v.add(p.w_up, p.inner, p.width, p.width, e, false, "w_up"));
+  return v.add(p.w_down, p.out, p.inner, p.inner, e, false, "w_down");
+}
+
+muon_status check_inner(Views& v, const muon_mlp& p, const muon_q8& q, bool written, const char* name) {
+  if (q.rows != p.rows || q.cols != p.inner)
+    return fail(MUON_ERR_INVALID_ARG, std::string(name) + " must be a rows x inner checkpoint");
+  return check_q8(v, q, written, name);
+}
+
+// An operand of a product: as the caller gave it, if it is bf16 in 16-byte aligned
+// rows of whole 16-byte chunks, else rewritten into the workspace first.
+struct Operand {
+  const void* p;
+  int64_t rows, cols, ld;
+  bool pack;
+  size_t at;
+};
+
+int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
+size_t planes_bytes(int64_t rows, int64_t cols, int parts) {
+  return round256(size_t(parts) * size_t(rows) * size_t(pad8(cols)) * 2);
+}
+
+struct Bump {
+  size_t at = 0;
+  size_t take(size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  }
+};
+
+bool in_place(const void* p, int64_t cols, int64_t ld, int32_t dtype) {
+  return dtype == MUON_BF16 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && cols % 8 == 0 && ld % 8 == 0 && 2 * ld <= kMaxPitch;
+}
+
+Operand operand(Bump& b, const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+  Operand o{p, rows, cols, ld, !in_place(p, cols, ld, dtype), 0};
+  if (o.pack) o.at = b.take(planes_bytes(rows, cols, dtype == MUON_F32 ? 3 : 1));
+  return o;
+}
+
+// One call's products and its workspace.
+struct MlpCall {
+  Operand ops[4];
+  int n_ops = 0;
+  muon::PrArgs first{}, second{};
+  size_t bytes = 0;
+};
+
+// Two operands of one item share a row stride and a distance of planes: where one
+// of two weights of the same shape is rewritten and the other is not, both are bf16
+// rows of the same multiple of 8.
+void put_operand(muon::PrItem& it, bool is_a, int which, const Operand& o, char* ws, int parts) {
+  const uint8_t* p = o.pack ? reinterpret_cast<const uint8_t*>(ws + o.at) : static_cast<const uint8_t*>(o.p);
+  const int64_t ld = o.pack ? pad8(o.cols) : o.ld, plane = parts == 3 ? o.rows * ld * 2 : 0;
+  (is_a ? it.a : it.b)[which] = p;
+  (is_a ? it.lda : it.ldb) = ld * 2;
+  (is_a ? it.pa : it.pb) = plane;
+}
+
+void start(muon::PrArgs& a, const muon_mlp& p, int64_t m, int64_t n, int64_t k, int sums) {
+  a.n_items = 1;
+  a.parts = p.dtype == MUON_F32 ? 3 : 1;
+  a.f32 = p.dtype == MUON_F32;
+  a.item[0].m = int32_t(m);
+  a.item[0].n = int32_t(n);
+  a.item[0].k = int32_t(k);
+  a.item[0].sums = sums;
+  a.mlp.act = p.act;
+}
+
+muon_status plan_forward(const muon_mlp& p, MlpCall& c, char* ws) {
+  Bump b;
+  const int parts = p.dtype == MUON_F32 ? 3 : 1;
+  c.ops[0] = operand(b, p.x, p.rows, p.width, p.ld_x, p.dtype);
+  c.ops[1] = operand(b, p.w_gate, p.inner, p.width, p.width, p.dtype);
+  c.ops[2] = operand(b, p.w_up, p.inner, p.width, p.width, p.dtype);
+  c.ops[3] = operand(b, p.w_down, p.out, p.inner, p.inner, p.dtype);
+  c.n_ops = p.y ? 4 : 3;
+  const Operand s{nullptr, p.rows, p.inner, pad8(p.inner), true, b.take(planes_bytes(p.rows, p.inner, parts))};
+  start(c.first, p, p.rows, p.inner, p.width, 1);
+  muon::PrItem& f = c.first.item[0];
+  put_operand(f, true, 0, c.ops[0], ws, parts);
+  put_operand(f, false, 0, c.ops[1], ws, parts);
+  put_operand(f, false, 1, c.ops[2], ws, parts);
+  muon::PrMlp& e = c.first.mlp;
+  e.a = p.a;
+  e.b = p.b;
+  e.s = p.s;
+  e.plane[0] = reinterpret_cast<uint16_t*>(ws + s.at);
+  e.ldp = pad8(p.inner);
+  e.pp = p.rows * e.ldp;
+  start(c.second, p, p.rows, p.out, p.inner, 1);
+  muon::PrItem& g = c.second.item[0];
+  put_operand(g, true, 0, s, ws, parts);
+  put_operand(g, false, 0, c.ops[3], ws, parts);
+  g.out = p.y;
+  g.ldo = p.ld_y;
+  size_t n1 = 0, n2 = 0;
+  MUON_TRY(lay_out(c.first, true, 2, &n1));
+  MUON_TRY(lay_out(c.second, false, 2, &n2));
+  c.first.partial = c.second.partial = reinterpret_cast<float*>(ws + b.at);
+  c.bytes = b.at + std::max(n1, n2);
+  return MUON_OK;
+}
+
+muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c, char* ws) {
+  Bump b;
+  const int parts = p.dtype == MUON_F32 ? 3 : 1;
+  c.ops[0] = operand(b, g.dy, p.rows, p.out, g.ld_dy, p.dtype);
+  c.ops[1] = operand(b, p.w_down, p.out, p.inner, p.inner, p.dtype);
+  c.ops[2] = operand(b, p.w_gate, p.inner, p.width, p.width, p.dtype);
+  c.ops[3] = operand(b, p.w_up, p.inner, p.width, p.width, p.dtype);
+  c.n_ops = g.d_x ? 4 : 2;
+  // da and db feed the next product as they are, or from the workspace, both alike
+  void* d[2] = {g.d_a, g.d_b};
+  const int64_t ld[2] = {g.ld_d_a, g.ld_d_b};
+  const bool same = in_place(d[0], p.inner, ld[0], p.dtype) && in_place(d[1], p.inner, ld[1], p.dtype) && ld[0] == ld[1];
+  start(c.first, p, p.rows, p.inner, p.out, 1);
+  muon::PrItem& f = c.first.item[0];
+  put_operand(f, true, 0, c.ops[0], ws, parts);
+  put_operand(f, false, 0, c.ops[1], ws, parts);
+  muon::PrMlp& e = c.first.mlp;
+  e.a = p.a;
+  e.b = p.b;
+  e.ldp = pad8(p.inner);
+  e.pp = p.rows * e.ldp;
+  start(c.second, p, p.rows, p.width, p.inner, 2);
+  muon::PrItem& s = c.second.item[0];
+  for (int i = 0; i < 2; ++i) {
+    e.d[i] = d[i];
+    e.ldd[i] = ld[i];
+    Operand o{d[i], p.rows, p.inner, ld[i], !same, 0};
+    if (!same) {
+      o.at = b.take(planes_bytes(p.rows, p.inner, parts));
+      if (g.d_x) e.plane[i] = reinterpret_cast<uint16_t*>(ws + o.at);
+    }
+    put_operand(s, true, i, o, ws, parts);
+    put_operand(s, false, i, c.ops[2 + i], ws, parts);
+  }
+  s.out = g.d_x;
+  s.ldo = g.ld_d_x;
+  size_t n1 = 0, n2 = 0;
+  MUON_TRY(lay_out(c.first, false, 2, &n1));
+  MUON_TRY(lay_out(c.second, false, 2, &n2));
+  c.first.partial = c.second.partial = reinterpret_cast<float*>(ws + b.at);
+  c.bytes = b.at + std::max(n1, n2);
+  return MUON_OK;
+}
+
+// The most that either pass takes, every operand rewritten.
+muon_status mlp_workspace(const muon_mlp& p, size_t* bytes) {
+  MUON_TRY(check_mlp(p));
+  muon_mlp q = p;
+  q.x = q.w_gate = q.w_up = q.w_down = reinterpret_cast<const void*>(uintptr_t(2));
+  q.y = reinterpret_cast<void*>(uintptr_t(2));
+  q.ld_x = q.width;
+  q.ld_y = q.out;
+  muon_mlp_grads g{};
+  g.dy = q.x;
+  g.d_x = g.d_a = g.d_b = q.y;
+  g.ld_dy = q.out;
+  g.ld_d_x = q.width;
+  g.ld_d_a = g.ld_d_b = q.inner;
+  *bytes = 0;
+  if (p.rows == 0) return MUON_OK;
+  MlpCall f, b;
+  MUON_TRY(plan_forward(q, f, nullptr));
+  MUON_TRY(plan_backward(q, g, b, nullptr));
+  *bytes = std::max(f.bytes, b.bytes);
+  return MUON_OK;
+}
+
+muon_status check_mlp_workspace(Views& v, const muon_mlp& p, size_t need) {
+  if (!need) return MUON_OK;
+  if (p.workspace_bytes < need)
+    return fail(MUON_ERR_INVALID_ARG, "the workspace has " + std::to_string(p.workspace_bytes) + " bytes, " +
+                                          std::to_string(need) + " are needed");
+  if (!p.workspace) return fail(MUON_ERR_INVALID_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(p.workspace) % 16) return fail(MUON_ERR_ALIGN, "workspace is not 16-byte aligned");
+  return v.add_range(p.workspace, need, "workspace");
+}
+
+muon_status run_packs(const MlpCall& c, const muon_mlp& p, char* ws, hipStream_t s) {
+  for (int i = 0; i < c.n_ops; ++i)
+    if (c.ops[i].pack)
+      MUON_TRY(hip_status(muon::launch_wgrad_pack(c.ops[i].p, c.ops[i].ld, p.dtype, ws + c.ops[i].at, int32_t(c.ops[i].rows),
+                                                  int32_t(c.ops[i].cols), pad8(c.ops[i].cols), s)));
+  return MUON_OK;
+}
+
+muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
+  if (!mlp) return fail(MUON_ERR_INVALID_ARG, "mlp is NULL");
+  const muon_mlp& p = *mlp;
+  MUON_TRY(check_mlp(p));
+  Views v;
+  MUON_TRY(check_mlp_weights(v, p));
+  const int e = elem_of(p.dtype);
+  MUON_TRY(v.add(p.x, p.rows, p.width, p.ld_x, e, false, "x"));
+  if (!p.y && !p.a.q && !p.b.q && !p.s.q && p.rows > 0) return fail(MUON_ERR_INVALID_ARG, "y, a, b and s are all NULL");
+  if (p.y) MUON_TRY(v.add(p.y, p.rows, p.out, p.ld_y, e, true, "y"));
+  if (p.a.q) MUON_TRY(check_inner(v, p, p.a, true, "a"));
+  if (p.b.q) MUON_TRY(check_inner(v, p, p.b, true, "b"));
+  if (p.s.q) MUON_TRY(check_inner(v, p, p.s, true, "s"));
+  if (p.rows == 0) return v.disjoint();
+  char* ws = static_cast<char*>(p.workspace);
+  MlpCall c;
+  MUON_TRY(plan_forward(p, c, ws));
+  MUON_TRY(check_mlp_workspace(v, p, c.bytes));
+  MUON_TRY(v.disjoint());
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  MUON_TRY(run_packs(c, p, ws, s));
+  MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGate, false, s)));
+  return p.y ? hip_status(muon::launch_mlp(c.second, muon::kPrStore, false, s)) : MUON_OK;
+}
+
+muon_status mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void* stream) {
+  if (!mlp || !grads) return fail(MUON_ERR_INVALID_ARG, "mlp or grads is NULL");
+  const muon_mlp& p = *mlp;
+  const muon_mlp_grads& g = *grads;
+  MUON_TRY(check_mlp(p));
+  Views v;
+  MUON_TRY(check_mlp_weights(v, p));
+  const int e = elem_of(p.dtype);
+  MUON_TRY(v.add(g.dy, p.rows, p.out, g.ld_dy, e, false, "dy"));
+  MUON_TRY(check_inner(v, p, p.a, false, "a"));
+  MUON_TRY(check_inner(v, p, p.b, false, "b"));
+  MUON_TRY(v.add(g.d_a, p.rows, p.inner, g.ld_d_a, e, true, "d_a"));
+  MUON_TRY(v.add(g.d_b, p.rows, p.inner, g.ld_d_b, e, true, "d_b"));
+  if (g.d_x) MUON_TRY(v.add(g.d_x, p.rows, p.width, g.ld_d_x, e, true, "d_x"));
+  if (p.rows == 0) return v.disjoint();
+  char* ws = static_cast<char*>(p.workspace);
+  MlpCall c;
+  MUON_TRY(plan_backward(p, g, c, ws));
+  MUON_TRY(check_mlp_workspace(v, p, c.bytes));
+  MUON_TRY(v.disjoint());
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  MUON_TRY(run_packs(c, p, ws, s));
+  MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGateGrad, true, s)));
+  return g.d_x ? hip_status(muon::launch_mlp(c.second, muon::kPrStore, true, s)) : MUON_OK;
+}
+
+// ------------------------------------------------------------ the 8-bit product
+
+muon_status check_w8(Views& v, const muon_w8& w, bool q, bool qt, bool written, const char* name, int item = -1) {
+  const std::string at = Views::at(item) + name;
+  if (w.n < 1 || w.n > kMaxCols || w.k < 1 || w.k > kMaxCols) return fail(MUON_ERR_INVALID_ARG, at + ": n and k must be in [1, 2^24]");
+  if (ceil_div(w.n, muon::kBlock) * ceil_div(w.k, muon::kBlock) > (int64_t(1) << 30))
+    return fail(MUON_ERR_INVALID_ARG, at + ": more than 2^30 blocks");
+  if (q) {
+    if (w.ldq % 16) return fail(MUON_ERR_ALIGN, at + ": ldq must be a multiple of 16");
+    MUON_TRY(v.add(w.q, w.n, (w.k + 15) / 16 * 16, w.ldq, 1, written, name, item, 16));
+  }
+  if (qt) {
+    if (!w.qt) return fail(MUON_ERR_INVALID_ARG, at + ".qt is NULL");
+    if (w.ldqt % 16) return fail(MUON_ERR_ALIGN, at + ": ldqt must be a multiple of 16");
+    MUON_TRY(v.add(w.qt, w.k, (w.n + 15) / 16 * 16, w.ldqt, 1, written, name, item, 16));
+  }
+  return v.add(w.e, ceil_div(w.n, muon::kBlock), ceil_div(w.k, muon::kBlock), w.lde, 1, written, name, item);
+}
+
+muon_status w8_call(const void* w, int64_t ldw, int32_t dtype, const muon_w8* p, bool save, void* stream) {
+  return guarded([&]() -> muon_status {
+    if (!p) return fail(MUON_ERR_INVALID_ARG, "the 8-bit weight is NULL");
+    MUON_TRY(check_dtype(dtype));
+    Views v;
+    MUON_TRY(check_w8(v, *p, true, save && p->qt, save, "weight"));
+    MUON_TRY(v.add(w, p->n, p->k, ldw, elem_of(dtype), !save, "w"));
+    MUON_TRY(v.disjoint());
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return hip_status(save ? muon::launch_w8_save(w, ldw, dtype, *p, s)
+                           : muon::launch_w8_load(*p, const_cast<void*>(w), ldw, dtype, s));
+  });
+}
+
+muon_status check_linear8(const muon_linear8_item* items, int32_t n, int32_t dtype, Views& v) {
+  if (!items) return fail(MUON_ERR_INVALID_ARG, "items is NULL");
+  if (n < 1) return fail(MUON_ERR_INVALID_ARG, "n_items must be >= 1");
+  MUON_TRY(check_dtype(dtype));
+  const int e = elem_of(dtype);
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_linear8_item& it = items[i];
+    const bool t = it.transposed != 0;
+    MUON_TRY(check_q8(v, it.x, false, "x", i));
+    if (it.x.kind != MUON_Q8_E4M3) return fail(MUON_ERR_UNSUPPORTED, Views::at(i) + "x must be an e4m3 checkpoint");
+    MUON_TRY(check_w8(v, it.w, !t, t, false, "w", i));
+    const int64_t k = t ? it.w.n : it.w.k, out = t ? it.w.k : it.w.n;
+    if (it.x.cols != k)
+      return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "x has " + std::to_string(it.x.cols) + " columns, the weight " + std::to_string(k));
+    MUON_TRY(v.add(it.y, it.x.rows, out, it.ld_y, e, true, "y", i));
+    if (!std::isfinite(it.beta)) return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "beta is not finite");
+    if (it.beta != 0.f && it.c == it.y && it.ld_c != it.ld_y)
+      return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "c is y, with another row stride");
+    if (it.beta != 0.f && it.c != it.y) MUON_TRY(v.add(it.c, it.x.rows, out, it.ld_c, e, false, "c", i));
+  }
+  return v.disjoint();
+}
+
+// The launches, of 16 items each, and the workspace of the largest: they follow each
+// other on one stream and share it. Items without rows have nothing to do.
+muon_status plan_linear8(const muon_linear8_item* items, int32_t n, int32_t dtype, std::vector<muon::PrArgs>& plans, size_t* bytes) {
+  *bytes = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_linear8_item& it = items[i];
+    if (it.x.rows == 0) continue;
+    if (plans.empty() || plans.back().n_items == muon::kPrItems) plans.push_back(muon::PrArgs{});
+    muon::PrArgs& a = plans.back();
+    muon::PrItem& d = a.item[a.n_items++];
+    const bool t = it.transposed != 0;
+    a.parts = 1;
+    a.f32 = dtype == MUON_F32;
+    d.a[0] = static_cast<const uint8_t*>(it.x.q);
+    d.lda = it.x.ldq;
+    d.ea = static_cast<const uint8_t*>(it.x.e);
+    d.lde = it.x.lde;
+    d.b[0] = static_cast<const uint8_t*>(t ? it.w.qt : it.w.q);
+    d.ldb = t ? it.w.ldqt : it.w.ldq;
+    d.eb = static_cast<const uint8_t*>(it.w.e);
+    d.ldeb_n = t ? 1 : it.w.lde;
+    d.ldeb_k = t ? it.w.lde : 1;
+    d.m = int32_t(it.x.rows);
+    d.n = int32_t(t ? it.w.k : it.w.n);
+    d.k = int32_t(t ? it.w.n : it.w.k);
+    d.sums = 1;
+    d.out = it.y;
+    d.ldo = it.ld_y;
+    d.c = it.c;
+    d.ldc = it.ld_c;
+    d.beta = it.beta;
+  }
+  for (muon::PrArgs& a : plans) {
+    size_t need = 0;
+    MUON_TRY(lay_out(a, false, 1, &need));
+    *bytes = std::max(*bytes, need);
+  }
+  return MUON_OK;
+}
+
+muon_status linear8(const muon_linear8_item* items, int32_t n, int32_t dtype, void* ws, size_t ws_bytes, void* stream) {
+  Views v;
+  MUON_TRY(check_linear8(items, n, dtype, v));
+  std::vector<muon::PrArgs> plans;
+  size_t need = 0;
+  MUON_TRY(plan_linear8(items, n, dtype, plans, &need));
+  if (need) {
+    if (ws_bytes < need)
+      return fail(MUON_ERR_INVALID_ARG, "the workspace has " + std::to_string(ws_bytes) + " bytes, " + std::to_string(need) + " are needed");
+    if (!ws) return fail(MUON_ERR_INVALID_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(ws) % 16) return fail(MUON_ERR_ALIGN, "workspace is not 16-byte aligned");
+    MUON_TRY(v.add_range(ws, need, "workspace"));
+    MUON_TRY(v.disjoint());
+  }
+  for (muon::PrArgs& a : plans) {
+    a.partial = static_cast<float*>(ws);
+    MUON_TRY(hip_status(muon::launch_linear8(a, static_cast<hipStream_t>(stream))));
+  }
+  return MUON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_mlp_forward(const muon_mlp* mlp, void* stream) {
+  return guarded([&] { return mlp_forward(mlp, stream); });
+}
+
+muon_status muon_mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void* stream) {
+  return guarded([&] { return mlp_backward(mlp, grads, stream); });
+}
+
+muon_status muon_mlp_workspace(const muon_mlp* mlp, size_t* bytes) {
+  return guarded([&]() -> muon_status {
+    if (!mlp || !bytes) return fail(MUON_ERR_INVALID_ARG, "mlp or bytes is NULL");
+    return mlp_workspace(*mlp, bytes);
+  });
+}
+
+muon_status muon_w8_save(const void* w, int64_t ldw, int32_t dtype, const muon_w8* out, void* stream) {
+  return w8_call(w, ldw, dtype, out, true, stream);
+}
+
+muon_status muon_w8_load(const muon_w8* in, void* w, int64_t ldw, int32_t dtype, void* stream) {
+  return w8_call(w, ldw, dtype, in, false, stream);
+}
+
+muon_status muon_linear8(const muon_linear8_item* items, int32_t n_items, int32_t dtype, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  return guarded([&] { return linear8(items, n_items, dtype, workspace, workspace_bytes, stream); });
+}
+
+muon_status muon_linear8_workspace(const muon_linear8_item* items, int32_t n_items, int32_t dtype, size_t* bytes) {
+  return guarded([&]() -> muon_status {
+    if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+    Views v;
+    MUON_TRY(check_linear8(items, n_items, dtype, v));
+    std::vector<muon::PrArgs> plans;
+    return plan_linear8(items, n_items, dtype, plans, bytes);
+  });
+}
+
+}  // extern "C"

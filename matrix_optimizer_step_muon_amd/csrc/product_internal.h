@@ -1,0 +1,81 @@
+// Descriptors shared by the host side of the layers' products (product_api.cpp)
+// and their kernels (mlp_kernels.hip, linear8_kernels.hip): C[m][n] = sum_k
+// A[m][k] B[n][k], or B[k][n].
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "muon.h"
+
+namespace muon {
+
+constexpr int kPrItems = 16;   // products per launch
+constexpr int kBlock = 128;    // edge of a weight's 8-bit block
+
+// Tiles that a launch's products are cut into.
+enum PrTile { kPrLarge = 0, kPrMedium = 1, kPrSmall = 2, kPrTiles = 3 };
+constexpr int kPrEdge[kPrTiles] = {256, 128, 64};
+
+// What becomes of a product.
+enum PrEpilogue {
+  kPrStore = 0,    // C (+ beta * another matrix), rounded
+  kPrGate = 1,     // two products a, b side by side: s = act(a) * b, and checkpoints of a, b and s
+  kPrGateGrad = 2  // ds, with the checkpoints of a and b: da = ds * b * act'(a), db = ds * act(a)
+};
+
+// One product of a launch. A sum may run over several pairs of matrices of the
+// same shapes: a[0] b[0]^T + a[1] b[1]^T (`sums` 2), and fp32 ones over pairs of
+// bf16 planes that add up to them (`parts` 3: planes lo, mid, hi, pa and pb bytes
+// apart). kPrGate: b[0] and b[1] are the two projections.
+struct PrItem {
+  const uint8_t* a[2];
+  const uint8_t* b[2];
+  int64_t lda, ldb;          // bytes; 16-byte aligned rows
+  int64_t pa, pb;
+  const uint8_t *ea, *eb;    // 8-bit operands: exponent bytes
+  int64_t lde, ldeb_n, ldeb_k;  // of A's rows; of B's blocks, along n and along k
+  int32_t m, n, k;
+  int32_t sums;
+  int32_t tiles_m, tiles_n;
+  int32_t splits;            // > 1: partial tiles go to the workspace
+  int32_t part0;             // first partial tile of this item in the workspace
+  // kPrStore
+  void* out;
+  const void* c;
+  int64_t ldo, ldc;
+  float beta;
+  int32_t reserved;
+};
+
+// The gated block's epilogues.
+struct PrMlp {
+  muon_q8 a, b, s;           // q null: not wanted (kPrGate)
+  uint16_t* plane[2];        // bf16 operands of the next product: s, or da and db; null: none
+  int64_t ldp, pp;           // their row stride and the distance of their planes, elements
+  void* d[2];                // kPrGateGrad: da, db as the caller wants them
+  int64_t ldd[2];
+  int32_t act;
+  int32_t reserved;
+};
+
+struct PrArgs {
+  int32_t unit0[kPrItems];   // each item's first unit (tiles x splits); past the last item INT32_MAX
+  PrItem item[kPrItems];
+  PrMlp mlp;
+  float* partial;
+  int32_t n_items, units;
+  int32_t parts;             // 1, or 3
+  int32_t f32;               // dtype of out, c and d
+  int32_t tile;              // PrTile
+  int32_t reserved;
+};
+
+static_assert(sizeof(PrArgs) <= 4000, "kernel arguments");
+
+hipError_t launch_mlp(const PrArgs& args, int epilogue, bool transposed_b, hipStream_t s);
+hipError_t launch_linear8(const PrArgs& args, hipStream_t s);
+hipError_t launch_w8_save(const void* w, int64_t ldw, int dtype, const muon_w8& out, hipStream_t s);
+hipError_t launch_w8_load(const muon_w8& in, void* w, int64_t ldw, int dtype, hipStream_t s);
+
+}  // namespace muon

@@ -1,6 +1,7 @@
 """The layer operators of libmuon.so (include/muon.h): 8-bit activation
-checkpoints, the norm sites between blocks, and the weight gradients that the
-optimizer step reads.
+checkpoints, the norm sites between blocks, the gated feed-forward block, linear
+products in 8-bit floating point, and the weight gradients that the optimizer
+step reads.
 
     site = layer.NormSite(branch, residual, w_pre, w_post=w, gate=g)
     site.forward()                          # site.y, site.h; checkpoints site.u, site.v
@@ -8,7 +9,16 @@ optimizer step reads.
     site.backward(dy, dh)                   # site.d_residual, site.d_branch, site.d_w_pre, ...
     layer.WGrad([(dY, site.u, G, w_pre)]).run()   # G = dY^T (u * w_pre), for muon.Plan
 
-Like the optimizer's plans, ``NormSite`` and ``WGrad`` take their tensors once
+    mlp = layer.GatedMLP(site.h, w_gate, w_up, w_down, out=next_branch)
+    mlp.forward()                           # mlp.y; checkpoints mlp.a, mlp.b, mlp.s
+    mlp.backward(dy)                        # mlp.d_x, mlp.d_a, mlp.d_b
+    layer.WGrad(mlp.wgrad_items(dy, site.u, g_gate, g_up, g_down, scale=w_pre)).run()
+
+    w8 = layer.w8_save(W, layer.W8(n, k))   # after every step
+    layer.Linear8([(x8, w8, y)]).run()      # y = x W^T
+    layer.Linear8([(dy8, w8, dx)], transposed=True).run()   # dx = dy W
+
+Like the optimizer's plans, ``NormSite``, ``GatedMLP``, ``Linear8`` and ``WGrad`` take their tensors once
 and keep them referenced; every call after that only launches kernels, on the
 current stream or the one it is given (a torch stream or a raw handle). They may
 be dropped while a stream still works on their buffers. Each has one set of
@@ -24,11 +34,13 @@ from typing import Iterable, List, Optional, Sequence
 
 import torch
 
-from .muon import (MUON_BF16, MUON_F32, MuonError, check, lib, muon_norm_grads, muon_norm_site, muon_q8,
-                   muon_wgrad_item)
+from .muon import (MUON_BF16, MUON_F32, MuonError, check, lib, muon_linear8_item, muon_mlp, muon_mlp_grads,
+                   muon_norm_grads, muon_norm_site, muon_q8, muon_w8, muon_wgrad_item)
 
 GROUP = 32
+BLOCK = 128
 KINDS = {"int8": 0, "e4m3": 1}
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 _CODES = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32}
 
 
@@ -326,3 +338,171 @@ class WGrad:
         tile, pieces = (ctypes.c_int32 * self._n)(), (ctypes.c_int32 * self._n)()
         check(lib().muon_wgrad_info(self._items, self._n, self._dtype, self._gdtype, tile, pieces))
         return [{"tile": t, "pieces": p} for t, p in zip(tile, pieces)]
+
+
+class GatedMLP:
+    """The gated feed-forward block (muon_mlp):
+
+        a = x Wgate^T,  b = x Wup^T,  s = act(a) * b,  y = s Wdown^T
+
+    ``x`` is rows x width, bf16 or fp32; ``w_gate`` and ``w_up`` (inner x width)
+    and ``w_down`` (out x inner) have its type and are contiguous, as
+    ``muon.Plan`` takes them. ``act``: "silu", "gelu", "gelu_tanh" or "relu".
+    ``out`` receives y (a new tensor otherwise): the branch of the next norm
+    site, say. With a ``kind`` ("int8" or "e4m3") the forward pass keeps the
+    checkpoints ``a`` and ``b``, which the backward pass needs, and ``s``, the
+    saved input of w_down; with None it keeps nothing. ``saved``: (a, b) or (a,
+    b, s) to use in place of new ones.
+
+    ``forward()`` writes ``y``. ``backward(dy)`` writes ``d_x``, ``d_a`` and
+    ``d_b``, the gradients of x and of the two projections; ``need_d_x=False``
+    leaves d_x out. ``wgrad_items`` are the weight gradients' items for
+    ``WGrad``."""
+
+    def __init__(self, x, w_gate, w_up, w_down, *, act: str = "silu", kind: Optional[str] = "int8", saved=None, out=None,
+                 need_d_x: bool = True):
+        if act not in ACTS:
+            raise MuonError(-4, f"act must be one of {sorted(ACTS)}, not {act!r}")
+        _matrix(x, "x")
+        code, dt = _code(x), x.dtype
+        rows, width = x.shape
+        _matrix(w_gate, "w_gate", dtype=dt)
+        inner = w_gate.shape[0]
+        _matrix(w_gate, "w_gate", (inner, width), dt)
+        _matrix(w_up, "w_up", (inner, width), dt)
+        _matrix(w_down, "w_down", dtype=dt)
+        if w_down.shape[1] != inner:
+            _bad(f"w_down has {w_down.shape[1]} columns, w_gate {inner} rows")
+        for t, name in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
+            if not t.is_contiguous():
+                _bad(f"{name} must be contiguous")
+        cols = w_down.shape[0]
+        if out is not None:
+            _matrix(out, "out", (rows, cols), dt)
+        self.x, self.w_gate, self.w_up, self.w_down, self.act = x, w_gate, w_up, w_down, act
+        new = lambda n: torch.empty(rows, n, dtype=dt, device=x.device)  # noqa: E731
+        self.y = new(cols) if out is None else out
+        self.a = self.b = self.s = self.d_x = self.d_a = self.d_b = None
+        if saved is not None:
+            self.a, self.b, self.s = tuple(saved) + (None,) * (3 - len(saved))
+        elif kind is not None:
+            self.a, self.b, self.s = (Q8(rows, inner, kind) for _ in range(3))
+        for q, name in ((self.a, "a"), (self.b, "b"), (self.s, "s")):
+            if q is not None and (q.rows, q.cols) != (rows, inner):
+                _bad(f"{name} must be a checkpoint of {rows} x {inner}")
+        kept = [q for q in (self.a, self.b, self.s) if q is not None]
+        self._grads = None
+        if self.a is not None and self.b is not None:
+            self.d_a, self.d_b, self.d_x = new(inner), new(inner), new(width) if need_d_x else None
+            self._grads = muon_mlp_grads(None, 0, _ptr(self.d_x), width, self.d_a.data_ptr(), inner, self.d_b.data_ptr(), inner)
+        none = muon_q8()
+        self._c = muon_mlp(rows, width, inner, cols, x.data_ptr(), _ld(x), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+                           self.y.data_ptr(), _ld(self.y), *(none if q is None else q._c for q in (self.a, self.b, self.s)),
+                           None, 0, ACTS[act], code)
+        need = ctypes.c_size_t()
+        check(lib().muon_mlp_workspace(ctypes.byref(self._c), ctypes.byref(need)))
+        self.workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+        self._c.workspace, self._c.workspace_bytes = self.workspace.data_ptr(), need.value
+        self._streams = _Streams([t for t in (x, w_gate, w_up, w_down, self.y, self.d_x, self.d_a, self.d_b, self.workspace)
+                                  if t is not None] + [t for q in kept for t in (q.q, q.e)])
+
+    def forward(self, stream=None) -> None:
+        check(lib().muon_mlp_forward(ctypes.byref(self._c), self._streams.use(stream)))
+
+    def backward(self, dy, stream=None) -> None:
+        if self._grads is None:
+            _bad("the block keeps no checkpoints: make it with a kind")
+        _matrix(dy, "dy", tuple(self.y.shape), self.y.dtype)
+        g = self._grads
+        g.dy, g.ld_dy = dy.data_ptr(), _ld(dy)
+        check(lib().muon_mlp_backward(ctypes.byref(self._c), ctypes.byref(g), self._streams.use(stream, (dy,))))
+
+    def wgrad_items(self, dy, x: Q8, g_gate, g_up, g_down, *, scale=None, beta: float = 0.0) -> List:
+        """Items for ``WGrad``: the gradients of w_gate and w_up from the checkpoint
+        ``x`` of the block's input (times ``scale``, where x keeps the normalised
+        rows before a norm's weight), that of w_down from ``s``. dy is what
+        backward gets; the items hold d_a and d_b, which it writes."""
+        if self._grads is None or self.s is None:
+            _bad("the block keeps no checkpoints: make it with a kind")
+        return [(self.d_a, x, g_gate, scale, beta), (self.d_b, x, g_up, scale, beta), (dy, self.s, g_down, None, beta)]
+
+
+class W8:
+    """An n x k weight in 8 bits: e4m3 with one power of two per block of 128 x
+    128 (muon_w8). ``q`` (n x a multiple of 16) and ``e`` (one byte per block), and
+    ``qt``, the same bytes transposed, for products with W itself; with
+    ``transposed=False`` it holds none."""
+
+    def __init__(self, n: int, k: int, transposed: bool = True):
+        if n < 1 or k < 1:
+            _bad("an 8-bit weight needs n >= 1 and k >= 1")
+        self.n, self.k = int(n), int(k)
+        dev = torch.device("cuda", torch.cuda.current_device())
+        up = lambda v, m: -(-v // m) * m  # noqa: E731
+        self.q = torch.empty(n, up(k, 16), dtype=torch.uint8, device=dev)
+        self.qt = torch.empty(k, up(n, 16), dtype=torch.uint8, device=dev) if transposed else None
+        self.e = torch.empty(-(-n // BLOCK), -(-k // BLOCK), dtype=torch.uint8, device=dev)
+        self._c = muon_w8(self.q.data_ptr(), _ptr(self.qt), self.e.data_ptr(), self.n, self.k, up(k, 16), up(n, 16), self.e.shape[1])
+        self._streams = _Streams(self.tensors())
+
+    def tensors(self) -> List:
+        return [t for t in (self.q, self.qt, self.e) if t is not None]
+
+    def nbytes(self) -> int:
+        return sum(t.numel() for t in self.tensors())
+
+
+def w8_save(w, out: W8, stream=None) -> W8:
+    """Saves w (bf16 or fp32) into ``out``, in both orientations."""
+    _matrix(w, "w", (out.n, out.k))
+    check(lib().muon_w8_save(w.data_ptr(), _ld(w), _code(w), ctypes.byref(out._c), out._streams.use(stream, (w,))))
+    return out
+
+
+def w8_load(w8: W8, out, stream=None):
+    """Writes the values that the weight stands for into ``out`` (bf16, which holds
+    them exactly, or fp32)."""
+    _matrix(out, "out", (w8.n, w8.k))
+    check(lib().muon_w8_load(ctypes.byref(w8._c), out.data_ptr(), _ld(out), _code(out), w8._streams.use(stream, (out,))))
+    return out
+
+
+class Linear8:
+    """Products of linear layers in 8-bit floating point, all in one go
+    (muon_linear8). Every item is ``(x, w, y[, beta[, C]])``:
+
+        y = x W^T + beta * C        (transposed: y = x W + beta * C)
+
+    with x an e4m3 Q8 checkpoint, w a W8, y bf16 or fp32 (the same for every
+    item), C like y (default: y itself, to accumulate)."""
+
+    def __init__(self, items: Iterable[Sequence], transposed: bool = False):
+        tensors: List = []
+        descs = []
+        dt = self._dtype = None
+        for item in items:
+            x, w, y = item[:3]
+            beta, C = (list(item[3:]) + [0.0, None][len(item) - 3:])[:2]
+            if not isinstance(x, Q8) or not isinstance(w, W8):
+                _bad("an item starts with a Q8 checkpoint and a W8 weight")
+            if dt is None:
+                self._dtype, dt = _code(y), y.dtype
+            shape = (x.rows, w.k if transposed else w.n)
+            _matrix(y, "y", shape, dt)
+            C = y if C is None else C
+            if C is not y:
+                _matrix(C, "C", shape, dt)
+            descs.append(muon_linear8_item(x._c, w._c, y.data_ptr(), _ld(y), C.data_ptr(), _ld(C), float(beta), int(bool(transposed))))
+            tensors += [x.q, x.e, *w.tensors(), y, C]
+        if not descs:
+            _bad("no items")
+        self._n = len(descs)
+        self._items = (muon_linear8_item * self._n)(*descs)
+        need = ctypes.c_size_t()
+        check(lib().muon_linear8_workspace(self._items, self._n, self._dtype, ctypes.byref(need)))
+        self.workspace = torch.empty(need.value, dtype=torch.uint8, device=tensors[0].device)
+        self._streams = _Streams(tensors + [self.workspace])
+
+    def run(self, stream=None) -> None:
+        check(lib().muon_linear8(self._items, self._n, self._dtype, self.workspace.data_ptr(), self.workspace.numel(),
+                                 self._streams.use(stream)))

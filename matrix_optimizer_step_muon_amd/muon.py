@@ -71,6 +71,30 @@ class muon_wgrad_item(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class muon_mlp(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("inner", ctypes.c_int64), ("out", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+                ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("a", muon_q8), ("b", muon_q8), ("s", muon_q8),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class muon_mlp_grads(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("d_x", ctypes.c_void_p), ("ld_d_x", ctypes.c_int64),
+                ("d_a", ctypes.c_void_p), ("ld_d_a", ctypes.c_int64), ("d_b", ctypes.c_void_p), ("ld_d_b", ctypes.c_int64)]
+
+
+class muon_w8(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("qt", ctypes.c_void_p), ("e", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("k", ctypes.c_int64), ("ldq", ctypes.c_int64), ("ldqt", ctypes.c_int64), ("lde", ctypes.c_int64)]
+
+
+class muon_linear8_item(ctypes.Structure):
+    _fields_ = [("x", muon_q8), ("w", muon_w8), ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("c", ctypes.c_void_p),
+                ("ld_c", ctypes.c_int64), ("beta", ctypes.c_float), ("transposed", ctypes.c_int32)]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"muon: {STATUS_NAMES.get(status, status)}: {message}")
@@ -87,7 +111,9 @@ EXPORTS = ("muon_hparams_default", "muon_plan", "muon_plan_workspace_bytes", "mu
            "muon_dp_partition_static", "muon_dp_partition", "muon_tp_micro_groups", "muon_mfma_probe",
            "muon_step_noalloc",
            "muon_q8_save", "muon_q8_load", "muon_norm_forward", "muon_norm_backward",
-           "muon_norm_backward_workspace", "muon_wgrad", "muon_wgrad_workspace", "muon_wgrad_info")
+           "muon_norm_backward_workspace", "muon_wgrad", "muon_wgrad_workspace", "muon_wgrad_info",
+           "muon_mlp_forward", "muon_mlp_backward", "muon_mlp_workspace", "muon_w8_save", "muon_w8_load", "muon_linear8",
+           "muon_linear8_workspace")
 
 
 def lib() -> ctypes.CDLL:
@@ -133,6 +159,13 @@ def lib() -> ctypes.CDLL:
                                        ctypes.POINTER(ctypes.c_size_t)]
     L.muon_wgrad_info.argtypes = [ctypes.POINTER(muon_wgrad_item), c_i32, c_i32, c_i32, ctypes.POINTER(c_i32),
                                   ctypes.POINTER(c_i32)]
+    L.muon_mlp_forward.argtypes = [ctypes.POINTER(muon_mlp), c_vp]
+    L.muon_mlp_backward.argtypes = [ctypes.POINTER(muon_mlp), ctypes.POINTER(muon_mlp_grads), c_vp]
+    L.muon_mlp_workspace.argtypes = [ctypes.POINTER(muon_mlp), ctypes.POINTER(ctypes.c_size_t)]
+    L.muon_w8_save.argtypes = [c_vp, c_i64, c_i32, ctypes.POINTER(muon_w8), c_vp]
+    L.muon_w8_load.argtypes = [ctypes.POINTER(muon_w8), c_vp, c_i64, c_i32, c_vp]
+    L.muon_linear8.argtypes = [ctypes.POINTER(muon_linear8_item), c_i32, c_i32, c_vp, ctypes.c_size_t, c_vp]
+    L.muon_linear8_workspace.argtypes = [ctypes.POINTER(muon_linear8_item), c_i32, c_i32, ctypes.POINTER(ctypes.c_size_t)]
     for name in EXPORTS:
         if name != "muon_last_error":
             getattr(L, name).restype = c_int
