@@ -15,7 +15,7 @@ namespace muon {
 template <class Z>
 __global__ void __launch_bounds__(Z::NT, Z::WG) linear8_kernel(PrArgs) {
   __shared__ __align__(1024) unsigned char smem[Z::LDS];
-  pr_unit_of<Z, PrStoreOut>(smem);
+  pr_run<Z, PrStoreOut>(smem);
 }
 
 __global__ void __launch_bounds__(256) linear8_join_kernel(PrArgs, int edge) { pr_join_of<PrStoreOut>(edge); }
@@ -25,10 +25,10 @@ static hipError_t launch_tiles(const PrArgs& args, hipStream_t s) {
   typedef PrCfg<256, 256, 128, 2, MODE, 1> Large;
   typedef PrCfg<128, 128, 128, 2, MODE, 2> Medium;
   typedef PrCfg<64, 64, 128, 4, MODE, 2> Small;
-  const dim3 grid(args.units), block(256);
-  if (args.tile == kPrLarge) hipLaunchKernelGGL(linear8_kernel<Large>, grid, block, 0, s, args);
-  else if (args.tile == kPrMedium) hipLaunchKernelGGL(linear8_kernel<Medium>, grid, block, 0, s, args);
-  else hipLaunchKernelGGL(linear8_kernel<Small>, grid, block, 0, s, args);
+  const dim3 block(256);
+  if (args.tile == kPrLarge) hipLaunchKernelGGL(linear8_kernel<Large>, dim3(pr_grid<Large>(args)), block, 0, s, args);
+  else if (args.tile == kPrMedium) hipLaunchKernelGGL(linear8_kernel<Medium>, dim3(pr_grid<Medium>(args)), block, 0, s, args);
+  else hipLaunchKernelGGL(linear8_kernel<Small>, dim3(pr_grid<Small>(args)), block, 0, s, args);
   const hipError_t e = hipGetLastError();
   const int64_t join = pr_join_blocks(args, false);
   if (e != hipSuccess || join == 0) return e;

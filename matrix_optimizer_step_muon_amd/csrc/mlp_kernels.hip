@@ -144,7 +144,7 @@ struct PrGateGradOut {
 template <class Z, class Out>
 __global__ void __launch_bounds__(Z::NT, Z::WG) mlp_product_kernel(PrArgs) {
   __shared__ __align__(1024) unsigned char smem[Z::LDS];
-  pr_unit_of<Z, Out>(smem);
+  pr_run<Z, Out>(smem);
 }
 
 template <class Out>
@@ -157,10 +157,10 @@ static hipError_t launch_tiles(const PrArgs& args, hipStream_t s) {
   typedef PrCfg<256, 256, 128, 2, MODE, 1> Large;
   typedef PrCfg<128, 128, 128, 2, MODE, 2> Medium;
   typedef PrCfg<64, 64, 128, 4, MODE, 2> Small;
-  const dim3 grid(args.units), block(256);
-  if (args.tile == kPrLarge) hipLaunchKernelGGL((mlp_product_kernel<Large, Out>), grid, block, 0, s, args);
-  else if (args.tile == kPrMedium) hipLaunchKernelGGL((mlp_product_kernel<Medium, Out>), grid, block, 0, s, args);
-  else hipLaunchKernelGGL((mlp_product_kernel<Small, Out>), grid, block, 0, s, args);
+  const dim3 block(256);
+  if (args.tile == kPrLarge) hipLaunchKernelGGL((mlp_product_kernel<Large, Out>), dim3(pr_grid<Large>(args)), block, 0, s, args);
+  else if (args.tile == kPrMedium) hipLaunchKernelGGL((mlp_product_kernel<Medium, Out>), dim3(pr_grid<Medium>(args)), block, 0, s, args);
+  else hipLaunchKernelGGL((mlp_product_kernel<Small, Out>), dim3(pr_grid<Small>(args)), block, 0, s, args);
   const hipError_t e = hipGetLastError();
   const int64_t join = pr_join_blocks(args, Out::OPS == 2);
   if (e != hipSuccess || join == 0) return e;

@@ -67,20 +67,18 @@ struct PrCfg {
   // The slot at which the workgroup meets: the last sub-step's fragments are in
   // registers, the next stage must be in LDS.
   static constexpr int MEET = SLOTS - (PER >= 16 ? 4 : PER >= 4 ? 2 : 1);
-  // 8-bit operands: exponents of eight stages (RB = 128: 1024 of K), twice
-  static constexpr int EX_A = 8 * BM * 4, EX_B = 8 * 2 * 4, EX = F8 ? 2 * (EX_A + EX_B) : 0;
+  // 8-bit operands: exponents of eight stages (RB = 128: 1024 of K), for as many runs
+  // of stages as a ring can hold parts of
+  static constexpr int TABS = ST, EX_A = 8 * BM * 4, EX_B = 8 * 2 * 4, EX = F8 ? TABS * (EX_A + EX_B) : 0;
   static constexpr int LDS = RING + EX;
-  static constexpr int PASSES = (BM * BN * 4 + RING - 1) / RING, IPP = FM / PASSES;  // of the epilogue
-  static_assert(KK % 2 == 0 && FM % PASSES == 0 && MEET >= SLOTS - PER && (!F8 || RB == 128), "schedule assumptions");
+  // The tile leaves through the stage that it used last: the others hold the next
+  // tile's first stages.
+  static constexpr int PASSES = BM * BN * 4 / STAGE, IPP = FM / PASSES;
+  static_assert(KK % 2 == 0 && PASSES * IPP == FM && MEET >= SLOTS - PER && (!F8 || RB == 128), "schedule assumptions");
+  static_assert(BM == BN && DA % 2 == 0 && (TABS & (TABS - 1)) == 0, "copies of A and B lie alike");
   typedef std::conditional_t<MODE == kNT8, i32x8, bf16x8> Frag;
 };
 
-// The unit of workgroup b: XCD b % 8 gets a contiguous range of units, so that
-// the tiles that run there together share operand panels in its L2.
-MUON_INLINE int pr_unit(int b, int units) {
-  const int x = b & 7, i = b >> 3, per = units >> 3, rest = units & 7;
-  return x * per + min(x, rest) + i;
-}
 MUON_INLINE int pr_item(PrArgsPtr a, int unit) {
   int idx = 0;
 #pragma unroll
@@ -102,341 +100,26 @@ MUON_INLINE void pr_tile(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
 MUON_INLINE int pr_plane_a(int p) { return p == 0 ? 0 : p == 1 ? 2 : p == 2 ? 1 : p == 3 ? 1 : 2; }
 MUON_INLINE int pr_plane_b(int p) { return p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 : p == 3 ? 2 : p == 4 ? 1 : 2; }
 
-// Sums units of stages [s_begin, s_end) of tile (m0, n0) into acc. DUAL: the tile's
-// first BN/2 columns are columns n0/2.. of b[0], the others the same of b[1].
-template <class Z, bool DUAL>
-MUON_INLINE void pr_sum(PrArgsPtr args, PrItemRef it, int m0, int n0, int s_begin, int s_end, unsigned char* smem,
-                        f32x16 (&acc)[Z::FM][Z::FN]) {
-  constexpr int FM = Z::FM, FN = Z::FN, RB = Z::RB, S = Z::S;
-  const int tid = fresh_tid(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  if (s_begin >= s_end) return;
-
-  // Held in scalar registers: reloaded in the loop, they would make it wait for
-  // every LDS access in flight (scalar loads share that counter).
-  int m = it.m, n = it.n, k = it.k;
-  int64_t lda = it.lda, ldb = it.ldb;
-  asm volatile("" : "+s"(m), "+s"(n), "+s"(k), "+s"(lda), "+s"(ldb));
-  const int kbytes = Z::F8 ? k : 2 * k;              // of an A row; whole 16-byte chunks are readable
-  const int kt = (k + Z::BK - 1) / Z::BK;            // stages of one pair of planes
-  const int pairs = args->parts == 3 ? 6 : 1;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
-
-  // Where a stage is read from: of its pair of planes, K step `ks`.
-  struct Cursor {
-    const uint8_t *a, *b0, *b1;
-    int seg, ks;
-  };
-  auto seat = [&](Cursor& c) __attribute__((always_inline)) {
-    const int sum = c.seg / pairs, p = c.seg - sum * pairs;
-    const int64_t pa = pairs == 6 ? pr_plane_a(p) * it.pa : 0, pb = pairs == 6 ? pr_plane_b(p) * it.pb : 0;
-    c.a = it.a[sum] + pa + (int64_t)m0 * lda;
-    if constexpr (DUAL) {
-      c.b0 = it.b[0] + pb + (int64_t)(n0 >> 1) * ldb;
-      c.b1 = it.b[1] + pb + (int64_t)(n0 >> 1) * ldb;
-    } else if constexpr (Z::NN) {
-      c.b0 = it.b[sum] + pb + 2 * n0;
-    } else {
-      c.b0 = it.b[sum] + pb + (int64_t)n0 * ldb;
-    }
-    c.a += (int64_t)c.ks * RB;
-    c.b0 += Z::NN ? (int64_t)c.ks * Z::BK * ldb : (int64_t)c.ks * RB;
-    if constexpr (DUAL) c.b1 += (int64_t)c.ks * RB;
-  };
-  auto advance = [&](Cursor& c) __attribute__((always_inline)) {
-    if (++c.ks == kt) {
-      c.ks = 0;
-      ++c.seg;
-      seat(c);
-    } else {
-      c.a += RB;
-      c.b0 += Z::NN ? (int64_t)Z::BK * ldb : (int64_t)RB;
-      if constexpr (DUAL) c.b1 += RB;
-    }
-  };
-  const bool ragged = kt * RB != kbytes;             // a plane's last stage is not whole
-  auto short_stage = [&](int ks) __attribute__((always_inline)) { return ragged && ks == kt - 1; };
-
-  // Copy q of an operand fills 1 KB: rows RPI*q .. +RPI-1, lane l slot l % S of row
-  // l / S, which holds chunk slot ^ swz(row). Rows past the last one read the last
-  // one, and are never stored. In a short stage, chunks past the end of a row read
-  // its last chunk (for a transposed B: rows of K past the last one the last one);
-  // what is not the product's becomes zero once it is in LDS.
-  uint32_t va[Z::DA], vb[Z::DB];
-  const int rows_a = m - m0, cols_b = DUAL ? n - (n0 >> 1) : n - n0;
-#pragma unroll
-  for (int p = 0; p < Z::DA; ++p) {
-    const int r = (wave * Z::DA + p) * Z::RPI + lane / S;
-    va[p] = (uint32_t)min(r, rows_a - 1) * (uint32_t)lda + (((lane % S) ^ pr_swz<S>(r)) << 4);
-  }
-#pragma unroll
-  for (int p = 0; p < Z::DB; ++p) {
-    if constexpr (Z::NN) {
-      const int r = (wave * Z::DB + p) * Z::BRPI + lane / Z::BS;
-      vb[p] = (uint32_t)r * (uint32_t)ldb + (min((lane % Z::BS) ^ pr_swz_k<Z::BN>(r), (cols_b + 7) / 8 - 1) << 4);
-    } else {
-      const int r = (wave * Z::DB + p) * Z::RPI + lane / S, c = DUAL ? r & (Z::BN / 2 - 1) : r;
-      vb[p] = (uint32_t)min(c, cols_b - 1) * (uint32_t)ldb + (((lane % S) ^ pr_swz<S>(r)) << 4);
-    }
-  }
-  auto copy = [&](const Cursor& c, uint32_t buf, int d, auto SHORT_) __attribute__((always_inline)) {
-    constexpr bool SHORT = decltype(SHORT_)::value;
-    const bool is_a = d < Z::DA;
-    const int p = is_a ? d : d - Z::DA, q = wave * (is_a ? Z::DA : Z::DB) + p;
-    const uint8_t* base = is_a ? c.a : DUAL && q * Z::RPI >= Z::BN / 2 ? c.b1 : c.b0;
-    uint32_t v = is_a ? va[p] : vb[p];
-    if constexpr (SHORT) {
-      if (is_a || !Z::NN) {
-        const int r = q * Z::RPI + lane / S, ch = (lane % S) ^ pr_swz<S>(r);
-        const int last = (kbytes - c.ks * RB + 15) / 16 - 1;
-        v -= (uint32_t)max(ch - last, 0) << 4;
-      } else {
-        const int r = q * Z::BRPI + lane / Z::BS, last = k - 1 - c.ks * Z::BK;
-        v -= (uint32_t)max(r - last, 0) * (uint32_t)ldb;
-      }
-    }
-    dma16s(base, v, lds0 + buf + (is_a ? 0 : Z::AB) + q * 1024);
-  };
-  // Zeros behind the end of K, in both operands (the other one may hold an
-  // infinity).
-  auto clear = [&](int ks, uint32_t buf) __attribute__((always_inline)) {
-    const int left = kbytes - ks * RB;               // bytes of K that are there
-    constexpr int ROWS = Z::NN ? Z::BM : Z::BM + Z::BN;
-    for (int i = tid; i < ROWS * S; i += Z::NT) {
-      const int r = i / S, ch = i % S;
-      const int br = r < Z::BM ? r : r - Z::BM;
-      u32x4* at = reinterpret_cast<u32x4*>(smem + buf + (r < Z::BM ? 0 : Z::AB) + br * RB + ((ch ^ pr_swz<S>(br)) << 4));
-      const int have = left - 16 * ch;
-      if (have <= 0) {
-        *at = u32x4{0u, 0u, 0u, 0u};
-      } else if (have < 16) {
-        u32x4 v = *at;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int b = have - 4 * w;
-          v[w] &= b >= 4 ? ~0u : b <= 0 ? 0u : (1u << (8 * b)) - 1u;
-        }
-        *at = v;
-      }
-    }
-    if constexpr (Z::NN) {
-      const int have = k - ks * Z::BK;
-      for (int i = tid; i < Z::BK * Z::BS; i += Z::NT)
-        if (i / Z::BS >= have) *reinterpret_cast<u32x4*>(smem + buf + Z::AB + i * 16) = u32x4{0u, 0u, 0u, 0u};
-    }
-    __syncthreads();
-  };
-
-  // Exponents (8-bit operands): eight stages of both, one dword of four groups per
-  // row of A and stage, one byte per 128 columns of B and stage. Thread t holds row
-  // t's on their way; groups past the end of K get 127, whatever they scale is 0.
-  const int groups = (k + kGroup - 1) / kGroup, kblocks = (k + kBlock - 1) / kBlock;
-  uint32_t ev[8], evb = 0;
-  auto load_ex = [&](int chunk) __attribute__((always_inline)) {
-    if constexpr (Z::F8) {
-      if (tid < Z::BM) {
-        const uint8_t* row = it.ea + (int64_t)(m0 + min(tid, rows_a - 1)) * it.lde + 32 * chunk;
-        if (32 * chunk + 32 <= groups) {
-#pragma unroll
-          for (int w = 0; w < 8; ++w) ev[w] = *((const g_u32_any*)(row + 4 * w));
-        } else {
-#pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            ev[w] = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int g = 4 * w + b;
-              ev[w] |= (32 * chunk + g < groups ? (uint32_t)*((const g_u8*)(row + g)) : 127u) << (8 * b);
-            }
-          }
-        }
-      }
-      if (tid < 16) {
-        const int nb = n0 / kBlock + (tid >> 3), kb = 8 * chunk + (tid & 7);
-        evb = nb * kBlock < n && kb < kblocks ? (uint32_t)*((const g_u8*)(it.eb + nb * it.ldeb_n + kb * it.ldeb_k)) : 127u;
-      }
-    }
-  };
-  auto write_ex = [&](int chunk) __attribute__((always_inline)) {
-    if constexpr (Z::F8) {
-      unsigned char* t = smem + Z::RING + (chunk & 1) * (Z::EX_A + Z::EX_B);
-      if (tid < Z::BM)
-#pragma unroll
-        for (int w = 0; w < 8; ++w) *reinterpret_cast<uint32_t*>(t + (w * Z::BM + tid) * 4) = ev[w];
-      if (tid < 16) *reinterpret_cast<uint32_t*>(t + Z::EX_A + tid * 4) = evb;
-    }
-  };
-
-  // Fragments. Lane l of a 32-row block reads row l % 32; of a sub-step of 16 bf16
-  // its half l / 32 takes chunk 2 kk + half (8 consecutive k), of 64 e4m3 chunks
-  // 4 kk + half and 4 kk + 2 + half: the 8-bit MFMA's halves hold k 0-15, 32-47 and
-  // 16-31, 48-63, and its scale of half h is that of k 32 h .. 32 h + 31.
-  const int r32 = lane & 31, h = lane >> 5, sw = pr_swz<S>(r32);
-  const int G = lane >> 4, i16 = lane & 15;
-  typename Z::Frag fa[2][FM], fb[2][FN];
-  uint32_t sa[FM], sb = 127;                         // this stage's scales
-  uint32_t na[FM], nb_ = 127;                        // the next one's
-  auto read_frag = [&](int b, uint32_t buf, int kk, int f) __attribute__((always_inline)) {
-    const bool is_a = f < FM;
-    const int i = is_a ? f : f - FM;
-    typename Z::Frag v;
-    if (Z::NN && !is_a) {
-      if constexpr (Z::NN) {
-        const int col = wn * Z::WN + 32 * i + 16 * (G & 1) + 4 * (i16 & 3);
-        const unsigned char* p = smem + buf + Z::AB + (kk * 16 + 8 * (G >> 1) + (i16 >> 2)) * Z::BROW +
-                                 (((col >> 3) ^ pr_swz_k<Z::BN>(i16 >> 2)) << 4) + 8 * (i16 & 1);
-        const v4i16 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * Z::BROW);
-        v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-      }
-    } else {
-      const unsigned char* row = smem + buf + (is_a ? (wm * Z::WM + 32 * i + r32) * RB : Z::AB + (wn * Z::WN + 32 * i + r32) * RB);
-      if constexpr (Z::MODE == kNT8) {
-        const u32x4 lo = *reinterpret_cast<const u32x4*>(row + (((4 * kk + h) ^ sw) << 4));
-        const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((4 * kk + 2 + h) ^ sw) << 4));
-        v = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-      } else if constexpr (Z::MODE == kNT8X) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(row + ((kk ^ sw) << 4) + 8 * h);
-        const uint32_t E = is_a ? (sa[i] >> (8 * (kk >> 1))) & 255u : sb;
-        const Q8Group<MUON_Q8_E4M3> grp(E, true);
-        const u32x2 x = grp.bf16x4(w[0]), y = grp.bf16x4(w[1]);
-        v = __builtin_bit_cast(bf16x8, (u32x4{x[0], x[1], y[0], y[1]}));
-      } else {
-        v = *reinterpret_cast<const bf16x8*>(row + (((2 * kk + h) ^ sw) << 4));
-      }
-    }
-    if (is_a) fa[b][i] = v;
-    else fb[b][i] = v;
-  };
-  // Scales of the K step ks, from the table.
-  auto read_ex = [&](int ks) __attribute__((always_inline)) {
-    if constexpr (Z::F8) {
-      const unsigned char* t = smem + Z::RING + ((ks >> 3) & 1) * (Z::EX_A + Z::EX_B);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-        na[i] = *reinterpret_cast<const uint32_t*>(t + ((ks & 7) * Z::BM + wm * Z::WM + 32 * i + r32) * 4);
-      nb_ = *reinterpret_cast<const uint32_t*>(t + Z::EX_A + ((ks & 7) + 8 * ((wn * Z::WN) / kBlock)) * 4);
-    }
-  };
-  auto take_ex = [&]() __attribute__((always_inline)) {
-    if constexpr (Z::F8) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) sa[i] = Z::MODE == kNT8 ? na[i] >> (8 * h) : na[i];
-      sb = nb_;
-    }
-  };
-  auto mfma = [&](int b, int kk, int q) __attribute__((always_inline)) {
-    const int i = q / FN, j = q % FN;
-    if constexpr (Z::MODE == kNT8) {
-      if (kk == 0)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0, (int)sb, 0, (int)sa[i]);
-      else
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0, (int)sb, 2, (int)sa[i]);
-    } else {
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0);
-    }
-  };
-
-  // The ring.
-  const int total = s_end - s_begin;
-  Cursor next{nullptr, nullptr, nullptr, s_begin / kt, s_begin % kt};  // the next stage to load
-  seat(next);
-  int loaded = 0;
-  const int first_chunk = next.ks >> 3;
-  load_ex(first_chunk);
-  write_ex(first_chunk);
-  int ks = next.ks;                                  // of the stage at hand
-  auto load_stage = [&](uint32_t buf) __attribute__((always_inline)) {
-    if (short_stage(next.ks)) {
-#pragma unroll
-      for (int d = 0; d < Z::PS; ++d) copy(next, buf, d, std::true_type{});
-    } else {
-#pragma unroll
-      for (int d = 0; d < Z::PS; ++d) copy(next, buf, d, std::false_type{});
-    }
-  };
-#pragma unroll
-  for (int s = 0; s < Z::ST - 1; ++s)
-    if (loaded < total) {
-      load_stage(s * Z::STAGE);
-      if (++loaded < total) advance(next);
-    }
-  wait_vmcnt<0>();
-  __syncthreads();
-  if (short_stage(ks)) clear(ks, 0);
-  read_ex(ks);
-  take_ex();
-#pragma unroll
-  for (int f = 0; f < Z::NF; ++f) read_frag(0, 0, 0, f);
-
-  uint32_t cur = 0, to = (Z::ST - 1) * Z::STAGE;     // the ring's stage at hand, and the one that is loaded
-  // One stage. LOAD: 0 nothing more to load, 1 a whole stage, 2 a short one.
-  auto stage = [&](int t, auto LOAD_) __attribute__((always_inline)) {
-    constexpr int LOAD = decltype(LOAD_)::value;
-    const uint32_t after = cur + Z::STAGE == Z::RING ? 0 : cur + Z::STAGE;
-    const int ks1 = ks + 1 == kt ? 0 : ks + 1;
-    if constexpr (Z::F8) {
-      if ((t == 0 || (ks & 7) == 0) && 8 * (ks >> 3) + 8 < kt) load_ex((ks >> 3) + 1);
-    }
-#pragma unroll
-    for (int kk = 0; kk < Z::KK; ++kk)
-#pragma unroll
-      for (int q = 0; q < Z::PER; ++q) {
-        const int slot = kk * Z::PER + q, b = kk & 1;
-        if (slot == Z::MEET) {
-          if constexpr (Z::F8) {
-            if ((ks & 7) == 7) write_ex((ks >> 3) + 1);
-          }
-          // the next stage's copies are the oldest in flight
-          if constexpr (LOAD != 0 && Z::ST > 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((Z::ST - 2) * Z::PS) : "memory");
-          else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          if (t + 1 < total && short_stage(ks1)) clear(ks1, after);
-          read_ex(ks1);
-        }
-        mfma(b, kk, q);
-        if (kk + 1 < Z::KK) {
-#pragma unroll
-          for (int f = 0; f < Z::NF; ++f)
-            if (f * Z::PER / Z::NF == q) read_frag(b ^ 1, cur, kk + 1, f);
-        }
-        if (slot == Z::SLOTS - 1) take_ex();
-        if constexpr (Z::MODE != kNT8X) {
-          if (slot >= Z::MEET) {
-#pragma unroll
-            for (int f = 0; f < Z::NF; ++f)
-              if (f * (Z::SLOTS - Z::MEET) / Z::NF == slot - Z::MEET) read_frag(0, after, 0, f);
-          }
-        }
-        if constexpr (LOAD != 0) {
-#pragma unroll
-          for (int d = 0; d < Z::PS; ++d)
-            if (d * Z::MEET / (Z::PS * (Z::ST == 2 ? 2 : 1)) == slot)
-              copy(next, to, d, std::integral_constant<bool, LOAD == 2>{});
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    if constexpr (Z::MODE == kNT8X) {  // these need the next stage's scales
-#pragma unroll
-      for (int f = 0; f < Z::NF; ++f) read_frag(0, after, 0, f);
-    }
-    if constexpr (LOAD != 0) {
-      if (++loaded < total) advance(next);
-    }
-    ks = ks1;
-    cur = after;
-    to = to + Z::STAGE == Z::RING ? 0 : to + Z::STAGE;
-  };
-  for (int t = 0; t < total; ++t) {
-    if (loaded >= total) stage(t, std::integral_constant<int, 0>{});
-    else if (short_stage(next.ks)) stage(t, std::integral_constant<int, 2>{});
-    else stage(t, std::integral_constant<int, 1>{});
-  }
-  __syncthreads();
+// A unit of a launch: a tile, or a piece of its sum.
+struct PrUnit {
+  int idx, local, m0, n0, begin, total;  // item; tile and piece; first row and column; first stage and how many
+};
+template <class Z>
+MUON_INLINE PrUnit pr_unit(PrArgsPtr args, int unit) {
+  PrUnit u;
+  u.idx = pr_item(args, unit);
+  PrItemRef it = args->item[u.idx];
+  const int tiles = it.tiles_m * it.tiles_n;
+  u.local = unit - args->unit0[u.idx];
+  const int split = u.local / tiles, tile = u.local - split * tiles;
+  int tm, tn;
+  pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
+  u.m0 = tm * Z::BM;
+  u.n0 = tn * Z::BN;
+  const int all = (it.k + Z::BK - 1) / Z::BK * it.sums * (args->parts == 3 ? 6 : 1);
+  u.begin = (int)((int64_t)all * split / it.splits);
+  u.total = (int)((int64_t)all * (split + 1) / it.splits) - u.begin;
+  return u;
 }
 
 // Columns of a tile that a thread holds together, and the rest of an epilogue's
@@ -503,28 +186,13 @@ struct PrStoreOut {
   }
 };
 
-// One unit of a launch: its part of the sum, then either its partial tile or the
-// epilogue Out. A tile's partial sums are BM x BN floats.
+// A tile's way out: its partial sums, BM x BN floats, or the epilogue Out. Through
+// LDS, IPP blocks of rows of every wave at a time: staged row r, whose 16-byte unit u
+// sits at u ^ (r % the row's units), is row WM*(r / PR) + PR*pass + r % PR of the
+// tile.
 template <class Z, class Out>
-MUON_INLINE void pr_unit_of(unsigned char* smem) {
+MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, const PrUnit& un, unsigned char* stage, const f32x16 (&acc)[Z::FM][Z::FN]) {
   constexpr bool DUAL = Out::OPS == 2;
-  const PrArgsPtr args = (PrArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
-  const int unit = pr_unit(blockIdx.x, args->units);
-  const int idx = pr_item(args, unit);
-  PrItemRef it = args->item[idx];
-  const int tiles = it.tiles_m * it.tiles_n;
-  const int local = unit - args->unit0[idx], split = local / tiles, tile = local - split * tiles;
-  int tm, tn;
-  pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
-  const int m0 = tm * Z::BM, n0 = tn * Z::BN;
-  const int total = (it.k + Z::BK - 1) / Z::BK * it.sums * (args->parts == 3 ? 6 : 1);
-  f32x16 acc[Z::FM][Z::FN];
-  pr_sum<Z, DUAL>(args, it, m0, n0, (int)((int64_t)total * split / it.splits), (int)((int64_t)total * (split + 1) / it.splits),
-                  smem, acc);
-
-  // Through LDS, IPP blocks of rows of every wave at a time: staged row r, whose
-  // 16-byte unit u sits at u ^ (r % the row's units), is row
-  // WM*(r / (32 IPP)) + 32*IPP*pass + r % (32 IPP) of the tile.
   constexpr int UNITS = Z::BN / 4, MASK = UNITS - 1, ROWS = 64 * Z::IPP, PR = 32 * Z::IPP;
   constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;  // lanes of a row
   const int tid = fresh_tid(), lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
@@ -540,12 +208,12 @@ MUON_INLINE void pr_unit_of(unsigned char* smem) {
         for (int g = 0; g < 4; ++g) {
           const int r = wm * PR + 32 * ii + (lane & 31), u = wn * (Z::WN / 4) + 8 * j + 2 * g + (lane >> 5);
           const f32x16& t = acc[pass * Z::IPP + ii][j];
-          *reinterpret_cast<f32x4*>(smem + r * Z::BN * 4 + ((u ^ (r & MASK)) << 4)) =
+          *reinterpret_cast<f32x4*>(stage + r * Z::BN * 4 + ((u ^ (r & MASK)) << 4)) =
               f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
         }
     __syncthreads();
     auto run_of = [&](int r, int col, float v[8]) __attribute__((always_inline)) {
-      const unsigned char* row = smem + r * Z::BN * 4;
+      const unsigned char* row = stage + r * Z::BN * 4;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const f32x4 t = *reinterpret_cast<const f32x4*>(row + (((col / 4 + q) ^ (r & MASK)) << 4));
@@ -555,7 +223,7 @@ MUON_INLINE void pr_unit_of(unsigned char* smem) {
     };
     auto tile_row = [&](int r) __attribute__((always_inline)) { return Z::WM * (r / PR) + PR * pass + r % PR; };
     if (it.splits > 1) {
-      float* p = args->partial + (int64_t)(it.part0 + local) * Z::BM * Z::BN;
+      float* p = args->partial + (int64_t)(it.part0 + un.local) * Z::BM * Z::BN;
 #pragma unroll 2
       for (int q = 0; q < ROWS * (Z::BN / kRun) / Z::NT; ++q) {
         const int i = q * Z::NT + tid, r = i / (Z::BN / kRun), col = i % (Z::BN / kRun) * kRun;
@@ -570,10 +238,367 @@ MUON_INLINE void pr_unit_of(unsigned char* smem) {
         float v[8], w[8];
         run_of(r, col, v);
         if constexpr (DUAL) run_of(r, Z::BN / 2 + col, w);
-        out.emit(m0 + tile_row(r), (DUAL ? n0 >> 1 : n0) + col, v, w);
+        out.emit(un.m0 + tile_row(r), (DUAL ? un.n0 >> 1 : un.n0) + col, v, w);
       }
     }
   }
+}
+
+// All units of one workgroup. XCD b % 8 gets a contiguous range of units, which its
+// workgroups take in turn, so that the tiles that run there together share operand
+// panels in its L2. The copies run ST - 1 stages ahead of the sum, across tiles: a
+// tile starts with its first stages in LDS, and its predecessor leaves under their
+// copies.
+template <class Z, class Out>
+MUON_INLINE void pr_run(unsigned char* smem) {
+  constexpr bool DUAL = Out::OPS == 2;
+  constexpr int FM = Z::FM, FN = Z::FN, RB = Z::RB, S = Z::S;
+  const PrArgsPtr args = (PrArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  const int xcd = blockIdx.x & 7, units = args->units, per = units >> 3, rest = units & 7;
+  const int first = xcd * per + min(xcd, rest), count = per + (xcd < rest);
+  const int step = ((int)gridDim.x >> 3) + (xcd < ((int)gridDim.x & 7));
+  int at = blockIdx.x >> 3;
+  if (at >= count) return;
+
+  const int tid = fresh_tid(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+  const int pairs = args->parts == 3 ? 6 : 1;
+
+  // ---- what is copied next: a stage of a unit, at K step `ks` of pair of planes `seg`
+  const uint8_t *la = nullptr, *lb0 = nullptr, *lb1 = nullptr;
+  int64_t lda = 0, ldb = 0;
+  int lat = at - step, lidx = 0, lm0 = 0, ln0 = 0, lks = 0, lseg = 0, lleft = 0, lk = 0, lkt = 1;
+  uint32_t limit = 0, limit_k = 0;  // where a row (of a transposed B: the rows) of the stage end
+  bool lfresh = false;              // the stage's exponents are not in a table yet
+  int ltab = -1;
+  // Copy q of an operand fills 1 KB: rows RPI*q .. +RPI-1, lane l slot l % S of row
+  // l / S, which holds chunk slot ^ swz(row). Rows past the last one read the last
+  // one, and are never stored. In a short stage, chunks past the end of a row read
+  // its last chunk (for a transposed B: rows of K past the last one the last one);
+  // what is not the product's becomes zero once it is in LDS.
+  uint32_t row_a[Z::DA], row_b[Z::DB], ch_a[2], ch_b[2];
+  auto limits = [&]() __attribute__((always_inline)) {
+    const int kbytes = Z::F8 ? lk : 2 * lk;
+    limit = (uint32_t)min((kbytes - lks * RB + 15) / 16, S) * 16 - 16;
+    if constexpr (Z::NN) limit_k = (uint32_t)(min(lk - lks * Z::BK, Z::BK) - 1) * (uint32_t)ldb;
+    lfresh = Z::F8 && (lfresh || (lks & 7) == 0);
+    if (Z::F8 && lfresh) ltab = (ltab + 1) & (Z::TABS - 1);
+  };
+  auto seat = [&]() __attribute__((always_inline)) {
+    PrItemRef it = args->item[lidx];
+    const int sum = lseg / pairs, p = lseg - sum * pairs;
+    const int64_t pa = pairs == 6 ? pr_plane_a(p) * it.pa : 0, pb = pairs == 6 ? pr_plane_b(p) * it.pb : 0;
+    la = it.a[sum] + pa + (int64_t)lm0 * lda + (int64_t)lks * RB;
+    if constexpr (DUAL) {
+      lb0 = it.b[0] + pb + (int64_t)(ln0 >> 1) * ldb + (int64_t)lks * RB;
+      lb1 = it.b[1] + pb + (int64_t)(ln0 >> 1) * ldb + (int64_t)lks * RB;
+    } else if constexpr (Z::NN) {
+      lb0 = it.b[sum] + pb + 2 * ln0 + (int64_t)lks * Z::BK * ldb;
+    } else {
+      lb0 = it.b[sum] + pb + (int64_t)ln0 * ldb + (int64_t)lks * RB;
+    }
+  };
+  auto open = [&]() __attribute__((always_inline)) {  // the next unit's first stage
+    lat += step;
+    const PrUnit u = pr_unit<Z>(args, first + lat);
+    PrItemRef it = args->item[u.idx];
+    lidx = u.idx;
+    lm0 = u.m0;
+    ln0 = u.n0;
+    lk = it.k;
+    lda = it.lda;
+    ldb = it.ldb;
+    lkt = (lk + Z::BK - 1) / Z::BK;
+    lseg = u.begin / lkt;
+    lks = u.begin - lseg * lkt;
+    lleft = u.total;
+    const int rows_a = it.m - lm0, cols_b = DUAL ? it.n - (ln0 >> 1) : it.n - ln0;
+#pragma unroll
+    for (int p = 0; p < Z::DA; ++p) {
+      const int r = (wave * Z::DA + p) * Z::RPI + lane / S;
+      row_a[p] = (uint32_t)min(r, rows_a - 1) * (uint32_t)lda;
+      if (p < 2) ch_a[p] = ((lane % S) ^ pr_swz<S>(r)) << 4;
+    }
+#pragma unroll
+    for (int p = 0; p < Z::DB; ++p) {
+      if constexpr (Z::NN) {
+        const int r = (wave * Z::DB + p) * Z::BRPI + lane / Z::BS;
+        row_b[p] = (uint32_t)r * (uint32_t)ldb;
+        if (p < 2) ch_b[p] = min((lane % Z::BS) ^ pr_swz_k<Z::BN>(r), (cols_b + 7) / 8 - 1) << 4;
+      } else {
+        const int r = (wave * Z::DB + p) * Z::RPI + lane / S, c = DUAL ? r & (Z::BN / 2 - 1) : r;
+        row_b[p] = (uint32_t)min(c, cols_b - 1) * (uint32_t)ldb;
+        if (p < 2) ch_b[p] = ch_a[p];
+      }
+    }
+    seat();
+    lfresh = true;
+    limits();
+  };
+  // The stage after this one. Past the last unit's last stage that one is copied
+  // again, and nothing of it is used.
+  auto advance = [&]() __attribute__((always_inline)) {
+    lfresh = false;
+    if (--lleft == 0) {
+      if (lat + step < count) open();
+      else lleft = 1;
+      return;
+    }
+    if (++lks == lkt) {
+      lks = 0;
+      ++lseg;
+      seat();
+    } else {
+      la += RB;
+      lb0 += Z::NN ? (int64_t)Z::BK * ldb : (int64_t)RB;
+      if constexpr (DUAL) lb1 += RB;
+    }
+    limits();
+  };
+  auto copy = [&](uint32_t buf, int d) __attribute__((always_inline)) {
+    const bool is_a = d < Z::DA;
+    const int p = is_a ? d : d - Z::DA, q = wave * (is_a ? Z::DA : Z::DB) + p;
+    const uint8_t* base = is_a ? la : DUAL && q * Z::RPI >= Z::BN / 2 ? lb1 : lb0;
+    const uint32_t v = is_a ? row_a[p] + min(ch_a[p & 1], limit)
+                       : Z::NN ? min(row_b[p], limit_k) + ch_b[p & 1] : row_b[p] + min(ch_b[p & 1], limit);
+    dma16s(base, v, lds0 + buf + (is_a ? 0 : Z::AB) + q * 1024);
+  };
+  // Exponents (8-bit operands): eight stages of both, one dword of four groups per
+  // row of A and stage, one byte per 128 columns of B and stage. Thread t carries row
+  // t's; groups past the end of K get 127, whatever they scale is 0.
+  uint32_t ev[8], evb = 0;
+  auto load_ex = [&]() __attribute__((always_inline)) {
+    if constexpr (Z::F8) {
+      PrItemRef it = args->item[lidx];
+      const int chunk = lks >> 3, groups = (lk + kGroup - 1) / kGroup, kblocks = (lk + kBlock - 1) / kBlock;
+      if (tid < Z::BM) {
+        const uint8_t* row = it.ea + (int64_t)min(lm0 + tid, it.m - 1) * it.lde + 32 * chunk;
+        if (32 * chunk + 32 <= groups) {
+#pragma unroll
+          for (int w = 0; w < 8; ++w) ev[w] = *((const g_u32_any*)(row + 4 * w));
+        } else {
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            ev[w] = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int g = 4 * w + b;
+              ev[w] |= (32 * chunk + g < groups ? (uint32_t)*((const g_u8*)(row + g)) : 127u) << (8 * b);
+            }
+          }
+        }
+      }
+      if (tid < 16) {
+        const int nb = ln0 / kBlock + (tid >> 3), kb = 8 * chunk + (tid & 7);
+        evb = nb * kBlock < it.n && kb < kblocks ? (uint32_t)*((const g_u8*)(it.eb + nb * it.ldeb_n + kb * it.ldeb_k)) : 127u;
+      }
+    }
+  };
+  auto write_ex = [&]() __attribute__((always_inline)) {
+    if constexpr (Z::F8) {
+      unsigned char* t = smem + Z::RING + ltab * (Z::EX_A + Z::EX_B);
+      if (tid < Z::BM)
+#pragma unroll
+        for (int w = 0; w < 8; ++w) *reinterpret_cast<uint32_t*>(t + (w * Z::BM + tid) * 4) = ev[w];
+      if (tid < 16) *reinterpret_cast<uint32_t*>(t + Z::EX_A + tid * 4) = evb;
+    }
+  };
+
+  // ---- the sum
+  f32x16 acc[FM][FN];
+  int k = 0, kt = 1, ks = 0, tab = -1;               // of the unit at hand, and its stage
+  auto short_stage = [&](int ks_) __attribute__((always_inline)) {
+    const int kbytes = Z::F8 ? k : 2 * k;
+    return ks_ * RB + RB > kbytes;
+  };
+  // Zeros behind the end of K, in both operands (the other one may hold an
+  // infinity).
+  auto clear = [&](int ks_, uint32_t buf) __attribute__((always_inline)) {
+    const int left = (Z::F8 ? k : 2 * k) - ks_ * RB; // bytes of K that are there
+    constexpr int ROWS = Z::NN ? Z::BM : Z::BM + Z::BN;
+    for (int i = tid; i < ROWS * S; i += Z::NT) {
+      const int r = i / S, ch = i % S;
+      const int br = r < Z::BM ? r : r - Z::BM;
+      u32x4* p = reinterpret_cast<u32x4*>(smem + buf + (r < Z::BM ? 0 : Z::AB) + br * RB + ((ch ^ pr_swz<S>(br)) << 4));
+      const int have = left - 16 * ch;
+      if (have <= 0) {
+        *p = u32x4{0u, 0u, 0u, 0u};
+      } else if (have < 16) {
+        u32x4 v = *p;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int b = have - 4 * w;
+          v[w] &= b >= 4 ? ~0u : b <= 0 ? 0u : (1u << (8 * b)) - 1u;
+        }
+        *p = v;
+      }
+    }
+    if constexpr (Z::NN) {
+      const int have = k - ks_ * Z::BK;
+      for (int i = tid; i < Z::BK * Z::BS; i += Z::NT)
+        if (i / Z::BS >= have) *reinterpret_cast<u32x4*>(smem + buf + Z::AB + i * 16) = u32x4{0u, 0u, 0u, 0u};
+    }
+    __syncthreads();
+  };
+
+  // Fragments. Lane l of a 32-row block reads row l % 32; of a sub-step of 16 bf16
+  // its half l / 32 takes chunk 2 kk + half (8 consecutive k), of 64 e4m3 chunks
+  // 4 kk + half and 4 kk + 2 + half: the 8-bit MFMA's halves hold k 0-15, 32-47 and
+  // 16-31, 48-63, and its scale of half h is that of k 32 h .. 32 h + 31.
+  const int r32 = lane & 31, h = lane >> 5, sw = pr_swz<S>(r32);
+  const int G = lane >> 4, i16 = lane & 15;
+  typename Z::Frag fa[2][FM], fb[2][FN];
+  uint32_t sa[FM], sb = 127, na[FM], nb_ = 127;      // this stage's scales, and the next one's
+  auto read_frag = [&](int b, uint32_t buf, int kk, int f) __attribute__((always_inline)) {
+    const bool is_a = f < FM;
+    const int i = is_a ? f : f - FM;
+    typename Z::Frag v;
+    if (Z::NN && !is_a) {
+      if constexpr (Z::NN) {
+        const int col = wn * Z::WN + 32 * i + 16 * (G & 1) + 4 * (i16 & 3);
+        const unsigned char* p = smem + buf + Z::AB + (kk * 16 + 8 * (G >> 1) + (i16 >> 2)) * Z::BROW +
+                                 (((col >> 3) ^ pr_swz_k<Z::BN>(i16 >> 2)) << 4) + 8 * (i16 & 1);
+        const v4i16 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * Z::BROW);
+        v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    } else {
+      const unsigned char* row = smem + buf + (is_a ? (wm * Z::WM + 32 * i + r32) * RB : Z::AB + (wn * Z::WN + 32 * i + r32) * RB);
+      if constexpr (Z::MODE == kNT8) {
+        const u32x4 lo = *reinterpret_cast<const u32x4*>(row + (((4 * kk + h) ^ sw) << 4));
+        const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((4 * kk + 2 + h) ^ sw) << 4));
+        v = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+      } else if constexpr (Z::MODE == kNT8X) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(row + ((kk ^ sw) << 4) + 8 * h);
+        const uint32_t E = is_a ? (sa[i] >> (8 * (kk >> 1))) & 255u : sb;
+        const Q8Group<MUON_Q8_E4M3> grp(E, true);
+        const u32x2 x = grp.bf16x4(w[0]), y = grp.bf16x4(w[1]);
+        v = __builtin_bit_cast(bf16x8, (u32x4{x[0], x[1], y[0], y[1]}));
+      } else {
+        v = *reinterpret_cast<const bf16x8*>(row + (((2 * kk + h) ^ sw) << 4));
+      }
+    }
+    if (is_a) fa[b][i] = v;
+    else fb[b][i] = v;
+  };
+  auto read_ex = [&](int ks_, int t_) __attribute__((always_inline)) {
+    if constexpr (Z::F8) {
+      const unsigned char* t = smem + Z::RING + t_ * (Z::EX_A + Z::EX_B);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        na[i] = *reinterpret_cast<const uint32_t*>(t + ((ks_ & 7) * Z::BM + wm * Z::WM + 32 * i + r32) * 4);
+      nb_ = *reinterpret_cast<const uint32_t*>(t + Z::EX_A + ((ks_ & 7) + 8 * ((wn * Z::WN) / kBlock)) * 4);
+    }
+  };
+  auto take_ex = [&]() __attribute__((always_inline)) {
+    if constexpr (Z::F8) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) sa[i] = Z::MODE == kNT8 ? na[i] >> (8 * h) : na[i];
+      sb = nb_;
+    }
+  };
+  auto mfma = [&](int b, int kk, int q) __attribute__((always_inline)) {
+    const int i = q / FN, j = q % FN;
+    if constexpr (Z::MODE == kNT8) {
+      if (kk == 0)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0, (int)sb, 0, (int)sa[i]);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0, (int)sb, 2, (int)sa[i]);
+    } else {
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  open();
+#pragma unroll 1
+  for (int s = 0; s < Z::ST - 1; ++s) {
+    if (lfresh) {
+      load_ex();
+      write_ex();
+    }
+#pragma unroll
+    for (int d = 0; d < Z::PS; ++d) copy(s * Z::STAGE, d);
+    advance();
+  }
+  wait_vmcnt<0>();
+  uint32_t cur = 0, to = (Z::ST - 1) * Z::STAGE;     // the ring's stage at hand, and the one that is loaded
+
+#pragma unroll 1
+  for (; at < count; at += step) {
+    const PrUnit u = pr_unit<Z>(args, first + at);
+    PrItemRef it = args->item[u.idx];
+    k = it.k;
+    kt = (k + Z::BK - 1) / Z::BK;
+    ks = u.begin % kt;
+    tab = (tab + 1) & (Z::TABS - 1);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    __syncthreads();                                 // its first stage is in LDS, and the last tile has left
+    if (short_stage(ks)) clear(ks, cur);
+    read_ex(ks, tab);
+    take_ex();
+#pragma unroll
+    for (int f = 0; f < Z::NF; ++f) read_frag(0, cur, 0, f);
+
+    // One stage: MFMAs, and between two of them a little of everything else, in a
+    // fixed order. The last sub-step's fragments are in registers a few MFMAs before
+    // its end: there the workgroup meets, and the next stage's first fragments are
+    // read under the remaining MFMAs (after the last stage: for nothing).
+#pragma unroll 1
+    for (int t = u.total; t; --t) {
+      const uint32_t after = cur + Z::STAGE == Z::RING ? 0 : cur + Z::STAGE;
+      const int ks1 = ks + 1 == kt ? 0 : ks + 1;
+      if (lfresh) load_ex();
+#pragma unroll
+      for (int kk = 0; kk < Z::KK; ++kk)
+#pragma unroll
+        for (int q = 0; q < Z::PER; ++q) {
+          const int slot = kk * Z::PER + q, b = kk & 1;
+          if (slot == Z::MEET) {
+            if (lfresh) write_ex();
+            // the next stage's copies are the oldest in flight
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((Z::ST - 2) * Z::PS) : "memory");
+            if (t > 1) {
+              if (short_stage(ks1)) clear(ks1, after);
+              if (Z::F8 && (ks1 & 7) == 0) tab = (tab + 1) & (Z::TABS - 1);
+            }
+            read_ex(ks1, tab);
+          }
+          mfma(b, kk, q);
+          if (kk + 1 < Z::KK) {
+#pragma unroll
+            for (int f = 0; f < Z::NF; ++f)
+              if (f * Z::PER / Z::NF == q) read_frag(b ^ 1, cur, kk + 1, f);
+          }
+          if (slot == Z::SLOTS - 1) take_ex();
+          if constexpr (Z::MODE != kNT8X) {
+            if (slot >= Z::MEET) {
+#pragma unroll
+              for (int f = 0; f < Z::NF; ++f)
+                if (f * (Z::SLOTS - Z::MEET) / Z::NF == slot - Z::MEET) read_frag(0, after, 0, f);
+            }
+          }
+#pragma unroll
+          for (int d = 0; d < Z::PS; ++d)
+            if (d * Z::MEET / (Z::PS * (Z::ST == 2 ? 2 : 1)) == slot) copy(to, d);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      if constexpr (Z::MODE == kNT8X) {  // these need the next stage's scales
+#pragma unroll
+        for (int f = 0; f < Z::NF; ++f) read_frag(0, after, 0, f);
+      }
+      advance();
+      ks = ks1;
+      cur = after;
+      to = to + Z::STAGE == Z::RING ? 0 : to + Z::STAGE;
+    }
+    pr_leave<Z, Out>(args, it, u, smem + to, acc);
+  }
+  wait_vmcnt<0>();  // the copies past the last stage
 }
 
 // Adds the pieces of a tile in order, then the epilogue. A workgroup takes 1024
@@ -614,6 +639,11 @@ MUON_INLINE void pr_join_of(int edge) {
   out.emit(tm * edge + r, (DUAL ? tn * edge / 2 : tn * edge) + col, v, w);
 }
 
+// Workgroups of a launch: as many as the CUs hold at once.
+template <class Z>
+inline uint32_t pr_grid(const PrArgs& a) {
+  return (uint32_t)(a.units < 256 * Z::WG ? a.units : 256 * Z::WG);
+}
 // Workgroups of a launch's join.
 inline int64_t pr_join_blocks(const PrArgs& a, bool dual) {
   const int edge = kPrEdge[a.tile];
