@@ -529,8 +529,8 @@ muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32
  * w_gate, w_up  inner x width, w_down  out x inner, contiguous (muon_matrix.w)
  * y       rows x out, written (NULL: only the checkpoints are wanted)
  * a, b, s rows x inner checkpoints of the unrounded a, b and s, written if their q
- *         is not NULL; a backward pass needs a and b, the weight gradient of
- *         w_down (muon_wgrad) s
+ *         is not NULL, all of the same kind; a backward pass needs a and b, the
+ *         weight gradient of w_down (muon_wgrad) s
  * width, inner and out are at most 2^22.
  * workspace: device memory of at least muon_mlp_workspace bytes, 16-byte aligned,
  * scratch of a call until it has run; a call on it in a captured graph writes it

@@ -31,112 +31,221 @@ MUON_INLINE void cut3(float x, float& hi, float& mid, float& lo) {
 // (|x| + 2) 2^-24 or so.
 MUON_INLINE float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x)); }
 
-// act(a) and act'(a).
-MUON_INLINE void activation(float a, int act, float& f, float& df) {
+// act(a) and act'(a) of eight values, given to `to` one by one. ACT -1: as act says.
+template <int ACT, class F>
+MUON_INLINE void activations(const float v[8], int act_, F to) {
+  const int act = ACT < 0 ? act_ : ACT;
   if (act == MUON_ACT_SILU) {
-    const float s = sigmoid(a);
-    f = a * s;
-    df = fmaf(f, 1.f - s, s);
-  } else if (act == MUON_ACT_GELU) {
-    const float phi = 0.5f + 0.5f * erff(a * 0.70710678f);
-    f = a * phi;
-    df = fmaf(a * 0.39894228f, __builtin_amdgcn_exp2f(-0.72134752f * a * a), phi);
-  } else if (act == MUON_ACT_GELU_TANH) {
-    // (1 + tanh u) / 2 = sigmoid(2 u); from |a| = 100 on it is 0 or 1 whatever a^2 is
-    const float a2 = fminf(a * a, 1e4f), s = sigmoid(1.5957691216f * a * fmaf(0.044715f, a2, 1.f));
-    f = a * s;
-    df = fmaf(f * (1.f - s), 1.5957691216f * fmaf(0.134145f, a2, 1.f), s);
-  } else {
-    f = a > 0.f ? a : a == a ? 0.f : a;
-    df = a > 0.f ? 1.f : 0.f;
-  }
-}
-
-// The bytes and the exponent of eight columns, four lanes a group, into a
-// checkpoint. Padding columns (up to a multiple of 16) get 0.
-MUON_INLINE void save_run(const __attribute__((address_space(4))) muon_q8& q, int row, int col, bool there, const float v[8]) {
-  u32x2 w;
-  const uint32_t E = q8_encode(v, q.kind, w);
-  if (there && col < ((int)q.cols + 15) / 16 * 16)
-    *((g_u32x2*)(static_cast<uint8_t*>(q.q) + (int64_t)row * q.ldq + col)) = w;
-  if (there && (col & (kGroup - 1)) == 0 && col < q.cols)
-    *((g_u8*)(static_cast<uint8_t*>(q.e) + (int64_t)row * q.lde + col / kGroup)) = (uint8_t)E;
-}
-
-// Eight columns as an operand of the next product: bf16, or three planes.
-template <class M>
-MUON_INLINE void put_planes(const M& mlp, u16* base, int parts, int row, int col, const float v[8]) {
-  u16* p = base + (int64_t)row * mlp.ldp + col;
-  if (parts == 1) {
-    *((g_u32x4*)p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-    return;
-  }
-  float t[3][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cut3(v[i], t[2][i], t[1][i], t[0][i]);
-#pragma unroll
-  for (int q = 0; q < 3; ++q)
-    *((g_u32x4*)(p + q * mlp.pp)) =
-        u32x4{pack_bf16x2(t[q][0], t[q][1]), pack_bf16x2(t[q][2], t[q][3]), pack_bf16x2(t[q][4], t[q][5]), pack_bf16x2(t[q][6], t[q][7])};
-}
-
-// a and b of eight columns: s for the down projection, and the checkpoints. Lanes
-// past the last column take part in their group with zeros.
-struct PrGateOut {
-  static constexpr int OPS = 2;
-  PrItemRef it;
-  const __attribute__((address_space(4))) PrMlp& mlp;
-  int parts;
-  MUON_INLINE PrGateOut(PrItemRef item, PrArgsPtr a) : it(item), mlp(a->mlp), parts(a->parts) {}
-  MUON_INLINE void emit(int row, int col, float a[8], float b[8]) const {
-    const bool there = row < it.m;
-    float s[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float f, df;
-      activation(a[i], mlp.act, f, df);
-      s[i] = f * b[i];
-      if (col + i >= it.n) a[i] = b[i] = s[i] = 0.f;
+      const float s = sigmoid(v[i]), f = v[i] * s;
+      to(i, f, fmaf(f, 1.f - s, s));
     }
-    if (there && col < it.n) put_planes(mlp, mlp.plane[0], parts, row, col, s);
-    if (mlp.a.q) save_run(mlp.a, row, col, there, a);
-    if (mlp.b.q) save_run(mlp.b, row, col, there, b);
-    if (mlp.s.q) save_run(mlp.s, row, col, there, s);
+  } else if (act == MUON_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = v[i], phi = 0.5f + 0.5f * erff(a * 0.70710678f);
+      to(i, a * phi, fmaf(a * 0.39894228f, __builtin_amdgcn_exp2f(-0.72134752f * a * a), phi));
+    }
+  } else if (act == MUON_ACT_GELU_TANH) {
+    // (1 + tanh u) / 2 = sigmoid(2 u); from |a| = 100 on it is 0 or 1 whatever a^2 is
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = v[i], a2 = fminf(a * a, 1e4f), s = sigmoid(1.5957691216f * a * fmaf(0.044715f, a2, 1.f)), f = a * s;
+      to(i, f, fmaf(f * (1.f - s), 1.5957691216f * fmaf(0.134145f, a2, 1.f), s));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) to(i, v[i] > 0.f ? v[i] : v[i] == v[i] ? 0.f : v[i], v[i] > 0.f ? 1.f : 0.f);  // NaN stays
+  }
+}
+
+// A checkpoint as a thread of an epilogue sees it: eight columns, always the same.
+struct Saved {
+  uint8_t *q, *e;
+  int64_t ldq, lde;
+  int kind;
+  uint32_t off, offe;
+  bool put_q, put_e;
+  MUON_INLINE Saved(const __attribute__((address_space(4))) muon_q8& s, PrLane at)
+      : q(static_cast<uint8_t*>(pinned(s.q))), e(static_cast<uint8_t*>(pinned(s.e))), ldq(pinned(s.ldq)), lde(pinned(s.lde)),
+        kind(pinned(s.kind)) {
+    off = (uint32_t)at.row * (uint32_t)ldq + (uint32_t)at.col;
+    offe = (uint32_t)at.row * (uint32_t)lde + (uint32_t)(at.col / kGroup);
+    put_q = at.col < ((int)s.cols + 15) / 16 * 16;
+    put_e = (at.col & (kGroup - 1)) == 0 && at.col < s.cols;
+  }
+  // Columns of a group are four lanes. Padding columns (up to a multiple of 16) get 0.
+  template <class V>
+  MUON_INLINE void save(int row, bool there, const float v[8]) const {
+    u32x2 w;
+    const uint32_t E = q8_encode(v, V::FULL ? V::B : kind, w);
+    uint8_t *pq = q + (int64_t)row * ldq, *pe = e + (int64_t)row * lde;
+    if (V::FULL || (there && put_q)) *((g_u32x2*)(pq + off)) = w;
+    if (there && put_e) *((g_u8*)(pe + offe)) = (uint8_t)E;
+  }
+  MUON_INLINE void load(int row, u32x2& w, uint32_t& E) const {
+    const uint8_t *pq = q + (int64_t)row * ldq, *pe = e + (int64_t)row * lde;
+    w = *((const g_u32x2*)(pq + off));
+    E = *((const g_u8*)(pe + offe));
   }
 };
 
-// ds of eight columns, with a and b from their checkpoints.
+// Eight columns as an operand of the next product: bf16, or three planes.
+struct Planes {
+  char* p;
+  int64_t ld, plane;  // bytes
+  uint32_t off;
+  int parts;
+  MUON_INLINE Planes(uint16_t* base, const __attribute__((address_space(4))) PrMlp& m, int parts_, PrLane at)
+      : p(reinterpret_cast<char*>(pinned(base))), ld(2 * pinned(m.ldp)), plane(2 * pinned(m.pp)), parts(parts_) {
+    off = (uint32_t)at.row * (uint32_t)ld + 2u * (uint32_t)at.col;
+  }
+  template <class V>
+  MUON_INLINE void put(int row, const float v[8]) const {
+    char* base = p + (int64_t)row * ld;
+    if (V::FULL || parts == 1) {
+      *((g_u32x4*)(base + off)) =
+          u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      return;
+    }
+    float t[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cut3(v[i], t[2][i], t[1][i], t[0][i]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      *((g_u32x4*)(base + q * plane + off)) =
+          u32x4{pack_bf16x2(t[q][0], t[q][1]), pack_bf16x2(t[q][2], t[q][3]), pack_bf16x2(t[q][4], t[q][5]), pack_bf16x2(t[q][6], t[q][7])};
+  }
+};
+
+constexpr int kNoSave = 2;  // a variant's B, beside the kinds: no checkpoint is kept
+
+// a and b of eight columns: s for the down projection, and the checkpoints. Lanes
+// past the last column take part in their group with zeros. Variants: the activation,
+// and the checkpoints' kind.
+struct PrGateOut {
+  static constexpr int OPS = 2;
+  struct Pre {};
+  PrLane at;
+  Planes s;
+  Saved qa, qb, qs;
+  int m, n, act;
+  MUON_INLINE PrGateOut(PrItemRef it, PrArgsPtr args, PrLane lane)
+      : at(lane), s(args->mlp.plane[0], args->mlp, pinned(args->parts), lane), qa(args->mlp.a, lane), qb(args->mlp.b, lane),
+        qs(args->mlp.s, lane), m(pinned(it.m)), n(pinned(it.n)), act(pinned(args->mlp.act)) {}
+  // All of the checkpoints or none, and s in bf16.
+  MUON_INLINE bool plain() const { return s.parts == 1 && !qa.q == !qb.q && !qa.q == !qs.q; }
+  template <int ACT, class F>
+  MUON_INLINE void dispatch_kind(F f) const {
+    if (!qa.q) f(PrVariant<true, ACT, kNoSave>{});
+    else if (qa.kind == MUON_Q8_INT8) f(PrVariant<true, ACT, MUON_Q8_INT8>{});
+    else f(PrVariant<true, ACT, MUON_Q8_E4M3>{});
+  }
+  template <class F>
+  MUON_INLINE void dispatch(F f) const {
+    if (act == MUON_ACT_SILU) dispatch_kind<MUON_ACT_SILU>(f);
+    else if (act == MUON_ACT_GELU) dispatch_kind<MUON_ACT_GELU>(f);
+    else if (act == MUON_ACT_GELU_TANH) dispatch_kind<MUON_ACT_GELU_TANH>(f);
+    else dispatch_kind<MUON_ACT_RELU>(f);
+  }
+  template <class V>
+  MUON_INLINE void pre(int, Pre&) const {}
+  template <class V>
+  MUON_INLINE void emit(int row, float a[8], float b[8], const Pre&) const {
+    const bool there = V::FULL || row + at.row < m;
+    float v[8];
+    activations<V::A>(a, act, [&](int i, float f, float) __attribute__((always_inline)) { v[i] = f * b[i]; });
+    if (!V::FULL && at.col + 8 > n) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (at.col + i >= n) a[i] = b[i] = v[i] = 0.f;
+    }
+    if (V::FULL || (there && at.col < n)) s.put<V>(row, v);
+    if constexpr (!V::FULL || V::B != kNoSave) {
+      if (V::FULL || qa.q) qa.save<V>(row, there, a);
+      if (V::FULL || qb.q) qb.save<V>(row, there, b);
+      if (V::FULL || qs.q) qs.save<V>(row, there, v);
+    }
+  }
+};
+
+// ds of eight columns, with a and b from their checkpoints. Variants as above.
 struct PrGateGradOut {
   static constexpr int OPS = 1;
-  PrItemRef it;
-  const __attribute__((address_space(4))) PrMlp& mlp;
-  int parts;
+  struct Pre {
+    u32x2 a, b;
+    uint32_t ea, eb;
+  };
+  PrLane at;
+  Saved qa, qb;
+  Planes pa, pb;
+  char *da, *db;
+  int64_t lda, ldb;
+  uint32_t offa, offb;
+  int m, live, act;
   bool f32;
-  MUON_INLINE PrGateGradOut(PrItemRef item, PrArgsPtr a) : it(item), mlp(a->mlp), parts(a->parts), f32(a->f32) {}
-  MUON_INLINE void load(const __attribute__((address_space(4))) muon_q8& q, int row, int col, float v[8]) const {
-    const u32x2 w = *((const g_u32x2*)(static_cast<const uint8_t*>(q.q) + (int64_t)row * q.ldq + col));
-    const uint32_t E = *((const g_u8*)(static_cast<const uint8_t*>(q.e) + (int64_t)row * q.lde + col / kGroup));
-    q8_decode(w, E, q.kind, v);
+  MUON_INLINE PrGateGradOut(PrItemRef it, PrArgsPtr args, PrLane lane)
+      : at(lane), qa(args->mlp.a, lane), qb(args->mlp.b, lane), pa(args->mlp.plane[0], args->mlp, pinned(args->parts), lane),
+        pb(args->mlp.plane[1], args->mlp, pinned(args->parts), lane), da(static_cast<char*>(pinned(args->mlp.d[0]))),
+        db(static_cast<char*>(pinned(args->mlp.d[1]))), lda(pinned(args->mlp.ldd[0])), ldb(pinned(args->mlp.ldd[1])),
+        m(pinned(it.m)), live(it.n - lane.col), act(pinned(args->mlp.act)), f32(pinned(args->f32)) {
+    const int shift = f32 ? 2 : 1;
+    offa = ((uint32_t)at.row * (uint32_t)lda + (uint32_t)at.col) << shift;
+    offb = ((uint32_t)at.row * (uint32_t)ldb + (uint32_t)at.col) << shift;
+    lda <<= shift;
+    ldb <<= shift;
   }
-  MUON_INLINE void emit(int row, int col, float ds[8], float*) const {
-    const int live = row < it.m ? it.n - col : 0;
-    if (live <= 0) return;
-    float a[8], b[8], da[8], db[8];
-    load(mlp.a, row, col, a);
-    load(mlp.b, row, col, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float f, df;
-      activation(a[i], mlp.act, f, df);
-      da[i] = i < live ? ds[i] * b[i] * df : 0.f;
-      db[i] = i < live ? ds[i] * f : 0.f;
+  MUON_INLINE bool plain() const { return !f32 && !pa.p; }  // da and db are the next product's operands as they are
+  template <int ACT, class F>
+  MUON_INLINE void dispatch_kind(F f) const {
+    if (qa.kind == MUON_Q8_INT8) f(PrVariant<true, ACT, MUON_Q8_INT8>{});
+    else f(PrVariant<true, ACT, MUON_Q8_E4M3>{});
+  }
+  template <class F>
+  MUON_INLINE void dispatch(F f) const {
+    if (act == MUON_ACT_SILU) dispatch_kind<MUON_ACT_SILU>(f);
+    else if (act == MUON_ACT_GELU) dispatch_kind<MUON_ACT_GELU>(f);
+    else if (act == MUON_ACT_GELU_TANH) dispatch_kind<MUON_ACT_GELU_TANH>(f);
+    else dispatch_kind<MUON_ACT_RELU>(f);
+  }
+  template <class V>
+  MUON_INLINE void pre(int row, Pre& p) const {
+    if (!V::FULL && (row + at.row >= m || live <= 0)) return;
+    qa.load(row, p.a, p.ea);
+    qb.load(row, p.b, p.eb);
+  }
+  template <class V>
+  MUON_INLINE void emit(int row, float ds[8], float*, const Pre& p) const {
+    if (!V::FULL && (row + at.row >= m || live <= 0)) return;
+    float a[8], b[8], ga[8], gb[8];
+    q8_decode(p.a, p.ea, V::FULL ? V::B : qa.kind, a);
+    q8_decode(p.b, p.eb, V::FULL ? V::B : qb.kind, b);
+    activations<V::A>(a, act, [&](int i, float f, float df) __attribute__((always_inline)) {
+      ga[i] = ds[i] * b[i] * df;
+      gb[i] = ds[i] * f;
+    });
+    char *ba = da + (int64_t)row * lda, *bb = db + (int64_t)row * ldb;
+    if constexpr (V::FULL) {
+      store_run(reinterpret_cast<u16*>(ba + offa), 8, ga);
+      store_run(reinterpret_cast<u16*>(bb + offb), 8, gb);
+      return;
     }
+    if (f32) {
+      store_run(reinterpret_cast<float*>(ba + offa), live, ga);
+      store_run(reinterpret_cast<float*>(bb + offb), live, gb);
+    } else {
+      store_run(reinterpret_cast<u16*>(ba + offa), live, ga);
+      store_run(reinterpret_cast<u16*>(bb + offb), live, gb);
+    }
+    if (pa.p) {
+      if (live < 8) {
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const float* v = d ? db : da;
-      if (f32) store_run(static_cast<float*>(mlp.d[d]) + (int64_t)row * mlp.ldd[d] + col, live, v);
-      else store_run(static_cast<u16*>(mlp.d[d]) + (int64_t)row * mlp.ldd[d] + col, live, v);
-      if (mlp.plane[d]) put_planes(mlp, mlp.plane[d], parts, row, col, v);
+        for (int i = 0; i < 8; ++i)
+          if (i >= live) ga[i] = gb[i] = 0.f;
+      }
+      pa.put<V>(row, ga);
+      pb.put<V>(row, gb);
     }
   }
 };

@@ -74,7 +74,7 @@ struct PrCfg {
   // The tile leaves through the stage that it used last: the others hold the next
   // tile's first stages.
   static constexpr int PASSES = BM * BN * 4 / STAGE, IPP = FM / PASSES;
-  static_assert(KK % 2 == 0 && PASSES * IPP == FM && MEET >= SLOTS - PER && (!F8 || RB == 128), "schedule assumptions");
+  static_assert(KK % 2 == 0 && PASSES * IPP == FM && (PASSES == 1 || PASSES == 2 || PASSES == 4) && MEET >= SLOTS - PER && (!F8 || RB == 128), "schedule assumptions");
   static_assert(BM == BN && DA % 2 == 0 && (TABS & (TABS - 1)) == 0, "copies of A and B lie alike");
   typedef std::conditional_t<MODE == kNT8, i32x8, bf16x8> Frag;
 };
@@ -165,24 +165,101 @@ MUON_INLINE void store_run(T* p, int live, const float v[8]) {
   }
 }
 
+// How an epilogue takes a tile apart. A thread holds eight consecutive columns of one
+// row at a time, always the same columns: its row is `row` plus one that all threads
+// share, col its first column. The addresses of a row are then a scalar and a 32-bit
+// offset that does not change.
+//
+// An epilogue comes in variants: PrAny takes every tile and looks at everything as it
+// goes; the others are for tiles without an edge, and know what they look at. They
+// have no branch that may leave out a load or a store, so that a wait is for what it
+// needs and not for all that may be in flight.
+struct PrLane {
+  int row, col;
+};
+template <bool FULL_, int A_ = -1, int B_ = -1>
+struct PrVariant {
+  static constexpr bool FULL = FULL_;
+  static constexpr int A = A_, B = B_;
+};
+typedef PrVariant<false> PrAny;
+
+// Values that stay in scalar registers: read again from the kernel's arguments, they
+// would cost a wait each.
+template <class T>
+MUON_INLINE T pinned(T v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
 // C's store: eight columns of a row, plus beta times those of c, rounded once.
 struct PrStoreOut {
   static constexpr int OPS = 1;
-  PrItemRef it;
+  struct Pre {
+    float c[8];
+  };
+  PrLane at;
+  char* out;
+  const char* c;
+  int64_t ldo, ldc;
+  int m, live;
+  float beta;
   bool f32;
-  MUON_INLINE PrStoreOut(PrItemRef item, PrArgsPtr a) : it(item), f32(a->f32) {}
-  MUON_INLINE void emit(int row, int col, float v[8], float*) const {
-    const int live = row < it.m ? it.n - col : 0;
-    if (live <= 0) return;
-    if (it.beta != 0.f) {
-      float c[8];
-      if (f32) load_run(static_cast<const float*>(it.c) + (int64_t)row * it.ldc + col, live, c);
-      else load_run(static_cast<const u16*>(it.c) + (int64_t)row * it.ldc + col, live, c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += it.beta * c[i];
+  uint32_t off, offc;
+  MUON_INLINE PrStoreOut(PrItemRef it, PrArgsPtr a, PrLane lane) : at(lane) {
+    out = static_cast<char*>(pinned(it.out));
+    c = static_cast<const char*>(pinned(it.c));
+    ldo = pinned(it.ldo);
+    ldc = pinned(it.ldc);
+    m = pinned(it.m);
+    beta = pinned(it.beta);
+    f32 = pinned(a->f32);
+    live = it.n - at.col;
+    const int shift = f32 ? 2 : 1;
+    off = ((uint32_t)at.row * (uint32_t)ldo + (uint32_t)at.col) << shift;
+    offc = ((uint32_t)at.row * (uint32_t)ldc + (uint32_t)at.col) << shift;
+    ldo <<= shift;
+    ldc <<= shift;
+  }
+  MUON_INLINE bool plain() const { return true; }
+  // Variants: A the type (1 fp32), B whether there is a c.
+  template <class F>
+  MUON_INLINE void dispatch(F f) const {
+    if (f32) beta != 0.f ? f(PrVariant<true, 1, 1>{}) : f(PrVariant<true, 1, 0>{});
+    else beta != 0.f ? f(PrVariant<true, 0, 1>{}) : f(PrVariant<true, 0, 0>{});
+  }
+  template <class V>
+  MUON_INLINE void pre(int row, Pre& p) const {
+    const char* base = c + (int64_t)row * ldc;
+    if constexpr (V::FULL && V::B >= 0) {
+      if constexpr (V::B != 0) {
+        if constexpr (V::A != 0) load_run(reinterpret_cast<const float*>(base + offc), 8, p.c);
+        else load_run(reinterpret_cast<const u16*>(base + offc), 8, p.c);
+      }
+    } else if (beta != 0.f && row + at.row < m && live > 0) {
+      if (f32) load_run(reinterpret_cast<const float*>(base + offc), live, p.c);
+      else load_run(reinterpret_cast<const u16*>(base + offc), live, p.c);
     }
-    if (f32) store_run(static_cast<float*>(it.out) + (int64_t)row * it.ldo + col, live, v);
-    else store_run(static_cast<u16*>(it.out) + (int64_t)row * it.ldo + col, live, v);
+  }
+  template <class V>
+  MUON_INLINE void emit(int row, float v[8], float*, const Pre& p) const {
+    char* base = out + (int64_t)row * ldo;
+    if constexpr (V::FULL) {
+      if constexpr (V::B != 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += beta * p.c[i];
+      }
+      if constexpr (V::A != 0) store_run(reinterpret_cast<float*>(base + off), 8, v);
+      else store_run(reinterpret_cast<u16*>(base + off), 8, v);
+    } else {
+      if (row + at.row >= m || live <= 0) return;
+      if (beta != 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += beta * p.c[i];
+      }
+      if (f32) store_run(reinterpret_cast<float*>(base + off), live, v);
+      else store_run(reinterpret_cast<u16*>(base + off), live, v);
+    }
   }
 };
 
@@ -190,16 +267,18 @@ struct PrStoreOut {
 // LDS, IPP blocks of rows of every wave at a time: staged row r, whose 16-byte unit u
 // sits at u ^ (r % the row's units), is row WM*(r / PR) + PR*pass + r % PR of the
 // tile.
-template <class Z, class Out>
-MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, const PrUnit& un, unsigned char* stage, const f32x16 (&acc)[Z::FM][Z::FN]) {
-  constexpr bool DUAL = Out::OPS == 2;
-  constexpr int UNITS = Z::BN / 4, MASK = UNITS - 1, ROWS = 64 * Z::IPP, PR = 32 * Z::IPP;
-  constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;  // lanes of a row
-  const int tid = fresh_tid(), lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  const Out out(it, args);
-#pragma unroll
-  for (int pass = 0; pass < Z::PASSES; ++pass) {
-    if (pass) __syncthreads();
+template <class Z>
+struct PrStage {
+  static constexpr int MASK = Z::BN / 4 - 1, ROWS = 64 * Z::IPP, PR = 32 * Z::IPP;
+  unsigned char* lds;
+  const f32x16 (&acc)[Z::FM][Z::FN];
+  MUON_INLINE static int tile_row(int pass, int r) { return Z::WM * (r / PR) + PR * pass + r % PR; }
+  // One pass's rows. The marks at both ends keep the passes apart: the compiler would
+  // make one of them all, with a pointer to the sums, which then live in memory.
+  template <int P>
+  MUON_INLINE void fill_from() const {
+    asm volatile("; pass %0" ::"n"(P) : "memory");
+    const int tid = fresh_tid(), lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
 #pragma unroll
     for (int ii = 0; ii < Z::IPP; ++ii)
 #pragma unroll
@@ -207,41 +286,97 @@ MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, const PrUnit& un, unsign
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int r = wm * PR + 32 * ii + (lane & 31), u = wn * (Z::WN / 4) + 8 * j + 2 * g + (lane >> 5);
-          const f32x16& t = acc[pass * Z::IPP + ii][j];
-          *reinterpret_cast<f32x4*>(stage + r * Z::BN * 4 + ((u ^ (r & MASK)) << 4)) =
+          const f32x16& t = acc[P * Z::IPP + ii][j];
+          *reinterpret_cast<f32x4*>(lds + r * Z::BN * 4 + ((u ^ (r & MASK)) << 4)) =
               f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
         }
+    asm volatile("; pass %0" ::"n"(P) : "memory");
+  }
+  // The barrier before is for the readers of the pass before.
+  MUON_INLINE void fill(int pass) const {
+    if (pass) __syncthreads();
+    if (pass == 0) fill_from<0>();
+    if constexpr (Z::PASSES > 1) {
+      if (pass == 1) fill_from<1>();
+    }
+    if constexpr (Z::PASSES > 2) {
+      if (pass == 2) fill_from<2>();
+      if (pass == 3) fill_from<3>();
+    }
     __syncthreads();
-    auto run_of = [&](int r, int col, float v[8]) __attribute__((always_inline)) {
-      const unsigned char* row = stage + r * Z::BN * 4;
+  }
+  MUON_INLINE void run(int r, int col, float v[8]) const {
+    const unsigned char* row = lds + r * Z::BN * 4;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const f32x4 t = *reinterpret_cast<const f32x4*>(row + (((col / 4 + q) ^ (r & MASK)) << 4));
+    for (int q = 0; q < 2; ++q) {
+      const f32x4 t = *reinterpret_cast<const f32x4*>(row + (((col / 4 + q) ^ (r & MASK)) << 4));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * q + e] = t[e];
-      }
-    };
-    auto tile_row = [&](int r) __attribute__((always_inline)) { return Z::WM * (r / PR) + PR * pass + r % PR; };
-    if (it.splits > 1) {
-      float* p = args->partial + (int64_t)(it.part0 + un.local) * Z::BM * Z::BN;
-#pragma unroll 2
-      for (int q = 0; q < ROWS * (Z::BN / kRun) / Z::NT; ++q) {
-        const int i = q * Z::NT + tid, r = i / (Z::BN / kRun), col = i % (Z::BN / kRun) * kRun;
-        float v[8];
-        run_of(r, col, v);
-        store_run(p + tile_row(r) * Z::BN + col, 8, v);
-      }
-    } else {
-#pragma unroll 2
-      for (int q = 0; q < ROWS * LW / Z::NT; ++q) {
-        const int i = q * Z::NT + tid, r = i / LW, col = i % LW * kRun;
-        float v[8], w[8];
-        run_of(r, col, v);
-        if constexpr (DUAL) run_of(r, Z::BN / 2 + col, w);
-        out.emit(un.m0 + tile_row(r), (DUAL ? un.n0 >> 1 : un.n0) + col, v, w);
-      }
+      for (int e = 0; e < 4; ++e) v[4 * q + e] = t[e];
     }
   }
+};
+
+// Thread t takes the runs of columns 8 (t % LW) .. of rows t / LW + STEP q of every
+// pass. What an epilogue reads from memory it asks for AHEAD runs before.
+template <class Z, class Out, bool FULL>
+MUON_INLINE void pr_leave_as(const PrStage<Z>& stage, const Out& out, int m0) {
+  constexpr bool DUAL = Out::OPS == 2;
+  constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;
+  constexpr int STEP = Z::NT / LW, IT = PrStage<Z>::ROWS / STEP, AHEAD = IT < 4 ? IT : 4, ALL = Z::PASSES * IT;
+  const int tid = fresh_tid(), row = tid / LW, col = tid % LW * kRun;
+  // The matrix's row of run g, without the thread's own part.
+  auto row_of = [&](int g) __attribute__((always_inline)) { return m0 + PrStage<Z>::tile_row(g / IT, g % IT * STEP); };
+  typename Out::Pre pre[AHEAD];
+#pragma unroll
+  for (int g = 0; g < AHEAD; ++g) out.template pre<PrVariant<FULL>>(row_of(g), pre[g]);
+#pragma unroll 1
+  for (int pass = 0; pass < Z::PASSES; ++pass) {
+    stage.fill(pass);
+    auto runs = [&](auto variant) __attribute__((always_inline)) {
+      typedef decltype(variant) V;
+#pragma unroll 1
+      for (int q0 = 0; q0 < IT; q0 += AHEAD)
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+          const int g = pass * IT + q0 + a;
+          float v[8], w[8];
+          stage.run((q0 + a) * STEP + row, col, v);
+          if constexpr (DUAL) stage.run((q0 + a) * STEP + row, Z::BN / 2 + col, w);
+          out.template emit<V>(row_of(g), v, w, pre[a]);
+          out.template pre<V>(row_of(min(g + AHEAD, ALL - 1)), pre[a]);  // past the end: the last one again
+        }
+    };
+    if constexpr (FULL) out.dispatch(runs);
+    else runs(PrAny{});
+  }
+}
+
+template <class Z, class Out>
+MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, int local, int m0, int n0, unsigned char* lds,
+                          const f32x16 (&acc)[Z::FM][Z::FN]) {
+  constexpr bool DUAL = Out::OPS == 2;
+  constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;
+  const int tid = fresh_tid(), c0 = DUAL ? n0 >> 1 : n0;
+  const PrStage<Z> stage{lds, acc};
+  if (it.splits > 1) {
+    constexpr int PLW = Z::BN / kRun, PSTEP = Z::NT / PLW;
+    const int row = tid / PLW, col = tid % PLW * kRun;
+    float* part = args->partial + (int64_t)(it.part0 + local) * Z::BM * Z::BN;
+#pragma unroll 1
+    for (int pass = 0; pass < Z::PASSES; ++pass) {
+      stage.fill(pass);
+#pragma unroll 4
+      for (int q = 0; q < PrStage<Z>::ROWS / PSTEP; ++q) {
+        float v[8];
+        stage.run(q * PSTEP + row, col, v);
+        store_run(part + PrStage<Z>::tile_row(pass, q * PSTEP) * Z::BN + row * Z::BN + col, 8, v);
+      }
+    }
+    return;
+  }
+  const Out out(it, args, PrLane{tid / LW, c0 + tid % LW * kRun});
+  if (out.plain() && m0 + Z::BM <= it.m && c0 + COLS <= it.n) pr_leave_as<Z, Out, true>(stage, out, m0);
+  else pr_leave_as<Z, Out, false>(stage, out, m0);
 }
 
 // All units of one workgroup. XCD b % 8 gets a contiguous range of units, which its
@@ -596,7 +731,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
       cur = after;
       to = to + Z::STAGE == Z::RING ? 0 : to + Z::STAGE;
     }
-    pr_leave<Z, Out>(args, it, u, smem + to, acc);
+    pr_leave<Z, Out>(args, it, u.local, u.m0, u.n0, smem + to, acc);
   }
   wait_vmcnt<0>();  // the copies past the last stage
 }
@@ -618,8 +753,11 @@ MUON_INLINE void pr_join_of(int edge) {
   const int tiles = it.tiles_m * it.tiles_n, tile = b / per;
   int tm, tn;
   pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
-  const int i = (b - tile * per) * 256 + threadIdx.x, r = i / lw, col = i % lw * kRun;
-  const float* p = args->partial + ((int64_t)(it.part0 + tile) * edge + r) * edge + col;
+  const int row0 = (b - tile * per) * (256 / lw), r = threadIdx.x / lw, col = threadIdx.x % lw * kRun;
+  const Out out(it, args, PrLane{r, (DUAL ? tn * edge / 2 : tn * edge) + col});
+  typename Out::Pre pre;
+  out.template pre<PrAny>(tm * edge + row0, pre);
+  const float* p = args->partial + ((int64_t)(it.part0 + tile) * edge + row0 + r) * edge + col;
   const int64_t step = (int64_t)tiles * edge * edge;
   float v[8], w[8];
 #pragma unroll
@@ -635,8 +773,7 @@ MUON_INLINE void pr_join_of(int edge) {
       if constexpr (DUAL) w[e] += y[e];
     }
   }
-  const Out out(it, args);
-  out.emit(tm * edge + r, (DUAL ? tn * edge / 2 : tn * edge) + col, v, w);
+  out.template emit<PrAny>(tm * edge + row0, v, w, pre);
 }
 
 // Workgroups of a launch: as many as the CUs hold at once.

@@ -101,6 +101,17 @@ muon_status check_inner(Views& v, const muon_mlp& p, const muon_q8& q, bool writ
   return check_q8(v, q, written, name);
 }
 
+muon_status check_kinds(const muon_mlp& p) {
+  const muon_q8* q[] = {&p.a, &p.b, &p.s};
+  int kind = -1;
+  for (const muon_q8* x : q) {
+    if (!x->q) continue;
+    if (kind >= 0 && x->kind != kind) return fail(MUON_ERR_INVALID_ARG, "a, b and s must be checkpoints of the same kind");
+    kind = x->kind;
+  }
+  return MUON_OK;
+}
+
 // An operand of a product: as the caller gave it, if it is bf16 in 16-byte aligned
 // rows of whole 16-byte chunks, else rewritten into the workspace first.
 struct Operand {
@@ -297,6 +308,7 @@ muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
   if (p.a.q) MUON_TRY(check_inner(v, p, p.a, true, "a"));
   if (p.b.q) MUON_TRY(check_inner(v, p, p.b, true, "b"));
   if (p.s.q) MUON_TRY(check_inner(v, p, p.s, true, "s"));
+  MUON_TRY(check_kinds(p));
   if (p.rows == 0) return v.disjoint();
   char* ws = static_cast<char*>(p.workspace);
   MlpCall c;
@@ -320,6 +332,7 @@ muon_status mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void*
   MUON_TRY(v.add(g.dy, p.rows, p.out, g.ld_dy, e, false, "dy"));
   MUON_TRY(check_inner(v, p, p.a, false, "a"));
   MUON_TRY(check_inner(v, p, p.b, false, "b"));
+  if (p.a.kind != p.b.kind) return fail(MUON_ERR_INVALID_ARG, "a and b must be checkpoints of the same kind");
   MUON_TRY(v.add(g.d_a, p.rows, p.inner, g.ld_d_a, e, true, "d_a"));
   MUON_TRY(v.add(g.d_b, p.rows, p.inner, g.ld_d_b, e, true, "d_b"));
   if (g.d_x) MUON_TRY(v.add(g.d_x, p.rows, p.width, g.ld_d_x, e, true, "d_x"));
