@@ -644,6 +644,18 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     }
   };
 
+  // Holds the MFMAs above this place: to the compiler they are sums that only later
+  // code reads, and it moves them there, behind the barrier.
+  auto anchor = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (FM * FN >= 16) asm volatile("" : "+a"(acc[i][j]));
+        else asm volatile("" : "+v"(acc[i][j]));
+      }
+  };
+
   open();
 #pragma unroll 1
   for (int s = 0; s < Z::ST - 1; ++s) {
@@ -694,6 +706,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
         for (int q = 0; q < Z::PER; ++q) {
           const int slot = kk * Z::PER + q, b = kk & 1;
           if (slot == Z::MEET) {
+            anchor();
             if (lfresh) write_ex();
             // the next stage's copies are the oldest in flight
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((Z::ST - 2) * Z::PS) : "memory");
@@ -709,7 +722,10 @@ MUON_INLINE void pr_run(unsigned char* smem) {
             for (int f = 0; f < Z::NF; ++f)
               if (f * Z::PER / Z::NF == q) read_frag(b ^ 1, cur, kk + 1, f);
           }
-          if (slot == Z::SLOTS - 1) take_ex();
+          if (slot == Z::SLOTS - 1) {
+            anchor();
+            take_ex();
+          }
           if constexpr (Z::MODE != kNT8X) {
             if (slot >= Z::MEET) {
 #pragma unroll
