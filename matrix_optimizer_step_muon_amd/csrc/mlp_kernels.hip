@@ -66,26 +66,29 @@ struct Saved {
   int64_t ldq, lde;
   int kind;
   uint32_t off, offe;
-  bool put_q, put_e;
+  int col, cols, cols16;
+  bool first;  // of the four lanes of a group
   MUON_INLINE Saved(const __attribute__((address_space(4))) muon_q8& s, PrLane at)
       : q(static_cast<uint8_t*>(pinned(s.q))), e(static_cast<uint8_t*>(pinned(s.e))), ldq(pinned(s.ldq)), lde(pinned(s.lde)),
         kind(pinned(s.kind)) {
     off = (uint32_t)at.row * (uint32_t)ldq + (uint32_t)at.col;
     offe = (uint32_t)at.row * (uint32_t)lde + (uint32_t)(at.col / kGroup);
-    put_q = at.col < ((int)s.cols + 15) / 16 * 16;
-    put_e = (at.col & (kGroup - 1)) == 0 && at.col < s.cols;
+    col = at.col;
+    cols = (int)s.cols;
+    cols16 = (cols + 15) / 16 * 16;
+    first = (col & (kGroup - 1)) == 0;
   }
   // Columns of a group are four lanes. Padding columns (up to a multiple of 16) get 0.
   template <class V>
-  MUON_INLINE void save(int row, bool there, const float v[8]) const {
+  MUON_INLINE void save(int row, int dc, bool there, const float v[8]) const {
     u32x2 w;
     const uint32_t E = q8_encode(v, V::FULL ? V::B : kind, w);
-    uint8_t *pq = q + (int64_t)row * ldq, *pe = e + (int64_t)row * lde;
-    if (V::FULL || (there && put_q)) *((g_u32x2*)(pq + off)) = w;
-    if (there && put_e) *((g_u8*)(pe + offe)) = (uint8_t)E;
+    uint8_t *pq = q + (int64_t)row * ldq + dc, *pe = e + (int64_t)row * lde + dc / kGroup;
+    if (V::FULL || (there && col + dc < cols16)) *((g_u32x2*)(pq + off)) = w;
+    if (first && (V::FULL || (there && col + dc < cols))) *((g_u8*)(pe + offe)) = (uint8_t)E;
   }
-  MUON_INLINE void load(int row, u32x2& w, uint32_t& E) const {
-    const uint8_t *pq = q + (int64_t)row * ldq, *pe = e + (int64_t)row * lde;
+  MUON_INLINE void load(int row, int dc, u32x2& w, uint32_t& E) const {
+    const uint8_t *pq = q + (int64_t)row * ldq + dc, *pe = e + (int64_t)row * lde + dc / kGroup;
     w = *((const g_u32x2*)(pq + off));
     E = *((const g_u8*)(pe + offe));
   }
@@ -102,8 +105,8 @@ struct Planes {
     off = (uint32_t)at.row * (uint32_t)ld + 2u * (uint32_t)at.col;
   }
   template <class V>
-  MUON_INLINE void put(int row, const float v[8]) const {
-    char* base = p + (int64_t)row * ld;
+  MUON_INLINE void put(int row, int dc, const float v[8]) const {
+    char* base = p + (int64_t)row * ld + 2 * dc;
     if (V::FULL || parts == 1) {
       *((g_u32x4*)(base + off)) =
           u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
@@ -125,7 +128,7 @@ constexpr int kNoSave = 2;  // a variant's B, beside the kinds: no checkpoint is
 // past the last column take part in their group with zeros. Variants: the activation,
 // and the checkpoints' kind.
 struct PrGateOut {
-  static constexpr int OPS = 2;
+  static constexpr int OPS = 2, AHEAD = 1;
   struct Pre {};
   PrLane at;
   Planes s;
@@ -150,29 +153,30 @@ struct PrGateOut {
     else dispatch_kind<MUON_ACT_RELU>(f);
   }
   template <class V>
-  MUON_INLINE void pre(int, Pre&) const {}
+  MUON_INLINE void pre(int, int, Pre&) const {}
   template <class V>
-  MUON_INLINE void emit(int row, float a[8], float b[8], const Pre&) const {
+  MUON_INLINE void emit(int row, int dc, float a[8], float b[8], const Pre&) const {
     const bool there = V::FULL || row + at.row < m;
+    const int live = n - at.col - dc;
     float v[8];
     activations<V::A>(a, act, [&](int i, float f, float) __attribute__((always_inline)) { v[i] = f * b[i]; });
-    if (!V::FULL && at.col + 8 > n) {
+    if (!V::FULL && live < 8) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (at.col + i >= n) a[i] = b[i] = v[i] = 0.f;
+        if (i >= live) a[i] = b[i] = v[i] = 0.f;
     }
-    if (V::FULL || (there && at.col < n)) s.put<V>(row, v);
+    if (V::FULL || (there && live > 0)) s.put<V>(row, dc, v);
     if constexpr (!V::FULL || V::B != kNoSave) {
-      if (V::FULL || qa.q) qa.save<V>(row, there, a);
-      if (V::FULL || qb.q) qb.save<V>(row, there, b);
-      if (V::FULL || qs.q) qs.save<V>(row, there, v);
+      if (V::FULL || qa.q) qa.save<V>(row, dc, there, a);
+      if (V::FULL || qb.q) qb.save<V>(row, dc, there, b);
+      if (V::FULL || qs.q) qs.save<V>(row, dc, there, v);
     }
   }
 };
 
 // ds of eight columns, with a and b from their checkpoints. Variants as above.
 struct PrGateGradOut {
-  static constexpr int OPS = 1;
+  static constexpr int OPS = 1, AHEAD = 8;
   struct Pre {
     u32x2 a, b;
     uint32_t ea, eb;
@@ -210,14 +214,14 @@ struct PrGateGradOut {
     else dispatch_kind<MUON_ACT_RELU>(f);
   }
   template <class V>
-  MUON_INLINE void pre(int row, Pre& p) const {
-    if (!V::FULL && (row + at.row >= m || live <= 0)) return;
-    qa.load(row, p.a, p.ea);
-    qb.load(row, p.b, p.eb);
+  MUON_INLINE void pre(int row, int dc, Pre& p) const {
+    if (!V::FULL && (row + at.row >= m || live <= dc)) return;
+    qa.load(row, dc, p.a, p.ea);
+    qb.load(row, dc, p.b, p.eb);
   }
   template <class V>
-  MUON_INLINE void emit(int row, float ds[8], float*, const Pre& p) const {
-    if (!V::FULL && (row + at.row >= m || live <= 0)) return;
+  MUON_INLINE void emit(int row, int dc, float ds[8], float*, const Pre& p) const {
+    if (!V::FULL && (row + at.row >= m || live <= dc)) return;
     float a[8], b[8], ga[8], gb[8];
     q8_decode(p.a, p.ea, V::FULL ? V::B : qa.kind, a);
     q8_decode(p.b, p.eb, V::FULL ? V::B : qb.kind, b);
@@ -225,27 +229,29 @@ struct PrGateGradOut {
       ga[i] = ds[i] * b[i] * df;
       gb[i] = ds[i] * f;
     });
-    char *ba = da + (int64_t)row * lda, *bb = db + (int64_t)row * ldb;
+    const int64_t shift = (int64_t)dc << (f32 ? 2 : 1);
+    char *ba = da + (int64_t)row * lda + shift, *bb = db + (int64_t)row * ldb + shift;
     if constexpr (V::FULL) {
       store_run(reinterpret_cast<u16*>(ba + offa), 8, ga);
       store_run(reinterpret_cast<u16*>(bb + offb), 8, gb);
       return;
     }
+    const int here = live - dc;
     if (f32) {
-      store_run(reinterpret_cast<float*>(ba + offa), live, ga);
-      store_run(reinterpret_cast<float*>(bb + offb), live, gb);
+      store_run(reinterpret_cast<float*>(ba + offa), here, ga);
+      store_run(reinterpret_cast<float*>(bb + offb), here, gb);
     } else {
-      store_run(reinterpret_cast<u16*>(ba + offa), live, ga);
-      store_run(reinterpret_cast<u16*>(bb + offb), live, gb);
+      store_run(reinterpret_cast<u16*>(ba + offa), here, ga);
+      store_run(reinterpret_cast<u16*>(bb + offb), here, gb);
     }
     if (pa.p) {
-      if (live < 8) {
+      if (here < 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i >= live) ga[i] = gb[i] = 0.f;
+          if (i >= here) ga[i] = gb[i] = 0.f;
       }
-      pa.put<V>(row, ga);
-      pb.put<V>(row, gb);
+      pa.put<V>(row, dc, ga);
+      pb.put<V>(row, dc, gb);
     }
   }
 };
@@ -257,8 +263,8 @@ __global__ void __launch_bounds__(Z::NT, Z::WG) mlp_product_kernel(PrArgs) {
 }
 
 template <class Out>
-__global__ void __launch_bounds__(256) mlp_join_kernel(PrArgs, int edge) {
-  pr_join_of<Out>(edge);
+__global__ void __launch_bounds__(256) mlp_join_kernel(PrArgs, int bm, int bn) {
+  pr_join_of<Out>(bm, bn);
 }
 
 template <int MODE, class Out>
@@ -266,14 +272,18 @@ static hipError_t launch_tiles(const PrArgs& args, hipStream_t s) {
   typedef PrCfg<256, 256, 128, 2, MODE, 1> Large;
   typedef PrCfg<128, 128, 128, 2, MODE, 2> Medium;
   typedef PrCfg<64, 64, 128, 4, MODE, 2> Small;
+  typedef PrCfg<128, 256, 64, 3, MODE, 2> Wide;
+  typedef PrCfg<256, 256, 64, 4, MODE, 1> Deep;
   const dim3 block(256);
   if (args.tile == kPrLarge) hipLaunchKernelGGL((mlp_product_kernel<Large, Out>), dim3(pr_grid<Large>(args)), block, 0, s, args);
   else if (args.tile == kPrMedium) hipLaunchKernelGGL((mlp_product_kernel<Medium, Out>), dim3(pr_grid<Medium>(args)), block, 0, s, args);
-  else hipLaunchKernelGGL((mlp_product_kernel<Small, Out>), dim3(pr_grid<Small>(args)), block, 0, s, args);
+  else if (args.tile == kPrSmall) hipLaunchKernelGGL((mlp_product_kernel<Small, Out>), dim3(pr_grid<Small>(args)), block, 0, s, args);
+  else if (args.tile == kPrWide) hipLaunchKernelGGL((mlp_product_kernel<Wide, Out>), dim3(pr_grid<Wide>(args)), block, 0, s, args);
+  else hipLaunchKernelGGL((mlp_product_kernel<Deep, Out>), dim3(pr_grid<Deep>(args)), block, 0, s, args);
   const hipError_t e = hipGetLastError();
   const int64_t join = pr_join_blocks(args, Out::OPS == 2);
   if (e != hipSuccess || join == 0) return e;
-  hipLaunchKernelGGL(mlp_join_kernel<Out>, dim3((uint32_t)join), dim3(256), 0, s, args, kPrEdge[args.tile]);
+  hipLaunchKernelGGL(mlp_join_kernel<Out>, dim3((uint32_t)join), dim3(256), 0, s, args, kPrBM[args.tile], kPrBN[args.tile]);
   return hipGetLastError();
 }
 

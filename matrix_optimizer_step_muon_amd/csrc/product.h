@@ -66,16 +66,21 @@ struct PrCfg {
   static constexpr int KK = RB / SUB, PER = FM * FN, SLOTS = KK * PER, NF = FM + FN;
   // The slot at which the workgroup meets: the last sub-step's fragments are in
   // registers, the next stage must be in LDS.
-  static constexpr int MEET = SLOTS - (PER >= 16 ? 4 : PER >= 4 ? 2 : 1);
-  // 8-bit operands: exponents of eight stages (RB = 128: 1024 of K), for as many runs
-  // of stages as a ring can hold parts of
-  static constexpr int TABS = ST, EX_A = 8 * BM * 4, EX_B = 8 * 2 * 4, EX = F8 ? TABS * (EX_A + EX_B) : 0;
+  static constexpr int MEET = KK == 1 ? PER / 2 : SLOTS - (PER >= 16 ? 4 : PER >= 4 ? 2 : 1);
+  // 8-bit operands: exponents of 1024 of K, for as many runs of stages as a ring can
+  // hold parts of
+  static constexpr int CHUNK = 1024 / RB, TABS = ST <= 2 ? 2 : 4, EX_A = 8 * BM * 4, EX_B = 8 * 2 * 4, EX = F8 ? TABS * (EX_A + EX_B) : 0;
   static constexpr int LDS = RING + EX;
-  // The tile leaves through the stage that it used last: the others hold the next
-  // tile's first stages.
-  static constexpr int PASSES = BM * BN * 4 / STAGE, IPP = FM / PASSES;
-  static_assert(KK % 2 == 0 && PASSES * IPP == FM && (PASSES == 1 || PASSES == 2 || PASSES == 4) && MEET >= SLOTS - PER && (!F8 || RB == 128), "schedule assumptions");
-  static_assert(BM == BN && DA % 2 == 0 && (TABS & (TABS - 1)) == 0, "copies of A and B lie alike");
+  // The tile leaves through the stage that it used last (the others hold the next
+  // tile's first stages): IPP blocks of 32 rows of every wave at a time, or, where
+  // that does not fit, one block of rows and NJ blocks of 32 columns.
+  static constexpr int ROW_BLOCK = 64 * BN * 4;
+  static constexpr int IPP = STAGE >= ROW_BLOCK ? STAGE / ROW_BLOCK : 1;
+  static constexpr int NJ = STAGE >= ROW_BLOCK ? FN : FN >= 4 && STAGE >= ROW_BLOCK / 2 ? FN / 2 : FN >= 4 ? FN / 4 : 1;
+  static constexpr int PASSES = FM / IPP * (FN / NJ), SCOLS = 64 * NJ;  // columns of a staged row
+  static_assert(FM % IPP == 0 && 64 * IPP * SCOLS * 4 <= STAGE && PASSES <= 8, "a pass fits a stage");
+  static_assert((KK % 2 == 0 || KK == 1) && MEET >= SLOTS - PER, "schedule assumptions");
+  static_assert(DA % 2 == 0 && DB % 2 == 0 && ST <= 4, "copies of A and B lie alike");
   typedef std::conditional_t<MODE == kNT8, i32x8, bf16x8> Frag;
 };
 
@@ -166,9 +171,9 @@ MUON_INLINE void store_run(T* p, int live, const float v[8]) {
 }
 
 // How an epilogue takes a tile apart. A thread holds eight consecutive columns of one
-// row at a time, always the same columns: its row is `row` plus one that all threads
-// share, col its first column. The addresses of a row are then a scalar and a 32-bit
-// offset that does not change.
+// row at a time: its row is `row` plus one that all threads share, its first column
+// col plus a shift that all share. The addresses are then a scalar and a 32-bit offset
+// that does not change.
 //
 // An epilogue comes in variants: PrAny takes every tile and looks at everything as it
 // goes; the others are for tiles without an edge, and know what they look at. They
@@ -194,7 +199,7 @@ MUON_INLINE T pinned(T v) {
 
 // C's store: eight columns of a row, plus beta times those of c, rounded once.
 struct PrStoreOut {
-  static constexpr int OPS = 1;
+  static constexpr int OPS = 1, AHEAD = 4;
   struct Pre {
     float c[8];
   };
@@ -229,21 +234,21 @@ struct PrStoreOut {
     else beta != 0.f ? f(PrVariant<true, 0, 1>{}) : f(PrVariant<true, 0, 0>{});
   }
   template <class V>
-  MUON_INLINE void pre(int row, Pre& p) const {
-    const char* base = c + (int64_t)row * ldc;
+  MUON_INLINE void pre(int row, int dc, Pre& p) const {
+    const char* base = c + (int64_t)row * ldc + ((int64_t)dc << (f32 ? 2 : 1));
     if constexpr (V::FULL && V::B >= 0) {
       if constexpr (V::B != 0) {
         if constexpr (V::A != 0) load_run(reinterpret_cast<const float*>(base + offc), 8, p.c);
         else load_run(reinterpret_cast<const u16*>(base + offc), 8, p.c);
       }
-    } else if (beta != 0.f && row + at.row < m && live > 0) {
-      if (f32) load_run(reinterpret_cast<const float*>(base + offc), live, p.c);
-      else load_run(reinterpret_cast<const u16*>(base + offc), live, p.c);
+    } else if (beta != 0.f && row + at.row < m && live > dc) {
+      if (f32) load_run(reinterpret_cast<const float*>(base + offc), live - dc, p.c);
+      else load_run(reinterpret_cast<const u16*>(base + offc), live - dc, p.c);
     }
   }
   template <class V>
-  MUON_INLINE void emit(int row, float v[8], float*, const Pre& p) const {
-    char* base = out + (int64_t)row * ldo;
+  MUON_INLINE void emit(int row, int dc, float v[8], float*, const Pre& p) const {
+    char* base = out + (int64_t)row * ldo + ((int64_t)dc << (f32 ? 2 : 1));
     if constexpr (V::FULL) {
       if constexpr (V::B != 0) {
 #pragma unroll
@@ -252,27 +257,32 @@ struct PrStoreOut {
       if constexpr (V::A != 0) store_run(reinterpret_cast<float*>(base + off), 8, v);
       else store_run(reinterpret_cast<u16*>(base + off), 8, v);
     } else {
-      if (row + at.row >= m || live <= 0) return;
+      if (row + at.row >= m || live <= dc) return;
       if (beta != 0.f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += beta * p.c[i];
       }
-      if (f32) store_run(reinterpret_cast<float*>(base + off), live, v);
-      else store_run(reinterpret_cast<u16*>(base + off), live, v);
+      if (f32) store_run(reinterpret_cast<float*>(base + off), live - dc, v);
+      else store_run(reinterpret_cast<u16*>(base + off), live - dc, v);
     }
   }
 };
 
 // A tile's way out: its partial sums, BM x BN floats, or the epilogue Out. Through
-// LDS, IPP blocks of rows of every wave at a time: staged row r, whose 16-byte unit u
-// sits at u ^ (r % the row's units), is row WM*(r / PR) + PR*pass + r % PR of the
-// tile.
+// LDS, a pass of rows and columns of every wave at a time: staged row r is row WM*(r /
+// PR) + PR*(the pass's block of rows) + r % PR of the tile, staged column c is column
+// WN*(c / (32 NJ)) + 32 NJ*(the pass's block of columns) + c % (32 NJ); its 16-byte
+// unit u sits at u ^ (r % the row's units).
 template <class Z>
 struct PrStage {
-  static constexpr int MASK = Z::BN / 4 - 1, ROWS = 64 * Z::IPP, PR = 32 * Z::IPP;
+  static constexpr int MASK = Z::SCOLS / 4 - 1, ROWS = 64 * Z::IPP, PR = 32 * Z::IPP, JB = Z::FN / Z::NJ;
   unsigned char* lds;
   const f32x16 (&acc)[Z::FM][Z::FN];
-  MUON_INLINE static int tile_row(int pass, int r) { return Z::WM * (r / PR) + PR * pass + r % PR; }
+  // The first of the tile's rows and columns that belong to staged row r (a multiple
+  // of what a pass's threads share) and to staged column 0.
+  MUON_INLINE static int tile_row(int pass, int r) { return Z::WM * (r / PR) + PR * (pass / JB) + r % PR; }
+  MUON_INLINE static int tile_col(int pass) { return 32 * Z::NJ * (pass % JB); }
+  MUON_INLINE static int own_col(int c) { return Z::WN * (c / (32 * Z::NJ)) + c % (32 * Z::NJ); }
   // One pass's rows. The marks at both ends keep the passes apart: the compiler would
   // make one of them all, with a pointer to the sums, which then live in memory.
   template <int P>
@@ -282,31 +292,31 @@ struct PrStage {
 #pragma unroll
     for (int ii = 0; ii < Z::IPP; ++ii)
 #pragma unroll
-      for (int j = 0; j < Z::FN; ++j)
+      for (int j = 0; j < Z::NJ; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int r = wm * PR + 32 * ii + (lane & 31), u = wn * (Z::WN / 4) + 8 * j + 2 * g + (lane >> 5);
-          const f32x16& t = acc[P * Z::IPP + ii][j];
-          *reinterpret_cast<f32x4*>(lds + r * Z::BN * 4 + ((u ^ (r & MASK)) << 4)) =
+          const int r = wm * PR + 32 * ii + (lane & 31), u = wn * (8 * Z::NJ) + 8 * j + 2 * g + (lane >> 5);
+          const f32x16& t = acc[P / JB * Z::IPP + ii][P % JB * Z::NJ + j];
+          *reinterpret_cast<f32x4*>(lds + r * Z::SCOLS * 4 + ((u ^ (r & MASK)) << 4)) =
               f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
         }
     asm volatile("; pass %0" ::"n"(P) : "memory");
   }
+  template <int P>
+  MUON_INLINE void fill_if(int pass) const {
+    if constexpr (P < Z::PASSES) {
+      if (pass == P) fill_from<P>();
+      fill_if<P + 1>(pass);
+    }
+  }
   // The barrier before is for the readers of the pass before.
   MUON_INLINE void fill(int pass) const {
     if (pass) __syncthreads();
-    if (pass == 0) fill_from<0>();
-    if constexpr (Z::PASSES > 1) {
-      if (pass == 1) fill_from<1>();
-    }
-    if constexpr (Z::PASSES > 2) {
-      if (pass == 2) fill_from<2>();
-      if (pass == 3) fill_from<3>();
-    }
+    fill_if<0>(pass);
     __syncthreads();
   }
   MUON_INLINE void run(int r, int col, float v[8]) const {
-    const unsigned char* row = lds + r * Z::BN * 4;
+    const unsigned char* row = lds + r * Z::SCOLS * 4;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const f32x4 t = *reinterpret_cast<const f32x4*>(row + (((col / 4 + q) ^ (r & MASK)) << 4));
@@ -316,19 +326,22 @@ struct PrStage {
   }
 };
 
-// Thread t takes the runs of columns 8 (t % LW) .. of rows t / LW + STEP q of every
-// pass. What an epilogue reads from memory it asks for AHEAD runs before.
+// Where a tile's two products lie side by side (DUAL), the waves' left column holds
+// the first and the right one the second.
 template <class Z, class Out, bool FULL>
 MUON_INLINE void pr_leave_as(const PrStage<Z>& stage, const Out& out, int m0) {
   constexpr bool DUAL = Out::OPS == 2;
-  constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;
-  constexpr int STEP = Z::NT / LW, IT = PrStage<Z>::ROWS / STEP, AHEAD = IT < 4 ? IT : 4, ALL = Z::PASSES * IT;
+  constexpr int COLS = DUAL ? Z::SCOLS / 2 : Z::SCOLS, LW = COLS / kRun;
+  constexpr int STEP = Z::NT / LW, IT = PrStage<Z>::ROWS / STEP, AHEAD = IT < Out::AHEAD ? IT : Out::AHEAD, ALL = Z::PASSES * IT;
+  static_assert(IT >= 1 && IT % AHEAD == 0 && (PrStage<Z>::PR % STEP == 0 || STEP % PrStage<Z>::PR == 0), "the threads of a pass take whole rows");
   const int tid = fresh_tid(), row = tid / LW, col = tid % LW * kRun;
-  // The matrix's row of run g, without the thread's own part.
+  // The matrix's row of run g, without the thread's own part, and the columns that
+  // its pass is shifted by.
   auto row_of = [&](int g) __attribute__((always_inline)) { return m0 + PrStage<Z>::tile_row(g / IT, g % IT * STEP); };
+  auto col_of = [&](int g) __attribute__((always_inline)) { return PrStage<Z>::tile_col(g / IT); };
   typename Out::Pre pre[AHEAD];
 #pragma unroll
-  for (int g = 0; g < AHEAD; ++g) out.template pre<PrVariant<FULL>>(row_of(g), pre[g]);
+  for (int g = 0; g < AHEAD; ++g) out.template pre<PrVariant<FULL>>(row_of(g), col_of(g), pre[g]);
 #pragma unroll 1
   for (int pass = 0; pass < Z::PASSES; ++pass) {
     stage.fill(pass);
@@ -338,12 +351,13 @@ MUON_INLINE void pr_leave_as(const PrStage<Z>& stage, const Out& out, int m0) {
       for (int q0 = 0; q0 < IT; q0 += AHEAD)
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
-          const int g = pass * IT + q0 + a;
+          const int g = pass * IT + q0 + a, n = min(g + AHEAD, ALL - 1);  // past the end: the last one again
           float v[8], w[8];
           stage.run((q0 + a) * STEP + row, col, v);
-          if constexpr (DUAL) stage.run((q0 + a) * STEP + row, Z::BN / 2 + col, w);
-          out.template emit<V>(row_of(g), v, w, pre[a]);
-          out.template pre<V>(row_of(min(g + AHEAD, ALL - 1)), pre[a]);  // past the end: the last one again
+          if constexpr (DUAL) stage.run((q0 + a) * STEP + row, COLS + col, w);
+          out.template emit<V>(row_of(g), col_of(g), v, w, pre[a]);
+          out.template pre<V>(row_of(n), col_of(n), pre[a]);
+          __builtin_amdgcn_sched_barrier(0);
         }
     };
     if constexpr (FULL) out.dispatch(runs);
@@ -355,13 +369,14 @@ template <class Z, class Out>
 MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, int local, int m0, int n0, unsigned char* lds,
                           const f32x16 (&acc)[Z::FM][Z::FN]) {
   constexpr bool DUAL = Out::OPS == 2;
-  constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;
+  constexpr int COLS = DUAL ? Z::SCOLS / 2 : Z::SCOLS, LW = COLS / kRun;
   const int tid = fresh_tid(), c0 = DUAL ? n0 >> 1 : n0;
   const PrStage<Z> stage{lds, acc};
   if (it.splits > 1) {
-    constexpr int PLW = Z::BN / kRun, PSTEP = Z::NT / PLW;
+    constexpr int PLW = Z::SCOLS / kRun, PSTEP = Z::NT / PLW;
     const int row = tid / PLW, col = tid % PLW * kRun;
-    float* part = args->partial + (int64_t)(it.part0 + local) * Z::BM * Z::BN;
+    float* part = args->partial + (int64_t)(it.part0 + local) * Z::BM * Z::BN +
+                  PrStage<Z>::tile_row(0, row) * Z::BN + PrStage<Z>::own_col(col);
 #pragma unroll 1
     for (int pass = 0; pass < Z::PASSES; ++pass) {
       stage.fill(pass);
@@ -369,13 +384,13 @@ MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, int local, int m0, int n
       for (int q = 0; q < PrStage<Z>::ROWS / PSTEP; ++q) {
         float v[8];
         stage.run(q * PSTEP + row, col, v);
-        store_run(part + PrStage<Z>::tile_row(pass, q * PSTEP) * Z::BN + row * Z::BN + col, 8, v);
+        store_run(part + PrStage<Z>::tile_row(pass, q * PSTEP) * Z::BN + PrStage<Z>::tile_col(pass), 8, v);
       }
     }
     return;
   }
-  const Out out(it, args, PrLane{tid / LW, c0 + tid % LW * kRun});
-  if (out.plain() && m0 + Z::BM <= it.m && c0 + COLS <= it.n) pr_leave_as<Z, Out, true>(stage, out, m0);
+  const Out out(it, args, PrLane{PrStage<Z>::tile_row(0, tid / LW), c0 + PrStage<Z>::own_col(tid % LW * kRun)});
+  if (out.plain() && m0 + Z::BM <= it.m && c0 + (DUAL ? Z::BN / 2 : Z::BN) <= it.n) pr_leave_as<Z, Out, true>(stage, out, m0);
   else pr_leave_as<Z, Out, false>(stage, out, m0);
 }
 
@@ -417,7 +432,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     const int kbytes = Z::F8 ? lk : 2 * lk;
     limit = (uint32_t)min((kbytes - lks * RB + 15) / 16, S) * 16 - 16;
     if constexpr (Z::NN) limit_k = (uint32_t)(min(lk - lks * Z::BK, Z::BK) - 1) * (uint32_t)ldb;
-    lfresh = Z::F8 && (lfresh || (lks & 7) == 0);
+    lfresh = Z::F8 && (lfresh || (lks & (Z::CHUNK - 1)) == 0);
     if (Z::F8 && lfresh) ltab = (ltab + 1) & (Z::TABS - 1);
   };
   auto seat = [&]() __attribute__((always_inline)) {
@@ -506,7 +521,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
   auto load_ex = [&]() __attribute__((always_inline)) {
     if constexpr (Z::F8) {
       PrItemRef it = args->item[lidx];
-      const int chunk = lks >> 3, groups = (lk + kGroup - 1) / kGroup, kblocks = (lk + kBlock - 1) / kBlock;
+      const int chunk = lks / Z::CHUNK, groups = (lk + kGroup - 1) / kGroup, kblocks = (lk + kBlock - 1) / kBlock;
       if (tid < Z::BM) {
         const uint8_t* row = it.ea + (int64_t)min(lm0 + tid, it.m - 1) * it.lde + 32 * chunk;
         if (32 * chunk + 32 <= groups) {
@@ -619,16 +634,18 @@ MUON_INLINE void pr_run(unsigned char* smem) {
   auto read_ex = [&](int ks_, int t_) __attribute__((always_inline)) {
     if constexpr (Z::F8) {
       const unsigned char* t = smem + Z::RING + t_ * (Z::EX_A + Z::EX_B);
+      const int row = ks_ * RB / kBlock & 7;
 #pragma unroll
       for (int i = 0; i < FM; ++i)
-        na[i] = *reinterpret_cast<const uint32_t*>(t + ((ks_ & 7) * Z::BM + wm * Z::WM + 32 * i + r32) * 4);
-      nb_ = *reinterpret_cast<const uint32_t*>(t + Z::EX_A + ((ks_ & 7) + 8 * ((wn * Z::WN) / kBlock)) * 4);
+        na[i] = *reinterpret_cast<const uint32_t*>(t + (row * Z::BM + wm * Z::WM + 32 * i + r32) * 4);
+      nb_ = *reinterpret_cast<const uint32_t*>(t + Z::EX_A + (row + 8 * ((wn * Z::WN) / kBlock)) * 4);
     }
   };
-  auto take_ex = [&]() __attribute__((always_inline)) {
+  auto take_ex = [&](int ks_) __attribute__((always_inline)) {  // of K step ks_
     if constexpr (Z::F8) {
+      const int half = RB < kBlock ? ks_ * RB % kBlock / 4 : 0;   // groups of 32, 8 bits each
 #pragma unroll
-      for (int i = 0; i < FM; ++i) sa[i] = Z::MODE == kNT8 ? na[i] >> (8 * h) : na[i];
+      for (int i = 0; i < FM; ++i) sa[i] = na[i] >> (Z::MODE == kNT8 ? 8 * h + half : half);
       sb = nb_;
     }
   };
@@ -687,16 +704,18 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     __syncthreads();                                 // its first stage is in LDS, and the last tile has left
     if (short_stage(ks)) clear(ks, cur);
     read_ex(ks, tab);
-    take_ex();
+    take_ex(ks);
 #pragma unroll
     for (int f = 0; f < Z::NF; ++f) read_frag(0, cur, 0, f);
 
     // One stage: MFMAs, and between two of them a little of everything else, in a
     // fixed order. The last sub-step's fragments are in registers a few MFMAs before
     // its end: there the workgroup meets, and the next stage's first fragments are
-    // read under the remaining MFMAs (after the last stage: for nothing).
-#pragma unroll 1
-    for (int t = u.total; t; --t) {
+    // read under the remaining MFMAs (after the last stage: for nothing). The
+    // fragments of its first sub-step are in buffer PAR.
+    int t = u.total;
+    auto stage = [&](auto PAR_) __attribute__((always_inline)) {
+      constexpr int PAR = decltype(PAR_)::value, NEXT = (PAR + Z::KK) & 1;
       const uint32_t after = cur + Z::STAGE == Z::RING ? 0 : cur + Z::STAGE;
       const int ks1 = ks + 1 == kt ? 0 : ks + 1;
       if (lfresh) load_ex();
@@ -704,7 +723,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
       for (int kk = 0; kk < Z::KK; ++kk)
 #pragma unroll
         for (int q = 0; q < Z::PER; ++q) {
-          const int slot = kk * Z::PER + q, b = kk & 1;
+          const int slot = kk * Z::PER + q, b = (PAR + kk) & 1;
           if (slot == Z::MEET) {
             anchor();
             if (lfresh) write_ex();
@@ -712,7 +731,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((Z::ST - 2) * Z::PS) : "memory");
             if (t > 1) {
               if (short_stage(ks1)) clear(ks1, after);
-              if (Z::F8 && (ks1 & 7) == 0) tab = (tab + 1) & (Z::TABS - 1);
+              if (Z::F8 && (ks1 & (Z::CHUNK - 1)) == 0) tab = (tab + 1) & (Z::TABS - 1);
             }
             read_ex(ks1, tab);
           }
@@ -722,43 +741,56 @@ MUON_INLINE void pr_run(unsigned char* smem) {
             for (int f = 0; f < Z::NF; ++f)
               if (f * Z::PER / Z::NF == q) read_frag(b ^ 1, cur, kk + 1, f);
           }
-          if (slot == Z::SLOTS - 1) {
-            anchor();
-            take_ex();
-          }
           if constexpr (Z::MODE != kNT8X) {
             if (slot >= Z::MEET) {
 #pragma unroll
               for (int f = 0; f < Z::NF; ++f)
-                if (f * (Z::SLOTS - Z::MEET) / Z::NF == slot - Z::MEET) read_frag(0, after, 0, f);
+                if (f * (Z::SLOTS - Z::MEET) / Z::NF == slot - Z::MEET) read_frag(NEXT, after, 0, f);
             }
           }
 #pragma unroll
           for (int d = 0; d < Z::PS; ++d)
             if (d * Z::MEET / (Z::PS * (Z::ST == 2 ? 2 : 1)) == slot) copy(to, d);
+          if (slot == Z::SLOTS - 1) {
+            anchor();
+            take_ex(ks1);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       if constexpr (Z::MODE == kNT8X) {  // these need the next stage's scales
 #pragma unroll
-        for (int f = 0; f < Z::NF; ++f) read_frag(0, after, 0, f);
+        for (int f = 0; f < Z::NF; ++f) read_frag(NEXT, after, 0, f);
       }
       advance();
       ks = ks1;
       cur = after;
       to = to + Z::STAGE == Z::RING ? 0 : to + Z::STAGE;
+      --t;
+    };
+    if constexpr (Z::KK % 2 == 0) {
+#pragma unroll 1
+      while (t) stage(std::integral_constant<int, 0>{});
+    } else {
+#pragma unroll 1
+      for (;;) {
+        stage(std::integral_constant<int, 0>{});
+        if (t == 0) break;
+        stage(std::integral_constant<int, 1>{});
+        if (t == 0) break;
+      }
     }
     pr_leave<Z, Out>(args, it, u.local, u.m0, u.n0, smem + to, acc);
   }
   wait_vmcnt<0>();  // the copies past the last stage
 }
 
-// Adds the pieces of a tile in order, then the epilogue. A workgroup takes 1024
-// columns' worth of runs of one tile: 256 threads, a run of eight each.
+// Adds the pieces of a tile in order, then the epilogue. A workgroup takes 256 runs of
+// eight columns of one tile.
 template <class Out>
-MUON_INLINE void pr_join_of(int edge) {
+MUON_INLINE void pr_join_of(int bm, int bn) {
   constexpr bool DUAL = Out::OPS == 2;
   const PrArgsPtr args = (PrArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
-  const int cols = DUAL ? edge / 2 : edge, lw = cols / kRun, per = edge * lw / 256;  // workgroups per tile
+  const int cols = DUAL ? bn / 2 : bn, lw = cols / kRun, per = bm * lw / 256;  // workgroups per tile
   int b = blockIdx.x, idx = 0;
   for (; idx < args->n_items; ++idx) {
     const int mine = args->item[idx].splits > 1 ? args->item[idx].tiles_m * args->item[idx].tiles_n * per : 0;
@@ -770,11 +802,11 @@ MUON_INLINE void pr_join_of(int edge) {
   int tm, tn;
   pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
   const int row0 = (b - tile * per) * (256 / lw), r = threadIdx.x / lw, col = threadIdx.x % lw * kRun;
-  const Out out(it, args, PrLane{r, (DUAL ? tn * edge / 2 : tn * edge) + col});
+  const Out out(it, args, PrLane{r, (DUAL ? tn * bn / 2 : tn * bn) + col});
   typename Out::Pre pre;
-  out.template pre<PrAny>(tm * edge + row0, pre);
-  const float* p = args->partial + ((int64_t)(it.part0 + tile) * edge + row0 + r) * edge + col;
-  const int64_t step = (int64_t)tiles * edge * edge;
+  out.template pre<PrAny>(tm * bm + row0, 0, pre);
+  const float* p = args->partial + ((int64_t)(it.part0 + tile) * bm + row0 + r) * bn + col;
+  const int64_t step = (int64_t)tiles * bm * bn;
   float v[8], w[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.f;
@@ -782,14 +814,14 @@ MUON_INLINE void pr_join_of(int edge) {
   for (int s = 0; s < it.splits; ++s) {
     float x[8], y[8];
     load_run(p + s * step, 8, x);
-    if constexpr (DUAL) load_run(p + s * step + edge / 2, 8, y);
+    if constexpr (DUAL) load_run(p + s * step + bn / 2, 8, y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] += x[e];
       if constexpr (DUAL) w[e] += y[e];
     }
   }
-  out.template emit<PrAny>(tm * edge + row0, v, w, pre);
+  out.template emit<PrAny>(tm * bm + row0, 0, v, w, pre);
 }
 
 // Workgroups of a launch: as many as the CUs hold at once.
@@ -799,10 +831,10 @@ inline uint32_t pr_grid(const PrArgs& a) {
 }
 // Workgroups of a launch's join.
 inline int64_t pr_join_blocks(const PrArgs& a, bool dual) {
-  const int edge = kPrEdge[a.tile];
+  const int bm = kPrBM[a.tile], bn = kPrBN[a.tile];
   int64_t n = 0;
   for (int i = 0; i < a.n_items; ++i)
-    if (a.item[i].splits > 1) n += (int64_t)a.item[i].tiles_m * a.item[i].tiles_n * (edge * (dual ? edge / 2 : edge) / kRun / 256);
+    if (a.item[i].splits > 1) n += (int64_t)a.item[i].tiles_m * a.item[i].tiles_n * (bm * (dual ? bn / 2 : bn) / kRun / 256);
   return n;
 }
 

@@ -28,7 +28,7 @@ Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, int64_t most) {
   // Per kind: workgroups per CU; us to fill and empty a tile; us per stage with one
   // and with all of a CU's; us per partial tile, written and read.
   static const struct { int per_cu; double fixed, one, all, part; } kCost[muon::kPrTiles] = {
-      {1, 12.0, 1.6, 1.6, 0.058}, {2, 7.0, 0.6, 1.0, 0.011}, {2, 3.0, 0.3, 0.45, 0.004}};
+      {1, 12.0, 1.6, 1.6, 0.058}, {2, 7.0, 0.6, 1.0, 0.011}, {2, 3.0, 0.3, 0.45, 0.004}, {2, 1e6, 0.3, 0.45, 0.004}};
   Choice best{muon::kPrLarge, 1, 1e300};
   for (int i = 0; i < muon::kPrTiles; ++i)
     for (int64_t s = 1; s <= std::min<int64_t>(most, std::max<int64_t>(1, stages / 4)); ++s) {
@@ -45,23 +45,23 @@ Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, int64_t most) {
 
 // A launch's items laid out: tiles, pieces, and the bytes of partial tiles.
 muon_status lay_out(muon::PrArgs& a, bool dual, int elem, size_t* bytes) {
-  int64_t t[muon::kPrTiles] = {0, 0, 0}, stages = 0;
+  int64_t t[muon::kPrTiles] = {}, stages = 0;
   const int pairs = a.parts == 3 ? 6 : 1, bk = 128 / elem;
   for (int i = 0; i < a.n_items; ++i) {
     const muon::PrItem& it = a.item[i];
     for (int j = 0; j < muon::kPrTiles; ++j)
-      t[j] += ceil_div(it.m, muon::kPrEdge[j]) * ceil_div(it.n, dual ? muon::kPrEdge[j] / 2 : muon::kPrEdge[j]);
+      t[j] += ceil_div(it.m, muon::kPrBM[j]) * ceil_div(it.n, dual ? muon::kPrBN[j] / 2 : muon::kPrBN[j]);
     stages = std::max(stages, ceil_div(it.k, bk) * it.sums * pairs);
   }
   const Choice c = choose(t, stages, 64);
   a.tile = c.tile;
-  const int edge = muon::kPrEdge[c.tile];
+  const int bm = muon::kPrBM[c.tile], bn = muon::kPrBN[c.tile];
   int64_t units = 0, partials = 0;
   std::fill(a.unit0, a.unit0 + muon::kPrItems, INT32_MAX);
   for (int i = 0; i < a.n_items; ++i) {
     muon::PrItem& it = a.item[i];
     const int64_t mine = ceil_div(it.k, bk) * it.sums * pairs;
-    const int64_t tm = ceil_div(it.m, edge), tn = ceil_div(it.n, dual ? edge / 2 : edge);
+    const int64_t tm = ceil_div(it.m, bm), tn = ceil_div(it.n, dual ? bn / 2 : bn);
     it.tiles_m = int32_t(tm);
     it.tiles_n = int32_t(tn);
     it.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(c.splits, mine / 2)));
@@ -72,7 +72,7 @@ muon_status lay_out(muon::PrArgs& a, bool dual, int elem, size_t* bytes) {
     if (units > kMaxUnits) return fail(MUON_ERR_INVALID_ARG, "more than 2^22 tiles in one launch");
   }
   a.units = int32_t(units);
-  *bytes = round256(size_t(partials) * edge * edge * sizeof(float));
+  *bytes = round256(size_t(partials) * bm * bn * sizeof(float));
   return MUON_OK;
 }
 

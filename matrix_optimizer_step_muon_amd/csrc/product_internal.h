@@ -14,8 +14,8 @@ constexpr int kPrItems = 16;   // products per launch
 constexpr int kBlock = 128;    // edge of a weight's 8-bit block
 
 // Tiles that a launch's products are cut into.
-enum PrTile { kPrLarge = 0, kPrMedium = 1, kPrSmall = 2, kPrTiles = 3 };
-constexpr int kPrEdge[kPrTiles] = {256, 128, 64};
+enum PrTile { kPrLarge = 0, kPrMedium = 1, kPrSmall = 2, kPrWide = 3, kPrTiles = 4 };
+constexpr int kPrBM[kPrTiles + 1] = {256, 128, 64, 128, 256}, kPrBN[kPrTiles + 1] = {256, 128, 64, 256, 256};
 
 // What becomes of a product.
 enum PrEpilogue {
