@@ -18,25 +18,21 @@ __global__ void __launch_bounds__(Z::NT, Z::WG) linear8_kernel(PrArgs) {
   pr_run<Z, PrStoreOut>(smem);
 }
 
-__global__ void __launch_bounds__(256) linear8_join_kernel(PrArgs, int bm, int bn) { pr_join_of<PrStoreOut>(bm, bn); }
+__global__ void __launch_bounds__(256) linear8_join_kernel(PrArgs, int edge) { pr_join_of<PrStoreOut>(edge); }
 
 template <int MODE>
 static hipError_t launch_tiles(const PrArgs& args, hipStream_t s) {
   typedef PrCfg<256, 256, 128, 2, MODE, 1> Large;
   typedef PrCfg<128, 128, 128, 2, MODE, 2> Medium;
   typedef PrCfg<64, 64, 128, 4, MODE, 2> Small;
-  typedef PrCfg<128, 256, 64, 2, MODE, 2> Wide;
-  typedef PrCfg<256, 256, 64, 3, MODE, 1> Deep;
   const dim3 block(256);
   if (args.tile == kPrLarge) hipLaunchKernelGGL(linear8_kernel<Large>, dim3(pr_grid<Large>(args)), block, 0, s, args);
   else if (args.tile == kPrMedium) hipLaunchKernelGGL(linear8_kernel<Medium>, dim3(pr_grid<Medium>(args)), block, 0, s, args);
-  else if (args.tile == kPrSmall) hipLaunchKernelGGL(linear8_kernel<Small>, dim3(pr_grid<Small>(args)), block, 0, s, args);
-  else if (args.tile == kPrWide) hipLaunchKernelGGL(linear8_kernel<Wide>, dim3(pr_grid<Wide>(args)), block, 0, s, args);
-  else hipLaunchKernelGGL(linear8_kernel<Deep>, dim3(pr_grid<Deep>(args)), block, 0, s, args);
+  else hipLaunchKernelGGL(linear8_kernel<Small>, dim3(pr_grid<Small>(args)), block, 0, s, args);
   const hipError_t e = hipGetLastError();
   const int64_t join = pr_join_blocks(args, false);
   if (e != hipSuccess || join == 0) return e;
-  hipLaunchKernelGGL(linear8_join_kernel, dim3((uint32_t)join), dim3(256), 0, s, args, kPrBM[args.tile], kPrBN[args.tile]);
+  hipLaunchKernelGGL(linear8_join_kernel, dim3((uint32_t)join), dim3(256), 0, s, args, kPrEdge[args.tile]);
   return hipGetLastError();
 }
 

@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(Z::NT, Z::WG) mlp_product_kernel(PrArgs) {
 }
 
 template <class Out>
-__global__ void __launch_bounds__(256) mlp_join_kernel(PrArgs, int bm, int bn) {
-  pr_join_of<Out>(bm, bn);
+__global__ void __launch_bounds__(256) mlp_join_kernel(PrArgs, int edge) {
+  pr_join_of<Out>(edge);
 }
 
 template <int MODE, class Out>
@@ -272,18 +272,14 @@ static hipError_t launch_tiles(const PrArgs& args, hipStream_t s) {
   typedef PrCfg<256, 256, 128, 2, MODE, 1> Large;
   typedef PrCfg<128, 128, 128, 2, MODE, 2> Medium;
   typedef PrCfg<64, 64, 128, 4, MODE, 2> Small;
-  typedef PrCfg<128, 256, 64, 3, MODE, 2> Wide;
-  typedef PrCfg<256, 256, 64, 4, MODE, 1> Deep;
   const dim3 block(256);
   if (args.tile == kPrLarge) hipLaunchKernelGGL((mlp_product_kernel<Large, Out>), dim3(pr_grid<Large>(args)), block, 0, s, args);
   else if (args.tile == kPrMedium) hipLaunchKernelGGL((mlp_product_kernel<Medium, Out>), dim3(pr_grid<Medium>(args)), block, 0, s, args);
-  else if (args.tile == kPrSmall) hipLaunchKernelGGL((mlp_product_kernel<Small, Out>), dim3(pr_grid<Small>(args)), block, 0, s, args);
-  else if (args.tile == kPrWide) hipLaunchKernelGGL((mlp_product_kernel<Wide, Out>), dim3(pr_grid<Wide>(args)), block, 0, s, args);
-  else hipLaunchKernelGGL((mlp_product_kernel<Deep, Out>), dim3(pr_grid<Deep>(args)), block, 0, s, args);
+  else hipLaunchKernelGGL((mlp_product_kernel<Small, Out>), dim3(pr_grid<Small>(args)), block, 0, s, args);
   const hipError_t e = hipGetLastError();
   const int64_t join = pr_join_blocks(args, Out::OPS == 2);
   if (e != hipSuccess || join == 0) return e;
-  hipLaunchKernelGGL(mlp_join_kernel<Out>, dim3((uint32_t)join), dim3(256), 0, s, args, kPrBM[args.tile], kPrBN[args.tile]);
+  hipLaunchKernelGGL(mlp_join_kernel<Out>, dim3((uint32_t)join), dim3(256), 0, s, args, kPrEdge[args.tile]);
   return hipGetLastError();
 }
 

@@ -84,11 +84,13 @@ struct PrCfg {
   typedef std::conditional_t<MODE == kNT8, i32x8, bf16x8> Frag;
 };
 
-MUON_INLINE int pr_item(PrArgsPtr a, int unit) {
+// The item that number `unit` of a numbering over the items belongs to.
+template <class P>
+MUON_INLINE int pr_item(P first, int unit) {
   int idx = 0;
 #pragma unroll
-  for (int i = 1; i < kPrItems; ++i) idx += unit >= a->unit0[i];
-  return idx;
+  for (int i = 1; i < kPrItems; ++i) idx += unit >= first[i];
+  return __builtin_amdgcn_readfirstlane(idx);
 }
 // Tile (tm, tn) of local tile number t: bands of 4 tile rows walked column by
 // column, so 32 consecutive tiles cover 4 x 8.
@@ -107,23 +109,31 @@ MUON_INLINE int pr_plane_b(int p) { return p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 
 
 // A unit of a launch: a tile, or a piece of its sum.
 struct PrUnit {
-  int idx, local, m0, n0, begin, total;  // item; tile and piece; first row and column; first stage and how many
+  int idx, piece, m0, n0, begin, total;  // item; piece of it (or -1); first row and column; first stage and how many
 };
 template <class Z>
-MUON_INLINE PrUnit pr_unit(PrArgsPtr args, int unit) {
+MUON_INLINE PrUnit pr_unit(PrArgsPtr args, bool whole, int unit) {
   PrUnit u;
-  u.idx = pr_item(args, unit);
+  u.idx = whole ? pr_item(args->whole0, unit) : pr_item(args->piece0, unit);
   PrItemRef it = args->item[u.idx];
-  const int tiles = it.tiles_m * it.tiles_n;
-  u.local = unit - args->unit0[u.idx];
-  const int split = u.local / tiles, tile = u.local - split * tiles;
+  int tile, split = 0, splits = 1;
+  if (whole) {
+    u.piece = -1;
+    tile = unit - args->whole0[u.idx];
+  } else {
+    const int rest = it.tiles_m * it.tiles_n - it.whole;
+    u.piece = unit - args->piece0[u.idx];
+    splits = it.splits;
+    split = u.piece / rest;
+    tile = it.whole + u.piece - split * rest;
+  }
   int tm, tn;
   pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
   u.m0 = tm * Z::BM;
   u.n0 = tn * Z::BN;
   const int all = (it.k + Z::BK - 1) / Z::BK * it.sums * (args->parts == 3 ? 6 : 1);
-  u.begin = (int)((int64_t)all * split / it.splits);
-  u.total = (int)((int64_t)all * (split + 1) / it.splits) - u.begin;
+  u.begin = (int)((int64_t)all * split / splits);
+  u.total = (int)((int64_t)all * (split + 1) / splits) - u.begin;
   return u;
 }
 
@@ -366,16 +376,16 @@ MUON_INLINE void pr_leave_as(const PrStage<Z>& stage, const Out& out, int m0) {
 }
 
 template <class Z, class Out>
-MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, int local, int m0, int n0, unsigned char* lds,
+MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, int piece, int m0, int n0, unsigned char* lds,
                           const f32x16 (&acc)[Z::FM][Z::FN]) {
   constexpr bool DUAL = Out::OPS == 2;
   constexpr int COLS = DUAL ? Z::SCOLS / 2 : Z::SCOLS, LW = COLS / kRun;
   const int tid = fresh_tid(), c0 = DUAL ? n0 >> 1 : n0;
   const PrStage<Z> stage{lds, acc};
-  if (it.splits > 1) {
+  if (piece >= 0) {
     constexpr int PLW = Z::SCOLS / kRun, PSTEP = Z::NT / PLW;
     const int row = tid / PLW, col = tid % PLW * kRun;
-    float* part = args->partial + (int64_t)(it.part0 + local) * Z::BM * Z::BN +
+    float* part = args->partial + (int64_t)(it.part0 + piece) * Z::BM * Z::BN +
                   PrStage<Z>::tile_row(0, row) * Z::BN + PrStage<Z>::own_col(col);
 #pragma unroll 1
     for (int pass = 0; pass < Z::PASSES; ++pass) {
@@ -394,9 +404,9 @@ MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, int local, int m0, int n
   else pr_leave_as<Z, Out, false>(stage, out, m0);
 }
 
-// All units of one workgroup. XCD b % 8 gets a contiguous range of units, which its
-// workgroups take in turn, so that the tiles that run there together share operand
-// panels in its L2. The copies run ST - 1 stages ahead of the sum, across tiles: a
+// All units of one workgroup. XCD b % 8 gets a contiguous range of the whole tiles and
+// one of the pieces, which its workgroups take in turn, so that the tiles that run
+// there together share operand panels in its L2. The copies run ST - 1 stages ahead of the sum, across tiles: a
 // tile starts with its first stages in LDS, and its predecessor leaves under their
 // copies.
 template <class Z, class Out>
@@ -404,8 +414,14 @@ MUON_INLINE void pr_run(unsigned char* smem) {
   constexpr bool DUAL = Out::OPS == 2;
   constexpr int FM = Z::FM, FN = Z::FN, RB = Z::RB, S = Z::S;
   const PrArgsPtr args = (PrArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
-  const int xcd = blockIdx.x & 7, units = args->units, per = units >> 3, rest = units & 7;
-  const int first = xcd * per + min(xcd, rest), count = per + (xcd < rest);
+  const int xcd = blockIdx.x & 7, wholes = args->wholes, pieces = args->pieces;
+  const int first_w = xcd * (wholes >> 3) + min(xcd, wholes & 7), count_w = (wholes >> 3) + (xcd < (wholes & 7));
+  // the pieces' remainder goes to the XCDs that the wholes' did not reach
+  const int turn = (xcd - (wholes & 7)) & 7;
+  const int first_p = turn * (pieces >> 3) + min(turn, pieces & 7), count = count_w + (pieces >> 3) + (turn < (pieces & 7));
+  auto unit_at = [&](int i) __attribute__((always_inline)) {
+    return pr_unit<Z>(args, i < count_w, i < count_w ? first_w + i : first_p + i - count_w);
+  };
   const int step = ((int)gridDim.x >> 3) + (xcd < ((int)gridDim.x & 7));
   int at = blockIdx.x >> 3;
   if (at >= count) return;
@@ -451,7 +467,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
   };
   auto open = [&]() __attribute__((always_inline)) {  // the next unit's first stage
     lat += step;
-    const PrUnit u = pr_unit<Z>(args, first + lat);
+    const PrUnit u = unit_at(lat);
     PrItemRef it = args->item[u.idx];
     lidx = u.idx;
     lm0 = u.m0;
@@ -689,7 +705,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
 
 #pragma unroll 1
   for (; at < count; at += step) {
-    const PrUnit u = pr_unit<Z>(args, first + at);
+    const PrUnit u = unit_at(at);
     PrItemRef it = args->item[u.idx];
     k = it.k;
     kt = (k + Z::BK - 1) / Z::BK;
@@ -779,7 +795,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
         if (t == 0) break;
       }
     }
-    pr_leave<Z, Out>(args, it, u.local, u.m0, u.n0, smem + to, acc);
+    pr_leave<Z, Out>(args, it, u.piece, u.m0, u.n0, smem + to, acc);
   }
   wait_vmcnt<0>();  // the copies past the last stage
 }
@@ -787,26 +803,26 @@ MUON_INLINE void pr_run(unsigned char* smem) {
 // Adds the pieces of a tile in order, then the epilogue. A workgroup takes 256 runs of
 // eight columns of one tile.
 template <class Out>
-MUON_INLINE void pr_join_of(int bm, int bn) {
+MUON_INLINE void pr_join_of(int edge) {
   constexpr bool DUAL = Out::OPS == 2;
   const PrArgsPtr args = (PrArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
-  const int cols = DUAL ? bn / 2 : bn, lw = cols / kRun, per = bm * lw / 256;  // workgroups per tile
+  const int cols = DUAL ? edge / 2 : edge, lw = cols / kRun, per = edge * lw / 256;  // workgroups per tile
   int b = blockIdx.x, idx = 0;
   for (; idx < args->n_items; ++idx) {
-    const int mine = args->item[idx].splits > 1 ? args->item[idx].tiles_m * args->item[idx].tiles_n * per : 0;
+    const int mine = (args->item[idx].tiles_m * args->item[idx].tiles_n - args->item[idx].whole) * per;
     if (b < mine) break;
     b -= mine;
   }
   PrItemRef it = args->item[idx];
-  const int tiles = it.tiles_m * it.tiles_n, tile = b / per;
+  const int tiles = it.tiles_m * it.tiles_n - it.whole, tile = b / per;
   int tm, tn;
-  pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
+  pr_tile(it.whole + tile, it.tiles_m, it.tiles_n, tm, tn);
   const int row0 = (b - tile * per) * (256 / lw), r = threadIdx.x / lw, col = threadIdx.x % lw * kRun;
-  const Out out(it, args, PrLane{r, (DUAL ? tn * bn / 2 : tn * bn) + col});
+  const Out out(it, args, PrLane{r, (DUAL ? tn * edge / 2 : tn * edge) + col});
   typename Out::Pre pre;
-  out.template pre<PrAny>(tm * bm + row0, 0, pre);
-  const float* p = args->partial + ((int64_t)(it.part0 + tile) * bm + row0 + r) * bn + col;
-  const int64_t step = (int64_t)tiles * bm * bn;
+  out.template pre<PrAny>(tm * edge + row0, 0, pre);
+  const float* p = args->partial + ((int64_t)(it.part0 + tile) * edge + row0 + r) * edge + col;
+  const int64_t step = (int64_t)tiles * edge * edge;
   float v[8], w[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.f;
@@ -814,27 +830,27 @@ MUON_INLINE void pr_join_of(int bm, int bn) {
   for (int s = 0; s < it.splits; ++s) {
     float x[8], y[8];
     load_run(p + s * step, 8, x);
-    if constexpr (DUAL) load_run(p + s * step + bn / 2, 8, y);
+    if constexpr (DUAL) load_run(p + s * step + edge / 2, 8, y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] += x[e];
       if constexpr (DUAL) w[e] += y[e];
     }
   }
-  out.template emit<PrAny>(tm * bm + row0, 0, v, w, pre);
+  out.template emit<PrAny>(tm * edge + row0, 0, v, w, pre);
 }
 
 // Workgroups of a launch: as many as the CUs hold at once.
 template <class Z>
 inline uint32_t pr_grid(const PrArgs& a) {
-  return (uint32_t)(a.units < 256 * Z::WG ? a.units : 256 * Z::WG);
+  return (uint32_t)(a.wholes + a.pieces < 256 * Z::WG ? a.wholes + a.pieces : 256 * Z::WG);
 }
 // Workgroups of a launch's join.
 inline int64_t pr_join_blocks(const PrArgs& a, bool dual) {
-  const int bm = kPrBM[a.tile], bn = kPrBN[a.tile];
+  const int edge = kPrEdge[a.tile];
   int64_t n = 0;
   for (int i = 0; i < a.n_items; ++i)
-    if (a.item[i].splits > 1) n += (int64_t)a.item[i].tiles_m * a.item[i].tiles_n * (bm * (dual ? bn / 2 : bn) / kRun / 256);
+    n += (int64_t)(a.item[i].tiles_m * a.item[i].tiles_n - a.item[i].whole) * (edge * (dual ? edge / 2 : edge) / kRun / 256);
   return n;
 }
 

@@ -14,65 +14,85 @@ constexpr int64_t kMaxUnits = int64_t(1) << 22;
 // Row strides, in bytes, up to which 256 rows are within 32-bit offsets.
 constexpr int64_t kMaxPitch = int64_t(1) << 24;
 
-// The tiles of a launch, how many pieces its sums are cut into, and what it is
-// expected to take.
+// How a launch is cut up: the tiles, how many of them are one unit each, how many
+// pieces the sums of the others are cut into, and what it is expected to take.
 struct Choice {
-  int tile, splits;
+  int tile;
+  int64_t whole;
+  int splits;
   double us;
 };
 
 // For products with t[i] tiles of kind i in all, and `stages` stages of 128 bytes of
-// K each.
-Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, int64_t most) {
+// K each. Either all tiles are whole, or all in pieces, or the last round, which
+// would leave CUs without work, is in as many pieces as there is room for.
+Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, double leave) {
   constexpr int64_t kCus = 256;
-  // Per kind: workgroups per CU; us to fill and empty a tile; us per stage with one
-  // and with all of a CU's; us per partial tile, written and read.
-  static const struct { int per_cu; double fixed, one, all, part; } kCost[muon::kPrTiles] = {
-      {1, 12.0, 1.6, 1.6, 0.058}, {2, 7.0, 0.6, 1.0, 0.011}, {2, 3.0, 0.3, 0.45, 0.004}, {2, 1e6, 0.3, 0.45, 0.004}};
-  Choice best{muon::kPrLarge, 1, 1e300};
-  for (int i = 0; i < muon::kPrTiles; ++i)
-    for (int64_t s = 1; s <= std::min<int64_t>(most, std::max<int64_t>(1, stages / 4)); ++s) {
-      const int64_t units = t[i] * s, each = ceil_div(stages, s), round = kCus * kCost[i].per_cu;
-      if (units > kMaxUnits) continue;
+  // Per kind: workgroups per CU; us to fill a tile and to let it out; us per stage
+  // with one and with all of a CU's; us per partial tile, written and read.
+  static const struct { int per_cu; double fill, leave, one, all, part; } kCost[muon::kPrTiles] = {
+      {1, 4.0, 1.0, 1.5, 1.5, 0.16}, {2, 4.0, 0.5, 0.6, 1.0, 0.04}, {2, 3.0, 0.12, 0.3, 0.45, 0.01}};
+  Choice best{muon::kPrLarge, t[0], 1, 1e300};
+  for (int i = 0; i < muon::kPrTiles; ++i) {
+    const auto& c = kCost[i];
+    const int64_t round = kCus * c.per_cu;
+    const double fixed = c.fill + leave * c.leave;
+    auto run = [&](int64_t units, int64_t n) {
       const int64_t full = units / round, rest = units % round;
-      double us = 2.0 + double(full) * (kCost[i].fixed + kCost[i].all * double(each));
-      if (rest) us += kCost[i].fixed + (rest <= kCus ? kCost[i].one : kCost[i].all) * double(each);
-      if (s > 1) us += 4.0 + 0.1 * double(s) + kCost[i].part * double(units);
-      if (us < best.us) best = {i, int(s), us};
+      return double(full) * (fixed + c.all * double(n)) + (rest ? fixed + (rest <= kCus ? c.one : c.all) * double(n) : 0.0);
+    };
+    auto take = [&](int64_t whole, int64_t s) {
+      const int64_t pieces = (t[i] - whole) * s;
+      if (whole + pieces > kMaxUnits || (s > 1 && s > stages / 4)) return;
+      double us = 2.0 + run(whole, stages);
+      if (pieces) us += run(pieces, ceil_div(stages, s)) + 4.0 + 0.1 * double(s) + c.part * double(pieces);
+      if (us < best.us) best = {i, whole, int(s), us};
+    };
+    take(t[i], 1);
+    for (int64_t s = 2; s <= 64; ++s) {
+      take(0, s);
+      if (t[i] > round && t[i] % round) take(t[i] / round * round, s);
     }
+  }
   return best;
 }
 
-// A launch's items laid out: tiles, pieces, and the bytes of partial tiles.
-muon_status lay_out(muon::PrArgs& a, bool dual, int elem, size_t* bytes) {
+// A launch's items laid out: tiles, pieces, and the bytes of partial tiles. leave: us
+// that a CU takes to let the sums of a large tile out.
+muon_status lay_out(muon::PrArgs& a, bool dual, int elem, double leave, size_t* bytes) {
   int64_t t[muon::kPrTiles] = {}, stages = 0;
   const int pairs = a.parts == 3 ? 6 : 1, bk = 128 / elem;
   for (int i = 0; i < a.n_items; ++i) {
     const muon::PrItem& it = a.item[i];
     for (int j = 0; j < muon::kPrTiles; ++j)
-      t[j] += ceil_div(it.m, muon::kPrBM[j]) * ceil_div(it.n, dual ? muon::kPrBN[j] / 2 : muon::kPrBN[j]);
+      t[j] += ceil_div(it.m, muon::kPrEdge[j]) * ceil_div(it.n, dual ? muon::kPrEdge[j] / 2 : muon::kPrEdge[j]);
     stages = std::max(stages, ceil_div(it.k, bk) * it.sums * pairs);
   }
-  const Choice c = choose(t, stages, 64);
+  const Choice c = choose(t, stages, leave);
   a.tile = c.tile;
-  const int bm = muon::kPrBM[c.tile], bn = muon::kPrBN[c.tile];
-  int64_t units = 0, partials = 0;
-  std::fill(a.unit0, a.unit0 + muon::kPrItems, INT32_MAX);
+  const int edge = muon::kPrEdge[c.tile];
+  std::fill(a.whole0, a.whole0 + muon::kPrItems, INT32_MAX);
+  std::fill(a.piece0, a.piece0 + muon::kPrItems, INT32_MAX);
+  int64_t wholes = 0, pieces = 0;
   for (int i = 0; i < a.n_items; ++i) {
     muon::PrItem& it = a.item[i];
     const int64_t mine = ceil_div(it.k, bk) * it.sums * pairs;
-    const int64_t tm = ceil_div(it.m, bm), tn = ceil_div(it.n, dual ? bn / 2 : bn);
+    const int64_t tm = ceil_div(it.m, edge), tn = ceil_div(it.n, dual ? edge / 2 : edge);
+    if (tm * tn > kMaxUnits) return fail(MUON_ERR_INVALID_ARG, "more than 2^22 tiles in one launch");
     it.tiles_m = int32_t(tm);
     it.tiles_n = int32_t(tn);
     it.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(c.splits, mine / 2)));
-    a.unit0[i] = int32_t(units);
-    it.part0 = int32_t(partials);
-    units += tm * tn * it.splits;
-    if (it.splits > 1) partials += tm * tn * it.splits;
-    if (units > kMaxUnits) return fail(MUON_ERR_INVALID_ARG, "more than 2^22 tiles in one launch");
+    const int64_t whole = it.splits == 1 ? tm * tn : std::min(tm * tn, std::max<int64_t>(0, c.whole - wholes));
+    it.whole = int32_t(whole);
+    a.whole0[i] = int32_t(wholes);
+    a.piece0[i] = it.part0 = int32_t(pieces);
+    wholes += whole;
+    pieces += (tm * tn - whole) * it.splits;
+    if (wholes + pieces > kMaxUnits) return fail(MUON_ERR_INVALID_ARG, "more than 2^22 tiles in one launch");
   }
-  a.units = int32_t(units);
-  *bytes = round256(size_t(partials) * bm * bn * sizeof(float));
+  a.wholes = int32_t(wholes);
+  a.pieces = int32_t(pieces);
+  *bytes = round256(size_t(pieces) * edge * edge * sizeof(float));
   return MUON_OK;
 }
 
@@ -203,8 +223,8 @@ muon_status plan_forward(const muon_mlp& p, MlpCall& c, char* ws) {
   g.out = p.y;
   g.ldo = p.ld_y;
   size_t n1 = 0, n2 = 0;
-  MUON_TRY(lay_out(c.first, true, 2, &n1));
-  MUON_TRY(lay_out(c.second, false, 2, &n2));
+  MUON_TRY(lay_out(c.first, true, 2, 16.0, &n1));
+  MUON_TRY(lay_out(c.second, false, 2, 4.0, &n2));
   c.first.partial = c.second.partial = reinterpret_cast<float*>(ws + b.at);
   c.bytes = b.at + std::max(n1, n2);
   return MUON_OK;
@@ -247,8 +267,8 @@ muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c
   s.out = g.d_x;
   s.ldo = g.ld_d_x;
   size_t n1 = 0, n2 = 0;
-  MUON_TRY(lay_out(c.first, false, 2, &n1));
-  MUON_TRY(lay_out(c.second, false, 2, &n2));
+  MUON_TRY(lay_out(c.first, false, 2, 24.0, &n1));
+  MUON_TRY(lay_out(c.second, false, 2, 4.0, &n2));
   c.first.partial = c.second.partial = reinterpret_cast<float*>(ws + b.at);
   c.bytes = b.at + std::max(n1, n2);
   return MUON_OK;
@@ -438,7 +458,7 @@ muon_status plan_linear8(const muon_linear8_item* items, int32_t n, int32_t dtyp
   }
   for (muon::PrArgs& a : plans) {
     size_t need = 0;
-    MUON_TRY(lay_out(a, false, 1, &need));
+    MUON_TRY(lay_out(a, false, 1, 4.0, &need));
     *bytes = std::max(*bytes, need);
   }
   return MUON_OK;

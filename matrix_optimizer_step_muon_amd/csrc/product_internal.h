@@ -14,8 +14,8 @@ constexpr int kPrItems = 16;   // products per launch
 constexpr int kBlock = 128;    // edge of a weight's 8-bit block
 
 // Tiles that a launch's products are cut into.
-enum PrTile { kPrLarge = 0, kPrMedium = 1, kPrSmall = 2, kPrWide = 3, kPrTiles = 4 };
-constexpr int kPrBM[kPrTiles + 1] = {256, 128, 64, 128, 256}, kPrBN[kPrTiles + 1] = {256, 128, 64, 256, 256};
+enum PrTile { kPrLarge = 0, kPrMedium = 1, kPrSmall = 2, kPrTiles = 3 };
+constexpr int kPrEdge[kPrTiles] = {256, 128, 64};
 
 // What becomes of a product.
 enum PrEpilogue {
@@ -38,14 +38,14 @@ struct PrItem {
   int32_t m, n, k;
   int32_t sums;
   int32_t tiles_m, tiles_n;
-  int32_t splits;            // > 1: partial tiles go to the workspace
+  int32_t whole;             // the first tiles are one unit each,
+  int32_t splits;            // the others as many pieces of the sum, whose partial tiles go to the workspace
   int32_t part0;             // first partial tile of this item in the workspace
   // kPrStore
   void* out;
   const void* c;
   int64_t ldo, ldc;
   float beta;
-  int32_t reserved;
 };
 
 // The gated block's epilogues.
@@ -60,15 +60,16 @@ struct PrMlp {
 };
 
 struct PrArgs {
-  int32_t unit0[kPrItems];   // each item's first unit (tiles x splits); past the last item INT32_MAX
+  // Units are the items' whole tiles, then their pieces, each numbered over the items:
+  // an item's first; past the last item INT32_MAX.
+  int32_t whole0[kPrItems], piece0[kPrItems];
   PrItem item[kPrItems];
   PrMlp mlp;
   float* partial;
-  int32_t n_items, units;
+  int32_t n_items, wholes, pieces;
   int32_t parts;             // 1, or 3
   int32_t f32;               // dtype of out, c and d
   int32_t tile;              // PrTile
-  int32_t reserved;
 };
 
 static_assert(sizeof(PrArgs) <= 4000, "kernel arguments");
