@@ -30,7 +30,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", f"-I{INCLUDE}"
           "-Wall", "-Wno-unused-function"]
 SOURCES = ["muon_kernels.hip", "muon_api.cpp", "muon_partition.cpp", "layer_kernels.hip",
            "wgrad_kernels.hip", "layer_api.cpp", "mlp_kernels.hip", "linear8_kernels.hip",
-           "product_api.cpp"]
+           "few_kernels.hip", "product_api.cpp"]
 
 
 def hipcc() -> str:

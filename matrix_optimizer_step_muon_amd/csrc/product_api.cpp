@@ -274,6 +274,42 @@ muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c
   return MUON_OK;
 }
 
+// Few rows, and nothing kept: the weights are read as they are, once, and s is all
+// that the workspace holds.
+bool few_rows(const muon_mlp& p) {
+  return p.rows <= muon::kFewRows && p.y && !p.a.q && !p.b.q && !p.s.q;
+}
+
+size_t few_bytes(const muon_mlp& p) { return round256(size_t(p.rows) * size_t(p.inner) * size_t(elem_of(p.dtype))); }
+
+muon_status few_forward(const muon_mlp& p, hipStream_t s) {
+  const bool f32 = p.dtype == MUON_F32;
+  muon::FewArgs a{};
+  a.a = p.x;
+  a.lda = p.ld_x;
+  a.b[0] = p.w_gate;
+  a.b[1] = p.w_up;
+  a.ldb = p.width;
+  a.m = int32_t(p.rows);
+  a.n = int32_t(p.inner);
+  a.k = int32_t(p.width);
+  a.act = p.act;
+  a.out = p.workspace;
+  a.ldo = p.inner;
+  MUON_TRY(hip_status(muon::launch_few(a, f32, 2, s)));
+  muon::FewArgs y{};
+  y.a = p.workspace;
+  y.lda = p.inner;
+  y.b[0] = p.w_down;
+  y.ldb = p.inner;
+  y.m = a.m;
+  y.n = int32_t(p.out);
+  y.k = int32_t(p.inner);
+  y.out = p.y;
+  y.ldo = p.ld_y;
+  return hip_status(muon::launch_few(y, f32, 1, s));
+}
+
 // The most that either pass takes, every operand rewritten.
 muon_status mlp_workspace(const muon_mlp& p, size_t* bytes) {
   MUON_TRY(check_mlp(p));
@@ -293,7 +329,7 @@ muon_status mlp_workspace(const muon_mlp& p, size_t* bytes) {
   MlpCall f, b;
   MUON_TRY(plan_forward(q, f, nullptr));
   MUON_TRY(plan_backward(q, g, b, nullptr));
-  *bytes = std::max(f.bytes, b.bytes);
+  *bytes = std::max({f.bytes, b.bytes, few_bytes(p)});
   return MUON_OK;
 }
 
@@ -331,6 +367,11 @@ muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
   MUON_TRY(check_kinds(p));
   if (p.rows == 0) return v.disjoint();
   char* ws = static_cast<char*>(p.workspace);
+  if (few_rows(p)) {
+    MUON_TRY(check_mlp_workspace(v, p, few_bytes(p)));
+    MUON_TRY(v.disjoint());
+    return few_forward(p, static_cast<hipStream_t>(stream));
+  }
   MlpCall c;
   MUON_TRY(plan_forward(p, c, ws));
   MUON_TRY(check_mlp_workspace(v, p, c.bytes));
@@ -424,13 +465,39 @@ muon_status check_linear8(const muon_linear8_item* items, int32_t n, int32_t dty
   return v.disjoint();
 }
 
+// Few rows with a bf16 result: a launch of their own, without a workspace.
+bool few_rows(const muon_linear8_item& it, int32_t dtype) { return it.x.rows <= muon::kFewRows && dtype == MUON_BF16; }
+
+muon_status few_linear8(const muon_linear8_item& it, hipStream_t s) {
+  const bool t = it.transposed != 0;
+  muon::FewArgs a{};
+  a.a = it.x.q;
+  a.lda = it.x.ldq;
+  a.ea = static_cast<const uint8_t*>(it.x.e);
+  a.lde = it.x.lde;
+  a.b[0] = t ? it.w.qt : it.w.q;
+  a.ldb = t ? it.w.ldqt : it.w.ldq;
+  a.eb = static_cast<const uint8_t*>(it.w.e);
+  a.ldeb_n = t ? 1 : it.w.lde;
+  a.ldeb_k = t ? it.w.lde : 1;
+  a.m = int32_t(it.x.rows);
+  a.n = int32_t(t ? it.w.k : it.w.n);
+  a.k = int32_t(t ? it.w.n : it.w.k);
+  a.out = it.y;
+  a.ldo = it.ld_y;
+  a.c = it.c;
+  a.ldc = it.ld_c;
+  a.beta = it.beta;
+  return hip_status(muon::launch_few8(a, s));
+}
+
 // The launches, of 16 items each, and the workspace of the largest: they follow each
 // other on one stream and share it. Items without rows have nothing to do.
 muon_status plan_linear8(const muon_linear8_item* items, int32_t n, int32_t dtype, std::vector<muon::PrArgs>& plans, size_t* bytes) {
   *bytes = 0;
   for (int32_t i = 0; i < n; ++i) {
     const muon_linear8_item& it = items[i];
-    if (it.x.rows == 0) continue;
+    if (it.x.rows == 0 || few_rows(it, dtype)) continue;
     if (plans.empty() || plans.back().n_items == muon::kPrItems) plans.push_back(muon::PrArgs{});
     muon::PrArgs& a = plans.back();
     muon::PrItem& d = a.item[a.n_items++];
@@ -478,6 +545,8 @@ muon_status linear8(const muon_linear8_item* items, int32_t n, int32_t dtype, vo
     MUON_TRY(v.add_range(ws, need, "workspace"));
     MUON_TRY(v.disjoint());
   }
+  for (int32_t i = 0; i < n; ++i)
+    if (items[i].x.rows > 0 && few_rows(items[i], dtype)) MUON_TRY(few_linear8(items[i], static_cast<hipStream_t>(stream)));
   for (muon::PrArgs& a : plans) {
     a.partial = static_cast<float*>(ws);
     MUON_TRY(hip_status(muon::launch_linear8(a, static_cast<hipStream_t>(stream))));

@@ -72,9 +72,26 @@ struct PrArgs {
   int32_t tile;              // PrTile
 };
 
+// A product of at most kFewRows rows (few_kernels.hip). Strides in elements.
+constexpr int kFewRows = 16;
+struct FewArgs {
+  const void* a;             // m x k
+  const void* b[2];          // n x k; the two projections of the gated block
+  const uint8_t *ea, *eb;    // as in PrItem
+  int64_t lda, ldb, lde, ldeb_n, ldeb_k;
+  int32_t m, n, k, act;
+  void* out;
+  const void* c;
+  int64_t ldo, ldc;
+  float beta;
+  int32_t reserved;
+};
+
 static_assert(sizeof(PrArgs) <= 4000, "kernel arguments");
 
 hipError_t launch_mlp(const PrArgs& args, int epilogue, bool transposed_b, hipStream_t s);
+hipError_t launch_few(const FewArgs& args, bool f32, int ops, hipStream_t s);
+hipError_t launch_few8(const FewArgs& args, hipStream_t s);
 hipError_t launch_linear8(const PrArgs& args, hipStream_t s);
 hipError_t launch_w8_save(const void* w, int64_t ldw, int dtype, const muon_w8& out, hipStream_t s);
 hipError_t launch_w8_load(const muon_w8& in, void* w, int64_t ldw, int dtype, hipStream_t s);
