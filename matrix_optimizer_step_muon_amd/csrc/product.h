@@ -209,9 +209,9 @@ MUON_INLINE T pinned(T v) {
 
 // C's store: eight columns of a row, plus beta times those of c, rounded once.
 struct PrStoreOut {
-  static constexpr int OPS = 1, AHEAD = 4;
+  static constexpr int OPS = 1, AHEAD = 8;
   struct Pre {
-    float c[8];
+    uint32_t c[8];  // of a whole tile as it came (what is done with it would wait for it), else fp32
   };
   PrLane at;
   char* out;
@@ -245,35 +245,46 @@ struct PrStoreOut {
   }
   template <class V>
   MUON_INLINE void pre(int row, int dc, Pre& p) const {
-    const char* base = c + (int64_t)row * ldc + ((int64_t)dc << (f32 ? 2 : 1));
-    if constexpr (V::FULL && V::B >= 0) {
-      if constexpr (V::B != 0) {
-        if constexpr (V::A != 0) load_run(reinterpret_cast<const float*>(base + offc), 8, p.c);
-        else load_run(reinterpret_cast<const u16*>(base + offc), 8, p.c);
+    const char* at_c = c + (int64_t)row * ldc + ((int64_t)dc << (f32 ? 2 : 1)) + offc;
+    if constexpr (V::FULL) {
+      // before the variant is known, both halves of what an fp32 c would need, if there is a c
+      if (V::B > 0 || (V::B < 0 && beta != 0.f)) {
+        const u32x4 lo = gload16_any(at_c), hi = V::A == 0 || (V::A < 0 && !f32) ? lo : gload16_any(at_c + 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p.c[i] = lo[i];
+          p.c[4 + i] = hi[i];
+        }
       }
     } else if (beta != 0.f && row + at.row < m && live > dc) {
-      if (f32) load_run(reinterpret_cast<const float*>(base + offc), live - dc, p.c);
-      else load_run(reinterpret_cast<const u16*>(base + offc), live - dc, p.c);
+      float x[8];
+      if (f32) load_run(reinterpret_cast<const float*>(at_c), live - dc, x);
+      else load_run(reinterpret_cast<const u16*>(at_c), live - dc, x);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) p.c[i] = __float_as_uint(x[i]);
+    }
+  }
+  // c as fp32 (WIDE), or as packed bf16.
+  template <bool WIDE>
+  MUON_INLINE void add(const Pre& p, float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const float x = __uint_as_float(WIDE ? p.c[i] : i & 1 ? p.c[i / 2] & 0xffff0000u : p.c[i / 2] << 16);
+      v[i] = fmaf(beta, x, v[i]);
     }
   }
   template <class V>
   MUON_INLINE void emit(int row, int dc, float v[8], float*, const Pre& p) const {
-    char* base = out + (int64_t)row * ldo + ((int64_t)dc << (f32 ? 2 : 1));
+    char* to = out + (int64_t)row * ldo + ((int64_t)dc << (f32 ? 2 : 1)) + off;
     if constexpr (V::FULL) {
-      if constexpr (V::B != 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += beta * p.c[i];
-      }
-      if constexpr (V::A != 0) store_run(reinterpret_cast<float*>(base + off), 8, v);
-      else store_run(reinterpret_cast<u16*>(base + off), 8, v);
+      if constexpr (V::B != 0) add<V::A != 0>(p, v);
+      if constexpr (V::A != 0) store_run(reinterpret_cast<float*>(to), 8, v);
+      else store_run(reinterpret_cast<u16*>(to), 8, v);
     } else {
       if (row + at.row >= m || live <= dc) return;
-      if (beta != 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += beta * p.c[i];
-      }
-      if (f32) store_run(reinterpret_cast<float*>(base + off), live - dc, v);
-      else store_run(reinterpret_cast<u16*>(base + off), live - dc, v);
+      if (beta != 0.f) add<true>(p, v);
+      if (f32) store_run(reinterpret_cast<float*>(to), live - dc, v);
+      else store_run(reinterpret_cast<u16*>(to), live - dc, v);
     }
   }
 };

@@ -14,6 +14,21 @@ constexpr int64_t kMaxUnits = int64_t(1) << 22;
 // Row strides, in bytes, up to which 256 rows are within 32-bit offsets.
 constexpr int64_t kMaxPitch = int64_t(1) << 24;
 
+constexpr int64_t kCus = 256;
+constexpr double kHbm = 5.2e6;  // bytes per us: what streaming the weights of few rows reaches
+
+// What few_kernels.hip is expected to take for weights of n rows (of each of `ops`)
+// of `row` bytes: workgroups of 16 rows, one after the other on a CU. A CU gets 21 KB a
+// us while all have work, and 36 when few have. One MI355X, one row: 5120 x 25600 bf16
+// 67.7 us (estimated 65), 2048 x 6144 8.5 (8.5), two of 25600 x 5120 97.4 (105); the
+// activations cost up to 40% more at 16 rows (94, 12.8, 115.5).
+double few_us(int64_t n, double row, int ops, int64_t rows) {
+  const int64_t groups = ceil_div(n, 16), full = groups / kCus;
+  const double unit = 16.0 * row * ops;
+  const double us = double(full) * unit / 21e3 + (groups % kCus ? unit / 36e3 : 0.0);
+  return 3.0 + us * (1.0 + 0.4 / ops * double(rows - 1) / 15.0);
+}
+
 // How a launch is cut up: the tiles, how many of them are one unit each, how many
 // pieces the sums of the others are cut into, and what it is expected to take.
 struct Choice {
@@ -23,52 +38,70 @@ struct Choice {
   double us;
 };
 
+// What a kind of product costs beside its stages: us that a CU takes to let the sums
+// of a large tile out (twice that, of its cost below), and a stage against one of
+// bf16 operands that are both read along K.
+struct Cost {
+  double leave, stage;
+};
+constexpr Cost kGateCost{10.5, 1.0}, kGateGradCost{19.6, 1.02}, kDownCost{2.6, 1.0}, kDxCost{2.6, 1.02}, kLinear8Cost{14.0, 0.96},
+    kLinear8F32Cost{14.0, 2.2};
+
 // For products with t[i] tiles of kind i in all, and `stages` stages of 128 bytes of
-// K each. Either all tiles are whole, or all in pieces, or the last round, which
-// would leave CUs without work, is in as many pieces as there is room for.
-Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, double leave) {
-  constexpr int64_t kCus = 256;
+// K each, that read `bytes` once. Either all tiles are whole, or all in pieces, or the
+// last round, which would leave CUs without work, is in as many pieces as there is
+// room for. The constants are fitted to a sweep on one MI355X: 12 sizes from 20 x 2048
+// x 6144 to 4096 x 2048 x 6144, six kinds of product, each tile in 1 to 24 pieces, 1061
+// times in all. The pick is 1.9% behind the best on average, over 10% in six of 72
+// (up to 20%, where large tiles in pieces take more than estimated).
+Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, const Cost& cost, double bytes) {
   // Per kind: workgroups per CU; us to fill a tile and to let it out; us per stage
   // with one and with all of a CU's; us per partial tile, written and read.
   static const struct { int per_cu; double fill, leave, one, all, part; } kCost[muon::kPrTiles] = {
-      {1, 4.0, 1.0, 1.5, 1.5, 0.16}, {2, 4.0, 0.5, 0.6, 1.0, 0.04}, {2, 3.0, 0.12, 0.3, 0.45, 0.01}};
+      {1, 3.2, 0.48, 1.34, 1.34, 0.077}, {2, 2.1, 0.21, 0.78, 1.04, 0.017}, {2, 1.1, 0.23, 0.325, 0.45, 0.003}};
   Choice best{muon::kPrLarge, t[0], 1, 1e300};
   for (int i = 0; i < muon::kPrTiles; ++i) {
     const auto& c = kCost[i];
     const int64_t round = kCus * c.per_cu;
-    const double fixed = c.fill + leave * c.leave;
+    const double fixed = c.fill + cost.leave * c.leave;
     auto run = [&](int64_t units, int64_t n) {
       const int64_t full = units / round, rest = units % round;
-      return double(full) * (fixed + c.all * double(n)) + (rest ? fixed + (rest <= kCus ? c.one : c.all) * double(n) : 0.0);
+      const double steps = cost.stage * double(n);
+      return double(full) * (fixed + c.all * steps) + (rest ? fixed + (rest <= kCus ? c.one : c.all) * steps : 0.0);
     };
     auto take = [&](int64_t whole, int64_t s) {
       const int64_t pieces = (t[i] - whole) * s;
-      if (whole + pieces > kMaxUnits || (s > 1 && s > stages / 4)) return;
+      if (whole + pieces > kMaxUnits) return;
       double us = 2.0 + run(whole, stages);
-      if (pieces) us += run(pieces, ceil_div(stages, s)) + 4.0 + 0.1 * double(s) + c.part * double(pieces);
+      if (pieces) us += run(pieces, ceil_div(stages, s)) + 3.6 + 0.1 * double(s) + c.part * double(pieces);
+      const double stream = 4.0 + bytes / kHbm;  // what is the least also counts a little
+      us = std::max(us, stream) + 0.15 * std::min(us, stream);
       if (us < best.us) best = {i, whole, int(s), us};
     };
     take(t[i], 1);
-    for (int64_t s = 2; s <= 64; ++s) {
-      take(0, s);
-      if (t[i] > round && t[i] % round) take(t[i] / round * round, s);
+    for (const int64_t s : {2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64}) {
+      if (s > stages / 4) break;
+      if (t[i] * s <= 4 * round) take(0, s);
+      if (t[i] > round && t[i] % round && t[i] % round * s <= 2 * round) take(t[i] / round * round, s);
     }
   }
   return best;
 }
 
-// A launch's items laid out: tiles, pieces, and the bytes of partial tiles. leave: us
-// that a CU takes to let the sums of a large tile out.
-muon_status lay_out(muon::PrArgs& a, bool dual, int elem, double leave, size_t* bytes) {
+// A launch's items laid out: tiles, pieces, and the bytes of partial tiles.
+muon_status lay_out(muon::PrArgs& a, bool dual, int elem, const Cost& cost, size_t* bytes, double* us = nullptr) {
   int64_t t[muon::kPrTiles] = {}, stages = 0;
+  double moved = 0.0;
   const int pairs = a.parts == 3 ? 6 : 1, bk = 128 / elem;
   for (int i = 0; i < a.n_items; ++i) {
     const muon::PrItem& it = a.item[i];
+    moved += double(it.k) * double(it.n + it.m) * elem * it.sums * a.parts * (dual ? 2 : 1);
     for (int j = 0; j < muon::kPrTiles; ++j)
       t[j] += ceil_div(it.m, muon::kPrEdge[j]) * ceil_div(it.n, dual ? muon::kPrEdge[j] / 2 : muon::kPrEdge[j]);
     stages = std::max(stages, ceil_div(it.k, bk) * it.sums * pairs);
   }
-  const Choice c = choose(t, stages, leave);
+  const Choice c = choose(t, stages, cost, moved);
+  if (us) *us = c.us;
   a.tile = c.tile;
   const int edge = muon::kPrEdge[c.tile];
   std::fill(a.whole0, a.whole0 + muon::kPrItems, INT32_MAX);
@@ -168,9 +201,9 @@ Operand operand(Bump& b, const void* p, int64_t rows, int64_t cols, int64_t ld, 
 // One call's products and its workspace.
 struct MlpCall {
   Operand ops[4];
-  int n_ops = 0;
   muon::PrArgs first{}, second{};
   size_t bytes = 0;
+  double first_us = 0.0, second_us = 0.0;  // expected
 };
 
 // Two operands of one item share a row stride and a distance of planes: where one
@@ -202,7 +235,6 @@ muon_status plan_forward(const muon_mlp& p, MlpCall& c, char* ws) {
   c.ops[1] = operand(b, p.w_gate, p.inner, p.width, p.width, p.dtype);
   c.ops[2] = operand(b, p.w_up, p.inner, p.width, p.width, p.dtype);
   c.ops[3] = operand(b, p.w_down, p.out, p.inner, p.inner, p.dtype);
-  c.n_ops = p.y ? 4 : 3;
   const Operand s{nullptr, p.rows, p.inner, pad8(p.inner), true, b.take(planes_bytes(p.rows, p.inner, parts))};
   start(c.first, p, p.rows, p.inner, p.width, 1);
   muon::PrItem& f = c.first.item[0];
@@ -223,8 +255,8 @@ muon_status plan_forward(const muon_mlp& p, MlpCall& c, char* ws) {
   g.out = p.y;
   g.ldo = p.ld_y;
   size_t n1 = 0, n2 = 0;
-  MUON_TRY(lay_out(c.first, true, 2, 16.0, &n1));
-  MUON_TRY(lay_out(c.second, false, 2, 4.0, &n2));
+  MUON_TRY(lay_out(c.first, true, 2, kGateCost, &n1, &c.first_us));
+  MUON_TRY(lay_out(c.second, false, 2, kDownCost, &n2, &c.second_us));
   c.first.partial = c.second.partial = reinterpret_cast<float*>(ws + b.at);
   c.bytes = b.at + std::max(n1, n2);
   return MUON_OK;
@@ -237,7 +269,6 @@ muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c
   c.ops[1] = operand(b, p.w_down, p.out, p.inner, p.inner, p.dtype);
   c.ops[2] = operand(b, p.w_gate, p.inner, p.width, p.width, p.dtype);
   c.ops[3] = operand(b, p.w_up, p.inner, p.width, p.width, p.dtype);
-  c.n_ops = g.d_x ? 4 : 2;
   // da and db feed the next product as they are, or from the workspace, both alike
   void* d[2] = {g.d_a, g.d_b};
   const int64_t ld[2] = {g.ld_d_a, g.ld_d_b};
@@ -267,23 +298,25 @@ muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c
   s.out = g.d_x;
   s.ldo = g.ld_d_x;
   size_t n1 = 0, n2 = 0;
-  MUON_TRY(lay_out(c.first, false, 2, 24.0, &n1));
-  MUON_TRY(lay_out(c.second, false, 2, 4.0, &n2));
+  MUON_TRY(lay_out(c.first, false, 2, kGateGradCost, &n1));
+  MUON_TRY(lay_out(c.second, false, 2, kDxCost, &n2));
   c.first.partial = c.second.partial = reinterpret_cast<float*>(ws + b.at);
   c.bytes = b.at + std::max(n1, n2);
   return MUON_OK;
 }
 
-// Few rows, and nothing kept: the weights are read as they are, once, and s is all
-// that the workspace holds.
-bool few_rows(const muon_mlp& p) {
-  return p.rows <= muon::kFewRows && p.y && !p.a.q && !p.b.q && !p.s.q;
+// Few rows: a product that reads its weights as they are, once, where that is
+// expected to be faster; fp32 always, since tiles would have the weights rewritten
+// first. The gate does so only if nothing is kept.
+bool few_gate(const muon_mlp& p, double tiles_us) {
+  return p.rows <= muon::kFewRows && p.y && !p.a.q && !p.b.q && !p.s.q &&
+         (p.dtype == MUON_F32 || few_us(p.inner, double(p.width) * 2, 2, p.rows) <= tiles_us);
+}
+bool few_down(const muon_mlp& p, double tiles_us) {
+  return p.rows <= muon::kFewRows && p.dtype == MUON_BF16 && few_us(p.out, double(p.inner) * 2, 1, p.rows) <= tiles_us;
 }
 
-size_t few_bytes(const muon_mlp& p) { return round256(size_t(p.rows) * size_t(p.inner) * size_t(elem_of(p.dtype))); }
-
-muon_status few_forward(const muon_mlp& p, hipStream_t s) {
-  const bool f32 = p.dtype == MUON_F32;
+muon_status launch_few_gate(const muon_mlp& p, void* s, int64_t ld, hipStream_t stream) {
   muon::FewArgs a{};
   a.a = p.x;
   a.lda = p.ld_x;
@@ -294,21 +327,26 @@ muon_status few_forward(const muon_mlp& p, hipStream_t s) {
   a.n = int32_t(p.inner);
   a.k = int32_t(p.width);
   a.act = p.act;
-  a.out = p.workspace;
-  a.ldo = p.inner;
-  MUON_TRY(hip_status(muon::launch_few(a, f32, 2, s)));
-  muon::FewArgs y{};
-  y.a = p.workspace;
-  y.lda = p.inner;
-  y.b[0] = p.w_down;
-  y.ldb = p.inner;
-  y.m = a.m;
-  y.n = int32_t(p.out);
-  y.k = int32_t(p.inner);
-  y.out = p.y;
-  y.ldo = p.ld_y;
-  return hip_status(muon::launch_few(y, f32, 1, s));
+  a.out = s;
+  a.ldo = ld;
+  return hip_status(muon::launch_few(a, p.dtype == MUON_F32, 2, stream));
 }
+
+muon_status launch_few_down(const muon_mlp& p, const void* s, int64_t ld, hipStream_t stream) {
+  muon::FewArgs a{};
+  a.a = s;
+  a.lda = ld;
+  a.b[0] = p.w_down;
+  a.ldb = p.inner;
+  a.m = int32_t(p.rows);
+  a.n = int32_t(p.out);
+  a.k = int32_t(p.inner);
+  a.out = p.y;
+  a.ldo = p.ld_y;
+  return hip_status(muon::launch_few(a, p.dtype == MUON_F32, 1, stream));
+}
+
+size_t few_bytes(const muon_mlp& p) { return round256(size_t(p.rows) * size_t(p.inner) * size_t(elem_of(p.dtype))); }
 
 // The most that either pass takes, every operand rewritten.
 muon_status mlp_workspace(const muon_mlp& p, size_t* bytes) {
@@ -343,12 +381,9 @@ muon_status check_mlp_workspace(Views& v, const muon_mlp& p, size_t need) {
   return v.add_range(p.workspace, need, "workspace");
 }
 
-muon_status run_packs(const MlpCall& c, const muon_mlp& p, char* ws, hipStream_t s) {
-  for (int i = 0; i < c.n_ops; ++i)
-    if (c.ops[i].pack)
-      MUON_TRY(hip_status(muon::launch_wgrad_pack(c.ops[i].p, c.ops[i].ld, p.dtype, ws + c.ops[i].at, int32_t(c.ops[i].rows),
-                                                  int32_t(c.ops[i].cols), pad8(c.ops[i].cols), s)));
-  return MUON_OK;
+muon_status run_pack(const Operand& o, const muon_mlp& p, char* ws, hipStream_t s) {
+  if (!o.pack) return MUON_OK;
+  return hip_status(muon::launch_wgrad_pack(o.p, o.ld, p.dtype, ws + o.at, int32_t(o.rows), int32_t(o.cols), pad8(o.cols), s));
 }
 
 muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
@@ -367,18 +402,24 @@ muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
   MUON_TRY(check_kinds(p));
   if (p.rows == 0) return v.disjoint();
   char* ws = static_cast<char*>(p.workspace);
-  if (few_rows(p)) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (p.dtype == MUON_F32 && few_gate(p, 0.0)) {
     MUON_TRY(check_mlp_workspace(v, p, few_bytes(p)));
     MUON_TRY(v.disjoint());
-    return few_forward(p, static_cast<hipStream_t>(stream));
+    MUON_TRY(launch_few_gate(p, ws, p.inner, s));
+    return launch_few_down(p, ws, p.inner, s);
   }
   MlpCall c;
   MUON_TRY(plan_forward(p, c, ws));
   MUON_TRY(check_mlp_workspace(v, p, c.bytes));
   MUON_TRY(v.disjoint());
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  MUON_TRY(run_packs(c, p, ws, s));
-  MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGate, false, s)));
+  const bool gate = few_gate(p, c.first_us), down = p.y && few_down(p, c.second_us);
+  const int used[] = {!gate, !gate, !gate, p.y && !down};
+  for (int i = 0; i < 4; ++i)
+    if (used[i]) MUON_TRY(run_pack(c.ops[i], p, ws, s));
+  if (gate) MUON_TRY(launch_few_gate(p, c.first.mlp.plane[0], c.first.mlp.ldp, s));
+  else MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGate, false, s)));
+  if (down) return launch_few_down(p, c.first.mlp.plane[0], c.first.mlp.ldp, s);
   return p.y ? hip_status(muon::launch_mlp(c.second, muon::kPrStore, false, s)) : MUON_OK;
 }
 
@@ -404,7 +445,7 @@ muon_status mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void*
   MUON_TRY(check_mlp_workspace(v, p, c.bytes));
   MUON_TRY(v.disjoint());
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  MUON_TRY(run_packs(c, p, ws, s));
+  for (int i = 0; i < (g.d_x ? 4 : 2); ++i) MUON_TRY(run_pack(c.ops[i], p, ws, s));
   MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGateGrad, true, s)));
   return g.d_x ? hip_status(muon::launch_mlp(c.second, muon::kPrStore, true, s)) : MUON_OK;
 }
@@ -412,17 +453,17 @@ muon_status mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void*
 // ------------------------------------------------------------ the 8-bit product
 
 muon_status check_w8(Views& v, const muon_w8& w, bool q, bool qt, bool written, const char* name, int item = -1) {
-  const std::string at = Views::at(item) + name;
-  if (w.n < 1 || w.n > kMaxCols || w.k < 1 || w.k > kMaxCols) return fail(MUON_ERR_INVALID_ARG, at + ": n and k must be in [1, 2^24]");
+  auto bad = [&](muon_status st, const char* what) { return fail(st, Views::at(item) + name + what); };
+  if (w.n < 1 || w.n > kMaxCols || w.k < 1 || w.k > kMaxCols) return bad(MUON_ERR_INVALID_ARG, ": n and k must be in [1, 2^24]");
   if (ceil_div(w.n, muon::kBlock) * ceil_div(w.k, muon::kBlock) > (int64_t(1) << 30))
-    return fail(MUON_ERR_INVALID_ARG, at + ": more than 2^30 blocks");
+    return bad(MUON_ERR_INVALID_ARG, ": more than 2^30 blocks");
   if (q) {
-    if (w.ldq % 16) return fail(MUON_ERR_ALIGN, at + ": ldq must be a multiple of 16");
+    if (w.ldq % 16) return bad(MUON_ERR_ALIGN, ": ldq must be a multiple of 16");
     MUON_TRY(v.add(w.q, w.n, (w.k + 15) / 16 * 16, w.ldq, 1, written, name, item, 16));
   }
   if (qt) {
-    if (!w.qt) return fail(MUON_ERR_INVALID_ARG, at + ".qt is NULL");
-    if (w.ldqt % 16) return fail(MUON_ERR_ALIGN, at + ": ldqt must be a multiple of 16");
+    if (!w.qt) return bad(MUON_ERR_INVALID_ARG, ".qt is NULL");
+    if (w.ldqt % 16) return bad(MUON_ERR_ALIGN, ": ldqt must be a multiple of 16");
     MUON_TRY(v.add(w.qt, w.k, (w.n + 15) / 16 * 16, w.ldqt, 1, written, name, item, 16));
   }
   return v.add(w.e, ceil_div(w.n, muon::kBlock), ceil_div(w.k, muon::kBlock), w.lde, 1, written, name, item);
@@ -525,7 +566,7 @@ muon_status plan_linear8(const muon_linear8_item* items, int32_t n, int32_t dtyp
   }
   for (muon::PrArgs& a : plans) {
     size_t need = 0;
-    MUON_TRY(lay_out(a, false, 1, 4.0, &need));
+    MUON_TRY(lay_out(a, false, 1, a.f32 ? kLinear8F32Cost : kLinear8Cost, &need));
     *bytes = std::max(*bytes, need);
   }
   return MUON_OK;

@@ -501,8 +501,8 @@ class Linear8:
         need = ctypes.c_size_t()
         check(lib().muon_linear8_workspace(self._items, self._n, self._dtype, ctypes.byref(need)))
         self.workspace = torch.empty(need.value, dtype=torch.uint8, device=tensors[0].device)
+        self._args = (self._items, self._n, self._dtype, self.workspace.data_ptr(), need.value)
         self._streams = _Streams(tensors + [self.workspace])
 
     def run(self, stream=None) -> None:
-        check(lib().muon_linear8(self._items, self._n, self._dtype, self.workspace.data_ptr(), self.workspace.numel(),
-                                 self._streams.use(stream)))
+        check(lib().muon_linear8(*self._args, self._streams.use(stream)))
