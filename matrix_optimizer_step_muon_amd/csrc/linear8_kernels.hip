@@ -26,8 +26,10 @@ static hipError_t launch_tiles(const PrArgs& args, hipStream_t s) {
   typedef PrCfg<128, 128, 128, 2, MODE, 2> Medium;
   typedef PrCfg<64, 64, 128, 4, MODE, 2> Small;
   const dim3 block(256);
-  if (args.tile == kPrLarge) hipLaunchKernelGGL(linear8_kernel<Large>, dim3(pr_grid<Large>(args)), block, 0, s, args);
-  else if (args.tile == kPrMedium) hipLaunchKernelGGL(linear8_kernel<Medium>, dim3(pr_grid<Medium>(args)), block, 0, s, args);
+  if (args.tile == kPrLarge) {
+    if constexpr (MODE == kNT8) hipLaunchKernelGGL(linear8_kernel<Large>, dim3(pr_grid<Large>(args)), block, 0, s, args);
+    else return hipErrorInvalidValue;  // not chosen for fp32
+  } else if (args.tile == kPrMedium) hipLaunchKernelGGL(linear8_kernel<Medium>, dim3(pr_grid<Medium>(args)), block, 0, s, args);
   else hipLaunchKernelGGL(linear8_kernel<Small>, dim3(pr_grid<Small>(args)), block, 0, s, args);
   const hipError_t e = hipGetLastError();
   const int64_t join = pr_join_blocks(args, false);

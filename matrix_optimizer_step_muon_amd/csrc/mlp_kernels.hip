@@ -87,6 +87,7 @@ constexpr int kNoSave = 2;  // a variant's B, beside the kinds: no checkpoint is
 struct PrGateOut {
   static constexpr int OPS = 2, AHEAD = 1;
   struct Pre {};
+  static MUON_INLINE void settle(const Pre&) {}
   PrLane at;
   Planes s;
   Saved qa, qb, qs;
@@ -138,6 +139,7 @@ struct PrGateGradOut {
     u32x2 a, b;
     uint32_t ea, eb;
   };
+  static MUON_INLINE void settle(const Pre& p) { asm volatile("" ::"v"(p.a), "v"(p.b), "v"(p.ea), "v"(p.eb)); }
   PrLane at;
   Saved qa, qb;
   Planes pa, pb;
@@ -237,6 +239,51 @@ static hipError_t launch_tiles(const PrArgs& args, hipStream_t s) {
   const int64_t join = pr_join_blocks(args, Out::OPS == 2);
   if (e != hipSuccess || join == 0) return e;
   hipLaunchKernelGGL(mlp_join_kernel<Out>, dim3((uint32_t)join), dim3(256), 0, s, args, kPrEdge[args.tile]);
+  return hipGetLastError();
+}
+
+// A thread takes octets of columns of one operand, 256 workgroups' worth apart. One
+// launch for all operands of a call. Bound by memory: 4 and 6 bytes per fp32 element,
+// 12.6 M of them in 22 us (5.7 TB/s).
+constexpr int kPackOctets = 8;  // per thread
+
+template <class T, int PARTS>
+__global__ void __launch_bounds__(256) pack_kernel(PrPacks args) {
+  int i = 0;
+  for (int j = 1; j < args.n; ++j) i += (int)blockIdx.x >= args.pack[j].first;
+  const PrPack& p = args.pack[i];
+  const int64_t count = p.octets * p.rows, blocks = (i + 1 < args.n ? args.pack[i + 1].first : args.blocks) - p.first;
+  const T* src = static_cast<const T*>(p.src);
+  for (int64_t at = (int64_t)((int)blockIdx.x - p.first) * 256 + threadIdx.x; at < count; at += blocks * 256) {
+    const int64_t row = at / p.octets, col = (at - row * p.octets) * 8;
+    float v[8];
+    load_run(src + row * p.ld + col, p.cols - (int)col, v);
+    u16* to = static_cast<u16*>(p.dst) + at * 8;
+    if constexpr (PARTS == 1) {
+      *((g_u32x4*)to) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    } else {
+      float t[3][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cut3(v[e], t[2][e], t[1][e], t[0][e]);
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        *((g_u32x4*)(to + q * count * 8)) = u32x4{pack_bf16x2(t[q][0], t[q][1]), pack_bf16x2(t[q][2], t[q][3]),
+                                                 pack_bf16x2(t[q][4], t[q][5]), pack_bf16x2(t[q][6], t[q][7])};
+    }
+  }
+}
+
+hipError_t launch_packs(const PrPacks& args, bool f32, hipStream_t s) {
+  if (args.n == 0) return hipSuccess;
+  PrPacks a = args;
+  a.blocks = 0;
+  for (int i = 0; i < a.n; ++i) {
+    const int64_t want = (a.pack[i].octets * a.pack[i].rows + 256 * kPackOctets - 1) / (256 * kPackOctets);
+    a.pack[i].first = a.blocks;
+    a.blocks += (int)(want < 1 ? 1 : want < 8192 ? want : 8192);
+  }
+  if (f32) hipLaunchKernelGGL((pack_kernel<float, 3>), dim3(a.blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((pack_kernel<u16, 1>), dim3(a.blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

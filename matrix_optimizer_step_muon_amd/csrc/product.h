@@ -64,12 +64,17 @@ struct PrCfg {
   static constexpr int BROW = BN * 2, BRPI = 1024 / BROW, BS = BN / 8;  // the same of a transposed B
   static constexpr int SUB = MODE == kNT8 ? 64 : MODE == kNT8X ? 16 : 32;  // bytes of K of a sub-step
   static constexpr int KK = RB / SUB, PER = FM * FN, SLOTS = KK * PER, NF = FM + FN;
-  // The slot at which the workgroup meets: the last sub-step's fragments are in
-  // registers, the next stage must be in LDS.
-  static constexpr int MEET = KK == 1 ? PER / 2 : SLOTS - (PER >= 16 ? 4 : PER >= 4 ? 2 : 1);
+  // Small tiles have too few MFMAs in a sub-step to cover a read from LDS: they hold the
+  // fragments of two whole stages (4096 x 2048 x 6144 in 64 x 64 tiles 165 us, with those
+  // of two sub-steps 174; few tiles gain 0 to 5%).
+  static constexpr bool AHEAD = PER <= 4;
+  static constexpr int KF = AHEAD ? KK : 1;
+  // The slot at which the workgroup meets: this stage's fragments are in registers, the
+  // next stage must be in LDS.
+  static constexpr int MEET = AHEAD ? (PER == 1 ? 0 : SLOTS / 2) : SLOTS - 4;
   // 8-bit operands: exponents of 1024 of K, for as many runs of stages as a ring can
   // hold parts of
-  static constexpr int CHUNK = 1024 / RB, TABS = ST <= 2 ? 2 : 4, EX_A = 8 * BM * 4, EX_B = 8 * 2 * 4, EX = F8 ? TABS * (EX_A + EX_B) : 0;
+  static constexpr int CHUNK = 1024 / RB, TABS = ST, EX_A = 8 * BM * 4, EX_B = 8 * 2 * 4, EX = F8 ? TABS * (EX_A + EX_B) : 0;
   static constexpr int LDS = RING + EX;
   // The tile leaves through the stage that it used last (the others hold the next
   // tile's first stages): IPP blocks of 32 rows of every wave at a time, or, where
@@ -79,9 +84,9 @@ struct PrCfg {
   static constexpr int NJ = STAGE >= ROW_BLOCK ? FN : FN >= 4 && STAGE >= ROW_BLOCK / 2 ? FN / 2 : FN >= 4 ? FN / 4 : 1;
   static constexpr int PASSES = FM / IPP * (FN / NJ), SCOLS = 64 * NJ;  // columns of a staged row
   static_assert(FM % IPP == 0 && 64 * IPP * SCOLS * 4 <= STAGE && PASSES <= 8, "a pass fits a stage");
-  static_assert((KK % 2 == 0 || KK == 1) && MEET >= SLOTS - PER, "schedule assumptions");
-  static_assert(DA % 2 == 0 && DB % 2 == 0 && ST <= 4, "copies of A and B lie alike");
-  typedef std::conditional_t<MODE == kNT8, i32x8, bf16x8> Frag;
+  static_assert(KK % 2 == 0 && (AHEAD || MEET >= SLOTS - PER) && (AHEAD || MODE != kNT8X), "schedule assumptions");
+  static_assert(DA % 2 == 0 && DB % 2 == 0 && (ST & (ST - 1)) == 0, "copies of A and B lie alike");
+  typedef std::conditional_t<MODE == kNT8, i32x8, std::conditional_t<MODE == kNT8X, u32x2, bf16x8>> Frag;  // as read
 };
 
 // The item that number `unit` of a numbering over the items belongs to.
@@ -264,6 +269,10 @@ struct PrStoreOut {
       for (int i = 0; i < kRun; ++i) p.c[i] = __float_as_uint(x[i]);
     }
   }
+  static MUON_INLINE void settle(const Pre& p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("" ::"v"(p.c[i]));
+  }
   // c as fp32 (WIDE), or as packed bf16.
   template <bool WIDE>
   MUON_INLINE void add(const Pre& p, float v[8]) const {
@@ -353,26 +362,26 @@ template <class Z, class Out, bool FULL>
 MUON_INLINE void pr_leave_as(const PrStage<Z>& stage, const Out& out, int m0) {
   constexpr bool DUAL = Out::OPS == 2;
   constexpr int COLS = DUAL ? Z::SCOLS / 2 : Z::SCOLS, LW = COLS / kRun;
-  constexpr int STEP = Z::NT / LW, IT = PrStage<Z>::ROWS / STEP, AHEAD = IT < Out::AHEAD ? IT : Out::AHEAD, ALL = Z::PASSES * IT;
-  static_assert(IT >= 1 && IT % AHEAD == 0 && (PrStage<Z>::PR % STEP == 0 || STEP % PrStage<Z>::PR == 0), "the threads of a pass take whole rows");
+  constexpr int STEP = Z::NT / LW, IT = PrStage<Z>::ROWS / STEP, PRE = IT < Out::AHEAD ? IT : Out::AHEAD, ALL = Z::PASSES * IT;
+  static_assert(IT >= 1 && IT % PRE == 0 && (PrStage<Z>::PR % STEP == 0 || STEP % PrStage<Z>::PR == 0), "the threads of a pass take whole rows");
   const int tid = fresh_tid(), row = tid / LW, col = tid % LW * kRun;
   // The matrix's row of run g, without the thread's own part, and the columns that
   // its pass is shifted by.
   auto row_of = [&](int g) __attribute__((always_inline)) { return m0 + PrStage<Z>::tile_row(g / IT, g % IT * STEP); };
   auto col_of = [&](int g) __attribute__((always_inline)) { return PrStage<Z>::tile_col(g / IT); };
-  typename Out::Pre pre[AHEAD];
+  typename Out::Pre pre[PRE];
 #pragma unroll
-  for (int g = 0; g < AHEAD; ++g) out.template pre<PrVariant<FULL>>(row_of(g), col_of(g), pre[g]);
+  for (int g = 0; g < PRE; ++g) out.template pre<PrVariant<FULL>>(row_of(g), col_of(g), pre[g]);
 #pragma unroll 1
   for (int pass = 0; pass < Z::PASSES; ++pass) {
     stage.fill(pass);
     auto runs = [&](auto variant) __attribute__((always_inline)) {
       typedef decltype(variant) V;
 #pragma unroll 1
-      for (int q0 = 0; q0 < IT; q0 += AHEAD)
+      for (int q0 = 0; q0 < IT; q0 += PRE)
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-          const int g = pass * IT + q0 + a, n = min(g + AHEAD, ALL - 1);  // past the end: the last one again
+        for (int a = 0; a < PRE; ++a) {
+          const int g = pass * IT + q0 + a, n = min(g + PRE, ALL - 1);  // past the end: the last one again
           float v[8], w[8];
           stage.run((q0 + a) * STEP + row, col, v);
           if constexpr (DUAL) stage.run((q0 + a) * STEP + row, COLS + col, w);
@@ -384,6 +393,10 @@ MUON_INLINE void pr_leave_as(const PrStage<Z>& stage, const Out& out, int m0) {
     if constexpr (FULL) out.dispatch(runs);
     else runs(PrAny{});
   }
+  // The loads past the end come in here: in flight, they would be waited for where
+  // their registers are next written, in the next tile's stages.
+#pragma unroll
+  for (int g = 0; g < PRE; ++g) Out::settle(pre[g]);
 }
 
 template <class Z, class Out>
@@ -460,7 +473,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     limit = (uint32_t)min((kbytes - lks * RB + 15) / 16, S) * 16 - 16;
     if constexpr (Z::NN) limit_k = (uint32_t)(min(lk - lks * Z::BK, Z::BK) - 1) * (uint32_t)ldb;
     lfresh = Z::F8 && (lfresh || (lks & (Z::CHUNK - 1)) == 0);
-    if (Z::F8 && lfresh) ltab = (ltab + 1) & (Z::TABS - 1);
+    if (Z::F8 && lfresh) ltab = __builtin_amdgcn_readfirstlane((ltab + 1) & (Z::TABS - 1));
   };
   auto seat = [&]() __attribute__((always_inline)) {
     PrItemRef it = args->item[lidx];
@@ -572,9 +585,9 @@ MUON_INLINE void pr_run(unsigned char* smem) {
       }
     }
   };
-  auto write_ex = [&]() __attribute__((always_inline)) {
+  auto write_ex = [&](int table) __attribute__((always_inline)) {
     if constexpr (Z::F8) {
-      unsigned char* t = smem + Z::RING + ltab * (Z::EX_A + Z::EX_B);
+      unsigned char* t = smem + Z::RING + table * (Z::EX_A + Z::EX_B);
       if (tid < Z::BM)
 #pragma unroll
         for (int w = 0; w < 8; ++w) *reinterpret_cast<uint32_t*>(t + (w * Z::BM + tid) * 4) = ev[w];
@@ -625,11 +638,13 @@ MUON_INLINE void pr_run(unsigned char* smem) {
   // 16-31, 48-63, and its scale of half h is that of k 32 h .. 32 h + 31.
   const int r32 = lane & 31, h = lane >> 5, sw = pr_swz<S>(r32);
   const int G = lane >> 4, i16 = lane & 15;
-  typename Z::Frag fa[2][FM], fb[2][FN];
+  typename Z::Frag fa[2][Z::KF][FM], fb[2][Z::KF][FN];
+  bf16x8 da[2][FM], db[2][FN];                       // kNT8X: a sub-step's, decoded
   uint32_t sa[FM], sb = 127, na[FM], nb_ = 127;      // this stage's scales, and the next one's
+  // Fragment f of sub-step kk into buffer b.
   auto read_frag = [&](int b, uint32_t buf, int kk, int f) __attribute__((always_inline)) {
     const bool is_a = f < FM;
-    const int i = is_a ? f : f - FM;
+    const int i = is_a ? f : f - FM, to = Z::AHEAD ? kk : 0;
     typename Z::Frag v;
     if (Z::NN && !is_a) {
       if constexpr (Z::NN) {
@@ -646,17 +661,26 @@ MUON_INLINE void pr_run(unsigned char* smem) {
         const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((4 * kk + 2 + h) ^ sw) << 4));
         v = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
       } else if constexpr (Z::MODE == kNT8X) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(row + ((kk ^ sw) << 4) + 8 * h);
-        const uint32_t E = is_a ? (sa[i] >> (8 * (kk >> 1))) & 255u : sb;
-        const Q8Group<MUON_Q8_E4M3> grp(E, true);
-        const u32x2 x = grp.bf16x4(w[0]), y = grp.bf16x4(w[1]);
-        v = __builtin_bit_cast(bf16x8, (u32x4{x[0], x[1], y[0], y[1]}));
+        v = *reinterpret_cast<const u32x2*>(row + ((kk ^ sw) << 4) + 8 * h);
       } else {
         v = *reinterpret_cast<const bf16x8*>(row + (((2 * kk + h) ^ sw) << 4));
       }
     }
-    if (is_a) fa[b][i] = v;
-    else fb[b][i] = v;
+    if (is_a) fa[b][to][i] = v;
+    else fb[b][to][i] = v;
+  };
+  // kNT8X: fragment f of sub-step kk in buffer b, decoded with the scales xa and xb of
+  // its stage.
+  auto decode = [&](int b, int kk, int f, const uint32_t (&xa)[FM], uint32_t xb) __attribute__((always_inline)) {
+    if constexpr (Z::MODE == kNT8X) {
+      const bool is_a = f < FM;
+      const int i = is_a ? f : f - FM;
+      const Q8Group<MUON_Q8_E4M3> grp(is_a ? (xa[i] >> (8 * (kk >> 1))) & 255u : xb, true);
+      const u32x2 w = is_a ? fa[b][kk][i] : fb[b][kk][i], x = grp.bf16x4(w[0]), y = grp.bf16x4(w[1]);
+      const bf16x8 v = __builtin_bit_cast(bf16x8, (u32x4{x[0], x[1], y[0], y[1]}));
+      if (is_a) da[kk & 1][i] = v;
+      else db[kk & 1][i] = v;
+    }
   };
   auto read_ex = [&](int ks_, int t_) __attribute__((always_inline)) {
     if constexpr (Z::F8) {
@@ -677,14 +701,16 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     }
   };
   auto mfma = [&](int b, int kk, int q) __attribute__((always_inline)) {
-    const int i = q / FN, j = q % FN;
+    const int i = q / FN, j = q % FN, at_k = Z::AHEAD ? kk : 0;
     if constexpr (Z::MODE == kNT8) {
       if (kk == 0)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0, (int)sb, 0, (int)sa[i]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][at_k][j], fa[b][at_k][i], acc[i][j], 0, 0, 0, (int)sb, 0, (int)sa[i]);
       else
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0, (int)sb, 2, (int)sa[i]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b][at_k][j], fa[b][at_k][i], acc[i][j], 0, 0, 0, (int)sb, 2, (int)sa[i]);
+    } else if constexpr (Z::MODE == kNT8X) {
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(db[kk & 1][j], da[kk & 1][i], acc[i][j], 0, 0, 0);
     } else {
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[b][at_k][j], fa[b][at_k][i], acc[i][j], 0, 0, 0);
     }
   };
 
@@ -705,14 +731,15 @@ MUON_INLINE void pr_run(unsigned char* smem) {
   for (int s = 0; s < Z::ST - 1; ++s) {
     if (lfresh) {
       load_ex();
-      write_ex();
+      write_ex(ltab);
     }
 #pragma unroll
     for (int d = 0; d < Z::PS; ++d) copy(s * Z::STAGE, d);
     advance();
   }
-  wait_vmcnt<0>();
+  wait_vmcnt<(Z::ST - 2) * Z::PS>();
   uint32_t cur = 0, to = (Z::ST - 1) * Z::STAGE;     // the ring's stage at hand, and the one that is loaded
+  int due = -1, due_tab = 0;                         // stages until the exponents on their way go to that table
 
 #pragma unroll 1
   for (; at < count; at += step) {
@@ -732,79 +759,119 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     if (short_stage(ks)) clear(ks, cur);
     read_ex(ks, tab);
     take_ex(ks);
+    // The first stage's fragments, into buffer b.
+    auto begin = [&](auto b_) __attribute__((always_inline)) {
+      constexpr int b = decltype(b_)::value;
 #pragma unroll
-    for (int f = 0; f < Z::NF; ++f) read_frag(0, cur, 0, f);
+      for (int kk = 0; kk < Z::KF; ++kk)
+#pragma unroll
+        for (int f = 0; f < Z::NF; ++f) read_frag(b, cur, kk, f);
+#pragma unroll
+      for (int f = 0; f < Z::NF; ++f) decode(b, 0, f, sa, sb);
+    };
 
     // One stage: MFMAs, and between two of them a little of everything else, in a
-    // fixed order. The last sub-step's fragments are in registers a few MFMAs before
-    // its end: there the workgroup meets, and the next stage's first fragments are
-    // read under the remaining MFMAs (after the last stage: for nothing). The
-    // fragments of its first sub-step are in buffer PAR.
+    // fixed order. What the MFMAs need next is in registers a few MFMAs before: at MEET
+    // the workgroup meets, and the next stage's first fragments (AHEAD: all of them) are
+    // read under the remaining MFMAs (after the last stage: for nothing). AHEAD: this
+    // stage's fragments are in buffer PAR.
     int t = u.total;
     auto stage = [&](auto PAR_) __attribute__((always_inline)) {
-      constexpr int PAR = decltype(PAR_)::value, NEXT = (PAR + Z::KK) & 1;
+      constexpr int PAR = decltype(PAR_)::value;
       const uint32_t after = cur + Z::STAGE == Z::RING ? 0 : cur + Z::STAGE;
       const int ks1 = ks + 1 == kt ? 0 : ks + 1;
-      if (lfresh) load_ex();
+      if (lfresh) {
+        // a table is due ST - 2 stages later
+        if (due >= 0) write_ex(due_tab);
+        load_ex();
+        due = Z::ST - 2;
+        due_tab = ltab;
+      }
+      if constexpr (Z::MEET == 0) {
+#pragma unroll
+        for (int d = 0; d < Z::PS; ++d) copy(to, d);
+      }
 #pragma unroll
       for (int kk = 0; kk < Z::KK; ++kk)
 #pragma unroll
         for (int q = 0; q < Z::PER; ++q) {
-          const int slot = kk * Z::PER + q, b = (PAR + kk) & 1;
+          const int slot = kk * Z::PER + q, b = Z::AHEAD ? PAR : kk & 1;
           if (slot == Z::MEET) {
             anchor();
-            if (lfresh) write_ex();
+            if (Z::F8 && due >= 0) {
+              if (due == 0) write_ex(due_tab);
+              --due;
+            }
             // the next stage's copies are the oldest in flight
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((Z::ST - 2) * Z::PS) : "memory");
             if (t > 1) {
               if (short_stage(ks1)) clear(ks1, after);
-              if (Z::F8 && (ks1 & (Z::CHUNK - 1)) == 0) tab = (tab + 1) & (Z::TABS - 1);
+              if (Z::F8 && (ks1 & (Z::CHUNK - 1)) == 0) tab = __builtin_amdgcn_readfirstlane((tab + 1) & (Z::TABS - 1));
             }
             read_ex(ks1, tab);
           }
           mfma(b, kk, q);
-          if (kk + 1 < Z::KK) {
+          if constexpr (Z::AHEAD) {
+            constexpr int ALL = Z::KK * Z::NF;
+            if (slot >= Z::MEET) {
 #pragma unroll
-            for (int f = 0; f < Z::NF; ++f)
-              if (f * Z::PER / Z::NF == q) read_frag(b ^ 1, cur, kk + 1, f);
-          }
-          if constexpr (Z::MODE != kNT8X) {
+              for (int f = 0; f < ALL; ++f)
+                if (f * (Z::SLOTS - Z::MEET) / ALL == slot - Z::MEET) read_frag(PAR ^ 1, after, f / Z::NF, f % Z::NF);
+            }
+            if constexpr (Z::MODE == kNT8X) {
+#pragma unroll
+              for (int f = 0; f < Z::NF; ++f)
+                if (kk + 1 < Z::KK && f * Z::PER / Z::NF == q) decode(PAR, kk + 1, f, sa, sb);
+            }
+          } else {
+            if (kk + 1 < Z::KK) {
+#pragma unroll
+              for (int f = 0; f < Z::NF; ++f)
+                if (f * Z::PER / Z::NF == q) read_frag(b ^ 1, cur, kk + 1, f);
+            }
             if (slot >= Z::MEET) {
 #pragma unroll
               for (int f = 0; f < Z::NF; ++f)
-                if (f * (Z::SLOTS - Z::MEET) / Z::NF == slot - Z::MEET) read_frag(NEXT, after, 0, f);
+                if (f * (Z::SLOTS - Z::MEET) / Z::NF == slot - Z::MEET) read_frag(0, after, 0, f);
             }
           }
+          if constexpr (Z::MEET != 0) {
 #pragma unroll
-          for (int d = 0; d < Z::PS; ++d)
-            if (d * Z::MEET / (Z::PS * (Z::ST == 2 ? 2 : 1)) == slot) copy(to, d);
+            for (int d = 0; d < Z::PS; ++d)
+              if (d * Z::MEET / (Z::PS * (Z::ST == 2 && !Z::AHEAD ? 2 : 1)) == slot) copy(to, d);
+          }
           if (slot == Z::SLOTS - 1) {
             anchor();
             take_ex(ks1);
+#pragma unroll
+            for (int f = 0; f < Z::NF; ++f) decode(PAR ^ 1, 0, f, sa, sb);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-      if constexpr (Z::MODE == kNT8X) {  // these need the next stage's scales
-#pragma unroll
-        for (int f = 0; f < Z::NF; ++f) read_frag(NEXT, after, 0, f);
-      }
       advance();
       ks = ks1;
       cur = after;
       to = to + Z::STAGE == Z::RING ? 0 : to + Z::STAGE;
       --t;
     };
-    if constexpr (Z::KK % 2 == 0) {
-#pragma unroll 1
-      while (t) stage(std::integral_constant<int, 0>{});
-    } else {
-#pragma unroll 1
-      for (;;) {
-        stage(std::integral_constant<int, 0>{});
-        if (t == 0) break;
-        stage(std::integral_constant<int, 1>{});
-        if (t == 0) break;
+    typedef std::integral_constant<int, 0> Even;
+    typedef std::integral_constant<int, 1> Odd;
+    if constexpr (Z::AHEAD) {
+      if (t & 1) {
+        begin(Odd{});
+        stage(Odd{});
+      } else {
+        begin(Even{});
       }
+#pragma unroll 1
+      while (t) {
+        stage(Even{});
+        stage(Odd{});
+      }
+    } else {
+      begin(Even{});
+#pragma unroll 1
+      while (t) stage(Even{});
     }
     pr_leave<Z, Out>(args, it, u.piece, u.m0, u.n0, smem + to, acc);
   }

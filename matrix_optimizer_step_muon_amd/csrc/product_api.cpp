@@ -39,28 +39,31 @@ struct Choice {
 };
 
 // What a kind of product costs beside its stages: us that a CU takes to let the sums
-// of a large tile out (twice that, of its cost below), and a stage against one of
+// of a tile out (times a factor of the tile's, below), and a stage against one of
 // bf16 operands that are both read along K.
 struct Cost {
   double leave, stage;
+  int first = muon::kPrLarge;  // the largest tile that it has
 };
-constexpr Cost kGateCost{10.5, 1.0}, kGateGradCost{19.6, 1.02}, kDownCost{2.6, 1.0}, kDxCost{2.6, 1.02}, kLinear8Cost{14.0, 0.96},
-    kLinear8F32Cost{14.0, 2.2};
+constexpr Cost kGateCost{9.9, 1.0}, kGateGradCost{14.0, 0.99}, kDownCost{3.4, 1.0}, kDxCost{3.4, 0.99}, kLinear8Cost{19.2, 0.96},
+    kLinear8F32Cost{19.2, 1.8, muon::kPrMedium};
 
 // For products with t[i] tiles of kind i in all, and `stages` stages of 128 bytes of
 // K each, that read `bytes` once. Either all tiles are whole, or all in pieces, or the
 // last round, which would leave CUs without work, is in as many pieces as there is
 // room for. The constants are fitted to a sweep on one MI355X: 12 sizes from 20 x 2048
-// x 6144 to 4096 x 2048 x 6144, six kinds of product, each tile in 1 to 24 pieces, 1061
-// times in all. The pick is 1.9% behind the best on average, over 10% in six of 72
-// (up to 20%, where large tiles in pieces take more than estimated).
+// x 6144 to 4096 x 2048 x 6144, six kinds of product, each tile in 1 to 24 pieces, 1014
+// times in all. The pick is 1.6% behind the best on average, over 10% in two of 72 (14%,
+// where tiles in pieces take more than estimated). At one size each, us of the best cut
+// of large, medium and small tiles: 4096 x 6144 x 2048 with both projections 199, 246,
+// 408; 2000 x 3200 x 1600 42, 29, 41; 64 x 2048 x 6144 29, 20, 13.
 Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, const Cost& cost, double bytes) {
   // Per kind: workgroups per CU; us to fill a tile and to let it out; us per stage
   // with one and with all of a CU's; us per partial tile, written and read.
   static const struct { int per_cu; double fill, leave, one, all, part; } kCost[muon::kPrTiles] = {
-      {1, 3.2, 0.48, 1.34, 1.34, 0.077}, {2, 2.1, 0.21, 0.78, 1.04, 0.017}, {2, 1.1, 0.23, 0.325, 0.45, 0.003}};
-  Choice best{muon::kPrLarge, t[0], 1, 1e300};
-  for (int i = 0; i < muon::kPrTiles; ++i) {
+      {1, 4.2, 0.3, 1.27, 1.27, 0.077}, {2, 3.2, 0.064, 0.79, 1.05, 0.017}, {2, 0.87, 0.22, 0.27, 0.43, 0.003}};
+  Choice best{cost.first, t[cost.first], 1, 1e300};
+  for (int i = cost.first; i < muon::kPrTiles; ++i) {
     const auto& c = kCost[i];
     const int64_t round = kCus * c.per_cu;
     const double fixed = c.fill + cost.leave * c.leave;
@@ -73,7 +76,7 @@ Choice choose(const int64_t t[muon::kPrTiles], int64_t stages, const Cost& cost,
       const int64_t pieces = (t[i] - whole) * s;
       if (whole + pieces > kMaxUnits) return;
       double us = 2.0 + run(whole, stages);
-      if (pieces) us += run(pieces, ceil_div(stages, s)) + 3.6 + 0.1 * double(s) + c.part * double(pieces);
+      if (pieces) us += run(pieces, ceil_div(stages, s)) + 2.9 + 0.1 * double(s) + c.part * double(pieces);
       const double stream = 4.0 + bytes / kHbm;  // what is the least also counts a little
       us = std::max(us, stream) + 0.15 * std::min(us, stream);
       if (us < best.us) best = {i, whole, int(s), us};
@@ -381,9 +384,20 @@ muon_status check_mlp_workspace(Views& v, const muon_mlp& p, size_t need) {
   return v.add_range(p.workspace, need, "workspace");
 }
 
-muon_status run_pack(const Operand& o, const muon_mlp& p, char* ws, hipStream_t s) {
-  if (!o.pack) return MUON_OK;
-  return hip_status(muon::launch_wgrad_pack(o.p, o.ld, p.dtype, ws + o.at, int32_t(o.rows), int32_t(o.cols), pad8(o.cols), s));
+// The operands of ops[0 .. n) that are used and not in place, rewritten in one launch.
+muon_status run_packs(const Operand* ops, const bool* used, int n, const muon_mlp& p, char* ws, hipStream_t s) {
+  muon::PrPacks a{};
+  for (int i = 0; i < n; ++i) {
+    if (!used[i] || !ops[i].pack) continue;
+    muon::PrPack& d = a.pack[a.n++];
+    d.src = ops[i].p;
+    d.dst = ws + ops[i].at;
+    d.ld = ops[i].ld;
+    d.octets = pad8(ops[i].cols) / 8;
+    d.rows = int32_t(ops[i].rows);
+    d.cols = int32_t(ops[i].cols);
+  }
+  return hip_status(muon::launch_packs(a, p.dtype == MUON_F32, s));
 }
 
 muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
@@ -414,9 +428,8 @@ muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
   MUON_TRY(check_mlp_workspace(v, p, c.bytes));
   MUON_TRY(v.disjoint());
   const bool gate = few_gate(p, c.first_us), down = p.y && few_down(p, c.second_us);
-  const int used[] = {!gate, !gate, !gate, p.y && !down};
-  for (int i = 0; i < 4; ++i)
-    if (used[i]) MUON_TRY(run_pack(c.ops[i], p, ws, s));
+  const bool used[] = {!gate, !gate, !gate, p.y && !down};
+  MUON_TRY(run_packs(c.ops, used, 4, p, ws, s));
   if (gate) MUON_TRY(launch_few_gate(p, c.first.mlp.plane[0], c.first.mlp.ldp, s));
   else MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGate, false, s)));
   if (down) return launch_few_down(p, c.first.mlp.plane[0], c.first.mlp.ldp, s);
@@ -445,7 +458,8 @@ muon_status mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void*
   MUON_TRY(check_mlp_workspace(v, p, c.bytes));
   MUON_TRY(v.disjoint());
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  for (int i = 0; i < (g.d_x ? 4 : 2); ++i) MUON_TRY(run_pack(c.ops[i], p, ws, s));
+  const bool used[] = {true, true, g.d_x != nullptr, g.d_x != nullptr};
+  MUON_TRY(run_packs(c.ops, used, 4, p, ws, s));
   MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGateGrad, true, s)));
   return g.d_x ? hip_status(muon::launch_mlp(c.second, muon::kPrStore, true, s)) : MUON_OK;
 }

@@ -89,6 +89,23 @@ struct FewArgs {
 
 static_assert(sizeof(PrArgs) <= 4000, "kernel arguments");
 
+// Operands rewritten into aligned bf16 rows (pad8 columns, zeros behind the last one),
+// one plane or, of fp32, the three planes lo, mid and hi.
+constexpr int kPrPacks = 4;
+struct PrPack {
+  const void* src;
+  void* dst;
+  int64_t ld, octets;        // source row stride; octets of columns of a row
+  int32_t rows, cols;
+  int32_t first;             // workgroup
+  int32_t reserved;
+};
+struct PrPacks {
+  PrPack pack[kPrPacks];
+  int32_t n, blocks;
+};
+
+hipError_t launch_packs(const PrPacks& args, bool f32, hipStream_t s);
 hipError_t launch_mlp(const PrArgs& args, int epilogue, bool transposed_b, hipStream_t s);
 hipError_t launch_few(const FewArgs& args, bool f32, int ops, hipStream_t s);
 hipError_t launch_few8(const FewArgs& args, hipStream_t s);
