@@ -11,8 +11,14 @@ using namespace muon::abi;
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;
 constexpr int64_t kMaxUnits = int64_t(1) << 22;
-// Row strides, in bytes, up to which 256 rows are within 32-bit offsets.
-constexpr int64_t kMaxPitch = int64_t(1) << 24;
+// Row strides, in bytes, up to which 256 rows are within 32-bit offsets; and those of
+// what the products' tiles write and add, in elements of up to 4 bytes.
+constexpr int64_t kMaxPitch = int64_t(1) << 24, kMaxStride = int64_t(1) << 22;
+
+muon_status check_stride(int64_t ld, const char* name, int item = -1) {
+  if (ld > kMaxStride) return fail(MUON_ERR_INVALID_ARG, Views::at(item) + name + ": row stride must be in [cols, 2^22]");
+  return MUON_OK;
+}
 
 constexpr int64_t kCus = 256;
 constexpr double kHbm = 5.2e6;  // bytes per us: what streaming the weights of few rows reaches
@@ -409,7 +415,10 @@ muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
   const int e = elem_of(p.dtype);
   MUON_TRY(v.add(p.x, p.rows, p.width, p.ld_x, e, false, "x"));
   if (!p.y && !p.a.q && !p.b.q && !p.s.q && p.rows > 0) return fail(MUON_ERR_INVALID_ARG, "y, a, b and s are all NULL");
-  if (p.y) MUON_TRY(v.add(p.y, p.rows, p.out, p.ld_y, e, true, "y"));
+  if (p.y) {
+    MUON_TRY(check_stride(p.ld_y, "y"));
+    MUON_TRY(v.add(p.y, p.rows, p.out, p.ld_y, e, true, "y"));
+  }
   if (p.a.q) MUON_TRY(check_inner(v, p, p.a, true, "a"));
   if (p.b.q) MUON_TRY(check_inner(v, p, p.b, true, "b"));
   if (p.s.q) MUON_TRY(check_inner(v, p, p.s, true, "s"));
@@ -448,9 +457,14 @@ muon_status mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void*
   MUON_TRY(check_inner(v, p, p.a, false, "a"));
   MUON_TRY(check_inner(v, p, p.b, false, "b"));
   if (p.a.kind != p.b.kind) return fail(MUON_ERR_INVALID_ARG, "a and b must be checkpoints of the same kind");
+  MUON_TRY(check_stride(g.ld_d_a, "d_a"));
   MUON_TRY(v.add(g.d_a, p.rows, p.inner, g.ld_d_a, e, true, "d_a"));
+  MUON_TRY(check_stride(g.ld_d_b, "d_b"));
   MUON_TRY(v.add(g.d_b, p.rows, p.inner, g.ld_d_b, e, true, "d_b"));
-  if (g.d_x) MUON_TRY(v.add(g.d_x, p.rows, p.width, g.ld_d_x, e, true, "d_x"));
+  if (g.d_x) {
+    MUON_TRY(check_stride(g.ld_d_x, "d_x"));
+    MUON_TRY(v.add(g.d_x, p.rows, p.width, g.ld_d_x, e, true, "d_x"));
+  }
   if (p.rows == 0) return v.disjoint();
   char* ws = static_cast<char*>(p.workspace);
   MlpCall c;
@@ -511,11 +525,16 @@ muon_status check_linear8(const muon_linear8_item* items, int32_t n, int32_t dty
     const int64_t k = t ? it.w.n : it.w.k, out = t ? it.w.k : it.w.n;
     if (it.x.cols != k)
       return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "x has " + std::to_string(it.x.cols) + " columns, the weight " + std::to_string(k));
+    if (it.w.n > kMaxWidth || it.w.k > kMaxWidth) return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "n and k must be in [1, 2^22]");
+    MUON_TRY(check_stride(it.ld_y, "y", i));
     MUON_TRY(v.add(it.y, it.x.rows, out, it.ld_y, e, true, "y", i));
     if (!std::isfinite(it.beta)) return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "beta is not finite");
     if (it.beta != 0.f && it.c == it.y && it.ld_c != it.ld_y)
       return fail(MUON_ERR_INVALID_ARG, Views::at(i) + "c is y, with another row stride");
-    if (it.beta != 0.f && it.c != it.y) MUON_TRY(v.add(it.c, it.x.rows, out, it.ld_c, e, false, "c", i));
+    if (it.beta != 0.f && it.c != it.y) {
+      MUON_TRY(check_stride(it.ld_c, "c", i));
+      MUON_TRY(v.add(it.c, it.x.rows, out, it.ld_c, e, false, "c", i));
+    }
   }
   return v.disjoint();
 }
