@@ -2,12 +2,18 @@
 checkpoints, weight gradients from them, and the Muon step on the matrices.
 
     python examples/train_layers.py --steps 20 --tokens 1024 --width 512 --layers 2
+    python examples/train_layers.py --act silu
+    python examples/train_layers.py --weights8
 
 Every block is h -> relu(h Wup^T)^2 Wdown^T, between norm sites: a norm after
 the block, a gate, the residual sum, and the norm before the next block. What
 the backward pass needs is kept in 8 bits only: each site's normalised rows u
 and v, and the block's inner activation s. s serves twice, as the saved input of
-Wdown and for the derivative of relu(a)^2, which is 2 sqrt(s). The data are
+Wdown and for the derivative of relu(a)^2, which is 2 sqrt(s). With --act the
+blocks are gated ones, h -> (act(h Wgate^T) * h Wup^T) Wdown^T, which keep their
+two projections and s. With --weights8 the products of h and of the gradients with
+the matrices are in 8 bits: the matrices are saved in e4m3 after every step (the
+optimizer's stay in bf16), and what meets them in e4m3 checkpoints. The data are
 random and the target is a random linear map of the input, learnt by regression.
 All buffers are made once; a training step then only launches kernels.
 """
@@ -27,10 +33,13 @@ BF16 = torch.bfloat16
 
 
 class Model:
-    def __init__(self, tokens: int, width: int, layers: int, kind: str = "int8", seed: int = 0):
+    def __init__(self, tokens: int, width: int, layers: int, kind: str = "int8", seed: int = 0, act: str = None,
+                 weights8: bool = False):
+        if weights8 and (act or kind != "e4m3"):
+            raise ValueError("8-bit weights go with the ungated block and e4m3 checkpoints")
         g = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *s, std=1.0: (std * torch.randn(*s, generator=g, device="cuda")).to(BF16)  # noqa: E731
-        inner = 4 * width
+        inner = -(-8 * width // 192) * 64 if act else 4 * width    # three matrices of 8/3 width, or two of 4
         self.x = rand(tokens, width)
         self.target = (self.x.float() @ torch.randn(width, width, generator=g, device="cuda") * width ** -0.5).to(BF16)
         self.w_up = [rand(inner, width, std=width ** -0.5) for _ in range(layers)]
@@ -40,26 +49,84 @@ class Model:
         # the site before the first block has no branch yet
         self.sites = [layer.NormSite(torch.zeros_like(self.x), self.x, ones(), kind=kind)]
         self.a = new(tokens, inner)
-        self.saved = []
-        for _ in range(layers):
+        self.saved, self.blocks = [], []
+        self.w_gate = [rand(inner, width, std=width ** -0.5) for _ in range(layers if act else 0)]
+        for k in range(layers):
             branch = new(tokens, width)
-            self.saved.append(layer.Q8(tokens, inner, kind))
+            if act:
+                self.blocks.append(layer.GatedMLP(self.sites[-1].h, self.w_gate[k], self.w_up[k], self.w_down[k], act=act, kind=kind,
+                                                  out=branch))
+            self.saved.append(self.blocks[k].s if act else layer.Q8(tokens, inner, kind))
             self.sites.append(layer.NormSite(branch, self.sites[-1].y, ones(), w_post=ones(), gate=ones() * 0.5, kind=kind))
         self.dh, self.ds = new(tokens, width), new(tokens, inner)
-        self.da = [new(tokens, inner) for _ in range(layers)]
-        self.g_up = [torch.empty_like(w) for w in self.w_up]
-        self.g_down = [torch.empty_like(w) for w in self.w_down]
+        self.da = [new(tokens, inner) for _ in range(0 if act else layers)]
+        matrices = self.w_gate + self.w_up + self.w_down
+        grads = [torch.empty_like(w) for w in matrices]
+        self.g_gate, self.g_up, self.g_down = grads[:len(self.w_gate)], grads[-2 * layers:-layers], grads[-layers:]
         self.wgrad = None
-        self.optimizer = muon.Plan([(w, d, torch.zeros_like(w)) for w, d in zip(self.w_up + self.w_down, self.g_up + self.g_down)])
+        self.optimizer = muon.Plan([(w, d, torch.zeros_like(w)) for w, d in zip(matrices, grads)])
+        self.weights8 = [(layer.W8(inner, width), layer.W8(width, inner)) for _ in range(layers if weights8 else 0)]
+        if weights8:
+            self.narrow, self.wide = layer.Q8(tokens, width, kind), layer.Q8(tokens, inner, kind)
+            self.up8 = [layer.Linear8([(self.narrow, up, self.a)]) for up, _ in self.weights8]
+            self.down8 = [layer.Linear8([(s, down, site.branch)]) for s, (_, down), site in zip(self.saved, self.weights8, self.sites[1:])]
+            self.down8_t = [layer.Linear8([(self.narrow, down, self.ds)], transposed=True) for _, down in self.weights8]
+            self.up8_t = [layer.Linear8([(self.wide, up, self.dh)], transposed=True) for up, _ in self.weights8]
+            self.refresh()
+
+    def refresh(self):
+        """The 8-bit weights, from the matrices."""
+        for (up, down), w_up, w_down in zip(self.weights8, self.w_up, self.w_down):
+            layer.w8_save(w_up, up), layer.w8_save(w_down, down)
+
+    def block(self, k, site):
+        """site.branch = the block of sites[k].h."""
+        if self.blocks:
+            return self.blocks[k].forward()
+        if self.weights8:
+            layer.q8_save(self.sites[k].h, self.narrow)
+            self.up8[k].run()
+        else:
+            torch.mm(self.sites[k].h, self.w_up[k].t(), out=self.a)
+        self.a.relu_().square_()
+        layer.q8_save(self.a, self.saved[k])
+        if self.weights8:
+            self.down8[k].run()
+        else:
+            torch.mm(self.a, self.w_down[k].t(), out=site.branch)
+
+    def block_backward(self, k, dy):
+        """The gradient of sites[k].h, from that of the block's output."""
+        if self.blocks:
+            self.blocks[k].backward(dy)
+            return self.blocks[k].d_x
+        if self.weights8:
+            layer.q8_save(dy, self.narrow)
+            self.down8_t[k].run()
+        else:
+            torch.mm(dy, self.w_down[k], out=self.ds)
+        da = layer.q8_load(self.saved[k], self.da[k])   # s, in place
+        da.sqrt_().mul_(2).mul_(self.ds)
+        if not self.weights8:
+            return torch.mm(da, self.w_up[k], out=self.dh)
+        layer.q8_save(da, self.wide)
+        self.up8_t[k].run()
+        return self.dh
+
+    def wgrad_items(self):
+        items = []
+        for k, (site, after) in enumerate(zip(self.sites, self.sites[1:])):
+            if self.blocks:
+                items += self.blocks[k].wgrad_items(after.d_branch, site.u, self.g_gate[k], self.g_up[k], self.g_down[k], scale=site.w_pre)
+            else:
+                items += [(self.da[k], site.u, self.g_up[k], site.w_pre), (after.d_branch, self.saved[k], self.g_down[k])]
+        return items
 
     def forward(self):
         """The loss, as a device scalar."""
         self.sites[0].forward()
         for k, site in enumerate(self.sites[1:]):
-            torch.mm(self.sites[k].h, self.w_up[k].t(), out=self.a)
-            self.a.relu_().square_()
-            layer.q8_save(self.a, self.saved[k])
-            torch.mm(self.a, self.w_down[k].t(), out=site.branch)
+            self.block(k, site)
             site.forward()
         self.diff = self.sites[-1].h.float() - self.target.float()
         return self.diff.square().mean()
@@ -69,14 +136,9 @@ class Model:
         for k in range(len(self.saved) - 1, -1, -1):
             site = self.sites[k + 1]
             site.backward(dy, dh)
-            torch.mm(site.d_branch, self.w_down[k], out=self.ds)
-            da = layer.q8_load(self.saved[k], self.da[k])   # s, in place
-            da.sqrt_().mul_(2).mul_(self.ds)
-            dy, dh = site.d_residual, torch.mm(da, self.w_up[k], out=self.dh)
+            dy, dh = site.d_residual, self.block_backward(k, site.d_branch)
         if self.wgrad is None:  # the sites' gradient buffers exist from their first backward pass on
-            self.wgrad = layer.WGrad(
-                [(da, site.u, g, site.w_pre) for da, site, g in zip(self.da, self.sites, self.g_up)]
-                + [(site.d_branch, s, g) for site, s, g in zip(self.sites[1:], self.saved, self.g_down)])
+            self.wgrad = layer.WGrad(self.wgrad_items())
         self.wgrad.run()
         self.sites[0].backward(dy, dh)   # the first norm's own weight gradient
 
@@ -84,6 +146,7 @@ class Model:
         loss = self.forward()
         self.backward()
         self.optimizer.step()
+        self.refresh()
         for site in self.sites:
             for w, d in ((site.w_pre, site.d_w_pre), (site.w_post, site.d_w_post), (site.gate, site.d_gate)):
                 if w is not None:
@@ -98,10 +161,14 @@ def main(argv=None):
     p.add_argument("--width", type=int, default=512)
     p.add_argument("--layers", type=int, default=2)
     p.add_argument("--kind", choices=sorted(layer.KINDS), default="int8")
+    p.add_argument("--act", choices=sorted(layer.ACTS), help="gated blocks with this activation")
+    p.add_argument("--weights8", action="store_true", help="8-bit products with the weights (e4m3 checkpoints)")
     args = p.parse_args(argv)
-    model = Model(args.tokens, args.width, args.layers, args.kind)
-    kept = sum(q.nbytes() for s in model.sites for q in (s.u, s.v) if q is not None) + sum(q.nbytes() for q in model.saved)
-    full = sum(2 * q.rows * q.cols for s in model.sites for q in (s.u, s.v) if q is not None) + sum(2 * q.rows * q.cols for q in model.saved)
+    if args.weights8:
+        args.kind = "e4m3"
+    model = Model(args.tokens, args.width, args.layers, args.kind, act=args.act, weights8=args.weights8)
+    checkpoints = [q for s in model.sites for q in (s.u, s.v) if q is not None] + model.saved + [q for b in model.blocks for q in (b.a, b.b)]
+    kept, full = sum(q.nbytes() for q in checkpoints), sum(2 * q.rows * q.cols for q in checkpoints)
     print(f"kept for the backward pass: {kept / 2**20:.1f} MiB (in bf16 {full / 2**20:.1f} MiB)")
     losses = [model.step() for _ in range(args.steps)]
     losses = [float(v) for v in torch.stack(losses).tolist()]
