@@ -1,16 +1,20 @@
 // gfx950 kernels of the layers' products for at most 16 rows (tokens that are being
 // decoded): C[m][n] = sum_k A[m][k] B[n][k] is then bound by reading B once.
 //
-// A workgroup takes 16 rows of B (of both projections, in the gated block) and its
-// waves blocks of K in turn, so that it reads runs of consecutive bytes of 16 rows.
-// Every lane loads the 16 bytes that its MFMA operand is, straight into registers: B's
-// rows are the MFMA's rows, A's its columns (past the last one the last one again).
-// A wave asks for its next block before it multiplies the one at hand: 8 to 16 KB in
-// flight a wave. The waves' sums meet in LDS, in a fixed order. No tile is filled, no
-// pieces are joined by a second launch, and any alignment will do.
+// A workgroup takes up to 32 rows of B (of both projections, in the gated block) and
+// its waves blocks of K in turn, so that it reads runs of consecutive bytes of these
+// rows. So many rows that every CU gets the same share: 16 always would leave 64 of
+// 256 CUs with twice the others' work at 5120 rows, and half of them without at 2048
+// (8-bit weights of 5120 x 25600 then take 32.9 us, and 24.4 as it is: 5.4 TB/s; in
+// bf16 2048 x 6144 9.0 and 7.1, both projections of 25600 x 5120 97.4 and 89.0). Every
+// lane loads the 16 bytes that its MFMA operand is, straight into registers: B's rows
+// are the MFMA's rows, A's its columns (past the last one the last one again). A wave
+// asks for its next block before it multiplies the one at hand: 8 to 16 KB in flight a
+// wave. The waves' sums meet in LDS, in a fixed order. No tile is filled, no pieces
+// are joined by a second launch, and any alignment will do.
 //
-// The other way, 64 x 64 tiles: 16.2 and 13.6 us where these take @ and @ (one token, 2048 x
-// 6144 weights), @.
+// The other way, 64 x 64 tiles: 16.2 and 13.6 us where these take 10.8 and 7.1 (one
+// token, both projections of 6144 x 2048 and the down projection).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -23,9 +27,9 @@ namespace muon {
 constexpr int kFewWaves = 16;  // at most
 
 // A block of K of one wave: so many steps of an MFMA's K that two blocks fit its 128
-// registers.
-template <int BYTES>  // of an element
-constexpr int kFewSteps = BYTES == 2 ? 4 : 2;
+// registers. WAYS: operands of B's kind.
+template <int BYTES, int WAYS>  // of an element
+constexpr int kFewSteps = BYTES == 2 ? (WAYS <= 2 ? 4 : 2) : BYTES == 4 ? 2 : WAYS == 1 ? 2 : 1;
 
 // 8 consecutive elements of a row as an MFMA operand: one, or in fp32 the three bf16
 // operands that add up to it.
@@ -88,48 +92,51 @@ MUON_INLINE f32x4 few_mfma(const bf16x8 (&b)[PARTS], const bf16x8 (&a)[PARTS], f
 }
 
 // The sums of all waves, of this thread's output (row t / 16 of A, row t % 16 of B of
-// the workgroup's). An MFMA's element r of lane l is B's row 4 (l / 16) + r, A's l % 16.
-template <int OPS>
-MUON_INLINE void few_join(float (&red)[kFewWaves][OPS][256], const f32x4 (&acc)[OPS], float v[OPS]) {
+// each 16 of the workgroup's). An MFMA's element r of lane l is B's row 4 (l / 16) + r,
+// A's l % 16.
+template <int WAYS>
+MUON_INLINE void few_join(float (&red)[kFewWaves][WAYS][256], const f32x4 (&acc)[WAYS], float v[WAYS]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
 #pragma unroll
-  for (int o = 0; o < OPS; ++o)
+  for (int o = 0; o < WAYS; ++o)
 #pragma unroll
     for (int r = 0; r < 4; ++r) red[wave][o][(lane & 15) * 16 + 4 * (lane >> 4) + r] = acc[o][r];
   __syncthreads();
 #pragma unroll
-  for (int o = 0; o < OPS; ++o) v[o] = 0.f;
+  for (int o = 0; o < WAYS; ++o) v[o] = 0.f;
   if (tid < 256)
     for (int w = 0; w < waves; ++w)
 #pragma unroll
-      for (int o = 0; o < OPS; ++o) v[o] += red[w][o][tid];
+      for (int o = 0; o < WAYS; ++o) v[o] += red[w][o][tid];
 }
 
-// bf16 or fp32. OPS 2: s = act(a) * b; 1: the product itself.
-template <class T, int OPS>
+// bf16 or fp32. OPS 2: s = act(a) * b; 1: the product itself. G: sixteens of rows of B.
+template <class T, int OPS, int G>
 __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(FewArgs p) {
   typedef FewRun<T> Run;
-  __shared__ float red[kFewWaves][OPS][256];
+  constexpr int WAYS = OPS * G;  // operand OPS * g + o: the g-th sixteen of weight o
+  __shared__ float red[kFewWaves][WAYS][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
-  const int n0 = blockIdx.x * 16, q = lane >> 4;
+  const int n0 = blockIdx.x * p.per, n1 = min(n0 + p.per, p.n), q = lane >> 4;
   const T* xr = static_cast<const T*>(p.a) + (int64_t)min(lane & 15, p.m - 1) * p.lda;
-  const T* wr[OPS];
+  const T* wr[WAYS];
 #pragma unroll
-  for (int o = 0; o < OPS; ++o) wr[o] = static_cast<const T*>(p.b[o]) + (int64_t)min(n0 + (lane & 15), p.n - 1) * p.ldb;
-  f32x4 acc[OPS];
+  for (int o = 0; o < WAYS; ++o)
+    wr[o] = static_cast<const T*>(p.b[o % OPS]) + (int64_t)min(n0 + o / OPS * 16 + (lane & 15), n1 - 1) * p.ldb;
+  f32x4 acc[WAYS];
 #pragma unroll
-  for (int o = 0; o < OPS; ++o) acc[o] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int STEPS = kFewSteps<sizeof(T)>, KB = 32 * STEPS;
+  for (int o = 0; o < WAYS; ++o) acc[o] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int STEPS = kFewSteps<sizeof(T), WAYS>, KB = 32 * STEPS;
   const int blocks = p.k / KB;
   struct Block {
-    Run x[STEPS], w[OPS][STEPS];
+    Run x[STEPS], w[WAYS][STEPS];
   };
   auto load = [&](Block& b, int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       const int64_t k = (int64_t)i * KB + 32 * s + 8 * q;
 #pragma unroll
-      for (int o = 0; o < OPS; ++o) b.w[o][s].load(wr[o] + k);
+      for (int o = 0; o < WAYS; ++o) b.w[o][s].load(wr[o] + k);
       b.x[s].load(xr + k);
     }
   };
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(FewArgs p) {
       bf16x8 x[Run::PARTS], w[Run::PARTS];
       b.x[s].operands(x);
 #pragma unroll
-      for (int o = 0; o < OPS; ++o) {
+      for (int o = 0; o < WAYS; ++o) {
         b.w[o][s].operands(w);
         acc[o] = few_mfma<Run::PARTS>(w, x, acc[o]);
       }
@@ -158,46 +165,57 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(FewArgs p) {
   if (blocks * KB < p.k && wave == blocks % waves) {  // what is left of K
 #pragma unroll 1
     for (int k = blocks * KB + 8 * q; k < (p.k + 31) / 32 * 32; k += 32) {
-      Run x, w[OPS];
+      Run x, w[WAYS];
       x.load_tail(xr + min(k, p.k - 1), p.k - k);
       bf16x8 xo[Run::PARTS], wo[Run::PARTS];
       x.operands(xo);
 #pragma unroll
-      for (int o = 0; o < OPS; ++o) {
+      for (int o = 0; o < WAYS; ++o) {
         w[o].load_tail(wr[o] + min(k, p.k - 1), p.k - k);
         w[o].operands(wo);
         acc[o] = few_mfma<Run::PARTS>(wo, xo, acc[o]);
       }
     }
   }
-  float v[OPS];
-  few_join<OPS>(red, acc, v);
-  const int row = tid >> 4, col = n0 + (tid & 15);
-  if (tid >= 256 || row >= p.m || col >= p.n) return;
-  float y = v[0];
-  if constexpr (OPS == 2) y = activation(v[0], p.act) * v[1];
-  T* out = static_cast<T*>(p.out) + (int64_t)row * p.ldo + col;
-  if (p.beta != 0.f) y += p.beta * Elem<T>::load(static_cast<const T*>(p.c) + (int64_t)row * p.ldc + col);
-  Elem<T>::store(out, y);
+  float v[WAYS];
+  few_join<WAYS>(red, acc, v);
+  const int row = tid >> 4;
+  if (tid >= 256 || row >= p.m) return;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int col = n0 + 16 * g + (tid & 15);
+    if (col >= n1) return;
+    float y = v[OPS * g];
+    if constexpr (OPS == 2) y = activation(y, p.act) * v[OPS * g + 1];
+    Elem<T>::store(static_cast<T*>(p.out) + (int64_t)row * p.ldo + col, y);
+  }
 }
 
-// e4m3 operands with scales, results in bf16. A step is the 8-bit MFMA's 128 of K; a lane's operand is bytes 16 q .. and 64 + 16 q .. of a step, its scale that
-// of bytes 32 q ...
+// e4m3 operands with scales, results in bf16. A step is the 8-bit MFMA's 128 of K; a
+// lane's operand is bytes 16 q .. and 64 + 16 q .. of a step, its scale that of bytes
+// 32 q ...
+template <int G>
 __global__ void __launch_bounds__(64 * kFewWaves) few8_kernel(FewArgs p) {
-  __shared__ float red[kFewWaves][1][256];
+  __shared__ float red[kFewWaves][G][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
-  const int n0 = blockIdx.x * 16, q = lane >> 4;
+  const int n0 = blockIdx.x * p.per, n1 = min(n0 + p.per, p.n), q = lane >> 4;
   const int row = min(lane & 15, p.m - 1);
-  const uint8_t* xr = static_cast<const uint8_t*>(p.a) + (int64_t)row * p.lda;
+  const uint8_t* xr = static_cast<const uint8_t*>(p.a) + (int64_t)row * p.lda + 16 * q;
   const uint8_t* xe = p.ea + (int64_t)row * p.lde;
-  const uint8_t* wr = static_cast<const uint8_t*>(p.b[0]) + (int64_t)min(n0 + (lane & 15), p.n - 1) * p.ldb;
-  const uint8_t* we = p.eb + n0 / kBlock * p.ldeb_n;
-  f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-  constexpr int STEPS = kFewSteps<1>, KB = kBlock * STEPS;
+  const uint8_t *wr[G], *we[G];
+  f32x4 acc[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int n = min(n0 + 16 * g + (lane & 15), n1 - 1);
+    wr[g] = static_cast<const uint8_t*>(p.b[0]) + (int64_t)n * p.ldb + 16 * q;
+    we[g] = p.eb + n / kBlock * p.ldeb_n;
+    acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  constexpr int STEPS = kFewSteps<1, G>, KB = kBlock * STEPS;
   const int blocks = p.k / KB, groups = (p.k + kGroup - 1) / kGroup;
   struct Block {
-    u32x4 x[STEPS][2], w[STEPS][2];
-    uint32_t ex[STEPS], ew[STEPS];
+    u32x4 x[STEPS][2], w[G][STEPS][2];
+    uint32_t ex[STEPS], ew[G][STEPS];
   };
   auto load = [&](Block& b, int i) __attribute__((always_inline)) {
 #pragma unroll
@@ -205,11 +223,13 @@ __global__ void __launch_bounds__(64 * kFewWaves) few8_kernel(FewArgs p) {
       const int64_t k = (int64_t)i * KB + kBlock * s;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        b.w[s][h] = gload16(wr + k + 64 * h + 16 * q);
-        b.x[s][h] = gload16(xr + k + 64 * h + 16 * q);
+#pragma unroll
+        for (int g = 0; g < G; ++g) b.w[g][s][h] = gload16(wr[g] + k + 64 * h);
+        b.x[s][h] = gload16(xr + k + 64 * h);
       }
       b.ex[s] = *((const g_u8*)(xe + k / kGroup + q));
-      b.ew[s] = *((const g_u8*)(we + k / kBlock * p.ldeb_k));
+#pragma unroll
+      for (int g = 0; g < G; ++g) b.ew[g][s] = *((const g_u8*)(we[g] + k / kBlock * p.ldeb_k));
     }
   };
   auto join = [&](const u32x4 v[2]) __attribute__((always_inline)) {
@@ -218,7 +238,10 @@ __global__ void __launch_bounds__(64 * kFewWaves) few8_kernel(FewArgs p) {
   auto sum = [&](const Block& b) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
-      acc[0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(b.w[s]), join(b.x[s]), acc[0], 0, 0, 0, (int)b.ew[s], 0, (int)b.ex[s]);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(b.w[g][s]), join(b.x[s]), acc[g], 0, 0, 0, (int)b.ew[g][s],
+                                                                  0, (int)b.ex[s]);
   };
   int i = wave;
   Block b0, b1;
@@ -234,8 +257,8 @@ __global__ void __launch_bounds__(64 * kFewWaves) few8_kernel(FewArgs p) {
     // What is left of K, 128 at a time: rows are readable up to a multiple of 16, and
     // what is behind K becomes 0 in both operands, with a scale of 1.
     const int padded = (p.k + 15) / 16 * 16;
-    auto half = [&](const uint8_t* r, int k) __attribute__((always_inline)) {
-      u32x4 v = gload16(r + min(k, padded - 16));
+    auto half = [&](const uint8_t* r, int k) __attribute__((always_inline)) {  // r is 16 q on
+      u32x4 v = gload16(r + (min(k, padded - 16) - 16 * q));
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const int b = p.k - k - 4 * w;
@@ -245,39 +268,58 @@ __global__ void __launch_bounds__(64 * kFewWaves) few8_kernel(FewArgs p) {
     };
 #pragma unroll 1
     for (int k = blocks * KB; k < p.k; k += kBlock) {
-      const u32x4 w[2] = {half(wr, k + 16 * q), half(wr, k + 64 + 16 * q)}, x[2] = {half(xr, k + 16 * q), half(xr, k + 64 + 16 * q)};
-      const int g = k / kGroup + q;
-      const uint32_t ex = g < groups ? (uint32_t)*((const g_u8*)(xe + g)) : 127u;
-      const uint32_t ew = *((const g_u8*)(we + k / kBlock * p.ldeb_k));
-      acc[0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w), join(x), acc[0], 0, 0, 0, (int)ew, 0, (int)ex);
+      const u32x4 x[2] = {half(xr, k + 16 * q), half(xr, k + 64 + 16 * q)};
+      const int at = k / kGroup + q;
+      const uint32_t ex = at < groups ? (uint32_t)*((const g_u8*)(xe + at)) : 127u;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const u32x4 w[2] = {half(wr[g], k + 16 * q), half(wr[g], k + 64 + 16 * q)};
+        const uint32_t ew = *((const g_u8*)(we[g] + k / kBlock * p.ldeb_k));
+        acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w), join(x), acc[g], 0, 0, 0, (int)ew, 0, (int)ex);
+      }
     }
   }
-  float v[1];
-  few_join<1>(red, acc, v);
-  const int m = tid >> 4, col = n0 + (tid & 15);
-  if (tid >= 256 || m >= p.m || col >= p.n) return;
-  if (p.beta != 0.f) v[0] += p.beta * Elem<u16>::load(static_cast<const u16*>(p.c) + (int64_t)m * p.ldc + col);
-  Elem<u16>::store(static_cast<u16*>(p.out) + (int64_t)m * p.ldo + col, v[0]);
+  float v[G];
+  few_join<G>(red, acc, v);
+  const int m = tid >> 4;
+  if (tid >= 256 || m >= p.m) return;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int col = n0 + 16 * g + (tid & 15);
+    if (col >= n1) return;
+    if (p.beta != 0.f) v[g] += p.beta * Elem<u16>::load(static_cast<const u16*>(p.c) + (int64_t)m * p.ldc + col);
+    Elem<u16>::store(static_cast<u16*>(p.out) + (int64_t)m * p.ldo + col, v[g]);
+  }
 }
 
-// Workgroups of 16 waves where there are fewer than CUs, else of 8 (two projections of
-// 6144 x 2048: 12.1 us, with 16 waves 13.9; one of 2048 x 6144 8.6 with 16).
-static dim3 few_block(const FewArgs& a) { return dim3(64 * ((a.n + 15) / 16 < 256 ? kFewWaves : kFewWaves / 2)); }
+// Waves: 16 where every CU gets one workgroup, else 8.
+struct FewGrid {
+  dim3 grid, block;
+};
+static FewGrid few_grid(FewArgs& a, int most) {
+  const FewShare f = few_share(a.n, most);
+  a.per = (int)f.per;
+  return {dim3((uint32_t)((a.n + f.per - 1) / f.per)), dim3(64 * (f.rounds == 1 ? kFewWaves : kFewWaves / 2))};
+}
 
-hipError_t launch_few(const FewArgs& a, bool f32, int ops, hipStream_t s) {
-  const dim3 grid((uint32_t)((a.n + 15) / 16)), block = few_block(a);
-  if (ops == 2) {
-    if (f32) hipLaunchKernelGGL((few_kernel<float, 2>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((few_kernel<u16, 2>), grid, block, 0, s, a);
-  } else {
-    if (f32) hipLaunchKernelGGL((few_kernel<float, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((few_kernel<u16, 1>), grid, block, 0, s, a);
-  }
+template <class T, int OPS>
+static hipError_t launch_few_of(FewArgs a, hipStream_t s) {
+  const FewGrid g = few_grid(a, sizeof(T) == 2 ? kFewMost : kFewMostF32);
+  if (a.per <= 16) hipLaunchKernelGGL((few_kernel<T, OPS, 1>), g.grid, g.block, 0, s, a);
+  else if constexpr (sizeof(T) == 2) hipLaunchKernelGGL((few_kernel<T, OPS, 2>), g.grid, g.block, 0, s, a);
   return hipGetLastError();
 }
 
-hipError_t launch_few8(const FewArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(few8_kernel, dim3((uint32_t)((a.n + 15) / 16)), few_block(a), 0, s, a);
+hipError_t launch_few(const FewArgs& a, bool f32, int ops, hipStream_t s) {
+  if (ops == 2) return f32 ? launch_few_of<float, 2>(a, s) : launch_few_of<u16, 2>(a, s);
+  return f32 ? launch_few_of<float, 1>(a, s) : launch_few_of<u16, 1>(a, s);
+}
+
+hipError_t launch_few8(const FewArgs& args, hipStream_t s) {
+  FewArgs a = args;
+  const FewGrid g = few_grid(a, kFewMost);
+  if (a.per <= 16) hipLaunchKernelGGL(few8_kernel<1>, g.grid, g.block, 0, s, a);
+  else hipLaunchKernelGGL(few8_kernel<2>, g.grid, g.block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -24,15 +24,15 @@ constexpr int64_t kCus = 256;
 constexpr double kHbm = 5.2e6;  // bytes per us: what streaming the weights of few rows reaches
 
 // What few_kernels.hip is expected to take for weights of n rows (of each of `ops`)
-// of `row` bytes: workgroups of 16 rows, one after the other on a CU. A CU gets 21 KB a
-// us while all have work, and 36 when few have. One MI355X, one row: 5120 x 25600 bf16
-// 67.7 us (estimated 65), 2048 x 6144 8.5 (8.5), two of 25600 x 5120 97.4 (105); the
-// activations cost up to 40% more at 16 rows (94, 12.8, 115.5).
+// of `row` bytes: every CU streams its share of them at 23.5 KB a us, and reads the
+// activations once for every share. One MI355X, bf16, 1 and 16 rows: both projections
+// of 25600 x 5120 89.0 and 104 us (estimated 89 and 98; in tiles 109 and 113), of 6144
+// x 2048 10.8 and 11.3 (10.4 and 11.2); one of 5120 x 25600 47.8 and 59.6 (45 and 57;
+// in tiles 56 and 57), of 2048 x 6144 7.1 and 11.0 (6.2 and 8.9; in tiles 13.6).
 double few_us(int64_t n, double row, int ops, int64_t rows) {
-  const int64_t groups = ceil_div(n, 16), full = groups / kCus;
-  const double unit = 16.0 * row * ops;
-  const double us = double(full) * unit / 21e3 + (groups % kCus ? unit / 36e3 : 0.0);
-  return 3.0 + us * (1.0 + 0.4 / ops * double(rows - 1) / 15.0);
+  const muon::FewShare f = muon::few_share(n, muon::kFewMost);
+  const double weights = double(f.per * ops);
+  return 2.0 + double(f.rounds) * weights * row / 23.5e3 * (1.0 + 0.35 * double(rows - 1) / weights);
 }
 
 // How a launch is cut up: the tiles, how many of them are one unit each, how many

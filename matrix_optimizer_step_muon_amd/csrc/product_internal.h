@@ -84,8 +84,20 @@ struct FewArgs {
   const void* c;
   int64_t ldo, ldc;
   float beta;
-  int32_t reserved;
+  int32_t per;               // rows of b per workgroup (set by the launch)
 };
+
+// Rows of b per workgroup: the same share for each of 256 CUs, in as many rounds as it
+// takes with at most `most`; at least 8, since lanes without a row of their own read
+// another's once more.
+struct FewShare {
+  int64_t per, rounds;
+};
+inline FewShare few_share(int64_t n, int64_t most) {
+  const int64_t cus = 256, rounds = (n + cus * most - 1) / (cus * most), per = (n + cus * rounds - 1) / (cus * rounds);
+  return {per < 8 ? 8 : per, rounds};
+}
+constexpr int kFewMost = 32, kFewMostF32 = 16;  // fp32's three parts need the registers
 
 static_assert(sizeof(PrArgs) <= 4000, "kernel arguments");
 
