@@ -242,10 +242,10 @@ static hipError_t launch_tiles(const PrArgs& args, hipStream_t s) {
   return hipGetLastError();
 }
 
-// A thread takes octets of columns of one operand, 256 workgroups' worth apart. One
-// launch for all operands of a call. Bound by memory: 4 and 6 bytes per fp32 element,
-// 12.6 M of them in 22 us (5.7 TB/s).
-constexpr int kPackOctets = 8;  // per thread
+// A thread takes octets of columns of one operand, all workgroups' worth apart: one
+// while there are few, then up to 8. One launch for all operands of a call. Bound by
+// memory: 4 and 6 bytes per fp32 element, 12.6 M of them in 22 us (5.7 TB/s).
+constexpr int kPackOctets = 8, kPackFew = 1024;  // per thread; workgroups
 
 template <class T, int PARTS>
 __global__ void __launch_bounds__(256) pack_kernel(PrPacks args) {
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(256) pack_kernel(PrPacks args) {
   const int64_t count = p.octets * p.rows, blocks = (i + 1 < args.n ? args.pack[i + 1].first : args.blocks) - p.first;
   const T* src = static_cast<const T*>(p.src);
   for (int64_t at = (int64_t)((int)blockIdx.x - p.first) * 256 + threadIdx.x; at < count; at += blocks * 256) {
-    const int64_t row = at / p.octets, col = (at - row * p.octets) * 8;
+    const int64_t row = count <= INT32_MAX ? (uint32_t)at / (uint32_t)p.octets : at / p.octets, col = (at - row * p.octets) * 8;
     float v[8];
     load_run(src + row * p.ld + col, p.cols - (int)col, v);
     u16* to = static_cast<u16*>(p.dst) + at * 8;
@@ -278,9 +278,9 @@ hipError_t launch_packs(const PrPacks& args, bool f32, hipStream_t s) {
   PrPacks a = args;
   a.blocks = 0;
   for (int i = 0; i < a.n; ++i) {
-    const int64_t want = (a.pack[i].octets * a.pack[i].rows + 256 * kPackOctets - 1) / (256 * kPackOctets);
+    const int64_t each = (a.pack[i].octets * a.pack[i].rows + 255) / 256, want = (each + kPackOctets - 1) / kPackOctets;
     a.pack[i].first = a.blocks;
-    a.blocks += (int)(want < 1 ? 1 : want < 8192 ? want : 8192);
+    a.blocks += (int)(each < kPackFew ? each : want < kPackFew ? kPackFew : want < 8192 ? want : 8192);
   }
   if (f32) hipLaunchKernelGGL((pack_kernel<float, 3>), dim3(a.blocks), dim3(256), 0, s, a);
   else hipLaunchKernelGGL((pack_kernel<u16, 1>), dim3(a.blocks), dim3(256), 0, s, a);
