@@ -101,9 +101,9 @@ MUON_INLINE int pr_item(P first, int unit) {
 // Tile (tm, tn) of local tile number t: bands of 4 tile rows walked column by
 // column, so 32 consecutive tiles cover 4 x 8.
 MUON_INLINE void pr_tile(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int band = t / (4 * tiles_n), r = t - band * 4 * tiles_n;
+  const int band = (uint32_t)t / (uint32_t)(4 * tiles_n), r = t - band * 4 * tiles_n;
   const int h = min(4, tiles_m - 4 * band);
-  tn = r / h;
+  tn = (uint32_t)r / (uint32_t)h;
   tm = 4 * band + (r - tn * h);
 }
 
@@ -122,24 +122,25 @@ MUON_INLINE PrUnit pr_unit(PrArgsPtr args, bool whole, int unit) {
   PrUnit u;
   u.idx = whole ? pr_item(args->whole0, unit) : pr_item(args->piece0, unit);
   PrItemRef it = args->item[u.idx];
-  int tile, split = 0, splits = 1;
+  int tile;
   if (whole) {
     u.piece = -1;
     tile = unit - args->whole0[u.idx];
+    u.begin = 0;
+    u.total = it.stages;
   } else {
-    const int rest = it.tiles_m * it.tiles_n - it.whole;
+    // the first of a tile's pieces are one stage longer, where the stages do not divide
+    const int rest = it.tiles_m * it.tiles_n - it.whole, more = it.stages - it.per * it.splits;
     u.piece = unit - args->piece0[u.idx];
-    splits = it.splits;
-    split = u.piece / rest;
+    const int split = (uint32_t)u.piece / (uint32_t)rest;
     tile = it.whole + u.piece - split * rest;
+    u.begin = split * it.per + min(split, more);
+    u.total = it.per + (split < more);
   }
   int tm, tn;
   pr_tile(tile, it.tiles_m, it.tiles_n, tm, tn);
   u.m0 = tm * Z::BM;
   u.n0 = tn * Z::BN;
-  const int all = (it.k + Z::BK - 1) / Z::BK * it.sums * (args->parts == 3 ? 6 : 1);
-  u.begin = (int)((int64_t)all * split / splits);
-  u.total = (int)((int64_t)all * (split + 1) / splits) - u.begin;
   return u;
 }
 
@@ -501,7 +502,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     lda = it.lda;
     ldb = it.ldb;
     lkt = (lk + Z::BK - 1) / Z::BK;
-    lseg = u.begin / lkt;
+    lseg = (uint32_t)u.begin / (uint32_t)lkt;
     lks = u.begin - lseg * lkt;
     lleft = u.total;
     const int rows_a = it.m - lm0, cols_b = DUAL ? it.n - (ln0 >> 1) : it.n - ln0;
@@ -748,7 +749,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     PrItemRef it = args->item[u.idx];
     k = it.k;
     kt = (k + Z::BK - 1) / Z::BK;
-    ks = u.begin % kt;
+    ks = (uint32_t)u.begin % (uint32_t)kt;
     tab = (tab + 1) & (Z::TABS - 1);
 #pragma unroll
     for (int i = 0; i < FM; ++i)

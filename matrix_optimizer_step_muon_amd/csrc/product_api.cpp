@@ -126,6 +126,8 @@ muon_status lay_out(muon::PrArgs& a, bool dual, int elem, const Cost& cost, size
     it.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(c.splits, mine / 2)));
     const int64_t whole = it.splits == 1 ? tm * tn : std::min(tm * tn, std::max<int64_t>(0, c.whole - wholes));
     it.whole = int32_t(whole);
+    it.stages = int32_t(mine);
+    it.per = int32_t(mine / it.splits);
     a.whole0[i] = int32_t(wholes);
     a.piece0[i] = it.part0 = int32_t(pieces);
     wholes += whole;

@@ -41,6 +41,7 @@ struct PrItem {
   int32_t whole;             // the first tiles are one unit each,
   int32_t splits;            // the others as many pieces of the sum, whose partial tiles go to the workspace
   int32_t part0;             // first partial tile of this item in the workspace
+  int32_t stages, per;       // of a tile's sum, and of each of its pieces (some have one more)
   // kPrStore
   void* out;
   const void* c;
