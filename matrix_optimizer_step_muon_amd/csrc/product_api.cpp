@@ -26,13 +26,13 @@ constexpr double kHbm = 5.2e6;  // bytes per us: what streaming the weights of f
 // What few_kernels.hip is expected to take for weights of n rows (of each of `ops`)
 // of `row` bytes: every CU streams its share of them at 23.5 KB a us, and reads the
 // activations once for every share. One MI355X, bf16, 1 and 16 rows: both projections
-// of 25600 x 5120 89.0 and 104 us (estimated 89 and 98; in tiles 109 and 113), of 6144
-// x 2048 10.8 and 11.3 (10.4 and 11.2); one of 5120 x 25600 47.8 and 59.6 (45 and 57;
-// in tiles 56 and 57), of 2048 x 6144 7.1 and 11.0 (6.2 and 8.9; in tiles 13.6).
+// of 25600 x 5120 89 and 104 us (estimated 89 and 102; in tiles 109 and 113), of 6144 x
+// 2048 10.8 and 11.3 (10.4 and 11.7); one of 5120 x 25600 48 and 60 to 65 (46 and 62; in
+// tiles 56 and 57), of 2048 x 6144 7.1 and 11.0 (6.2 and 10.1; in tiles 13.6).
 double few_us(int64_t n, double row, int ops, int64_t rows) {
   const muon::FewShare f = muon::few_share(n, muon::kFewMost);
   const double weights = double(f.per * ops);
-  return 2.0 + double(f.rounds) * weights * row / 23.5e3 * (1.0 + 0.35 * double(rows - 1) / weights);
+  return 2.0 + double(f.rounds) * weights * row / 23.5e3 * (1.0 + 0.5 * double(rows - 1) / weights);
 }
 
 // How a launch is cut up: the tiles, how many of them are one unit each, how many

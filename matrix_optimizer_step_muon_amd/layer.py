@@ -18,9 +18,10 @@ step reads.
     layer.Linear8([(x8, w8, y)]).run()      # y = x W^T
     layer.Linear8([(dy8, w8, dx)], transposed=True).run()   # dx = dy W
 
-Like the optimizer's plans, ``NormSite``, ``GatedMLP``, ``Linear8`` and ``WGrad`` take their tensors once
-and keep them referenced; every call after that only launches kernels, on the
-current stream or the one it is given (a torch stream or a raw handle). They may
+Like the optimizer's plans, ``NormSite``, ``GatedMLP``, ``Linear8`` and ``WGrad``
+take their tensors once and keep them referenced; every call after that only
+launches kernels, on the current stream or the one it is given (a torch stream or
+a raw handle). They may
 be dropped while a stream still works on their buffers. Each has one set of
 buffers: calls on two streams need an order between them, as any two writers of
 a tensor do. Tensors are 2-D (weights 1-D) device tensors with unit column
@@ -75,6 +76,12 @@ def _matrix(t, name: str, shape=None, dtype=None, vector=False):
     if dtype is not None and t.dtype != dtype:
         _bad(f"{name} must be {dtype}, not {t.dtype}")
     return t
+
+
+def _same_device(index: int) -> None:
+    """Calls of an object that was made on one device, from another."""
+    if torch.cuda.current_device() != index:
+        _bad(f"the current device is not cuda:{index}, on which the object was made")
 
 
 def _ld(t) -> int:
@@ -388,8 +395,11 @@ class GatedMLP:
         elif kind is not None:
             self.a, self.b, self.s = (Q8(rows, inner, kind) for _ in range(3))
         for q, name in ((self.a, "a"), (self.b, "b"), (self.s, "s")):
-            if q is not None and (q.rows, q.cols) != (rows, inner):
-                _bad(f"{name} must be a checkpoint of {rows} x {inner}")
+            if q is not None:
+                if (q.rows, q.cols) != (rows, inner):
+                    _bad(f"{name} must be a checkpoint of {rows} x {inner}")
+                _matrix(q.q, name)
+        self._device = torch.cuda.current_device()
         kept = [q for q in (self.a, self.b, self.s) if q is not None]
         self._grads = None
         if self.a is not None and self.b is not None:
@@ -407,11 +417,13 @@ class GatedMLP:
                                   if t is not None] + [t for q in kept for t in (q.q, q.e)])
 
     def forward(self, stream=None) -> None:
+        _same_device(self._device)
         check(lib().muon_mlp_forward(ctypes.byref(self._c), self._streams.use(stream)))
 
     def backward(self, dy, stream=None) -> None:
         if self._grads is None:
             _bad("the block keeps no checkpoints: make it with a kind")
+        _same_device(self._device)
         _matrix(dy, "dy", tuple(self.y.shape), self.y.dtype)
         g = self._grads
         g.dy, g.ld_dy = dy.data_ptr(), _ld(dy)
@@ -454,7 +466,7 @@ class W8:
 
 def w8_save(w, out: W8, stream=None) -> W8:
     """Saves w (bf16 or fp32) into ``out``, in both orientations."""
-    _matrix(w, "w", (out.n, out.k))
+    _matrix(w, "w", (out.n, out.k)), _matrix(out.q, "out")
     check(lib().muon_w8_save(w.data_ptr(), _ld(w), _code(w), ctypes.byref(out._c), out._streams.use(stream, (w,))))
     return out
 
@@ -462,7 +474,7 @@ def w8_save(w, out: W8, stream=None) -> W8:
 def w8_load(w8: W8, out, stream=None):
     """Writes the values that the weight stands for into ``out`` (bf16, which holds
     them exactly, or fp32)."""
-    _matrix(out, "out", (w8.n, w8.k))
+    _matrix(out, "out", (w8.n, w8.k)), _matrix(w8.q, "w8")
     check(lib().muon_w8_load(ctypes.byref(w8._c), out.data_ptr(), _ld(out), _code(out), w8._streams.use(stream, (out,))))
     return out
 
@@ -485,6 +497,7 @@ class Linear8:
             beta, C = (list(item[3:]) + [0.0, None][len(item) - 3:])[:2]
             if not isinstance(x, Q8) or not isinstance(w, W8):
                 _bad("an item starts with a Q8 checkpoint and a W8 weight")
+            _matrix(x.q, "x"), _matrix(w.q, "w")
             if dt is None:
                 self._dtype, dt = _code(y), y.dtype
             shape = (x.rows, w.k if transposed else w.n)
@@ -502,7 +515,9 @@ class Linear8:
         check(lib().muon_linear8_workspace(self._items, self._n, self._dtype, ctypes.byref(need)))
         self.workspace = torch.empty(need.value, dtype=torch.uint8, device=tensors[0].device)
         self._args = (self._items, self._n, self._dtype, self.workspace.data_ptr(), need.value)
+        self._device = torch.cuda.current_device()
         self._streams = _Streams(tensors + [self.workspace])
 
     def run(self, stream=None) -> None:
+        _same_device(self._device)
         check(lib().muon_linear8(*self._args, self._streams.use(stream)))

@@ -71,3 +71,33 @@ def test_a_named_stream_is_recorded_on_the_calls_own_tensors(on_cpu):
     assert dy.data_ptr() in on_cpu.on(5)
     layer.w8_save(x, w, Stream(6))
     assert on_cpu.on(6) == {t.data_ptr() for t in w.tensors()} | {x.data_ptr()}
+
+
+def test_another_current_device_is_refused(on_cpu, monkeypatch):
+    (m, _), (p, _, _) = mlp(), linear(on_cpu)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (m.forward, p.run):
+        with pytest.raises(layer.MuonError, match="cuda:0"):
+            call()
+    assert not on_cpu.launched
+    monkeypatch.undo()
+
+
+def test_checkpoints_and_weights_elsewhere_are_refused(on_cpu, monkeypatch):
+    """What holds no device tensors of the current device."""
+    def matrix(t, name, *a, **k):
+        if t.data_ptr() in away:
+            raise layer.MuonError(-1, f"{name} is elsewhere")
+        return t
+    x = q8(40, 64)
+    x8 = layer.Q8(40, 64, "e4m3", q=x.q, e=x.e)
+    w, y = layer.W8(96, 64), torch.zeros(40, 96)
+    a, b = q8(40, 96), q8(40, 96)
+    t = [torch.zeros(40, 64), torch.zeros(96, 64), torch.zeros(96, 64), torch.zeros(64, 96)]
+    monkeypatch.setattr(layer, "_matrix", matrix)
+    for bad, call in ((x.q, lambda: layer.Linear8([(x8, w, y)])), (w.q, lambda: layer.Linear8([(x8, w, y)])),
+                      (b.q, lambda: layer.GatedMLP(*t, saved=(a, b))), (w.q, lambda: layer.w8_save(t[1], w)),
+                      (w.q, lambda: layer.w8_load(w, t[1]))):
+        away = {bad.data_ptr()}
+        with pytest.raises(layer.MuonError, match="elsewhere"):
+            call()
