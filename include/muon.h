@@ -519,7 +519,9 @@ muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32
 
 /* The gated feed-forward block of a layer,
  *   a = x Wgate^T,  b = x Wup^T,  s = act(a) * b,  y = s Wdown^T,
- * in two launches: both projections, the activation and the product are one.
+ * in two launches: both projections, the activation and the product are one. (fp32
+ * operands, and bf16 ones that are not 16-byte aligned, are rewritten by a launch
+ * before; where there are few tiles, a launch after joins the pieces of their sums.)
  * dtype is that of x, y and the weights. Sums are fp32; s is rounded to dtype
  * once, as the operand of the last product, y once. bf16: bf16 MFMA. fp32: every
  * operand is cut into three bf16 numbers that add up to it (24 bits, of numbers

@@ -8,6 +8,11 @@
 // epilogue; the down projection; ds, whose epilogue makes da and db; and dx, one sum
 // over both pairs. The weights are read as they lie: forward along their rows,
 // backward with transposing LDS reads.
+//
+// 4096 x 2048 x 6144 bf16, silu, int8 checkpoints: 212, 96 + 14, 146 and 178 + 14 us (974,
+// 940, 708 and 1074 TFLOP/s), the second terms joining pieces. The epilogues of the first
+// and the third are vector instructions: 17 of 70 us of a 256 x 256 tile, with the
+// matrix units idle; at 5120 x 25600 they weigh 40% of that (1054 and 1020 TFLOP/s).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

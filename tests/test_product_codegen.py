@@ -16,7 +16,7 @@ HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 FILES = ("mlp_kernels", "linear8_kernels", "few_kernels")
 # The largest one is fp32 in few rows with two weights: its two blocks of loads and
 # their three bf16 parts need a few registers more than 16 waves leave.
-SPILLS = {"few_kernelIfLi2EE": 128}
+SPILLS = {"few_kernelIfLi2E": 128}
 
 
 @pytest.fixture(scope="module")
