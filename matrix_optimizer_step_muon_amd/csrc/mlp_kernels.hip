@@ -11,8 +11,10 @@
 //
 // 4096 x 2048 x 6144 bf16, silu, int8 checkpoints: 212, 96 + 14, 146 and 178 + 14 us (974,
 // 940, 708 and 1074 TFLOP/s), the second terms joining pieces. The epilogues of the first
-// and the third are vector instructions: 17 of 70 us of a 256 x 256 tile, with the
-// matrix units idle; at 5120 x 25600 they weigh 40% of that (1054 and 1020 TFLOP/s).
+// and the third are 17 and 22 of 70 us of a 256 x 256 tile, with the matrix units idle:
+// all CUs come to them together and move 43 and 84 MB a round (2.7 and 4.2 TB/s; more
+// of a thread's runs at once gained nothing). At 5120 x 25600 the products reach 1054
+// and 1020 TFLOP/s.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
