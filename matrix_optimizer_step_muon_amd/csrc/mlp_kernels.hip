@@ -43,12 +43,15 @@ struct Saved {
     first = (col & (kGroup - 1)) == 0;
   }
   // Columns of a group are four lanes. Padding columns (up to a multiple of 16) get 0.
+  // Nontemporal: the next launch reads s as its operand, the backward pass these (a
+  // training step of 4096 x 2048 x 6144 1008 -> 1000 us; da and db, which are read at
+  // once, 1004 with them too).
   template <class V>
   MUON_INLINE void save(int row, int dc, bool there, const float v[8]) const {
     u32x2 w;
     const uint32_t E = q8_encode(v, V::FULL ? V::B : kind, w);
     uint8_t *pq = q + (int64_t)row * ldq + dc, *pe = e + (int64_t)row * lde + dc / kGroup;
-    if (V::FULL || (there && col + dc < cols16)) *((g_u32x2*)(pq + off)) = w;
+    if (V::FULL || (there && col + dc < cols16)) __builtin_nontemporal_store(w, (g_u32x2*)(pq + off));
     if (first && (V::FULL || (there && col + dc < cols))) *((g_u8*)(pe + offe)) = (uint8_t)E;
   }
   MUON_INLINE void load(int row, int dc, u32x2& w, uint32_t& E) const {
