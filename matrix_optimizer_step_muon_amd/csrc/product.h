@@ -194,6 +194,15 @@ MUON_INLINE void store_run(T* p, int live, const float v[8]) {
   }
 }
 
+// The same for eight bf16 of an output that no tile reads again: past the caches, which
+// leaves them to the operands (8-bit products of 8192 x 25600 x 5120, 4096 x 6144 x 2048 and
+// 1024 x 8192 x 5120, both ways, with what saves their inputs: 2196 -> 2133, 158 -> 151 and
+// 161 -> 156 us; the gated block +-0.5%).
+MUON_INLINE void stream_run(void* p, const float v[8]) {
+  __builtin_nontemporal_store(
+      u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])}, (g_u32x4_any*)p);
+}
+
 // How an epilogue takes a tile apart. A thread holds eight consecutive columns of one
 // row at a time: its row is `row` plus one that all threads share, its first column
 // col plus a shift that all share. The addresses are then a scalar and a 32-bit offset
@@ -297,7 +306,7 @@ struct PrStoreOut {
     if constexpr (V::FULL) {
       if constexpr (V::B != 0) add<V::A != 0>(p, v);
       if constexpr (V::A != 0) store_run(reinterpret_cast<float*>(to), 8, v);
-      else store_run(reinterpret_cast<u16*>(to), 8, v);
+      else stream_run(to, v);
     } else {
       if (row + at.row >= m || live <= dc) return;
       if (beta != 0.f) add<true>(p, v);
