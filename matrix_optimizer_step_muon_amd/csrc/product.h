@@ -194,10 +194,11 @@ MUON_INLINE void store_run(T* p, int live, const float v[8]) {
   }
 }
 
-// The same for eight bf16 of an output that no tile reads again: past the caches, which
-// leaves them to the operands (8-bit products of 8192 x 25600 x 5120, 4096 x 6144 x 2048 and
-// 1024 x 8192 x 5120, both ways, with what saves their inputs: 2196 -> 2133, 158 -> 151 and
-// 161 -> 156 us; the gated block +-0.5%).
+// The same for eight bf16 past the caches, which leaves them to the operands: for
+// outputs of more than the 32 MB that all L2s hold. 8-bit products both ways, inputs
+// saved before: 8192 x 25600 x 5120 2228 -> 2168 us, 4096 x 6144 x 2048 (one of two outputs)
+// 186.8 -> 183.6; with smaller outputs stored so too 1024 x 8192 x 5120 167.4 -> 169.8.
+constexpr int64_t kStreamFrom = int64_t(16) << 20;  // elements
 MUON_INLINE void stream_run(void* p, const float v[8]) {
   __builtin_nontemporal_store(
       u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])}, (g_u32x4_any*)p);
@@ -242,7 +243,7 @@ struct PrStoreOut {
   int64_t ldo, ldc;
   int m, live;
   float beta;
-  bool f32;
+  bool f32, stream;
   uint32_t off, offc;
   MUON_INLINE PrStoreOut(PrItemRef it, PrArgsPtr a, PrLane lane) : at(lane) {
     out = static_cast<char*>(pinned(it.out));
@@ -253,6 +254,7 @@ struct PrStoreOut {
     beta = pinned(it.beta);
     f32 = pinned(a->f32);
     live = it.n - at.col;
+    stream = (int64_t)m * it.n > kStreamFrom;
     const int shift = f32 ? 2 : 1;
     off = ((uint32_t)at.row * (uint32_t)ldo + (uint32_t)at.col) << shift;
     offc = ((uint32_t)at.row * (uint32_t)ldc + (uint32_t)at.col) << shift;
@@ -260,10 +262,11 @@ struct PrStoreOut {
     ldc <<= shift;
   }
   MUON_INLINE bool plain() const { return true; }
-  // Variants: A the type (1 fp32), B whether there is a c.
+  // Variants: A the type (1 fp32), B whether there is a c (1) and bf16 streams (2).
   template <class F>
   MUON_INLINE void dispatch(F f) const {
     if (f32) beta != 0.f ? f(PrVariant<true, 1, 1>{}) : f(PrVariant<true, 1, 0>{});
+    else if (stream) beta != 0.f ? f(PrVariant<true, 0, 3>{}) : f(PrVariant<true, 0, 2>{});
     else beta != 0.f ? f(PrVariant<true, 0, 1>{}) : f(PrVariant<true, 0, 0>{});
   }
   template <class V>
@@ -271,7 +274,7 @@ struct PrStoreOut {
     const char* at_c = c + (int64_t)row * ldc + ((int64_t)dc << (f32 ? 2 : 1)) + offc;
     if constexpr (V::FULL) {
       // before the variant is known, both halves of what an fp32 c would need, if there is a c
-      if (V::B > 0 || (V::B < 0 && beta != 0.f)) {
+      if (V::B < 0 ? beta != 0.f : V::B & 1) {
         const u32x4 lo = gload16_any(at_c), hi = V::A == 0 || (V::A < 0 && !f32) ? lo : gload16_any(at_c + 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -304,9 +307,10 @@ struct PrStoreOut {
   MUON_INLINE void emit(int row, int dc, float v[8], float*, const Pre& p) const {
     char* to = out + (int64_t)row * ldo + ((int64_t)dc << (f32 ? 2 : 1)) + off;
     if constexpr (V::FULL) {
-      if constexpr (V::B != 0) add<V::A != 0>(p, v);
+      if constexpr (V::B & 1) add<V::A != 0>(p, v);
       if constexpr (V::A != 0) store_run(reinterpret_cast<float*>(to), 8, v);
-      else stream_run(to, v);
+      else if constexpr (V::B & 2) stream_run(to, v);
+      else store_run(reinterpret_cast<u16*>(to), 8, v);
     } else {
       if (row + at.row >= m || live <= dc) return;
       if (beta != 0.f) add<true>(p, v);
