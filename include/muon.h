@@ -526,7 +526,8 @@ muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32
  * once, as the operand of the last product, y once. bf16: bf16 MFMA. fp32: every
  * operand is cut into three bf16 numbers that add up to it (24 bits, of numbers
  * below 2^-110 fewer), and the six products down to 2^-24 of the largest are
- * summed: fp32 accuracy at six times the work.
+ * summed: fp32 accuracy at six times the work. Infinities are what they are in an
+ * fp32 sum, but for products with numbers below 2^-62, which may be NaN.
  * x       rows x width
  * w_gate, w_up  inner x width, w_down  out x inner, contiguous (muon_matrix.w)
  * y       rows x out, written (NULL: only the checkpoints are wanted)

@@ -65,13 +65,10 @@ struct FewRun<float> {
     for (int i = 0; i < 8; ++i) v[i] = i < live ? Elem<float>::load(p + i) : 0.f;
   }
   MUON_INLINE void operands(bf16x8 o[3]) const {  // lo, mid, hi
-    float t[3][8];
+    u32x4 t[3];
+    cut3(v, t);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cut3(v[i], t[2][i], t[1][i], t[0][i]);
-#pragma unroll
-    for (int q = 0; q < 3; ++q)
-      o[q] = __builtin_bit_cast(bf16x8, (u32x4{pack_bf16x2(t[q][0], t[q][1]), pack_bf16x2(t[q][2], t[q][3]),
-                                               pack_bf16x2(t[q][4], t[q][5]), pack_bf16x2(t[q][6], t[q][7])}));
+    for (int q = 0; q < 3; ++q) o[q] = __builtin_bit_cast(bf16x8, t[q]);
   }
 };
 

@@ -79,13 +79,10 @@ struct Planes {
           u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
       return;
     }
-    float t[3][8];
+    u32x4 t[3];
+    cut3(v, t);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cut3(v[i], t[2][i], t[1][i], t[0][i]);
-#pragma unroll
-    for (int q = 0; q < 3; ++q)
-      *((g_u32x4*)(base + q * plane + off)) =
-          u32x4{pack_bf16x2(t[q][0], t[q][1]), pack_bf16x2(t[q][2], t[q][3]), pack_bf16x2(t[q][4], t[q][5]), pack_bf16x2(t[q][6], t[q][7])};
+    for (int q = 0; q < 3; ++q) *((g_u32x4*)(base + q * plane + off)) = t[q];
   }
 };
 
@@ -272,13 +269,10 @@ __global__ void __launch_bounds__(256) pack_kernel(PrPacks args) {
     if constexpr (PARTS == 1) {
       *((g_u32x4*)to) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
     } else {
-      float t[3][8];
+      u32x4 t[3];
+      cut3(v, t);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) cut3(v[e], t[2][e], t[1][e], t[0][e]);
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-        *((g_u32x4*)(to + q * count * 8)) = u32x4{pack_bf16x2(t[q][0], t[q][1]), pack_bf16x2(t[q][2], t[q][3]),
-                                                 pack_bf16x2(t[q][4], t[q][5]), pack_bf16x2(t[q][6], t[q][7])};
+      for (int q = 0; q < 3; ++q) *((g_u32x4*)(to + q * count * 8)) = t[q];
     }
   }
 }

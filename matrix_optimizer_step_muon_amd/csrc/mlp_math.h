@@ -7,15 +7,29 @@
 
 namespace muon {
 
-// x = hi + mid + lo, each the rest rounded toward zero to bf16 (24 bits of numbers
-// of at least 2^-110). Infinities and NaNs stay in hi alone.
-MUON_INLINE void cut3(float x, float& hi, float& mid, float& lo) {
-  const uint32_t bits = __float_as_uint(x);
-  const bool fine = (bits & 0x7f800000u) != 0x7f800000u;
-  hi = fine ? __uint_as_float(bits & 0xffff0000u) : x;
-  const float r = fine ? x - hi : 0.f;
-  mid = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
-  lo = __uint_as_float(__float_as_uint(r - mid) & 0xffff0000u);
+// Eight fp32 numbers as bf16 operands that add up to them: x = hi + mid + lo, each the
+// rest rounded toward zero (24 bits of numbers of at least 2^-110); `parts` are the
+// eight lo, mid and hi. A part of which nothing is left is 2^-64 of x in place of 0: less
+// than a sum in fp32 sees, but an infinity in the other operand keeps its sign in that
+// product too, where 0 would make it a NaN. All parts of an infinity are that infinity,
+// and one of a NaN's at least is a NaN.
+MUON_INLINE void cut3(const float v[8], u32x4 parts[3]) {
+  uint32_t p[3][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    auto cut = [](float f) __attribute__((always_inline)) { return __uint_as_float(__float_as_uint(f) & 0xffff0000u); };
+    // The maxima are the rest itself where there is one, 2^-23 of x at least; of the NaN
+    // that an infinity leaves, and a number, they are the number.
+    const float x = v[i], least = fabsf(x * 0x1p-64f), r = x - cut(x);
+    const float mid = copysignf(fmaxf(fabsf(r), least), x), rest = r - cut(mid);
+    p[2][i] = __float_as_uint(x);
+    p[1][i] = __float_as_uint(mid);
+    p[0][i] = __float_as_uint(copysignf(fmaxf(fabsf(rest), least), x));
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) parts[q][i] = __builtin_amdgcn_perm(p[q][2 * i + 1], p[q][2 * i], 0x07060302u);  // the upper halves
 }
 
 // 1 / (1 + e^-x); e^-x in the hardware's exponential of base 2: a relative error of
