@@ -49,7 +49,8 @@ MUON_INLINE void activations(const float v[8], int act_, F to) {
   } else if (act == MUON_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float a = v[i], phi = 0.5f + 0.5f * erff(a * 0.70710678f);
+      // Phi from its smaller side: (1 + erf) / 2 would keep nothing of it from a = -5 on
+      const float a = v[i], tail = 0.5f * erfcf(fabsf(a) * 0.70710678f), phi = a < 0.f ? tail : 1.f - tail;
       to(i, a * phi, fmaf(a * 0.39894228f, __builtin_amdgcn_exp2f(-0.72134752f * a * a), phi));
     }
   } else if (act == MUON_ACT_GELU_TANH) {
