@@ -49,8 +49,10 @@ MUON_INLINE void activations(const float v[8], int act_, F to) {
   } else if (act == MUON_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // Phi from its smaller side: (1 + erf) / 2 would keep nothing of it from a = -5 on
-      const float a = v[i], tail = 0.5f * erfcf(fabsf(a) * 0.70710678f), phi = a < 0.f ? tail : 1.f - tail;
+      // Phi from its smaller side: (1 + erf) / 2 would keep nothing of it from a = -5 on.
+      // Below 2^-110 (a < -12.1) it is 0: its products would underflow in part.
+      const float a = v[i], near = 0.5f * erfcf(fabsf(a) * 0.70710678f), tail = near < 0x1p-110f ? 0.f : near;
+      const float phi = a < 0.f ? tail : 1.f - tail;
       to(i, a * phi, fmaf(a * 0.39894228f, __builtin_amdgcn_exp2f(-0.72134752f * a * a), phi));
     }
   } else if (act == MUON_ACT_GELU_TANH) {
