@@ -536,8 +536,8 @@ muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32
  *         weight gradient of w_down (muon_wgrad) s
  * width, inner and out are at most 2^22, and so are the row strides of y, d_x, d_a
  * and d_b.
- * workspace: device memory of at least muon_mlp_workspace bytes, 16-byte aligned,
- * scratch of a call until it has run; a call on it in a captured graph writes it
+ * workspace: device memory of at least muon_mlp_exact_workspace bytes (muon_mlp_workspace
+ * for any tensors of these sizes), 16-byte aligned, scratch of a call until it has run; a call on it in a captured graph writes it
  * anew with every replay.
  * act: MUON_ACT_SILU a/(1+e^-a), MUON_ACT_GELU a Phi(a) (Phi the normal
  * distribution), MUON_ACT_GELU_TANH its approximation by a tanh, a (1 +
@@ -594,6 +594,13 @@ muon_status muon_mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, 
  * alignment and the strides of its tensors (host, no GPU; reads rows, width, inner,
  * out and dtype). */
 muon_status muon_mlp_workspace(const muon_mlp* mlp, size_t* bytes);
+
+/* What one pass asks for with the tensors given, forward (grads NULL) or backward:
+ * operands that are read where they lie take none of it, so that of aligned bf16
+ * tensors it is s, or nothing, and the pieces of sums. x, the weights, dy, d_a and
+ * d_b that are NULL count as unaligned ones (host, no GPU; reads those pointers and
+ * their strides, and which of y, d_x and the checkpoints are wanted). */
+muon_status muon_mlp_exact_workspace(const muon_mlp* mlp, const muon_mlp_grads* grads, size_t* bytes);
 
 /* Weights in 8 bits. An n x k weight is cut into blocks of 128 x 128 (those at the
  * edges may be smaller). A block has one exponent byte E, an element is one e4m3

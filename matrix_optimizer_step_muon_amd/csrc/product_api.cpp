@@ -177,7 +177,8 @@ muon_status check_kinds(const muon_mlp& p) {
 }
 
 // An operand of a product: as the caller gave it, if it is bf16 in 16-byte aligned
-// rows of whole 16-byte chunks, else rewritten into the workspace first.
+// rows of whole 16-byte chunks, else rewritten into the workspace first. A null one
+// counts as one to rewrite (where only the workspace's size is asked for).
 struct Operand {
   const void* p;
   int64_t rows, cols, ld;
@@ -200,11 +201,11 @@ struct Bump {
 };
 
 bool in_place(const void* p, int64_t cols, int64_t ld, int32_t dtype) {
-  return dtype == MUON_BF16 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && cols % 8 == 0 && ld % 8 == 0 && 2 * ld <= kMaxPitch;
+  return dtype == MUON_BF16 && p && reinterpret_cast<uintptr_t>(p) % 16 == 0 && cols % 8 == 0 && ld % 8 == 0 && 2 * ld <= kMaxPitch;
 }
 
-Operand operand(Bump& b, const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
-  Operand o{p, rows, cols, ld, !in_place(p, cols, ld, dtype), 0};
+Operand operand(Bump& b, bool used, const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+  Operand o{p, rows, cols, ld, used && !in_place(p, cols, ld, dtype), 0};
   if (o.pack) o.at = b.take(planes_bytes(rows, cols, dtype == MUON_F32 ? 3 : 1));
   return o;
 }
@@ -213,8 +214,10 @@ Operand operand(Bump& b, const void* p, int64_t rows, int64_t cols, int64_t ld, 
 struct MlpCall {
   Operand ops[4];
   muon::PrArgs first{}, second{};
+  bool few_first = false, few_second = false;  // forward: by the kernels for few rows
+  char* s = nullptr;                           // forward: s between the two products
+  int64_t ld_s = 0;
   size_t bytes = 0;
-  double first_us = 0.0, second_us = 0.0;  // expected
 };
 
 // Two operands of one item share a row stride and a distance of planes: where one
@@ -239,15 +242,42 @@ void start(muon::PrArgs& a, const muon_mlp& p, int64_t m, int64_t n, int64_t k, 
   a.mlp.act = p.act;
 }
 
+// Few rows: a product that reads its weights as they are, once, where that is
+// expected to be faster; fp32 always, since tiles would have the weights rewritten
+// first. The gate does so only if nothing is kept.
+bool few_gate(const muon_mlp& p, double tiles_us) {
+  return p.rows <= muon::kFewRows && p.y && !p.a.q && !p.b.q && !p.s.q &&
+         (p.dtype == MUON_F32 || few_us(p.inner, double(p.width) * 2, 2, p.rows) <= tiles_us);
+}
+bool few_down(const muon_mlp& p, double tiles_us) {
+  return p.rows <= muon::kFewRows && p.dtype == MUON_BF16 && few_us(p.out, double(p.inner) * 2, 1, p.rows) <= tiles_us;
+}
+
 muon_status plan_forward(const muon_mlp& p, MlpCall& c, char* ws) {
   Bump b;
   const int parts = p.dtype == MUON_F32 ? 3 : 1;
-  c.ops[0] = operand(b, p.x, p.rows, p.width, p.ld_x, p.dtype);
-  c.ops[1] = operand(b, p.w_gate, p.inner, p.width, p.width, p.dtype);
-  c.ops[2] = operand(b, p.w_up, p.inner, p.width, p.width, p.dtype);
-  c.ops[3] = operand(b, p.w_down, p.out, p.inner, p.inner, p.dtype);
-  const Operand s{nullptr, p.rows, p.inner, pad8(p.inner), true, b.take(planes_bytes(p.rows, p.inner, parts))};
+  size_t n1 = 0, n2 = 0;
+  double us1 = 0.0, us2 = 0.0;
   start(c.first, p, p.rows, p.inner, p.width, 1);
+  start(c.second, p, p.rows, p.out, p.inner, 1);
+  // fp32 goes through both kernels for few rows or none, and s between them stays fp32
+  const bool plain = p.dtype == MUON_F32 && few_gate(p, 0.0);
+  c.few_first = c.few_second = plain;
+  if (!plain) {
+    MUON_TRY(lay_out(c.first, true, 2, kGateCost, &n1, &us1));
+    MUON_TRY(lay_out(c.second, false, 2, kDownCost, &n2, &us2));
+    c.few_first = few_gate(p, us1);
+    c.few_second = few_down(p, us2);
+  }
+  const bool first = !c.few_first, second = p.y && !c.few_second;  // in tiles
+  c.ops[0] = operand(b, first, p.x, p.rows, p.width, p.ld_x, p.dtype);
+  c.ops[1] = operand(b, first, p.w_gate, p.inner, p.width, p.width, p.dtype);
+  c.ops[2] = operand(b, first, p.w_up, p.inner, p.width, p.width, p.dtype);
+  c.ops[3] = operand(b, second, p.w_down, p.out, p.inner, p.inner, p.dtype);
+  c.ld_s = plain ? p.inner : pad8(p.inner);
+  const Operand s{nullptr, p.rows, p.inner, c.ld_s, true,
+                  b.take(plain ? size_t(p.rows) * size_t(p.inner) * 4 : planes_bytes(p.rows, p.inner, parts))};
+  c.s = ws + s.at;
   muon::PrItem& f = c.first.item[0];
   put_operand(f, true, 0, c.ops[0], ws, parts);
   put_operand(f, false, 0, c.ops[1], ws, parts);
@@ -256,30 +286,27 @@ muon_status plan_forward(const muon_mlp& p, MlpCall& c, char* ws) {
   e.a = p.a;
   e.b = p.b;
   e.s = p.s;
-  e.plane[0] = reinterpret_cast<uint16_t*>(ws + s.at);
-  e.ldp = pad8(p.inner);
+  e.plane[0] = reinterpret_cast<uint16_t*>(c.s);
+  e.ldp = c.ld_s;
   e.pp = p.rows * e.ldp;
-  start(c.second, p, p.rows, p.out, p.inner, 1);
   muon::PrItem& g = c.second.item[0];
   put_operand(g, true, 0, s, ws, parts);
   put_operand(g, false, 0, c.ops[3], ws, parts);
   g.out = p.y;
   g.ldo = p.ld_y;
-  size_t n1 = 0, n2 = 0;
-  MUON_TRY(lay_out(c.first, true, 2, kGateCost, &n1, &c.first_us));
-  MUON_TRY(lay_out(c.second, false, 2, kDownCost, &n2, &c.second_us));
   c.first.partial = c.second.partial = reinterpret_cast<float*>(ws + b.at);
-  c.bytes = b.at + std::max(n1, n2);
+  c.bytes = b.at + std::max(first ? n1 : 0, second ? n2 : 0);
   return MUON_OK;
 }
 
 muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c, char* ws) {
   Bump b;
   const int parts = p.dtype == MUON_F32 ? 3 : 1;
-  c.ops[0] = operand(b, g.dy, p.rows, p.out, g.ld_dy, p.dtype);
-  c.ops[1] = operand(b, p.w_down, p.out, p.inner, p.inner, p.dtype);
-  c.ops[2] = operand(b, p.w_gate, p.inner, p.width, p.width, p.dtype);
-  c.ops[3] = operand(b, p.w_up, p.inner, p.width, p.width, p.dtype);
+  const bool second = g.d_x != nullptr;
+  c.ops[0] = operand(b, true, g.dy, p.rows, p.out, g.ld_dy, p.dtype);
+  c.ops[1] = operand(b, true, p.w_down, p.out, p.inner, p.inner, p.dtype);
+  c.ops[2] = operand(b, second, p.w_gate, p.inner, p.width, p.width, p.dtype);
+  c.ops[3] = operand(b, second, p.w_up, p.inner, p.width, p.width, p.dtype);
   // da and db feed the next product as they are, or from the workspace, both alike
   void* d[2] = {g.d_a, g.d_b};
   const int64_t ld[2] = {g.ld_d_a, g.ld_d_b};
@@ -298,10 +325,10 @@ muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c
   for (int i = 0; i < 2; ++i) {
     e.d[i] = d[i];
     e.ldd[i] = ld[i];
-    Operand o{d[i], p.rows, p.inner, ld[i], !same, 0};
-    if (!same) {
+    Operand o{d[i], p.rows, p.inner, ld[i], second && !same, 0};
+    if (o.pack) {
       o.at = b.take(planes_bytes(p.rows, p.inner, parts));
-      if (g.d_x) e.plane[i] = reinterpret_cast<uint16_t*>(ws + o.at);
+      e.plane[i] = reinterpret_cast<uint16_t*>(ws + o.at);
     }
     put_operand(s, true, i, o, ws, parts);
     put_operand(s, false, i, c.ops[2 + i], ws, parts);
@@ -312,19 +339,8 @@ muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c
   MUON_TRY(lay_out(c.first, false, 2, kGateGradCost, &n1));
   MUON_TRY(lay_out(c.second, false, 2, kDxCost, &n2));
   c.first.partial = c.second.partial = reinterpret_cast<float*>(ws + b.at);
-  c.bytes = b.at + std::max(n1, n2);
+  c.bytes = b.at + std::max(n1, second ? n2 : 0);
   return MUON_OK;
-}
-
-// Few rows: a product that reads its weights as they are, once, where that is
-// expected to be faster; fp32 always, since tiles would have the weights rewritten
-// first. The gate does so only if nothing is kept.
-bool few_gate(const muon_mlp& p, double tiles_us) {
-  return p.rows <= muon::kFewRows && p.y && !p.a.q && !p.b.q && !p.s.q &&
-         (p.dtype == MUON_F32 || few_us(p.inner, double(p.width) * 2, 2, p.rows) <= tiles_us);
-}
-bool few_down(const muon_mlp& p, double tiles_us) {
-  return p.rows <= muon::kFewRows && p.dtype == MUON_BF16 && few_us(p.out, double(p.inner) * 2, 1, p.rows) <= tiles_us;
 }
 
 muon_status launch_few_gate(const muon_mlp& p, void* s, int64_t ld, hipStream_t stream) {
@@ -357,28 +373,28 @@ muon_status launch_few_down(const muon_mlp& p, const void* s, int64_t ld, hipStr
   return hip_status(muon::launch_few(a, p.dtype == MUON_F32, 1, stream));
 }
 
-size_t few_bytes(const muon_mlp& p) { return round256(size_t(p.rows) * size_t(p.inner) * size_t(elem_of(p.dtype))); }
-
-// The most that either pass takes, every operand rewritten.
-muon_status mlp_workspace(const muon_mlp& p, size_t* bytes) {
+// For the tensors of a pass.
+muon_status mlp_workspace(const muon_mlp& p, const muon_mlp_grads* g, size_t* bytes) {
   MUON_TRY(check_mlp(p));
-  muon_mlp q = p;
-  q.x = q.w_gate = q.w_up = q.w_down = reinterpret_cast<const void*>(uintptr_t(2));
-  q.y = reinterpret_cast<void*>(uintptr_t(2));
-  q.ld_x = q.width;
-  q.ld_y = q.out;
-  muon_mlp_grads g{};
-  g.dy = q.x;
-  g.d_x = g.d_a = g.d_b = q.y;
-  g.ld_dy = q.out;
-  g.ld_d_x = q.width;
-  g.ld_d_a = g.ld_d_b = q.inner;
   *bytes = 0;
   if (p.rows == 0) return MUON_OK;
-  MlpCall f, b;
-  MUON_TRY(plan_forward(q, f, nullptr));
-  MUON_TRY(plan_backward(q, g, b, nullptr));
-  *bytes = std::max({f.bytes, b.bytes, few_bytes(p)});
+  MlpCall c;
+  MUON_TRY(g ? plan_backward(p, *g, c, nullptr) : plan_forward(p, c, nullptr));
+  *bytes = c.bytes;
+  return MUON_OK;
+}
+
+// The most that either pass takes: everything is wanted, and every operand rewritten.
+muon_status mlp_workspace(const muon_mlp& p, size_t* bytes) {
+  muon_mlp q = p;
+  q.x = q.w_gate = q.w_up = q.w_down = nullptr;
+  q.y = q.a.q = &q;
+  muon_mlp_grads g{};
+  g.d_x = &g;
+  size_t forward = 0, backward = 0;
+  MUON_TRY(mlp_workspace(q, nullptr, &forward));
+  MUON_TRY(mlp_workspace(q, &g, &backward));
+  *bytes = std::max(forward, backward);
   return MUON_OK;
 }
 
@@ -392,18 +408,18 @@ muon_status check_mlp_workspace(Views& v, const muon_mlp& p, size_t need) {
   return v.add_range(p.workspace, need, "workspace");
 }
 
-// The operands of ops[0 .. n) that are used and not in place, rewritten in one launch.
-muon_status run_packs(const Operand* ops, const bool* used, int n, const muon_mlp& p, char* ws, hipStream_t s) {
+// The operands that are not in place, rewritten in one launch.
+muon_status run_packs(const MlpCall& c, const muon_mlp& p, char* ws, hipStream_t s) {
   muon::PrPacks a{};
-  for (int i = 0; i < n; ++i) {
-    if (!used[i] || !ops[i].pack) continue;
+  for (const Operand& o : c.ops) {
+    if (!o.pack) continue;
     muon::PrPack& d = a.pack[a.n++];
-    d.src = ops[i].p;
-    d.dst = ws + ops[i].at;
-    d.ld = ops[i].ld;
-    d.octets = pad8(ops[i].cols) / 8;
-    d.rows = int32_t(ops[i].rows);
-    d.cols = int32_t(ops[i].cols);
+    d.src = o.p;
+    d.dst = ws + o.at;
+    d.ld = o.ld;
+    d.octets = pad8(o.cols) / 8;
+    d.rows = int32_t(o.rows);
+    d.cols = int32_t(o.cols);
   }
   return hip_status(muon::launch_packs(a, p.dtype == MUON_F32, s));
 }
@@ -428,23 +444,16 @@ muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
   if (p.rows == 0) return v.disjoint();
   char* ws = static_cast<char*>(p.workspace);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (p.dtype == MUON_F32 && few_gate(p, 0.0)) {
-    MUON_TRY(check_mlp_workspace(v, p, few_bytes(p)));
-    MUON_TRY(v.disjoint());
-    MUON_TRY(launch_few_gate(p, ws, p.inner, s));
-    return launch_few_down(p, ws, p.inner, s);
-  }
   MlpCall c;
   MUON_TRY(plan_forward(p, c, ws));
   MUON_TRY(check_mlp_workspace(v, p, c.bytes));
   MUON_TRY(v.disjoint());
-  const bool gate = few_gate(p, c.first_us), down = p.y && few_down(p, c.second_us);
-  const bool used[] = {!gate, !gate, !gate, p.y && !down};
-  MUON_TRY(run_packs(c.ops, used, 4, p, ws, s));
-  if (gate) MUON_TRY(launch_few_gate(p, c.first.mlp.plane[0], c.first.mlp.ldp, s));
+  MUON_TRY(run_packs(c, p, ws, s));
+  if (c.few_first) MUON_TRY(launch_few_gate(p, c.s, c.ld_s, s));
   else MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGate, false, s)));
-  if (down) return launch_few_down(p, c.first.mlp.plane[0], c.first.mlp.ldp, s);
-  return p.y ? hip_status(muon::launch_mlp(c.second, muon::kPrStore, false, s)) : MUON_OK;
+  if (!p.y) return MUON_OK;
+  if (c.few_second) return launch_few_down(p, c.s, c.ld_s, s);
+  return hip_status(muon::launch_mlp(c.second, muon::kPrStore, false, s));
 }
 
 muon_status mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void* stream) {
@@ -474,8 +483,7 @@ muon_status mlp_backward(const muon_mlp* mlp, const muon_mlp_grads* grads, void*
   MUON_TRY(check_mlp_workspace(v, p, c.bytes));
   MUON_TRY(v.disjoint());
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool used[] = {true, true, g.d_x != nullptr, g.d_x != nullptr};
-  MUON_TRY(run_packs(c.ops, used, 4, p, ws, s));
+  MUON_TRY(run_packs(c, p, ws, s));
   MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGateGrad, true, s)));
   return g.d_x ? hip_status(muon::launch_mlp(c.second, muon::kPrStore, true, s)) : MUON_OK;
 }
@@ -646,6 +654,13 @@ muon_status muon_mlp_workspace(const muon_mlp* mlp, size_t* bytes) {
   return guarded([&]() -> muon_status {
     if (!mlp || !bytes) return fail(MUON_ERR_INVALID_ARG, "mlp or bytes is NULL");
     return mlp_workspace(*mlp, bytes);
+  });
+}
+
+muon_status muon_mlp_exact_workspace(const muon_mlp* mlp, const muon_mlp_grads* grads, size_t* bytes) {
+  return guarded([&]() -> muon_status {
+    if (!mlp || !bytes) return fail(MUON_ERR_INVALID_ARG, "mlp or bytes is NULL");
+    return mlp_workspace(*mlp, grads, bytes);
   });
 }
 

@@ -409,10 +409,14 @@ class GatedMLP:
         self._c = muon_mlp(rows, width, inner, cols, x.data_ptr(), _ld(x), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
                            self.y.data_ptr(), _ld(self.y), *(none if q is None else q._c for q in (self.a, self.b, self.s)),
                            None, 0, ACTS[act], code)
-        need = ctypes.c_size_t()
-        check(lib().muon_mlp_workspace(ctypes.byref(self._c), ctypes.byref(need)))
-        self.workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        self._c.workspace, self._c.workspace_bytes = self.workspace.data_ptr(), need.value
+        # for these tensors, and a dy of any alignment
+        need, back = ctypes.c_size_t(), ctypes.c_size_t()
+        check(lib().muon_mlp_exact_workspace(ctypes.byref(self._c), None, ctypes.byref(need)))
+        if self._grads is not None:
+            check(lib().muon_mlp_exact_workspace(ctypes.byref(self._c), ctypes.byref(self._grads), ctypes.byref(back)))
+        need = max(need.value, back.value)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        self._c.workspace, self._c.workspace_bytes = self.workspace.data_ptr(), need
         self._streams = _Streams([t for t in (x, w_gate, w_up, w_down, self.y, self.d_x, self.d_a, self.d_b, self.workspace)
                                   if t is not None] + [t for q in kept for t in (q.q, q.e)])
 
