@@ -602,6 +602,13 @@ muon_status muon_mlp_workspace(const muon_mlp* mlp, size_t* bytes);
  * their strides, and which of y, d_x and the checkpoints are wanted). */
 muon_status muon_mlp_exact_workspace(const muon_mlp* mlp, const muon_mlp_grads* grads, size_t* bytes);
 
+/* How a pass cuts its two products up, forward (grads NULL: the projections, y) or
+ * backward (ds, d_x): the edge of the output tiles (0: a kernel for at most 16 rows, or
+ * no product), how many tiles are summed whole, and the pieces that the sums of the
+ * others are cut into (1: there are none). Two numbers each (host, no GPU; reads what
+ * muon_mlp_exact_workspace reads). */
+muon_status muon_mlp_info(const muon_mlp* mlp, const muon_mlp_grads* grads, int32_t* tile, int32_t* whole, int32_t* pieces);
+
 /* Weights in 8 bits. An n x k weight is cut into blocks of 128 x 128 (those at the
  * edges may be smaller). A block has one exponent byte E, an element is one e4m3
  * byte q and stands for q * 2^(E-127); E and q are chosen as for a checkpoint (E =
@@ -661,6 +668,10 @@ typedef struct {
 muon_status muon_linear8(const muon_linear8_item* items, int32_t n_items, int32_t dtype, void* workspace,
                          size_t workspace_bytes, void* stream);
 muon_status muon_linear8_workspace(const muon_linear8_item* items, int32_t n_items, int32_t dtype, size_t* bytes);
+/* How muon_linear8 cuts each item's product up, as muon_mlp_info says it (after the
+ * same checks of the items, without a GPU). n_items numbers each. */
+muon_status muon_linear8_info(const muon_linear8_item* items, int32_t n_items, int32_t dtype, int32_t* tile, int32_t* whole,
+                              int32_t* pieces);
 
 #ifdef __cplusplus
 }

@@ -384,6 +384,27 @@ muon_status mlp_workspace(const muon_mlp& p, const muon_mlp_grads* g, size_t* by
   return MUON_OK;
 }
 
+// How an item of a launch is cut up.
+void cut_of(const muon::PrArgs& a, const muon::PrItem& it, int32_t* tile, int32_t* whole, int32_t* pieces) {
+  *tile = muon::kPrEdge[a.tile];
+  *whole = it.whole;
+  *pieces = it.whole == it.tiles_m * it.tiles_n ? 1 : it.splits;
+}
+
+muon_status mlp_info(const muon_mlp& p, const muon_mlp_grads* g, int32_t* tile, int32_t* whole, int32_t* pieces) {
+  MUON_TRY(check_mlp(p));
+  for (int i = 0; i < 2; ++i) {
+    tile[i] = whole[i] = 0;
+    pieces[i] = 1;
+  }
+  if (p.rows == 0) return MUON_OK;
+  MlpCall c;
+  MUON_TRY(g ? plan_backward(p, *g, c, nullptr) : plan_forward(p, c, nullptr));
+  if (!c.few_first) cut_of(c.first, c.first.item[0], tile, whole, pieces);
+  if ((g ? g->d_x : p.y) && !c.few_second) cut_of(c.second, c.second.item[0], tile + 1, whole + 1, pieces + 1);
+  return MUON_OK;
+}
+
 // The most that either pass takes: everything is wanted, and every operand rewritten.
 muon_status mlp_workspace(const muon_mlp& p, size_t* bytes) {
   muon_mlp q = p;
@@ -549,8 +570,10 @@ muon_status check_linear8(const muon_linear8_item* items, int32_t n, int32_t dty
   return v.disjoint();
 }
 
-// Few rows with a bf16 result: a launch of their own, without a workspace.
+// Few rows with a bf16 result: a launch of their own, without a workspace. Items
+// without rows have nothing to do.
 bool few_rows(const muon_linear8_item& it, int32_t dtype) { return it.x.rows <= muon::kFewRows && dtype == MUON_BF16; }
+bool in_tiles(const muon_linear8_item& it, int32_t dtype) { return it.x.rows > 0 && !few_rows(it, dtype); }
 
 muon_status few_linear8(const muon_linear8_item& it, hipStream_t s) {
   const bool t = it.transposed != 0;
@@ -576,12 +599,12 @@ muon_status few_linear8(const muon_linear8_item& it, hipStream_t s) {
 }
 
 // The launches, of 16 items each, and the workspace of the largest: they follow each
-// other on one stream and share it. Items without rows have nothing to do.
+// other on one stream and share it.
 muon_status plan_linear8(const muon_linear8_item* items, int32_t n, int32_t dtype, std::vector<muon::PrArgs>& plans, size_t* bytes) {
   *bytes = 0;
   for (int32_t i = 0; i < n; ++i) {
     const muon_linear8_item& it = items[i];
-    if (it.x.rows == 0 || few_rows(it, dtype)) continue;
+    if (!in_tiles(it, dtype)) continue;
     if (plans.empty() || plans.back().n_items == muon::kPrItems) plans.push_back(muon::PrArgs{});
     muon::PrArgs& a = plans.back();
     muon::PrItem& d = a.item[a.n_items++];
@@ -664,6 +687,13 @@ muon_status muon_mlp_exact_workspace(const muon_mlp* mlp, const muon_mlp_grads* 
   });
 }
 
+muon_status muon_mlp_info(const muon_mlp* mlp, const muon_mlp_grads* grads, int32_t* tile, int32_t* whole, int32_t* pieces) {
+  return guarded([&]() -> muon_status {
+    if (!mlp || !tile || !whole || !pieces) return fail(MUON_ERR_INVALID_ARG, "mlp, tile, whole or pieces is NULL");
+    return mlp_info(*mlp, grads, tile, whole, pieces);
+  });
+}
+
 muon_status muon_w8_save(const void* w, int64_t ldw, int32_t dtype, const muon_w8* out, void* stream) {
   return w8_call(w, ldw, dtype, out, true, stream);
 }
@@ -684,6 +714,28 @@ muon_status muon_linear8_workspace(const muon_linear8_item* items, int32_t n_ite
     MUON_TRY(check_linear8(items, n_items, dtype, v));
     std::vector<muon::PrArgs> plans;
     return plan_linear8(items, n_items, dtype, plans, bytes);
+  });
+}
+
+muon_status muon_linear8_info(const muon_linear8_item* items, int32_t n_items, int32_t dtype, int32_t* tile, int32_t* whole,
+                              int32_t* pieces) {
+  return guarded([&]() -> muon_status {
+    if (!tile || !whole || !pieces) return fail(MUON_ERR_INVALID_ARG, "tile, whole or pieces is NULL");
+    Views v;
+    MUON_TRY(check_linear8(items, n_items, dtype, v));
+    std::vector<muon::PrArgs> plans;
+    size_t bytes = 0;
+    MUON_TRY(plan_linear8(items, n_items, dtype, plans, &bytes));
+    int at = 0;  // of the items that go in tiles
+    for (int32_t i = 0; i < n_items; ++i) {
+      tile[i] = whole[i] = 0;
+      pieces[i] = 1;
+      if (!in_tiles(items[i], dtype)) continue;
+      const muon::PrArgs& a = plans[size_t(at / muon::kPrItems)];
+      cut_of(a, a.item[at % muon::kPrItems], tile + i, whole + i, pieces + i);
+      ++at;
+    }
+    return MUON_OK;
   });
 }
 

@@ -347,6 +347,10 @@ class WGrad:
         return [{"tile": t, "pieces": p} for t, p in zip(tile, pieces)]
 
 
+def _cuts(tile, whole, pieces) -> List[dict]:
+    return [{"tile": t, "whole": w, "pieces": p} for t, w, p in zip(tile, whole, pieces)]
+
+
 class GatedMLP:
     """The gated feed-forward block (muon_mlp):
 
@@ -432,6 +436,18 @@ class GatedMLP:
         g = self._grads
         g.dy, g.ld_dy = dy.data_ptr(), _ld(dy)
         check(lib().muon_mlp_backward(ctypes.byref(self._c), ctypes.byref(g), self._streams.use(stream, (dy,))))
+
+    def info(self) -> dict:
+        """How the products of the forward pass (the projections, y) and of the backward
+        pass (ds, d_x) are cut up: the edge of their tiles (0: a kernel for at most 16
+        rows, or no product), the tiles summed whole, the pieces of the others' sums."""
+        out = {}
+        for name, grads in (("forward", None), ("backward", self._grads)):
+            if name == "forward" or grads is not None:
+                t = [(ctypes.c_int32 * 2)() for _ in range(3)]
+                check(lib().muon_mlp_info(ctypes.byref(self._c), grads and ctypes.byref(grads), *t))
+                out[name] = _cuts(*t)
+        return out
 
     def wgrad_items(self, dy, x: Q8, g_gate, g_up, g_down, *, scale=None, beta: float = 0.0) -> List:
         """Items for ``WGrad``: the gradients of w_gate and w_up from the checkpoint
@@ -525,3 +541,9 @@ class Linear8:
     def run(self, stream=None) -> None:
         _same_device(self._device)
         check(lib().muon_linear8(*self._args, self._streams.use(stream)))
+
+    def info(self) -> List[dict]:
+        """How each item's product is cut up, as in ``GatedMLP.info``."""
+        t = [(ctypes.c_int32 * self._n)() for _ in range(3)]
+        check(lib().muon_linear8_info(self._items, self._n, self._dtype, *t))
+        return _cuts(*t)

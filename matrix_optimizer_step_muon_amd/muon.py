@@ -113,7 +113,7 @@ EXPORTS = ("muon_hparams_default", "muon_plan", "muon_plan_workspace_bytes", "mu
            "muon_q8_save", "muon_q8_load", "muon_norm_forward", "muon_norm_backward",
            "muon_norm_backward_workspace", "muon_wgrad", "muon_wgrad_workspace", "muon_wgrad_info",
            "muon_mlp_forward", "muon_mlp_backward", "muon_mlp_workspace", "muon_mlp_exact_workspace", "muon_w8_save", "muon_w8_load", "muon_linear8",
-           "muon_linear8_workspace")
+           "muon_linear8_workspace", "muon_mlp_info", "muon_linear8_info")
 
 
 def lib() -> ctypes.CDLL:
@@ -163,6 +163,8 @@ def lib() -> ctypes.CDLL:
     L.muon_mlp_backward.argtypes = [ctypes.POINTER(muon_mlp), ctypes.POINTER(muon_mlp_grads), c_vp]
     L.muon_mlp_workspace.argtypes = [ctypes.POINTER(muon_mlp), ctypes.POINTER(ctypes.c_size_t)]
     L.muon_mlp_exact_workspace.argtypes = [ctypes.POINTER(muon_mlp), ctypes.POINTER(muon_mlp_grads), ctypes.POINTER(ctypes.c_size_t)]
+    L.muon_mlp_info.argtypes = [ctypes.POINTER(muon_mlp), ctypes.POINTER(muon_mlp_grads)] + [ctypes.POINTER(c_i32)] * 3
+    L.muon_linear8_info.argtypes = [ctypes.POINTER(muon_linear8_item), c_i32, c_i32] + [ctypes.POINTER(c_i32)] * 3
     L.muon_w8_save.argtypes = [c_vp, c_i64, c_i32, ctypes.POINTER(muon_w8), c_vp]
     L.muon_w8_load.argtypes = [ctypes.POINTER(muon_w8), c_vp, c_i64, c_i32, c_vp]
     L.muon_linear8.argtypes = [ctypes.POINTER(muon_linear8_item), c_i32, c_i32, c_vp, ctypes.c_size_t, c_vp]
