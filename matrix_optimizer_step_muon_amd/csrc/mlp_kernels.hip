@@ -47,15 +47,15 @@ struct Saved {
   // training step of 4096 x 2048 x 6144 1008 -> 1000 us; da and db, which are read at
   // once, 1004 with them too).
   template <class V>
-  MUON_INLINE void save(int row, int dc, bool there, const float v[8]) const {
+  MUON_INLINE void save(int row, bool there, const float v[8]) const {
     u32x2 w;
     const uint32_t E = q8_encode(v, V::FULL ? V::B : kind, w);
-    uint8_t *pq = q + (int64_t)row * ldq + dc, *pe = e + (int64_t)row * lde + dc / kGroup;
-    if (V::FULL || (there && col + dc < cols16)) __builtin_nontemporal_store(w, (g_u32x2*)(pq + off));
-    if (first && (V::FULL || (there && col + dc < cols))) *((g_u8*)(pe + offe)) = (uint8_t)E;
+    uint8_t *pq = q + (int64_t)row * ldq, *pe = e + (int64_t)row * lde;
+    if (V::FULL || (there && col < cols16)) __builtin_nontemporal_store(w, (g_u32x2*)(pq + off));
+    if (first && (V::FULL || (there && col < cols))) *((g_u8*)(pe + offe)) = (uint8_t)E;
   }
-  MUON_INLINE void load(int row, int dc, u32x2& w, uint32_t& E) const {
-    const uint8_t *pq = q + (int64_t)row * ldq + dc, *pe = e + (int64_t)row * lde + dc / kGroup;
+  MUON_INLINE void load(int row, u32x2& w, uint32_t& E) const {
+    const uint8_t *pq = q + (int64_t)row * ldq, *pe = e + (int64_t)row * lde;
     w = *((const g_u32x2*)(pq + off));
     E = *((const g_u8*)(pe + offe));
   }
@@ -72,8 +72,8 @@ struct Planes {
     off = (uint32_t)at.row * (uint32_t)ld + 2u * (uint32_t)at.col;
   }
   template <class V>
-  MUON_INLINE void put(int row, int dc, const float v[8]) const {
-    char* base = p + (int64_t)row * ld + 2 * dc;
+  MUON_INLINE void put(int row, const float v[8]) const {
+    char* base = p + (int64_t)row * ld;
     if (V::FULL || parts == 1) {
       *((g_u32x4*)(base + off)) =
           u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
@@ -118,11 +118,11 @@ struct PrGateOut {
     else dispatch_kind<MUON_ACT_RELU>(f);
   }
   template <class V>
-  MUON_INLINE void pre(int, int, Pre&) const {}
+  MUON_INLINE void pre(int, Pre&) const {}
   template <class V>
-  MUON_INLINE void emit(int row, int dc, float a[8], float b[8], const Pre&) const {
+  MUON_INLINE void emit(int row, float a[8], float b[8], const Pre&) const {
     const bool there = V::FULL || row + at.row < m;
-    const int live = n - at.col - dc;
+    const int live = n - at.col;
     float v[8];
     activations<V::A>(a, act, [&](int i, float f, float) __attribute__((always_inline)) { v[i] = f * b[i]; });
     if (!V::FULL && live < 8) {
@@ -130,11 +130,11 @@ struct PrGateOut {
       for (int i = 0; i < 8; ++i)
         if (i >= live) a[i] = b[i] = v[i] = 0.f;
     }
-    if (V::FULL || (there && live > 0)) s.put<V>(row, dc, v);
+    if (V::FULL || (there && live > 0)) s.put<V>(row, v);
     if constexpr (!V::FULL || V::B != kNoSave) {
-      if (V::FULL || qa.q) qa.save<V>(row, dc, there, a);
-      if (V::FULL || qb.q) qb.save<V>(row, dc, there, b);
-      if (V::FULL || qs.q) qs.save<V>(row, dc, there, v);
+      if (V::FULL || qa.q) qa.save<V>(row, there, a);
+      if (V::FULL || qb.q) qb.save<V>(row, there, b);
+      if (V::FULL || qs.q) qs.save<V>(row, there, v);
     }
   }
 };
@@ -180,14 +180,14 @@ struct PrGateGradOut {
     else dispatch_kind<MUON_ACT_RELU>(f);
   }
   template <class V>
-  MUON_INLINE void pre(int row, int dc, Pre& p) const {
-    if (!V::FULL && (row + at.row >= m || live <= dc)) return;
-    qa.load(row, dc, p.a, p.ea);
-    qb.load(row, dc, p.b, p.eb);
+  MUON_INLINE void pre(int row, Pre& p) const {
+    if (!V::FULL && (row + at.row >= m || live <= 0)) return;
+    qa.load(row, p.a, p.ea);
+    qb.load(row, p.b, p.eb);
   }
   template <class V>
-  MUON_INLINE void emit(int row, int dc, float ds[8], float*, const Pre& p) const {
-    if (!V::FULL && (row + at.row >= m || live <= dc)) return;
+  MUON_INLINE void emit(int row, float ds[8], float*, const Pre& p) const {
+    if (!V::FULL && (row + at.row >= m || live <= 0)) return;
     float a[8], b[8], ga[8], gb[8];
     q8_decode(p.a, p.ea, V::FULL ? V::B : qa.kind, a);
     q8_decode(p.b, p.eb, V::FULL ? V::B : qb.kind, b);
@@ -195,29 +195,27 @@ struct PrGateGradOut {
       ga[i] = ds[i] * b[i] * df;
       gb[i] = ds[i] * f;
     });
-    const int64_t shift = (int64_t)dc << (f32 ? 2 : 1);
-    char *ba = da + (int64_t)row * lda + shift, *bb = db + (int64_t)row * ldb + shift;
+    char *ba = da + (int64_t)row * lda, *bb = db + (int64_t)row * ldb;
     if constexpr (V::FULL) {
       store_run(reinterpret_cast<u16*>(ba + offa), 8, ga);
       store_run(reinterpret_cast<u16*>(bb + offb), 8, gb);
       return;
     }
-    const int here = live - dc;
     if (f32) {
-      store_run(reinterpret_cast<float*>(ba + offa), here, ga);
-      store_run(reinterpret_cast<float*>(bb + offb), here, gb);
+      store_run(reinterpret_cast<float*>(ba + offa), live, ga);
+      store_run(reinterpret_cast<float*>(bb + offb), live, gb);
     } else {
-      store_run(reinterpret_cast<u16*>(ba + offa), here, ga);
-      store_run(reinterpret_cast<u16*>(bb + offb), here, gb);
+      store_run(reinterpret_cast<u16*>(ba + offa), live, ga);
+      store_run(reinterpret_cast<u16*>(bb + offb), live, gb);
     }
     if (pa.p) {
-      if (here < 8) {
+      if (live < 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i >= here) ga[i] = gb[i] = 0.f;
+          if (i >= live) ga[i] = gb[i] = 0.f;
       }
-      pa.put<V>(row, dc, ga);
-      pb.put<V>(row, dc, gb);
+      pa.put<V>(row, ga);
+      pb.put<V>(row, gb);
     }
   }
 };

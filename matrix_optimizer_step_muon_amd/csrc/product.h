@@ -44,13 +44,9 @@ typedef u32_any __attribute__((address_space(1))) g_u32_any;
 // from LDS, and the bf16 MFMA.
 enum PrMode { kNT16, kNN16, kNT8, kNT8X };
 
-// The slot of 16-byte chunk c of row r in an LDS row of S slots is c ^ swz(r):
-// the rows that the lanes of a fragment read together lie in different banks.
-template <int S>
-MUON_INLINE int pr_swz(int r) {
-  if constexpr (S == 4) return ((r >> 1) ^ (r >> 3)) & 3;
-  else return (r & 7) ^ ((r >> 3) & 1);
-}
+// The slot of 16-byte chunk c of row r in an LDS row of 8 slots is c ^ swz(r): the
+// rows that the lanes of a fragment read together lie in different banks.
+MUON_INLINE int pr_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 // The same for a row of K of a transposed B, read four rows at a time.
 template <int BN>
 MUON_INLINE int pr_swz_k(int r) {
@@ -85,13 +81,10 @@ struct PrCfg {
   static constexpr int CHUNK = 1024 / RB, TABS = ST, EX_A = 8 * BM * 4, EX_B = 8 * 2 * 4, EX = F8 ? TABS * (EX_A + EX_B) : 0;
   static constexpr int LDS = RING + EX;
   // The tile leaves through the stage that it used last (the others hold the next
-  // tile's first stages): IPP blocks of 32 rows of every wave at a time, or, where
-  // that does not fit, one block of rows and NJ blocks of 32 columns.
-  static constexpr int ROW_BLOCK = 64 * BN * 4;
-  static constexpr int IPP = STAGE >= ROW_BLOCK ? STAGE / ROW_BLOCK : 1;
-  static constexpr int NJ = STAGE >= ROW_BLOCK ? FN : FN >= 4 && STAGE >= ROW_BLOCK / 2 ? FN / 2 : FN >= 4 ? FN / 4 : 1;
-  static constexpr int PASSES = FM / IPP * (FN / NJ), SCOLS = 64 * NJ;  // columns of a staged row
-  static_assert(FM % IPP == 0 && 64 * IPP * SCOLS * 4 <= STAGE && PASSES <= 8, "a pass fits a stage");
+  // tile's first stages), which is as large as one block of 32 rows of every wave.
+  static constexpr int PASSES = FM;
+  static_assert(RB == kBlock, "a stage's row is 8 slots, and 128 of K in 8 bits: one scale of a weight's");
+  static_assert(BM == BN && 64 * BN * 4 == STAGE, "a pass fills a stage");
   static_assert(KK % 2 == 0 && (AHEAD || MEET >= SLOTS - PER) && (AHEAD || MODE != kNT8X), "schedule assumptions");
   static_assert(DA % 2 == 0 && DB % 2 == 0 && (ST & (ST - 1)) == 0, "copies of A and B lie alike");
   typedef std::conditional_t<MODE == kNT8, i32x8, std::conditional_t<MODE == kNT8X, u32x2, bf16x8>> Frag;  // as read
@@ -206,8 +199,7 @@ MUON_INLINE void stream_run(void* p, const float v[8]) {
 
 // How an epilogue takes a tile apart. A thread holds eight consecutive columns of one
 // row at a time: its row is `row` plus one that all threads share, its first column
-// col plus a shift that all share. The addresses are then a scalar and a 32-bit offset
-// that does not change.
+// always col. The addresses are then a scalar and a 32-bit offset that does not change.
 //
 // An epilogue comes in variants: PrAny takes every tile and looks at everything as it
 // goes; the others are for tiles without an edge, and know what they look at. They
@@ -270,8 +262,8 @@ struct PrStoreOut {
     else beta != 0.f ? f(PrVariant<true, 0, 1>{}) : f(PrVariant<true, 0, 0>{});
   }
   template <class V>
-  MUON_INLINE void pre(int row, int dc, Pre& p) const {
-    const char* at_c = c + (int64_t)row * ldc + ((int64_t)dc << (f32 ? 2 : 1)) + offc;
+  MUON_INLINE void pre(int row, Pre& p) const {
+    const char* at_c = c + (int64_t)row * ldc + offc;
     if constexpr (V::FULL) {
       // before the variant is known, both halves of what an fp32 c would need, if there is a c
       if (V::B < 0 ? beta != 0.f : V::B & 1) {
@@ -282,10 +274,10 @@ struct PrStoreOut {
           p.c[4 + i] = hi[i];
         }
       }
-    } else if (beta != 0.f && row + at.row < m && live > dc) {
+    } else if (beta != 0.f && row + at.row < m && live > 0) {
       float x[8];
-      if (f32) load_run(reinterpret_cast<const float*>(at_c), live - dc, x);
-      else load_run(reinterpret_cast<const u16*>(at_c), live - dc, x);
+      if (f32) load_run(reinterpret_cast<const float*>(at_c), live, x);
+      else load_run(reinterpret_cast<const u16*>(at_c), live, x);
 #pragma unroll
       for (int i = 0; i < kRun; ++i) p.c[i] = __float_as_uint(x[i]);
     }
@@ -304,37 +296,33 @@ struct PrStoreOut {
     }
   }
   template <class V>
-  MUON_INLINE void emit(int row, int dc, float v[8], float*, const Pre& p) const {
-    char* to = out + (int64_t)row * ldo + ((int64_t)dc << (f32 ? 2 : 1)) + off;
+  MUON_INLINE void emit(int row, float v[8], float*, const Pre& p) const {
+    char* to = out + (int64_t)row * ldo + off;
     if constexpr (V::FULL) {
       if constexpr (V::B & 1) add<V::A != 0>(p, v);
       if constexpr (V::A != 0) store_run(reinterpret_cast<float*>(to), 8, v);
       else if constexpr (V::B & 2) stream_run(to, v);
       else store_run(reinterpret_cast<u16*>(to), 8, v);
     } else {
-      if (row + at.row >= m || live <= dc) return;
+      if (row + at.row >= m || live <= 0) return;
       if (beta != 0.f) add<true>(p, v);
-      if (f32) store_run(reinterpret_cast<float*>(to), live - dc, v);
-      else store_run(reinterpret_cast<u16*>(to), live - dc, v);
+      if (f32) store_run(reinterpret_cast<float*>(to), live, v);
+      else store_run(reinterpret_cast<u16*>(to), live, v);
     }
   }
 };
 
 // A tile's way out: its partial sums, BM x BN floats, or the epilogue Out. Through
-// LDS, a pass of rows and columns of every wave at a time: staged row r is row WM*(r /
-// PR) + PR*(the pass's block of rows) + r % PR of the tile, staged column c is column
-// WN*(c / (32 NJ)) + 32 NJ*(the pass's block of columns) + c % (32 NJ); its 16-byte
-// unit u sits at u ^ (r % the row's units).
+// LDS, a pass of 32 rows of every wave at a time: staged row r is row WM*(r / 32) +
+// 32*pass + r % 32 of the tile; its 16-byte unit u sits at u ^ (r % the row's units).
 template <class Z>
 struct PrStage {
-  static constexpr int MASK = Z::SCOLS / 4 - 1, ROWS = 64 * Z::IPP, PR = 32 * Z::IPP, JB = Z::FN / Z::NJ;
+  static constexpr int MASK = Z::BN / 4 - 1, ROWS = 64;
   unsigned char* lds;
   const f32x16 (&acc)[Z::FM][Z::FN];
-  // The first of the tile's rows and columns that belong to staged row r (a multiple
-  // of what a pass's threads share) and to staged column 0.
-  MUON_INLINE static int tile_row(int pass, int r) { return Z::WM * (r / PR) + PR * (pass / JB) + r % PR; }
-  MUON_INLINE static int tile_col(int pass) { return 32 * Z::NJ * (pass % JB); }
-  MUON_INLINE static int own_col(int c) { return Z::WN * (c / (32 * Z::NJ)) + c % (32 * Z::NJ); }
+  // The first of the tile's rows that belong to staged row r (a multiple of what a
+  // pass's threads share).
+  MUON_INLINE static int tile_row(int pass, int r) { return Z::WM * (r / 32) + 32 * pass + r % 32; }
   // One pass's rows. The marks at both ends keep the passes apart: the compiler would
   // make one of them all, with a pointer to the sums, which then live in memory.
   template <int P>
@@ -342,16 +330,14 @@ struct PrStage {
     asm volatile("; pass %0" ::"n"(P) : "memory");
     const int tid = fresh_tid(), lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
 #pragma unroll
-    for (int ii = 0; ii < Z::IPP; ++ii)
+    for (int j = 0; j < Z::FN; ++j)
 #pragma unroll
-      for (int j = 0; j < Z::NJ; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int r = wm * PR + 32 * ii + (lane & 31), u = wn * (8 * Z::NJ) + 8 * j + 2 * g + (lane >> 5);
-          const f32x16& t = acc[P / JB * Z::IPP + ii][P % JB * Z::NJ + j];
-          *reinterpret_cast<f32x4*>(lds + r * Z::SCOLS * 4 + ((u ^ (r & MASK)) << 4)) =
-              f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
-        }
+      for (int g = 0; g < 4; ++g) {
+        const int r = wm * 32 + (lane & 31), u = wn * (8 * Z::FN) + 8 * j + 2 * g + (lane >> 5);
+        const f32x16& t = acc[P][j];
+        *reinterpret_cast<f32x4*>(lds + r * Z::BN * 4 + ((u ^ (r & MASK)) << 4)) =
+            f32x4{t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
+      }
     asm volatile("; pass %0" ::"n"(P) : "memory");
   }
   template <int P>
@@ -368,7 +354,7 @@ struct PrStage {
     __syncthreads();
   }
   MUON_INLINE void run(int r, int col, float v[8]) const {
-    const unsigned char* row = lds + r * Z::SCOLS * 4;
+    const unsigned char* row = lds + r * Z::BN * 4;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const f32x4 t = *reinterpret_cast<const f32x4*>(row + (((col / 4 + q) ^ (r & MASK)) << 4));
@@ -383,17 +369,15 @@ struct PrStage {
 template <class Z, class Out, bool FULL>
 MUON_INLINE void pr_leave_as(const PrStage<Z>& stage, const Out& out, int m0) {
   constexpr bool DUAL = Out::OPS == 2;
-  constexpr int COLS = DUAL ? Z::SCOLS / 2 : Z::SCOLS, LW = COLS / kRun;
+  constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;
   constexpr int STEP = Z::NT / LW, IT = PrStage<Z>::ROWS / STEP, PRE = IT < Out::AHEAD ? IT : Out::AHEAD, ALL = Z::PASSES * IT;
-  static_assert(IT >= 1 && IT % PRE == 0 && (PrStage<Z>::PR % STEP == 0 || STEP % PrStage<Z>::PR == 0), "the threads of a pass take whole rows");
+  static_assert(IT >= 1 && IT % PRE == 0 && (32 % STEP == 0 || STEP % 32 == 0), "the threads of a pass take whole rows");
   const int tid = fresh_tid(), row = tid / LW, col = tid % LW * kRun;
-  // The matrix's row of run g, without the thread's own part, and the columns that
-  // its pass is shifted by.
+  // The matrix's row of run g, without the thread's own part.
   auto row_of = [&](int g) __attribute__((always_inline)) { return m0 + PrStage<Z>::tile_row(g / IT, g % IT * STEP); };
-  auto col_of = [&](int g) __attribute__((always_inline)) { return PrStage<Z>::tile_col(g / IT); };
   typename Out::Pre pre[PRE];
 #pragma unroll
-  for (int g = 0; g < PRE; ++g) out.template pre<PrVariant<FULL>>(row_of(g), col_of(g), pre[g]);
+  for (int g = 0; g < PRE; ++g) out.template pre<PrVariant<FULL>>(row_of(g), pre[g]);
 #pragma unroll 1
   for (int pass = 0; pass < Z::PASSES; ++pass) {
     stage.fill(pass);
@@ -407,8 +391,8 @@ MUON_INLINE void pr_leave_as(const PrStage<Z>& stage, const Out& out, int m0) {
           float v[8], w[8];
           stage.run((q0 + a) * STEP + row, col, v);
           if constexpr (DUAL) stage.run((q0 + a) * STEP + row, COLS + col, w);
-          out.template emit<V>(row_of(g), col_of(g), v, w, pre[a]);
-          out.template pre<V>(row_of(n), col_of(n), pre[a]);
+          out.template emit<V>(row_of(g), v, w, pre[a]);
+          out.template pre<V>(row_of(n), pre[a]);
           __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -425,14 +409,13 @@ template <class Z, class Out>
 MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, int piece, int m0, int n0, unsigned char* lds,
                           const f32x16 (&acc)[Z::FM][Z::FN]) {
   constexpr bool DUAL = Out::OPS == 2;
-  constexpr int COLS = DUAL ? Z::SCOLS / 2 : Z::SCOLS, LW = COLS / kRun;
+  constexpr int COLS = DUAL ? Z::BN / 2 : Z::BN, LW = COLS / kRun;
   const int tid = fresh_tid(), c0 = DUAL ? n0 >> 1 : n0;
   const PrStage<Z> stage{lds, acc};
   if (piece >= 0) {
-    constexpr int PLW = Z::SCOLS / kRun, PSTEP = Z::NT / PLW;
+    constexpr int PLW = Z::BN / kRun, PSTEP = Z::NT / PLW;
     const int row = tid / PLW, col = tid % PLW * kRun;
-    float* part = args->partial + (int64_t)(it.part0 + piece) * Z::BM * Z::BN +
-                  PrStage<Z>::tile_row(0, row) * Z::BN + PrStage<Z>::own_col(col);
+    float* part = args->partial + (int64_t)(it.part0 + piece) * Z::BM * Z::BN + PrStage<Z>::tile_row(0, row) * Z::BN + col;
 #pragma unroll 1
     for (int pass = 0; pass < Z::PASSES; ++pass) {
       stage.fill(pass);
@@ -440,12 +423,12 @@ MUON_INLINE void pr_leave(PrArgsPtr args, PrItemRef it, int piece, int m0, int n
       for (int q = 0; q < PrStage<Z>::ROWS / PSTEP; ++q) {
         float v[8];
         stage.run(q * PSTEP + row, col, v);
-        store_run(part + PrStage<Z>::tile_row(pass, q * PSTEP) * Z::BN + PrStage<Z>::tile_col(pass), 8, v);
+        store_run(part + PrStage<Z>::tile_row(pass, q * PSTEP) * Z::BN, 8, v);
       }
     }
     return;
   }
-  const Out out(it, args, PrLane{PrStage<Z>::tile_row(0, tid / LW), c0 + PrStage<Z>::own_col(tid % LW * kRun)});
+  const Out out(it, args, PrLane{PrStage<Z>::tile_row(0, tid / LW), c0 + tid % LW * kRun});
   if (out.plain() && m0 + Z::BM <= it.m && c0 + (DUAL ? Z::BN / 2 : Z::BN) <= it.n) pr_leave_as<Z, Out, true>(stage, out, m0);
   else pr_leave_as<Z, Out, false>(stage, out, m0);
 }
@@ -546,7 +529,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     for (int p = 0; p < Z::DA; ++p) {
       const int r = (wave * Z::DA + p) * Z::RPI + lane / S;
       row_a[p] = (uint32_t)min(r, rows_a - 1) * (uint32_t)lda;
-      if (p < 2) ch_a[p] = ((lane % S) ^ pr_swz<S>(r)) << 4;
+      if (p < 2) ch_a[p] = ((lane % S) ^ pr_swz(r)) << 4;
     }
 #pragma unroll
     for (int p = 0; p < Z::DB; ++p) {
@@ -648,7 +631,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     for (int i = tid; i < ROWS * S; i += Z::NT) {
       const int r = i / S, ch = i % S;
       const int br = r < Z::BM ? r : r - Z::BM;
-      u32x4* p = reinterpret_cast<u32x4*>(smem + buf + (r < Z::BM ? 0 : Z::AB) + br * RB + ((ch ^ pr_swz<S>(br)) << 4));
+      u32x4* p = reinterpret_cast<u32x4*>(smem + buf + (r < Z::BM ? 0 : Z::AB) + br * RB + ((ch ^ pr_swz(br)) << 4));
       const int have = left - 16 * ch;
       if (have <= 0) {
         *p = u32x4{0u, 0u, 0u, 0u};
@@ -674,7 +657,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
   // its half l / 32 takes chunk 2 kk + half (8 consecutive k), of 64 e4m3 chunks
   // 4 kk + half and 4 kk + 2 + half: the 8-bit MFMA's halves hold k 0-15, 32-47 and
   // 16-31, 48-63, and its scale of half h is that of k 32 h .. 32 h + 31.
-  const int r32 = lane & 31, h = lane >> 5, sw = pr_swz<S>(r32);
+  const int r32 = lane & 31, h = lane >> 5, sw = pr_swz(r32);
   const int G = lane >> 4, i16 = lane & 15;
   typename Z::Frag fa[2][Z::KF][FM], fb[2][Z::KF][FN];
   bf16x8 da[2][FM], db[2][FN];                       // kNT8X: a sub-step's, decoded
@@ -723,18 +706,17 @@ MUON_INLINE void pr_run(unsigned char* smem) {
   auto read_ex = [&](int ks_, int t_) __attribute__((always_inline)) {
     if constexpr (Z::F8) {
       const unsigned char* t = smem + Z::RING + t_ * (Z::EX_A + Z::EX_B);
-      const int row = ks_ * RB / kBlock & 7;
+      const int row = ks_ & 7;
 #pragma unroll
       for (int i = 0; i < FM; ++i)
         na[i] = *reinterpret_cast<const uint32_t*>(t + (row * Z::BM + wm * Z::WM + 32 * i + r32) * 4);
       nb_ = *reinterpret_cast<const uint32_t*>(t + Z::EX_A + (row + 8 * ((wn * Z::WN) / kBlock)) * 4);
     }
   };
-  auto take_ex = [&](int ks_) __attribute__((always_inline)) {  // of K step ks_
+  auto take_ex = [&]() __attribute__((always_inline)) {
     if constexpr (Z::F8) {
-      const int half = RB < kBlock ? ks_ * RB % kBlock / 4 : 0;   // groups of 32, 8 bits each
 #pragma unroll
-      for (int i = 0; i < FM; ++i) sa[i] = na[i] >> (Z::MODE == kNT8 ? 8 * h + half : half);
+      for (int i = 0; i < FM; ++i) sa[i] = Z::MODE == kNT8 ? na[i] >> 8 * h : na[i];  // groups of 32, 8 bits each
       sb = nb_;
     }
   };
@@ -796,7 +778,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
     __syncthreads();                                 // its first stage is in LDS, and the last tile has left
     if (short_stage(ks)) clear(ks, cur);
     read_ex(ks, tab);
-    take_ex(ks);
+    take_ex();
     // The first stage's fragments, into buffer b.
     auto begin = [&](auto b_) __attribute__((always_inline)) {
       constexpr int b = decltype(b_)::value;
@@ -880,7 +862,7 @@ MUON_INLINE void pr_run(unsigned char* smem) {
           }
           if (slot == Z::SLOTS - 1) {
             anchor();
-            take_ex(ks1);
+            take_ex();
 #pragma unroll
             for (int f = 0; f < Z::NF; ++f) decode(PAR ^ 1, 0, f, sa, sb);
           }
@@ -936,7 +918,7 @@ MUON_INLINE void pr_join_of(int edge) {
   const int row0 = (b - tile * per) * (256 / lw), r = threadIdx.x / lw, col = threadIdx.x % lw * kRun;
   const Out out(it, args, PrLane{r, (DUAL ? tn * edge / 2 : tn * edge) + col});
   typename Out::Pre pre;
-  out.template pre<PrAny>(tm * edge + row0, 0, pre);
+  out.template pre<PrAny>(tm * edge + row0, pre);
   const float* p = args->partial + ((int64_t)(it.part0 + tile) * edge + row0 + r) * edge + col;
   const int64_t step = (int64_t)tiles * edge * edge;
   float v[8], w[8];
@@ -953,7 +935,7 @@ MUON_INLINE void pr_join_of(int edge) {
       if constexpr (DUAL) w[e] += y[e];
     }
   }
-  out.template emit<PrAny>(tm * edge + row0, 0, v, w, pre);
+  out.template emit<PrAny>(tm * edge + row0, v, w, pre);
 }
 
 // Workgroups of a launch: as many as the CUs hold at once.
