@@ -174,7 +174,7 @@ class Q8:
 
 def q8_save(x, out: Q8, stream=None) -> Q8:
     """Saves x (bf16 or fp32) into the checkpoint ``out``."""
-    _matrix(x, "x", (out.rows, out.cols))
+    _matrix(x, "x", (out.rows, out.cols)), _matrix(out.q, "out")
     check(lib().muon_q8_save(x.data_ptr(), _ld(x), _code(x), ctypes.byref(out._c),
                              out._streams.use(stream, (x,))))
     return out
@@ -183,7 +183,7 @@ def q8_save(x, out: Q8, stream=None) -> Q8:
 def q8_load(ckpt: Q8, out, stream=None):
     """Writes the values that the checkpoint stands for into ``out`` (bf16, which
     holds them exactly, or fp32)."""
-    _matrix(out, "out", (ckpt.rows, ckpt.cols))
+    _matrix(out, "out", (ckpt.rows, ckpt.cols)), _matrix(ckpt.q, "ckpt")
     check(lib().muon_q8_load(ctypes.byref(ckpt._c), out.data_ptr(), _ld(out), _code(out),
                              ckpt._streams.use(stream, (out,))))
     return out
@@ -240,8 +240,12 @@ class NormSite:
         for t, name in ((self.rstd_y, "rstd_y"), (self.rstd_b, "rstd_b")):
             if t is not None:
                 _matrix(t, name, (rows,), torch.float32, vector=True)
+        for q, name in ((self.u, "u"), (self.v, "v")):
+            if q is not None:
+                _matrix(q.q, name)
         self.d_residual = self.d_branch = self.d_w_pre = self.d_w_post = self.d_gate = None
         self._grads = self._workspace = self._grad_streams = None
+        self._device = torch.cuda.current_device()
         none = muon_q8()
         self._c = muon_norm_site(
             rows, cols, branch.data_ptr(), _ld(branch), residual.data_ptr(), _ld(residual), w_pre.data_ptr(),
@@ -253,12 +257,14 @@ class NormSite:
                                   if t is not None] + [t for q in (self.u, self.v) if q is not None for t in (q.q, q.e)])
 
     def forward(self, stream=None) -> None:
+        _same_device(self._device)
         check(lib().muon_norm_forward(ctypes.byref(self._c), self._streams.use(stream)))
 
     def backward(self, dy, dh, stream=None) -> None:
         shape, dt = tuple(self.y.shape), self.y.dtype
         if self.u is None or self.rstd_y is None:
             _bad("the site keeps no checkpoints: make it with a kind")
+        _same_device(self._device)
         if dy is not None:
             _matrix(dy, "dy", shape, dt)
         _matrix(dh, "dh", shape, dt)
@@ -308,6 +314,7 @@ class WGrad:
             scale, beta, C = (list(item[3:]) + [None, 0.0, None][len(item) - 3:])[:3]
             if not isinstance(x, Q8):
                 _bad("the second entry of an item must be a Q8 checkpoint")
+            _matrix(x.q, "the checkpoint")
             if dts is None:
                 self._dtype, self._gdtype, dts = _code(dY), _code(G), (dY.dtype, G.dtype)
             _matrix(G, "G", dtype=dts[1])
@@ -334,9 +341,11 @@ class WGrad:
         need = ctypes.c_size_t()
         check(lib().muon_wgrad_workspace(self._items, self._n, self._dtype, self._gdtype, ctypes.byref(need)))
         self.workspace = torch.empty(need.value, dtype=torch.uint8, device=tensors[0].device)
+        self._device = torch.cuda.current_device()
         self._streams = _Streams(tensors + [self.workspace])
 
     def run(self, stream=None) -> None:
+        _same_device(self._device)
         check(lib().muon_wgrad(self._items, self._n, self._dtype, self._gdtype, self.workspace.data_ptr(),
                                self.workspace.numel(), self._streams.use(stream)))
 
