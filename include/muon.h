@@ -523,7 +523,8 @@ muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32
  * operands, and bf16 ones that are not 16-byte aligned, are rewritten by a launch
  * before; where there are few tiles, a launch after joins the pieces of their sums.)
  * dtype is that of x, y and the weights. Sums are fp32; s is rounded to dtype
- * once, as the operand of the last product, y once. bf16: bf16 MFMA. fp32: every
+ * once, as the operand of the last product (to 16 bits where one or two rows keep no
+ * checkpoints), y once. bf16: bf16 MFMA. fp32: every
  * operand is cut into three bf16 numbers that add up to it (24 bits, of numbers
  * below 2^-110 fewer), and the six products down to 2^-24 of the largest are
  * summed: fp32 accuracy at six times the work. Infinities are what they are in an

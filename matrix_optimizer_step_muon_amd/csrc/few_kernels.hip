@@ -90,9 +90,9 @@ MUON_INLINE f32x4 few_mfma(const bf16x8 (&b)[PARTS], const bf16x8 (&a)[PARTS], f
 
 // The sums of all waves, of this thread's output (row t / 16 of A, row t % 16 of B of
 // each 16 of the workgroup's). An MFMA's element r of lane l is B's row 4 (l / 16) + r,
-// A's l % 16.
+// A's l % 16. `halves`: A's rows 8 to 15 are what rows 0 to 7 have beside.
 template <int WAYS>
-MUON_INLINE void few_join(float (&red)[kFewWaves][WAYS][256], const f32x4 (&acc)[WAYS], float v[WAYS]) {
+MUON_INLINE void few_join(float (&red)[kFewWaves][WAYS][256], const f32x4 (&acc)[WAYS], float v[WAYS], bool halves = false) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
 #pragma unroll
   for (int o = 0; o < WAYS; ++o)
@@ -101,6 +101,10 @@ MUON_INLINE void few_join(float (&red)[kFewWaves][WAYS][256], const f32x4 (&acc)
   __syncthreads();
 #pragma unroll
   for (int o = 0; o < WAYS; ++o) v[o] = 0.f;
+  if (halves && tid < 128)
+    for (int w = 0; w < waves; ++w)
+#pragma unroll
+      for (int o = 0; o < WAYS; ++o) v[o] += red[w][o][tid + 128];
   if (tid < 256)
     for (int w = 0; w < waves; ++w)
 #pragma unroll
@@ -108,6 +112,11 @@ MUON_INLINE void few_join(float (&red)[kFewWaves][WAYS][256], const f32x4 (&acc)
 }
 
 // bf16 or fp32. OPS 2: s = act(a) * b; 1: the product itself. G: sixteens of rows of B.
+// Rounding s to bf16 costs as much accuracy as rounding y does. With up to kFewHalves rows
+// s has a second plane with the next 8 bits in columns of the MFMA that are idle. What
+// that takes is reading twice the rows of s: 2048 x 6144, weights from HBM, with one plane
+// and two, 1 row 20.8 and 21.0 us, 2 rows 20.8 and 21.2, 4 rows 21.1 and 22.2, 8 rows 22.1
+// and 24.3; 5120 x 25600, 1 row 137.0 and 137.6, 8 rows 147 and 159.
 template <class T, int OPS, int G>
 __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(FewArgs p) {
   typedef FewRun<T> Run;
@@ -115,7 +124,9 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(FewArgs p) {
   __shared__ float red[kFewWaves][WAYS][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int n0 = blockIdx.x * p.per, n1 = min(n0 + p.per, p.n), q = lane >> 4;
-  const T* xr = static_cast<const T*>(p.a) + (int64_t)min(lane & 15, p.m - 1) * p.lda;
+  const bool halves = OPS == 1 && sizeof(T) == 2 && p.plane;
+  const T* xr = static_cast<const T*>(p.a) + (int64_t)min(halves ? lane & 7 : lane & 15, p.m - 1) * p.lda;
+  if (halves && lane & 8) xr += p.plane;
   const T* wr[WAYS];
 #pragma unroll
   for (int o = 0; o < WAYS; ++o)
@@ -175,7 +186,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(FewArgs p) {
     }
   }
   float v[WAYS];
-  few_join<WAYS>(red, acc, v);
+  few_join<WAYS>(red, acc, v, halves);
   const int row = tid >> 4;
   if (tid >= 256 || row >= p.m) return;
 #pragma unroll
@@ -184,7 +195,17 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_kernel(FewArgs p) {
     if (col >= n1) return;
     float y = v[OPS * g];
     if constexpr (OPS == 2) y = activation(y, p.act) * v[OPS * g + 1];
-    Elem<T>::store(static_cast<T*>(p.out) + (int64_t)row * p.ldo + col, y);
+    T* to = static_cast<T*>(p.out) + (int64_t)row * p.ldo + col;
+    if constexpr (OPS == 2 && sizeof(T) == 2) {
+      if (p.plane) {
+        u16 hi, lo;
+        cut2(y, hi, lo);
+        *((g_u16*)to) = hi;
+        *((g_u16*)(to + p.plane)) = lo;
+        continue;
+      }
+    }
+    Elem<T>::store(to, y);
   }
 }
 

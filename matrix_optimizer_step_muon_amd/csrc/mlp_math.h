@@ -32,6 +32,14 @@ MUON_INLINE void cut3(const float v[8], u32x4 parts[3]) {
     for (int i = 0; i < 4; ++i) parts[q][i] = __builtin_amdgcn_perm(p[q][2 * i + 1], p[q][2 * i], 0x07060302u);  // the upper halves
 }
 
+// An fp32 number as two bf16 ones that add up to 16 bits of it, with the same care for
+// infinities in the other operand.
+MUON_INLINE void cut2(float x, u16& hi, u16& lo) {
+  const float most = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  hi = (u16)(__float_as_uint(x) >> 16);
+  lo = f32_to_bf16(copysignf(fmaxf(fabsf(x - most), fabsf(x * 0x1p-64f)), x));
+}
+
 // 1 / (1 + e^-x); e^-x in the hardware's exponential of base 2: a relative error of
 // (|x| + 2) 2^-24 or so.
 MUON_INLINE float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x)); }

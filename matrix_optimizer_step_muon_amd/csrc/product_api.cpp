@@ -216,7 +216,7 @@ struct MlpCall {
   muon::PrArgs first{}, second{};
   bool few_first = false, few_second = false;  // forward: by the kernels for few rows
   char* s = nullptr;                           // forward: s between the two products
-  int64_t ld_s = 0;
+  int64_t ld_s = 0, plane_s = 0;               // plane_s: in two planes, so far apart
   size_t bytes = 0;
 };
 
@@ -274,9 +274,12 @@ muon_status plan_forward(const muon_mlp& p, MlpCall& c, char* ws) {
   c.ops[1] = operand(b, first, p.w_gate, p.inner, p.width, p.width, p.dtype);
   c.ops[2] = operand(b, first, p.w_up, p.inner, p.width, p.width, p.dtype);
   c.ops[3] = operand(b, second, p.w_down, p.out, p.inner, p.inner, p.dtype);
+  // and between those kernels bf16 is two planes, for so few rows that it costs 1 or 2%
+  const bool two = !plain && p.y && c.few_first && c.few_second && p.rows <= muon::kFewHalves;
   c.ld_s = plain ? p.inner : pad8(p.inner);
+  c.plane_s = two ? p.rows * c.ld_s : 0;
   const Operand s{nullptr, p.rows, p.inner, c.ld_s, true,
-                  b.take(plain ? size_t(p.rows) * size_t(p.inner) * 4 : planes_bytes(p.rows, p.inner, parts))};
+                  b.take(plain ? size_t(p.rows) * size_t(p.inner) * 4 : planes_bytes(p.rows, p.inner, two ? 2 : parts))};
   c.s = ws + s.at;
   muon::PrItem& f = c.first.item[0];
   put_operand(f, true, 0, c.ops[0], ws, parts);
@@ -343,7 +346,7 @@ muon_status plan_backward(const muon_mlp& p, const muon_mlp_grads& g, MlpCall& c
   return MUON_OK;
 }
 
-muon_status launch_few_gate(const muon_mlp& p, void* s, int64_t ld, hipStream_t stream) {
+muon_status launch_few_gate(const muon_mlp& p, const MlpCall& c, hipStream_t stream) {
   muon::FewArgs a{};
   a.a = p.x;
   a.lda = p.ld_x;
@@ -354,15 +357,17 @@ muon_status launch_few_gate(const muon_mlp& p, void* s, int64_t ld, hipStream_t 
   a.n = int32_t(p.inner);
   a.k = int32_t(p.width);
   a.act = p.act;
-  a.out = s;
-  a.ldo = ld;
+  a.out = c.s;
+  a.ldo = c.ld_s;
+  a.plane = c.plane_s;
   return hip_status(muon::launch_few(a, p.dtype == MUON_F32, 2, stream));
 }
 
-muon_status launch_few_down(const muon_mlp& p, const void* s, int64_t ld, hipStream_t stream) {
+muon_status launch_few_down(const muon_mlp& p, const MlpCall& c, hipStream_t stream) {
   muon::FewArgs a{};
-  a.a = s;
-  a.lda = ld;
+  a.a = c.s;
+  a.lda = c.ld_s;
+  a.plane = c.plane_s;
   a.b[0] = p.w_down;
   a.ldb = p.inner;
   a.m = int32_t(p.rows);
@@ -470,10 +475,10 @@ muon_status mlp_forward(const muon_mlp* mlp, void* stream) {
   MUON_TRY(check_mlp_workspace(v, p, c.bytes));
   MUON_TRY(v.disjoint());
   MUON_TRY(run_packs(c, p, ws, s));
-  if (c.few_first) MUON_TRY(launch_few_gate(p, c.s, c.ld_s, s));
+  if (c.few_first) MUON_TRY(launch_few_gate(p, c, s));
   else MUON_TRY(hip_status(muon::launch_mlp(c.first, muon::kPrGate, false, s)));
   if (!p.y) return MUON_OK;
-  if (c.few_second) return launch_few_down(p, c.s, c.ld_s, s);
+  if (c.few_second) return launch_few_down(p, c, s);
   return hip_status(muon::launch_mlp(c.second, muon::kPrStore, false, s));
 }
 

@@ -74,9 +74,10 @@ struct PrArgs {
 };
 
 // A product of at most kFewRows rows (few_kernels.hip). Strides in elements.
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 16, kFewHalves = 2;
 struct FewArgs {
   const void* a;             // m x k
+  int64_t plane;             // bf16 gated block: distance of the two planes (hi, lo) that s is cut into, or 0: one
   const void* b[2];          // n x k; the two projections of the gated block
   const uint8_t *ea, *eb;    // as in PrItem
   int64_t lda, ldb, lde, ldeb_n, ldeb_k;
