@@ -5,8 +5,9 @@
 // its waves blocks of K in turn, so that it reads runs of consecutive bytes of these
 // rows. So many rows that every CU gets the same share: 16 always would leave 64 of
 // 256 CUs with twice the others' work at 5120 rows, and half of them without at 2048
-// (8-bit weights of 5120 x 25600 then take 32.9 us, and 24.4 as it is: 5.4 TB/s; in
-// bf16 2048 x 6144 9.0 and 7.1, both projections of 25600 x 5120 97.4 and 89.0). Every
+// (8-bit weights of 5120 x 25600 then take 32.9 us, and 24.4 as it is; in bf16 2048 x
+// 6144 9.0 and 7.1, both projections of 25600 x 5120 97.4 and 89.0: the first two from the
+// last-level cache, from HBM 28.5, 4.6 TB/s, and 8.4; the last, 5.9 TB/s, from HBM). Every
 // lane loads the 16 bytes that its MFMA operand is, straight into registers: B's rows
 // are the MFMA's rows, A's its columns (past the last one the last one again). A wave
 // asks for its next block before it multiplies the one at hand: 8 to 16 KB in flight a

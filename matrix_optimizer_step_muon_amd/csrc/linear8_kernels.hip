@@ -4,7 +4,7 @@
 //
 // The weight is kept in both orientations, so both products read their operands
 // along K. Scales are powers of two, which the 8-bit MFMA applies by itself. 8192 x
-// 25600 x 5120 979 us either way (2190 TFLOP/s), 1024 x 8192 x 5120 60 (1430), in tiles of
+// 25600 x 5120 976 us either way (2200 TFLOP/s), 1024 x 8192 x 5120 57 (1500), in tiles of
 // 128 x 128.
 
 #include <hip/hip_runtime.h>

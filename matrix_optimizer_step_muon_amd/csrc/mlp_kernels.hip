@@ -9,12 +9,12 @@
 // over both pairs. The weights are read as they lie: forward along their rows,
 // backward with transposing LDS reads.
 //
-// 4096 x 2048 x 6144 bf16, silu, int8 checkpoints: 212, 96 + 14, 146 and 178 + 14 us (974,
-// 940, 708 and 1074 TFLOP/s), the second terms joining pieces. The epilogues of the first
+// 4096 x 2048 x 6144 bf16, silu, int8 checkpoints: 212, 95 + 15, 143 and 175 + 15 us (973,
+// 937, 721 and 1085 TFLOP/s), the second terms joining pieces. The epilogues of the first
 // and the third are 17 and 22 of 70 us of a 256 x 256 tile, with the matrix units idle:
 // all CUs come to them together and move 43 and 84 MB a round (2.7 and 4.2 TB/s; more
-// of a thread's runs at once gained nothing). At 5120 x 25600 the products reach 1054
-// and 1020 TFLOP/s.
+// of a thread's runs at once gained nothing). At 5120 x 25600 the products reach 1075
+// and 1014 TFLOP/s.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -11,9 +11,9 @@
 // instruction covers whole lines, and a group of a checkpoint is four lanes.
 //
 // Bound by the matrix units and what goes between their instructions: 256 x 256 tiles
-// with one wave per SIMD, 1200 to 1250 TFLOP/s in bf16 (4096 x 5120 x 25600: 893 us; MFMA
-// busy 60% of the cycles at 1.9 GHz, near the power limit) and 2190 in 8 bits (8192 x
-// 25600 x 5120: 979 us, 51%). Smaller tiles where there are fewer: 128 x 128, two
+// with one wave per SIMD, 1200 to 1250 TFLOP/s in bf16 (4096 x 5120 x 25600: 881 us; MFMA
+// busy 60% of the cycles at 1.9 GHz, near the power limit) and 2200 in 8 bits (8192 x
+// 25600 x 5120: 976 us, 51%). Smaller tiles where there are fewer: 128 x 128, two
 // workgroups per CU, and 64 x 64. They are bound by LDS, which a stage's copies and
 // fragments keep busy 1.5 and 3 times as long as its MFMAs the matrix units.
 #pragma once

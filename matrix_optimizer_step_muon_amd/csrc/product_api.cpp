@@ -28,7 +28,8 @@ constexpr double kHbm = 5.2e6;  // bytes per us: what streaming the weights of f
 // activations once for every share. One MI355X, bf16, 1 and 16 rows: both projections
 // of 25600 x 5120 89 and 104 us (estimated 89 and 102; in tiles 109 and 113), of 6144 x
 // 2048 10.8 and 11.3 (10.4 and 11.7); one of 5120 x 25600 48 and 60 to 65 (46 and 62; in
-// tiles 56 and 57), of 2048 x 6144 7.1 and 11.0 (6.2 and 10.1; in tiles 13.6).
+// tiles 56 and 57), of 2048 x 6144 7.1 and 11.0 (6.2 and 10.1; in tiles 13.6). Those of 6144
+// x 2048 were in the last-level cache both ways; from HBM they take 12.4 and 8.4 (1 row).
 double few_us(int64_t n, double row, int ops, int64_t rows) {
   const muon::FewShare f = muon::few_share(n, muon::kFewMost);
   const double weights = double(f.per * ops);
