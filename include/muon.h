@@ -523,12 +523,12 @@ muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32
  * operands, and bf16 ones that are not 16-byte aligned, are rewritten by a launch
  * before; where there are few tiles, a launch after joins the pieces of their sums.)
  * dtype is that of x, y and the weights. Sums are fp32; s is rounded to dtype
- * once, as the operand of the last product (to 16 bits where one or two rows keep no
- * checkpoints), y once. bf16: bf16 MFMA. fp32: every
- * operand is cut into three bf16 numbers that add up to it (24 bits, of numbers
- * below 2^-110 fewer), and the six products down to 2^-24 of the largest are
- * summed: fp32 accuracy at six times the work. Infinities are what they are in an
- * fp32 sum, but for products with numbers below 2^-62, which may be NaN.
+ * once, as the operand of the last product (to 16 bits where one or two rows keep
+ * no checkpoints), y once. bf16: bf16 MFMA. fp32: every operand is cut into three
+ * bf16 numbers that add up to it (24 bits, of numbers below 2^-110 fewer), and the
+ * six products down to 2^-24 of the largest are summed: fp32 accuracy at six times
+ * the work. Infinities are what they are in an fp32 sum, but for products with
+ * numbers below 2^-62, which may be NaN.
  * x       rows x width
  * w_gate, w_up  inner x width, w_down  out x inner, contiguous (muon_matrix.w)
  * y       rows x out, written (NULL: only the checkpoints are wanted)
@@ -537,9 +537,10 @@ muon_status muon_wgrad_info(const muon_wgrad_item* items, int32_t n_items, int32
  *         weight gradient of w_down (muon_wgrad) s
  * width, inner and out are at most 2^22, and so are the row strides of y, d_x, d_a
  * and d_b.
- * workspace: device memory of at least muon_mlp_exact_workspace bytes (muon_mlp_workspace
- * for any tensors of these sizes), 16-byte aligned, scratch of a call until it has run; a call on it in a captured graph writes it
- * anew with every replay.
+ * workspace: device memory of at least muon_mlp_exact_workspace bytes
+ * (muon_mlp_workspace for any tensors of these sizes), 16-byte aligned, scratch of a
+ * call until it has run; a call on it in a captured graph writes it anew with every
+ * replay.
  * act: MUON_ACT_SILU a/(1+e^-a), MUON_ACT_GELU a Phi(a) (Phi the normal
  * distribution), MUON_ACT_GELU_TANH its approximation by a tanh, a (1 +
  * tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2, MUON_ACT_RELU max(a, 0). */
